@@ -2,7 +2,7 @@
 
 Argument marshalling only: every function here turns torch tensors into device
 pointers and calls the C entry point of the same name declared in
-``include/tbe.h``; all computation happens in the library's HIP kernels.
+``include/tbe.h`` or ``include/tbe_tower.h`` (tower.py); all computation happens in the library's HIP kernels.
 PyTorch provides device memory and the current stream.  There is no fallback:
 if the library is missing or a call fails, an exception is raised.
 """
@@ -66,7 +66,7 @@ class tbe_runs_view(ctypes.Structure):
 
 
 # every symbol the headers in include/ declare, with its ctypes signature
-_P = ctypes.c_void_p
+_P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 _SIGS = {
     "tbe_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "tbe_last_error": ([], ctypes.c_char_p),
@@ -93,6 +93,23 @@ _SIGS = {
                                       ctypes.c_size_t, _P, _P], ctypes.c_int),
     "tbe_transpose": ([_P, _P, ctypes.c_int32, _P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
                        _P, ctypes.c_size_t, _P, _P, _P], ctypes.c_int),
+    # the dense tower (include/tbe_tower.h)
+    "tbe_layer_norm_forward": ([_I64, _I64, _P, _I64, _I32, _P, _P, _I32, ctypes.c_float, _P, _I64,
+                                _I32, _P, _P, _P], ctypes.c_int),
+    "tbe_layer_norm_backward_workspace_bytes": ([_I64, _I64], ctypes.c_size_t),
+    "tbe_layer_norm_backward": ([_I64, _I64, _P, _I64, _I32, _P, _I64, _I32, _P, _P, _P, _I32, _P,
+                                 _I64, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "tbe_grouped_linear_forward": ([_I64, _I32, _I64, _I64, _P, _I64, _P, _P, _I32, _P, _I32, _P,
+                                    _I64, _I32, _P], ctypes.c_int),
+    "tbe_grouped_linear_backward_input": ([_I64, _I32, _I64, _I64, _P, _I64, _P, _I32, _P, _I32, _P,
+                                           _I64, _I32, _P], ctypes.c_int),
+    "tbe_grouped_linear_backward_weight_workspace_bytes": ([_I64, _I32, _I64, _I64], ctypes.c_size_t),
+    "tbe_grouped_linear_backward_weight": ([_I64, _I32, _I64, _I64, _P, _I64, _P, _I64, _I32, _P,
+                                            _I32, _P, _P, _I32, _P, ctypes.c_size_t, _P],
+                                           ctypes.c_int),
+    "tbe_adamw_step": ([_P, _I32, _I64, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                        ctypes.c_double, _P, _P], ctypes.c_int),
+    "tbe_adamw_state_read": ([_P, _I32, _P, _P, _I32, _P], ctypes.c_int),
     # measurement hooks (include/tbe_measure.h)
     "tbe_profile_select": ([ctypes.c_char_p], ctypes.c_int),
     "tbe_profile_read": ([_P, _P], ctypes.c_int),
@@ -318,3 +335,12 @@ def device_view(ptr: int, n: int, dtype: torch.dtype, like: torch.Tensor) -> tor
     assert 0 <= off and off + n * esize <= like.numel() * like.element_size() and off % esize == 0
     flat = like.view(torch.uint8)[off:off + n * esize]
     return flat.view(dtype).clone()
+
+
+from .tower import (AdamWTensors, TBE_ADAMW_BLOCK, TBE_ADAMW_CONTROL, TBE_LAYER_NORM_MAX_WIDTH,  # noqa: E402,F401
+                    TBE_STATE_8BIT, TBE_STATE_F32, tbe_adamw_state_read, tbe_adamw_step,
+                    tbe_adamw_tensor, tbe_grouped_linear_backward_input,
+                    tbe_grouped_linear_backward_weight,
+                    tbe_grouped_linear_backward_weight_workspace_bytes, tbe_grouped_linear_forward,
+                    tbe_layer_norm_backward, tbe_layer_norm_backward_workspace_bytes,
+                    tbe_layer_norm_forward)
