@@ -1,6 +1,7 @@
 // Linear layers of E experts on rows grouped by expert: argument validation, dispatch and the
 // kernel.
 #include "grouped_linear.h"
+#include "grouped_tile.h"
 
 #include "../../include/tbe_tower.h"
 
@@ -123,9 +124,39 @@ tbe_status launch_any(const GroupedArgs& a, hipStream_t s) {
   return check_launch(what);
 }
 
+const char* name_of(int op) { return op == kForward ? "grouped_forward" : op == kBackwardInput ? "grouped_input" : "grouped_weight"; }
+
+template <int DT, int OP, int BM, int BN, int WM, int WN, bool DIRECT>
+tbe_status launch_tile(const GroupedArgs& a, hipStream_t s) {
+  const int n = OP == kForward ? a.outer : a.inner;
+  const int n_tiles = (n + BN - 1) / BN;
+  const int64_t tiles = OP == kBackwardWeight ? static_cast<int64_t>(a.experts) * ((a.outer + BM - 1) / BM) : row_tiles_bound(a, BM);
+  ProfScope ps(name_of(OP), s);
+  hipLaunchKernelGGL((grouped_tile_kernel<DT, OP, BM, BN, WM, WN, DIRECT>), dim3(static_cast<unsigned>(tiles * n_tiles)),
+                     dim3(WM * WN * kWave), 0, s, a, n_tiles);
+  return check_launch(name_of(OP));
+}
+
+// Whether every 16-byte chunk of the operands is whole and starts on 16 bytes, and a tile's offsets
+// stay below 2^31.
+bool chunked(const GroupedArgs& a, int op) {
+  auto whole = [](const void* p, int64_t ld, int64_t contiguous) {
+    return !(reinterpret_cast<uintptr_t>(p) & 15) && ld % 8 == 0 && contiguous % 8 == 0 && ld < (int64_t{1} << 21);
+  };
+  const int64_t xs = a.rows > 1 ? a.x_stride : a.inner, gs = a.rows > 1 ? a.gy_stride : a.outer;
+  if (op == kForward) return whole(a.x, xs, a.inner) && whole(a.w, a.inner, a.inner);
+  if (op == kBackwardInput) return whole(a.gy, gs, a.outer) && whole(a.w, a.inner, a.inner);
+  return whole(a.gy, gs, a.outer) && whole(a.x, xs, a.inner);
+}
+
+template <int DT, int OP>
+tbe_status launch_type(const GroupedArgs& a, hipStream_t s) {
+  return chunked(a, OP) ? launch_tile<DT, OP, 256, 256, 2, 4, true>(a, s) : launch_tile<DT, OP, 256, 256, 2, 4, false>(a, s);
+}
+
 template <int OP>
 tbe_status launch(const GroupedArgs& a, int dtype, hipStream_t s) {
-  return dtype == TBE_F16 ? launch_any<1, OP>(a, s) : launch_any<2, OP>(a, s);
+  return dtype == TBE_F16 ? launch_type<1, OP>(a, s) : launch_type<2, OP>(a, s);
 }
 
 bool aligned_to(const void* p, int dt) { return !(reinterpret_cast<uintptr_t>(p) & (dt == TBE_F32 ? 3u : 1u)); }
