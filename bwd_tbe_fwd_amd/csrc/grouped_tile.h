@@ -1,5 +1,5 @@
 // The tiled kernel of the grouped products (grouped_linear.h says what m, n, k, "along" and
-// "across" are): a workgroup takes BM x BN of C and walks k in steps of 64 through two LDS buffers.
+// "across" are): a workgroup takes BM x BN of C and walks k in steps of 32 through S LDS buffers.
 //
 // Bound by the matrix instructions where the sides are large, so everything else has to stay out of
 // their way:
@@ -8,9 +8,10 @@
 //    matrix's edge get an offset past the buffer's range and so write zeros: the edges of the
 //    groups cost no branch in the loop.  Rows that do not start on 16 bytes (or k or n that are not
 //    whole 16 bytes) go through registers instead, with the same LDS layout.
-//  * LDS holds an operand as it lies in memory, along: [m][64 k], across: [64 k][m].  The 16-byte
-//    columns of a row are exchanged by a pattern of the row (along) or the 32-byte columns by one of
-//    k (across), so that the 16 rows that a read takes lie in different banks.
+//  * LDS holds an operand as it lies in memory, along: [m][32 k], across: [32 k][m].  The 16-byte
+//    columns of an along row are exchanged by a pattern of the row, and the across rows are put in an
+//    order with gaps, so that what a read takes lies in different banks.  A lane's place in a read
+//    is a base that never changes plus a constant: no address arithmetic between the products.
 //  * An across operand is turned on the way from LDS to the registers (ds_read_b64_tr_b16: 16 lanes
 //    read 4 k x 16 m and each gets 4 k of one m).
 //  * The products are taken as C^T: a lane then holds adjacent n of one m, 4 of each product.  Where B
@@ -18,10 +19,13 @@
 //    products give 4 NF adjacent n (an across read of such n would meet in the same banks).
 #pragma once
 
+#include <type_traits>
+
 #include "grouped_linear.h"
 
 namespace tbe {
 
+constexpr int kStepK = 32;                  // k of a step: one product's
 constexpr uint32_t kOutside = 0x80000000u;  // a buffer offset past any range
 
 typedef uint16_t u16x4_t __attribute__((ext_vector_type(4)));
@@ -29,20 +33,23 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
-// Exchange of an along row's K / 8 columns of 16 bytes.  A 16-byte LDS read is served 16 lanes at a
-// time, lanes 0-3, 12-15 and 20-27, then 4-11, 16-19 and 28-31: of rows q = row / 4 (or the 4 blocks of
-// 16 that a read of B takes), 0 and 3 at one column with 1 and 2 at the next.  With these patterns
-// they differ in their place within 256 bytes, all banks (conflict counter: 0).
-template <int K>
+// Exchange of an along row's 4 columns of 16 bytes.  A 16-byte LDS read is served 16 lanes at a time,
+// lanes 0-3, 12-15 and 20-27, then 4-11, 16-19 and 28-31: of the blocks q = 0 .. 3 of 4 rows that a
+// read takes, 0 and 3 at one column with 1 and 2 at the next.  With these patterns they differ in
+// their place within 256 bytes, all banks (conflict counter: 0).  A read's blocks lie `GAP` rows apart.
+template <int GAP>
 __device__ __forceinline__ int along_pattern(int r) {
-  const int h = ((r >> 2) ^ (r >> 4)) & 3;
-  return K == 64 ? ((r >> 1) & 1) | h << 1 : h ^ (h & 1) << 1;
+  const int q = (r / GAP) & 3;
+  return q ^ (q & 1) << 1;
 }
-// Exchange of an across row's columns of 32 bytes: k of the 4 x 4 rows that a read takes differ.
+// Place of an across row k in LDS, in elements.  A load instruction fills 1024 bytes: rows k = 8 g + 4 h
+// + r of one r together (h = 0, 1, and g & 1 where a row has 256 bytes), 32 bytes before those of
+// the next r: the 4 rows of a read, and those of the next 16 lanes' read, lie in different banks.
 template <int SIDE>
-__device__ __forceinline__ int across_pattern(int k) {
-  const int f = (k & 3) | ((k >> 3) & 1) << 2;
-  return SIDE >= 128 ? f : f & 3;
+__device__ __forceinline__ int across_place(int k) {
+  const int r = k & 3, h = (k >> 2) & 1, g = k >> 3;
+  if constexpr (SIDE == 256) return (4 * g + r) * (512 + 16) + h * SIDE;
+  else return (4 * (g >> 1) + r) * (512 + 16) + ((g & 1) * 2 + h) * SIDE;
 }
 
 // 16 bytes a lane from offset `o` of the buffer to LDS, lane l's at lds + 16 l.  Written as an
@@ -53,13 +60,15 @@ __device__ __forceinline__ void load_to_lds(u32x4 r, uint32_t o, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(o), "s"(r) : "memory");
 }
 
-// One operand's tile of SIDE m by K k, THREADS threads.
-template <bool ALONG, int SIDE, int K, int THREADS, bool DIRECT>
+// One operand's tile of SIDE m by kStepK k, THREADS threads.
+template <bool ALONG, int SIDE, int GAP, int THREADS, bool DIRECT>
 struct Operand {
-  static constexpr int kChunks = SIDE * K / 8;     // of 16 bytes
+  static constexpr int K = kStepK;
+  static constexpr int kChunks = SIDE * K / 8;          // of 16 bytes
   static constexpr int kEach = kChunks / THREADS;
-  static constexpr int kRowChunks = ALONG ? K / 8 : SIDE / 8;
+  static constexpr int kElems = ALONG ? SIDE * K : SIDE * K / 512 * (512 + 16);  // of an LDS buffer
   static_assert(kChunks % THREADS == 0, "whole chunks a thread");
+  static_assert(ALONG || SIDE == 256 || SIDE == 128, "1024 bytes a load instruction");
 
   const uint16_t* base;  // (m0, k = 0)
   int64_t ld;
@@ -67,12 +76,23 @@ struct Operand {
   uint32_t at[kEach];    // DIRECT: byte offset of a chunk, or kOutside
   u16x8_t reg[DIRECT ? 1 : kEach];
 
-  // row of LDS (m or k) and the chunk of the matrix's row that a thread's i-th chunk holds
+  // row of the matrix (m or k within the tile) and its chunk that a thread's i-th chunk holds
   __device__ __forceinline__ static void place(int i, int& row, int& chunk) {
     const int q = i * THREADS + threadIdx.x;
-    row = q / kRowChunks;
-    const int slot = q % kRowChunks;
-    chunk = ALONG ? slot ^ along_pattern<K>(row) : slot ^ (across_pattern<SIDE>(row) << 1);
+    if constexpr (ALONG) {
+      row = q / (K / 8);
+      chunk = q % (K / 8) ^ along_pattern<GAP>(row);
+    } else {
+      const int u = q / 64, v = q % 64;  // load instruction, lane
+      chunk = v % (SIDE / 8);
+      if constexpr (SIDE == 256) row = 8 * (u >> 2) + (u & 3) + 4 * (v >> 5);
+      else row = 16 * (u >> 2) + (u & 3) + 4 * (v >> 4);
+    }
+  }
+  // where a thread's i-th chunk lies in LDS, in elements: lane l's 8 l after lane 0's
+  __device__ __forceinline__ static int lds_place(int i) {
+    const int q = i * THREADS + threadIdx.x;
+    return ALONG ? q * 8 : q / 64 * (512 + 16) + q % 64 * 8;
   }
   __device__ __forceinline__ void init(const uint16_t* p, int64_t stride, int64_t m_left, int64_t k_left) {
     base = p;
@@ -89,67 +109,57 @@ struct Operand {
       }
     }
   }
-  // Starts the loads of step k0.
-  __device__ __forceinline__ void load(int64_t k0, uint16_t* __restrict s) {
+  // Starts the i-th load of step k0 (of kEach).
+  __device__ __forceinline__ void load(int i, int64_t k0, uint16_t* s) {
     const uint16_t* p = base + (ALONG ? k0 : k0 * ld);
-    const int64_t left = ks - k0;
+    int row, chunk;
+    place(i, row, chunk);
     if constexpr (DIRECT) {
       const uint64_t u = reinterpret_cast<uint64_t>(p);
       const u32x4 r = {static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32) & 0xffffu, 0x7fffffffu, 0x00027000u};
-      const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)s)) +
-                           __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (kWave * 16);
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        uint32_t o = at[i];
-        if (left < K) {
-          int row, chunk;
-          place(i, row, chunk);
-          if ((ALONG ? chunk * 8 : row) >= left) o = kOutside;
-        }
-        load_to_lds(r, o, lds + i * THREADS * 16);
-      }
+      const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      const int to = ALONG ? (i * THREADS + w * kWave) * 8 : (i * (THREADS / kWave) + w) * (512 + 16);
+      uint32_t o = at[i];
+      const int left = static_cast<int>(min(ks - k0, static_cast<int64_t>(K)));
+      if (left < K && (ALONG ? chunk * 8 : row) >= left) o = kOutside;
+      load_to_lds(r, o, static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)(s + to))));
     } else {
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        int row, chunk;
-        place(i, row, chunk);
-        Vec<uint16_t, 8> v;
-        const int64_t n = (ALONG ? row < ms : row < left) ? (ALONG ? left : ms) - chunk * 8 : 0;
-        load_vec_part<uint16_t, 8>(p + row * ld + chunk * 8, n, v);
-        __builtin_memcpy(&reg[i], v.e, 16);
-      }
+      const int64_t left = ks - k0;
+      Vec<uint16_t, 8> v;
+      const int64_t n = (ALONG ? row < ms : row < left) ? (ALONG ? left : ms) - chunk * 8 : 0;
+      load_vec_part<uint16_t, 8>(p + row * ld + chunk * 8, n, v);
+      __builtin_memcpy(&reg[i], v.e, 16);
     }
   }
   // Registers to LDS, where the loads went there.
   __device__ __forceinline__ void store(uint16_t* s) {
     if constexpr (!DIRECT) {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) *reinterpret_cast<u16x8_t*>(s + (i * THREADS + threadIdx.x) * 8) = reg[i];
+      for (int i = 0; i < kEach; ++i) *reinterpret_cast<u16x8_t*>(s + lds_place(i)) = reg[i];
+    }
+  }
+  // This lane's place in a read of the 8 k from 8 (lane / 16) on of one m.  Along: of m itself.  Across:
+  // m is the first of the 4 adjacent m that this lane reads for its 16 lanes; it gets the (lane %
+  // 16)-th.  read() takes an m that is a multiple of 16 (or, along, of 4 within GAP) further.
+  __device__ __forceinline__ static int read_place(int m) {
+    const int l = lane_id(), g = l >> 4;
+    return ALONG ? m * K + ((g ^ along_pattern<GAP>(m)) << 3) : across_place<SIDE>(8 * g + ((l & 15) >> 2)) + m;
+  }
+  __device__ __forceinline__ static u16x8_t read(const uint16_t* s, int m_further) {
+    if constexpr (ALONG) {
+      return *reinterpret_cast<const u16x8_t*>(s + m_further * K);
+    } else {
+      u16x8_t r;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(s + m_further + h * SIDE));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[4 * h + i] = static_cast<uint16_t>(v[i]);
+      }
+      return r;
     }
   }
 };
-
-// The 8 k from 32 step + 8 (lane / 16) on of one m: along: m = `m` of this lane; across: `m` is the
-// first of the 4 adjacent m that this lane reads for its group of 16, and the lane gets the group's
-// (lane % 16)-th.
-template <bool ALONG, int SIDE, int K>
-__device__ __forceinline__ u16x8_t fragment(const uint16_t* s, int m, int step) {
-  const int l = lane_id(), g = l >> 4;
-  if constexpr (ALONG) {
-    return *reinterpret_cast<const u16x8_t*>(s + m * K + (((4 * step + g) ^ along_pattern<K>(m)) << 3));
-  } else {
-    u16x8_t r;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = 32 * step + 8 * g + 4 * h + ((l & 15) >> 2);
-      const uint16_t* p = s + k * SIDE + (((m >> 4) ^ across_pattern<SIDE>(k)) << 4) + (m & 15);
-      const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[4 * h + i] = static_cast<uint16_t>(v[i]);
-    }
-    return r;
-  }
-}
 
 // N floats of row `p` of out from column n on, `left` of them inside.
 template <int N>
@@ -184,16 +194,16 @@ __device__ __forceinline__ unsigned chiplet_order(unsigned id, unsigned n) {
   return x * q + min(x, r) + id / 8;
 }
 
-// K: k of a step; S: LDS buffers, S - 1 steps are on their way while one is read.
-template <int DT, int OP, int BM, int BN, int WM, int WN, int K, int S, bool DIRECT>
+// S: LDS buffers.
+template <int DT, int OP, int BM, int BN, int WM, int WN, int S, bool DIRECT>
 __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(GroupedArgs a, int n_tiles) {
   constexpr int T = WM * WN * kWave;
   constexpr int MF = BM / WM / 16, NF = BN / WN / 16;  // products of 16 x 16 a wave
   constexpr bool A_ALONG = OP != kBackwardWeight, B_ALONG = OP == kForward;
-  static_assert(DIRECT || S == 2, "through registers: one step ahead");
-  __shared__ __align__(16) uint16_t sa[S][BM * K], sb[S][BN * K];
-  using OA = Operand<A_ALONG, BM, K, T, DIRECT>;
-  using OB = Operand<B_ALONG, BN, K, T, DIRECT>;
+  constexpr int K = kStepK, GA = 4, GB = 4 * NF;
+  using OA = Operand<A_ALONG, BM, GA, T, DIRECT>;
+  using OB = Operand<B_ALONG, BN, GB, T, DIRECT>;
+  __shared__ __align__(16) uint16_t sa[S][OA::kElems], sb[S][OB::kElems];
   OA A;
   OB B;
   const int64_t io = static_cast<int64_t>(a.inner) * a.outer;
@@ -225,61 +235,89 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
   const int wm = (w / WN) * (MF * 16), wn = (w % WN) * (NF * 16);
   // this lane's place in a product's 16 m and 16 n
-  const int am = wm + (A_ALONG ? l & 15 : 4 * (l & 3));
-  const int bn = wn + (B_ALONG ? ((l & 15) >> 2) * (4 * NF) + (l & 3) : 4 * (l & 3));
+  const int a_place = OA::read_place(wm + (A_ALONG ? l & 15 : 4 * (l & 3)));
+  const int b_place = OB::read_place(wn + (B_ALONG ? ((l & 15) >> 2) * (4 * NF) + (l & 3) : 4 * (l & 3)));
   constexpr int kNext = B_ALONG ? 4 : 16;  // n from one product to the next
   const bool sums = OP == kBackwardWeight && a.grad_bias && n0 == 0 && wn == 0;
-  f32x4 acc[MF][NF], acc1[OP == kBackwardWeight ? MF : 1];
+  f32x4 acc[MF][NF];
+  float sum[OP == kBackwardWeight ? MF : 1];  // of this lane's values of A
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
 #pragma unroll
     for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    if constexpr (OP == kBackwardWeight) acc1[i] = f32x4{0, 0, 0, 0};
+    if constexpr (OP == kBackwardWeight) sum[i] = 0.0f;
   }
 
+  // At step `it` its operands are in registers; those of it + 1 are read from LDS and the loads of a
+  // later step go to the buffer of `it`, which all waves have read, between the products: neither
+  // holds them up.  Loads are started past the end too, with nothing in range, so that the number
+  // under way is the same at every wait.
+  constexpr int kLoads = OA::kEach + OB::kEach;
   const int steps = static_cast<int>((A.ks + K - 1) / K);
-  u16x8_t ones;
+  u16x8_t fa[2][MF], fb[2][NF];
+  auto load = [&](int i, int step, uint16_t* pa, uint16_t* pb) {
+    if (i < OA::kEach) A.load(i, static_cast<int64_t>(step) * K, pa);
+    else B.load(i - OA::kEach, static_cast<int64_t>(step) * K, pb);
+  };
+  if (steps > 0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ones[i] = DT == 2 ? 0x3f80 : 0x3c00;
+    for (int k = 0; k < S; ++k) {
 #pragma unroll
-  for (int k = 0; k < S - 1; ++k) {
-    A.load(static_cast<int64_t>(k) * K, sa[k]);
-    B.load(static_cast<int64_t>(k) * K, sb[k]);
-    A.store(sa[k]);
-    B.store(sb[k]);
-  }
-  // A step's loads are always started, past the end with nothing in range, so that the number under
-  // way is the same at every wait.  At `it`, steps it + 1 .. it + S - 2 may still be under way; the
-  // buffer read at it - 1 takes step it + S - 1.
-  int cur = 0, nxt = S - 1;
-  for (int it = 0; it < steps; ++it) {
-    wait_loads<DIRECT ? (S - 2) * (OA::kEach + OB::kEach) : 63>();
+      for (int i = 0; i < kLoads; ++i) load(i, k, sa[k], sb[k]);
+      A.store(sa[k]);
+      B.store(sb[k]);
+    }
+    if constexpr (!DIRECT) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load(i, S, nullptr, nullptr);
+    }
+    wait_loads<DIRECT ? (S - 1) * kLoads : 63>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    A.load(static_cast<int64_t>(it + S - 1) * K, sa[nxt]);
-    B.load(static_cast<int64_t>(it + S - 1) * K, sb[nxt]);
 #pragma unroll
-    for (int k = 0; k < K / 32; ++k) {
-      u16x8_t fa[MF], fb[NF];
+    for (int j = 0; j < NF; ++j) fb[0][j] = OB::read(sb[0] + b_place, kNext * j);
 #pragma unroll
-      for (int j = 0; j < NF; ++j) fb[j] = fragment<B_ALONG, BN, K>(sb[cur], bn + kNext * j, k);
+    for (int i = 0; i < MF; ++i) fa[0][i] = OA::read(sa[0] + a_place, 16 * i);
+  }
+  int cur = 0;
+  auto step = [&](int it, auto odd) {
+    constexpr int P = decltype(odd)::value, Q = 1 - P;
+    const int next = cur + 1 == S ? 0 : cur + 1;
+    const uint16_t *ra = sa[next] + a_place, *rb = sb[next] + b_place;
+    wait_loads<DIRECT ? (S - 2) * kLoads : 63>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if constexpr (!DIRECT) {
+      A.store(sa[cur]);
+      B.store(sb[cur]);
+    }
 #pragma unroll
-      for (int i = 0; i < MF; ++i) fa[i] = fragment<A_ALONG, BM, K>(sa[cur], am + 16 * i, k);
+    for (int i = 0; i < MF; ++i) {
+      fa[Q][i] = OA::read(ra, 16 * i);
 #pragma unroll
-      for (int i = 0; i < MF; ++i)
+      for (int j = i * NF / MF; j < (i + 1) * NF / MF; ++j) fb[Q][j] = OB::read(rb, kNext * j);
 #pragma unroll
-        for (int j = 0; j < NF; ++j) acc[i][j] = mfma16<DT>(fb[j], fa[i], acc[i][j]);
-      if constexpr (OP == kBackwardWeight) {
-        if (sums) {
+      for (int j = 0; j < NF; ++j) acc[i][j] = mfma16<DT>(fb[P][j], fa[P][i], acc[i][j]);
 #pragma unroll
-          for (int i = 0; i < MF; ++i) acc1[i] = mfma16<DT>(ones, fa[i], acc1[i]);
+      for (int k = i * kLoads / MF; k < (i + 1) * kLoads / MF; ++k) load(k, it + S + (DIRECT ? 0 : 1), sa[cur], sb[cur]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (OP == kBackwardWeight) {
+      if (sums) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          float t[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[e] = Fmt<DT>::to_f(fa[P][i][e]);
+          sum[i] += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
         }
       }
     }
-    A.store(sa[nxt]);
-    B.store(sb[nxt]);
-    cur = cur + 1 == S ? 0 : cur + 1;
-    nxt = nxt + 1 == S ? 0 : nxt + 1;
+    cur = next;
+  };
+  for (int it = 0; it < steps; it += 2) {  // an odd last step is followed by one of zeros
+    step(it, std::integral_constant<int, 0>{});
+    step(it + 1, std::integral_constant<int, 1>{});
   }
   wait_loads<0>();  // LDS stays this workgroup's until the last load is done
 
@@ -310,7 +348,11 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
       store_out<LEN>(a.out, a.out_dt, at + 16 * u, B.ms - n - 16 * u, v);
     }
     if constexpr (OP == kBackwardWeight) {
-      if (sums && l < 16) store_any(a.grad_bias, a.out_dt, static_cast<int64_t>(expert) * a.outer + m0 + m, acc1[i][0]);
+      if (sums) {  // the 4 lanes of an m have its rows 8 at a time
+        float t = sum[i] + __shfl_xor(sum[i], 16);
+        t += __shfl_xor(t, 32);
+        if (l < 16) store_any(a.grad_bias, a.out_dt, static_cast<int64_t>(expert) * a.outer + m0 + m, t);
+      }
     }
   }
 }
