@@ -127,7 +127,7 @@ tbe_status launch_any(const GroupedArgs& a, hipStream_t s) {
 constexpr int64_t kMaxGroups = int64_t{1} << 22;  // a launch has fewer than 2^32 threads
 const char* name_of(int op) { return op == kForward ? "grouped_forward" : op == kBackwardInput ? "grouped_input" : "grouped_weight"; }
 
-template <int DT, int OP, int BM, int BN, int WM, int WN, int S, bool DIRECT>
+template <int DT, int OP, int BM, int BN, int WM, int WN, bool DIRECT>
 tbe_status launch_tile(const GroupedArgs& a, hipStream_t s) {
   const int n = OP == kForward ? a.outer : a.inner;
   const int n_tiles = (n + BN - 1) / BN;
@@ -137,7 +137,7 @@ tbe_status launch_tile(const GroupedArgs& a, hipStream_t s) {
     return TBE_ERR_UNSUPPORTED;
   }
   ProfScope ps(name_of(OP), s);
-  hipLaunchKernelGGL((grouped_tile_kernel<DT, OP, BM, BN, WM, WN, S, DIRECT>), dim3(static_cast<unsigned>(tiles * n_tiles)),
+  hipLaunchKernelGGL((grouped_tile_kernel<DT, OP, BM, BN, WM, WN, DIRECT>), dim3(static_cast<unsigned>(tiles * n_tiles)),
                      dim3(WM * WN * kWave), 0, s, a, n_tiles);
   return check_launch(name_of(OP));
 }
@@ -156,7 +156,7 @@ bool chunked(const GroupedArgs& a, int op) {
 
 template <int DT, int OP>
 tbe_status launch_type(const GroupedArgs& a, hipStream_t s) {
-  return chunked(a, OP) ? launch_tile<DT, OP, 256, 256, 2, 4, 4, true>(a, s) : launch_tile<DT, OP, 256, 128, 2, 4, 2, false>(a, s);
+  return chunked(a, OP) ? launch_tile<DT, OP, 256, 256, 2, 4, true>(a, s) : launch_tile<DT, OP, 256, 128, 2, 4, false>(a, s);
 }
 
 template <int OP>

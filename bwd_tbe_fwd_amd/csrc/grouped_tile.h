@@ -1,5 +1,5 @@
 // The tiled kernel of the grouped products (grouped_linear.h says what m, n, k, "along" and
-// "across" are): a workgroup takes BM x BN of C and walks k in steps of 32 through S LDS buffers.
+// "across" are): a workgroup takes BM x BN of C and walks k through two LDS buffers of 64 k.
 //
 // Bound by the matrix instructions where the sides are large, so everything else has to stay out of
 // their way:
@@ -8,7 +8,7 @@
 //    matrix's edge get an offset past the buffer's range and so write zeros: the edges of the
 //    groups cost no branch in the loop.  Rows that do not start on 16 bytes (or k or n that are not
 //    whole 16 bytes) go through registers instead, with the same LDS layout.
-//  * LDS holds an operand as it lies in memory, along: [m][32 k], across: [32 k][m].  The 16-byte
+//  * LDS holds an operand as it lies in memory, along: [m][64 k], across: [64 k][m].  The 16-byte
 //    columns of an along row are exchanged by a pattern of the row, and the across rows are put in an
 //    order with gaps, so that what a read takes lies in different banks.  A lane's place in a read
 //    is a base that never changes plus a constant: no address arithmetic between the products.
@@ -19,13 +19,11 @@
 //    products give 4 NF adjacent n (an across read of such n would meet in the same banks).
 #pragma once
 
-#include <type_traits>
-
 #include "grouped_linear.h"
 
 namespace tbe {
 
-constexpr int kStepK = 32;                  // k of a step: one product's
+constexpr int kStepK = 64;                  // k of an LDS buffer: two products'
 constexpr uint32_t kOutside = 0x80000000u;  // a buffer offset past any range
 
 typedef uint16_t u16x4_t __attribute__((ext_vector_type(4)));
@@ -33,14 +31,13 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
-// Exchange of an along row's 4 columns of 16 bytes.  A 16-byte LDS read is served 16 lanes at a time,
+// Exchange of an along row's 8 columns of 16 bytes.  A 16-byte LDS read is served 16 lanes at a time,
 // lanes 0-3, 12-15 and 20-27, then 4-11, 16-19 and 28-31: of the blocks q = 0 .. 3 of 4 rows that a
 // read takes, 0 and 3 at one column with 1 and 2 at the next.  With these patterns they differ in
-// their place within 256 bytes, all banks (conflict counter: 0).  A read's blocks lie `GAP` rows apart.
+// their place within 256 bytes, all banks (conflict counter: 0).  A read's blocks lie GAP rows apart.
 template <int GAP>
 __device__ __forceinline__ int along_pattern(int r) {
-  const int q = (r / GAP) & 3;
-  return q ^ (q & 1) << 1;
+  return ((r >> 1) & 1) | ((r / GAP) & 3) << 1;
 }
 // Place of an across row k in LDS, in elements.  A load instruction fills 1024 bytes: rows k = 8 g + 4 h
 // + r of one r together (h = 0, 1, and g & 1 where a row has 256 bytes), 32 bytes before those of
@@ -145,6 +142,10 @@ struct Operand {
     const int l = lane_id(), g = l >> 4;
     return ALONG ? m * K + ((g ^ along_pattern<GAP>(m)) << 3) : across_place<SIDE>(8 * g + ((l & 15) >> 2)) + m;
   }
+  // The place of the buffer's second 32 k.
+  __device__ __forceinline__ static int second_half(int place) {
+    return ALONG ? place ^ 32 : place + across_place<SIDE>(32);
+  }
   __device__ __forceinline__ static u16x8_t read(const uint16_t* s, int m_further) {
     if constexpr (ALONG) {
       return *reinterpret_cast<const u16x8_t*>(s + m_further * K);
@@ -194,8 +195,7 @@ __device__ __forceinline__ unsigned chiplet_order(unsigned id, unsigned n) {
   return x * q + min(x, r) + id / 8;
 }
 
-// S: LDS buffers.
-template <int DT, int OP, int BM, int BN, int WM, int WN, int S, bool DIRECT>
+template <int DT, int OP, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(GroupedArgs a, int n_tiles) {
   constexpr int T = WM * WN * kWave;
   constexpr int MF = BM / WM / 16, NF = BN / WN / 16;  // products of 16 x 16 a wave
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
   constexpr int K = kStepK, GA = 4, GB = 4 * NF;
   using OA = Operand<A_ALONG, BM, GA, T, DIRECT>;
   using OB = Operand<B_ALONG, BN, GB, T, DIRECT>;
-  __shared__ __align__(16) uint16_t sa[S][OA::kElems], sb[S][OB::kElems];
+  __shared__ __align__(16) uint16_t sa[2][OA::kElems], sb[2][OB::kElems];
   OA A;
   OB B;
   const int64_t io = static_cast<int64_t>(a.inner) * a.outer;
@@ -248,20 +248,21 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
     if constexpr (OP == kBackwardWeight) sum[i] = 0.0f;
   }
 
-  // At step `it` its operands are in registers; those of it + 1 are read from LDS and the loads of a
-  // later step go to the buffer of `it`, which all waves have read, between the products: neither
-  // holds them up.  Loads are started past the end too, with nothing in range, so that the number
-  // under way is the same at every wait.
+  // The operands of 32 k are in registers while those of the next 32 k are read from LDS, between the
+  // products.  Two LDS buffers of 64 k each: when the second half of buffer `it` has been read by all
+  // waves, the loads of it + 2 start there, also between the products, and have the products of 64
+  // k to arrive.  Loads are started past the end too, with nothing in range.
   constexpr int kLoads = OA::kEach + OB::kEach;
   const int steps = static_cast<int>((A.ks + K - 1) / K);
   u16x8_t fa[2][MF], fb[2][NF];
+  const int a_half[2] = {a_place, OA::second_half(a_place)}, b_half[2] = {b_place, OB::second_half(b_place)};
   auto load = [&](int i, int step, uint16_t* pa, uint16_t* pb) {
     if (i < OA::kEach) A.load(i, static_cast<int64_t>(step) * K, pa);
     else B.load(i - OA::kEach, static_cast<int64_t>(step) * K, pb);
   };
   if (steps > 0) {
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) load(i, k, sa[k], sb[k]);
       A.store(sa[k]);
@@ -269,9 +270,9 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
     }
     if constexpr (!DIRECT) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) load(i, S, nullptr, nullptr);
+      for (int i = 0; i < kLoads; ++i) load(i, 2, nullptr, nullptr);
     }
-    wait_loads<DIRECT ? (S - 1) * kLoads : 63>();
+    wait_loads<DIRECT ? kLoads : 63>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -279,45 +280,46 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
 #pragma unroll
     for (int i = 0; i < MF; ++i) fa[0][i] = OA::read(sa[0] + a_place, 16 * i);
   }
-  int cur = 0;
-  auto step = [&](int it, auto odd) {
-    constexpr int P = decltype(odd)::value, Q = 1 - P;
-    const int next = cur + 1 == S ? 0 : cur + 1;
-    const uint16_t *ra = sa[next] + a_place, *rb = sb[next] + b_place;
-    wait_loads<DIRECT ? (S - 2) * kLoads : 63>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if constexpr (!DIRECT) {
-      A.store(sa[cur]);
-      B.store(sb[cur]);
-    }
+  for (int it = 0; it < steps; ++it) {
+    const int cur = it & 1;
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      fa[Q][i] = OA::read(ra, 16 * i);
+    for (int P = 0; P < 2; ++P) {  // the half in registers
+      const int Q = 1 - P, from = P == 0 ? cur : cur ^ 1;
+      if (P == 1) {
+        wait_loads<DIRECT ? 0 : 63>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if constexpr (!DIRECT) {
+          A.store(sa[cur]);
+          B.store(sb[cur]);
+        }
+      }
+      const uint16_t *ra = sa[from] + a_half[Q], *rb = sb[from] + b_half[Q];
 #pragma unroll
-      for (int j = i * NF / MF; j < (i + 1) * NF / MF; ++j) fb[Q][j] = OB::read(rb, kNext * j);
+      for (int i = 0; i < MF; ++i) {
+        fa[Q][i] = OA::read(ra, 16 * i);
 #pragma unroll
-      for (int j = 0; j < NF; ++j) acc[i][j] = mfma16<DT>(fb[P][j], fa[P][i], acc[i][j]);
+        for (int j = i * NF / MF; j < (i + 1) * NF / MF; ++j) fb[Q][j] = OB::read(rb, kNext * j);
 #pragma unroll
-      for (int k = i * kLoads / MF; k < (i + 1) * kLoads / MF; ++k) load(k, it + S + (DIRECT ? 0 : 1), sa[cur], sb[cur]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if constexpr (OP == kBackwardWeight) {
-      if (sums) {
+        for (int j = 0; j < NF; ++j) acc[i][j] = mfma16<DT>(fb[P][j], fa[P][i], acc[i][j]);
+        if (P == 1) {
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
-          float t[8];
+          for (int k = i * kLoads / MF; k < (i + 1) * kLoads / MF; ++k) load(k, it + (DIRECT ? 2 : 3), sa[cur], sb[cur]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (OP == kBackwardWeight) {
+        if (sums) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[e] = Fmt<DT>::to_f(fa[P][i][e]);
-          sum[i] += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+          for (int i = 0; i < MF; ++i) {
+            float t[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = Fmt<DT>::to_f(fa[P][i][e]);
+            sum[i] += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+          }
         }
       }
     }
-    cur = next;
-  };
-  for (int it = 0; it < steps; it += 2) {  // an odd last step is followed by one of zeros
-    step(it, std::integral_constant<int, 0>{});
-    step(it + 1, std::integral_constant<int, 1>{});
   }
   wait_loads<0>();  // LDS stays this workgroup's until the last load is done
 
