@@ -44,6 +44,7 @@ struct GroupedArgs {
   int32_t out_dt;
   void* grad_bias;      // backward by weight; NULL: none
   void* workspace;
+  int32_t split;        // backward by weight: rows of a unit, 0: an expert's rows are one
 };
 
 // Rows [lo, hi) of expert e < experts, inside [0, rows]; e = experts: the rows of no expert.
@@ -61,40 +62,67 @@ __device__ __forceinline__ RowRange rows_of(const GroupedArgs& a, int e) {
   return r;
 }
 
-// Row tile `tile` of tiles of BM rows counted over the experts in order and then the rows of no
-// expert: its expert and first row; false past the last tile.  Every wave finds it by itself: 64
-// experts a step, their tile counts summed over the lanes.
+// Tiles of BM rows are counted over the experts in order and then the rows of no expert.  Every wave
+// counts them by itself, 64 experts a step, a lane each.
 struct RowTile {
   int expert;
-  int64_t row, hi;
+  int64_t row, hi;   // first row, and where its expert's end
 };
-__device__ __forceinline__ bool find_row_tile(const GroupedArgs& a, int BM, int64_t tile, RowTile& t) {
-  const int l = lane_id();
-  int64_t before = 0;
-  for (int base = 0; base <= a.experts; base += kWave) {
-    const int e = base + l;
-    RowRange r = {0, 0};
+struct RowTiles {
+  RowRange r;        // of this lane's expert, and its tiles: how many, and with those of the lanes before
+  int32_t n, upto;
+  __device__ __forceinline__ int32_t count(const GroupedArgs& a, int BM, int base) {
+    const int l = lane_id(), e = base + l;
+    r = RowRange{0, 0};
     if (e <= a.experts) r = rows_of(a, e);
-    const int32_t n = static_cast<int32_t>((r.hi - r.lo + BM - 1) / BM);
-    int32_t upto = n;  // tiles of lanes 0 .. l
+    n = static_cast<int32_t>((r.hi - r.lo + BM - 1) / BM);
+    upto = n;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
       const int32_t up = __shfl_up(upto, d);
       if (l >= d) upto += up;
     }
-    const int32_t total = read_lane(upto, kWave - 1);
-    if (tile < before + total) {
-      // the first lane whose tiles reach past this one
-      const int src = __ffsll(static_cast<unsigned long long>(__ballot(before + upto > tile))) - 1;
-      const int64_t first = read_lane64(r.lo + (tile - before - (upto - n)) * BM, src);
-      t.expert = base + src;
-      t.row = first;
-      t.hi = read_lane64(r.hi, src);
-      return true;
-    }
-    before += total;
+    return read_lane(upto, kWave - 1);
   }
-  return false;
+  // All tiles.
+  __device__ __forceinline__ int total(const GroupedArgs& a, int BM) {
+    int all = 0;
+    for (int base = 0; base <= a.experts; base += kWave) all += count(a, BM, base);
+    return all;
+  }
+  // Tile `tile`; false past the last one.  After total(), with up to 63 experts the lanes still hold them.
+  __device__ __forceinline__ bool find(const GroupedArgs& a, int BM, int tile, bool counted, RowTile& t) {
+    for (int base = 0; base <= a.experts; base += kWave) {
+      const int here = counted && a.experts < kWave ? read_lane(upto, kWave - 1) : count(a, BM, base);
+      if (tile < here) {
+        const int src = __ffsll(static_cast<unsigned long long>(__ballot(upto > tile))) - 1;
+        t.expert = base + src;
+        t.row = read_lane64(r.lo + static_cast<int64_t>(tile - (upto - n)) * BM, src);
+        t.hi = read_lane64(r.hi, src);
+        return true;
+      }
+      tile -= here;
+    }
+    return false;
+  }
+};
+
+// The expert with the k-th most rows (the lower one first among equals); with more than 64 experts,
+// expert k.
+__device__ __forceinline__ int expert_by_rows(const GroupedArgs& a, int k) {
+  if (a.experts > kWave) return k;
+  const int l = lane_id();
+  int64_t n = -1;
+  if (l < a.experts) {
+    const RowRange r = rows_of(a, l);
+    n = r.hi - r.lo;
+  }
+  int rank = 0;
+  for (int e = 0; e < a.experts; ++e) {
+    const int64_t m = read_lane64(n, e);
+    rank += m > n || (m == n && e < l) ? 1 : 0;
+  }
+  return __ffsll(static_cast<unsigned long long>(__ballot(l < a.experts && rank == k))) - 1;
 }
 
 // Row tiles at most: a partly filled one for every expert and the rows of no expert.

@@ -45,8 +45,9 @@ __global__ __launch_bounds__(kBlock) void grouped_any_kernel(GroupedArgs a) {
     pa = static_cast<const uint16_t*>(a.gy) + r.lo * lda + m0;
     pb = static_cast<const uint16_t*>(a.x) + r.lo * ldb + n0;
   } else {
+    RowTiles tiles;
     RowTile t;
-    if (!find_row_tile(a, kTile, blockIdx.x, t)) return;
+    if (!tiles.find(a, kTile, blockIdx.x, false, t)) return;
     expert = t.expert;
     row = t.row;
     ms = t.hi - t.row;
@@ -129,17 +130,62 @@ const char* name_of(int op) { return op == kForward ? "grouped_forward" : op == 
 
 template <int DT, int OP, int BM, int BN, int WM, int WN, bool DIRECT>
 tbe_status launch_tile(const GroupedArgs& a, hipStream_t s) {
+  auto kernel = grouped_tile_kernel<DT, OP, BM, BN, WM, WN, DIRECT>;
+  constexpr int kThreads = WM * WN * kWave;
   const int n = OP == kForward ? a.outer : a.inner;
   const int n_tiles = (n + BN - 1) / BN;
-  const int64_t tiles = OP == kBackwardWeight ? static_cast<int64_t>(a.experts) * ((a.outer + BM - 1) / BM) : row_tiles_bound(a, BM);
-  if (tiles * n_tiles > kMaxGroups) {
-    set_error("grouped linear: %lld tiles are more than a launch takes", static_cast<long long>(tiles * n_tiles));
+  const int64_t units = OP != kBackwardWeight ? row_tiles_bound(a, BM) : a.split ? row_tiles_bound(a, a.split) : a.experts;
+  // rows: a multiple of 8, for the chiplets' shares
+  const int64_t groups = OP == kBackwardWeight ? units * ((a.outer + BM - 1) / BM) * n_tiles : (units * n_tiles + 7) / 8 * 8;
+  if (groups > kMaxGroups) {
+    set_error("grouped linear: %lld tiles are more than a launch takes", static_cast<long long>(groups));
     return TBE_ERR_UNSUPPORTED;
   }
   ProfScope ps(name_of(OP), s);
-  hipLaunchKernelGGL((grouped_tile_kernel<DT, OP, BM, BN, WM, WN, DIRECT>), dim3(static_cast<unsigned>(tiles * n_tiles)),
-                     dim3(WM * WN * kWave), 0, s, a, n_tiles);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0, s, a, n_tiles);
   return check_launch(name_of(OP));
+}
+
+// Sum of the units' partial weight gradients of the experts that have more than one, in the order of
+// their rows; zeros for the experts without rows, which have no unit.
+__global__ __launch_bounds__(kBlock) void grouped_reduce_kernel(GroupedArgs a) {
+  const int e = blockIdx.y;
+  const int64_t io = static_cast<int64_t>(a.inner) * a.outer, each = io + a.outer;
+  auto units_of = [&](int k) {
+    const RowRange r = rows_of(a, k);
+    return (r.hi - r.lo + a.split - 1) / a.split;
+  };
+  const int64_t n = units_of(e);
+  if (n == 1) return;
+  int64_t first = 0;  // units of the experts before
+  for (int k = lane_id(); k < e; k += kWave) first += units_of(k);
+  for (int d = 1; d < kWave; d <<= 1) first += __shfl_xor(first, d);
+  const float* p = static_cast<const float*>(a.workspace) + first * each;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x) * 4; i < each; i += static_cast<int64_t>(gridDim.x) * kBlock * 4) {
+    Vec<float, 4> sum = {};
+    for (int64_t u = 0; u < n; ++u) {
+      Vec<float, 4> v;
+      load_vec_part<float, 4>(p + u * each + i, each - i, v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum.e[k] += v.e[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + k < io) store_any(a.out, a.out_dt, e * io + i + k, sum.e[k]);
+      else if (i + k < each && a.grad_bias) store_any(a.grad_bias, a.out_dt, static_cast<int64_t>(e) * a.outer + i + k - io, sum.e[k]);
+    }
+  }
+}
+
+// Rows of a unit of the weight gradient.  With few tiles for the 256 CUs, or experts of unequal rows,
+// an expert's rows are shared among workgroups whose partial sums a second kernel adds: units of at
+// least 512 rows (the partial sums of shorter ones cost more than the products), as many as give
+// two workgroups a CU.  0: the tiles of the experts are enough.
+int split_rows(int64_t rows, int64_t experts, int64_t inner, int64_t outer) {
+  const int64_t tiles = ((outer + 255) / 256) * ((inner + 255) / 256);
+  if (experts * tiles >= 512 || rows <= 512) return 0;
+  const int64_t c = (rows * tiles / 512 + 63) / 64 * 64;
+  return static_cast<int>(hmax(512, c));
 }
 
 // Whether every 16-byte chunk of the operands is whole and starts on 16 bytes, and a tile's offsets
@@ -161,7 +207,13 @@ tbe_status launch_type(const GroupedArgs& a, hipStream_t s) {
 
 template <int OP>
 tbe_status launch(const GroupedArgs& a, int dtype, hipStream_t s) {
-  return dtype == TBE_F16 ? launch_type<1, OP>(a, s) : launch_type<2, OP>(a, s);
+  const tbe_status st = dtype == TBE_F16 ? launch_type<1, OP>(a, s) : launch_type<2, OP>(a, s);
+  if (st != TBE_OK || OP != kBackwardWeight || !a.split) return st;
+  const int64_t each = static_cast<int64_t>(a.inner + 1) * a.outer;
+  ProfScope ps("grouped_reduce", s);
+  hipLaunchKernelGGL(grouped_reduce_kernel, dim3(static_cast<unsigned>(hmin(1024, (each + 4 * kBlock - 1) / (4 * kBlock))), a.experts),
+                     dim3(kBlock), 0, s, a);
+  return check_launch("grouped_reduce");
 }
 
 bool aligned_to(const void* p, int dt) { return !(reinterpret_cast<uintptr_t>(p) & (dt == TBE_F32 ? 3u : 1u)); }
@@ -252,8 +304,11 @@ extern "C" tbe_status tbe_grouped_linear_backward_input(int64_t rows, int32_t ex
 
 extern "C" size_t tbe_grouped_linear_backward_weight_workspace_bytes(int64_t rows, int32_t experts, int64_t inner,
                                                                      int64_t outer) {
-  (void)rows; (void)experts; (void)inner; (void)outer;
-  return 0;
+  if (rows < 0 || rows > kMaxRows || experts < 1 || experts > kMaxExperts || inner < 1 || inner > kMaxSide || outer < 1 ||
+      outer > kMaxSide)
+    return 0;
+  const int64_t split = split_rows(rows, experts, inner, outer);
+  return split ? static_cast<size_t>((rows / split + experts + 1) * (inner + 1) * outer) * 4 : 0;
 }
 
 extern "C" tbe_status tbe_grouped_linear_backward_weight(int64_t rows, int32_t experts, int64_t inner, int64_t outer,
@@ -279,5 +334,6 @@ extern "C" tbe_status tbe_grouped_linear_backward_weight(int64_t rows, int32_t e
   a.x = x; a.x_stride = x_stride; a.gy = grad_y; a.gy_stride = grad_y_stride;
   a.offsets = offsets; a.offset64 = offset_type == TBE_I64;
   a.out = grad_weight; a.out_dt = out_dtype; a.grad_bias = grad_bias; a.workspace = workspace;
+  a.split = split_rows(rows, experts, inner, outer);
   return launch<kBackwardWeight>(a, dtype, static_cast<hipStream_t>(stream));
 }

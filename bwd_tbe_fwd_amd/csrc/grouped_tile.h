@@ -69,13 +69,13 @@ struct Operand {
 
   const uint16_t* base;  // (m0, k = 0)
   int64_t ld;
-  int64_t ms, ks;
+  int ms, ks;            // that lie inside from there on
   uint32_t at[kEach];    // DIRECT: byte offset of a chunk, or kOutside
   u16x8_t reg[DIRECT ? 1 : kEach];
 
   // row of the matrix (m or k within the tile) and its chunk that a thread's i-th chunk holds
-  __device__ __forceinline__ static void place(int i, int& row, int& chunk) {
-    const int q = i * THREADS + threadIdx.x;
+  __device__ __forceinline__ static void place(int i, int tid, int& row, int& chunk) {
+    const int q = i * THREADS + tid;
     if constexpr (ALONG) {
       row = q / (K / 8);
       chunk = q % (K / 8) ^ along_pattern<GAP>(row);
@@ -91,39 +91,42 @@ struct Operand {
     const int q = i * THREADS + threadIdx.x;
     return ALONG ? q * 8 : q / 64 * (512 + 16) + q % 64 * 8;
   }
-  __device__ __forceinline__ void init(const uint16_t* p, int64_t stride, int64_t m_left, int64_t k_left) {
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t stride, int m_left, int k_left) {
     base = p;
     ld = stride;
     ms = m_left;
     ks = k_left;
     if constexpr (DIRECT) {
+      // computed anew for each tile: kept from one to the next they would cost registers in the loop
+      uint32_t pitch = static_cast<uint32_t>(stride) * 2;
+      int tid = threadIdx.x;
+      asm volatile("" : "+s"(pitch), "+v"(tid));
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         int row, chunk;
-        place(i, row, chunk);
+        place(i, tid, row, chunk);
         const bool in = ALONG ? row < ms : chunk * 8 < ms;
-        at[i] = in ? static_cast<uint32_t>(row * ld * 2 + chunk * 16) : kOutside;
+        at[i] = in ? row * pitch + chunk * 16 : kOutside;
       }
     }
   }
   // Starts the i-th load of step k0 (of kEach).
-  __device__ __forceinline__ void load(int i, int64_t k0, uint16_t* s) {
+  __device__ __forceinline__ void load(int i, int k0, uint16_t* s) {
     const uint16_t* p = base + (ALONG ? k0 : k0 * ld);
+    const int left = ks - k0;
     int row, chunk;
-    place(i, row, chunk);
+    place(i, threadIdx.x, row, chunk);
     if constexpr (DIRECT) {
       const uint64_t u = reinterpret_cast<uint64_t>(p);
       const u32x4 r = {static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32) & 0xffffu, 0x7fffffffu, 0x00027000u};
       const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
       const int to = ALONG ? (i * THREADS + w * kWave) * 8 : (i * (THREADS / kWave) + w) * (512 + 16);
       uint32_t o = at[i];
-      const int left = static_cast<int>(min(ks - k0, static_cast<int64_t>(K)));
       if (left < K && (ALONG ? chunk * 8 : row) >= left) o = kOutside;
       load_to_lds(r, o, static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)(s + to))));
     } else {
-      const int64_t left = ks - k0;
       Vec<uint16_t, 8> v;
-      const int64_t n = (ALONG ? row < ms : row < left) ? (ALONG ? left : ms) - chunk * 8 : 0;
+      const int n = (ALONG ? row < ms : row < left) ? (ALONG ? left : ms) - chunk * 8 : 0;
       load_vec_part<uint16_t, 8>(p + row * ld + chunk * 8, n, v);
       __builtin_memcpy(&reg[i], v.e, 16);
     }
@@ -162,22 +165,6 @@ struct Operand {
   }
 };
 
-// N floats of row `p` of out from column n on, `left` of them inside.
-template <int N>
-__device__ __forceinline__ void store_out(void* out, int dt, int64_t at, int64_t left, const float (&v)[N]) {
-  if (dt == 0) {
-    Vec<float, N> o;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o.e[i] = v[i];
-    store_vec_part<float, N>(static_cast<float*>(out) + at, left, o);
-  } else {
-    Vec<uint16_t, N> o;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o.e[i] = dt == 1 ? tower_from_f<1>(v[i]) : tower_from_f<2>(v[i]);
-    store_vec_part<uint16_t, N>(static_cast<uint16_t*>(out) + at, left, o);
-  }
-}
-
 // Waits until at most N of this wave's loads are on their way and its LDS reads are done.  (Fields of
 // the counter word: loads in bits 0-3 and 14-15, LDS in 8-11, exports in 4-6, left alone.)
 template <int N>
@@ -195,6 +182,41 @@ __device__ __forceinline__ unsigned chiplet_order(unsigned id, unsigned n) {
   return x * q + min(x, r) + id / 8;
 }
 
+// A wave's results, MF x NF products, to rows `out` + m * pitch, of type S: through LDS, a few rows at a
+// time, so that each row's bytes leave in whole cache lines (16 lanes' 4 adjacent values each reach
+// memory as 32-byte pieces: 1.07 GB of them took 0.34 ms of 1.23).  `s`: this wave's part of LDS.
+template <typename S, int MF, int NF, int LEN, int BYTES, typename Value>
+__device__ __forceinline__ void store_tile(S* out, int64_t pitch, int m_left, int n_left, char* s, Value value) {
+  constexpr int kRow = NF * 16 * static_cast<int>(sizeof(S)), kPitch = kRow + 16;  // 16: the rows of a write in different banks
+  constexpr int kFit = BYTES / (16 * kPitch);
+  constexpr int R = kFit >= MF ? MF : kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;           // products of m at a time
+  static_assert(kFit >= 1 && MF % R == 0, "16 rows fit");
+  constexpr int kPer = 16 / static_cast<int>(sizeof(S)), kLanes = kRow / 16;       // values of 16 bytes, lanes of a row
+  const int l = lane_id(), g = l >> 4;
+#pragma unroll
+  for (int i0 = 0; i0 < MF; i0 += R) {
+#pragma unroll
+    for (int i = i0; i < i0 + R; ++i) {
+      char* p = s + (16 * (i - i0) + (l & 15)) * kPitch;
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        Vec<S, 4> v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v.e[e] = value(i, j, e);
+        // products' n: 4 NF adjacent ones a lane (LEN > 4), or 4 of every 16
+        __builtin_memcpy(p + (LEN > 4 ? g * LEN + 4 * j : 16 * j + 4 * g) * sizeof(S), v.e, 4 * sizeof(S));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 16 * R * kLanes / kWave; ++k) {
+      const int m = k * (kWave / kLanes) + l / kLanes, n = (l % kLanes) * kPer;
+      Vec<S, kPer> v;
+      __builtin_memcpy(v.e, s + m * kPitch + n * sizeof(S), 16);
+      if (16 * i0 + m < m_left) store_vec_part<S, kPer>(out + (16 * i0 + m) * pitch + n, n_left - n, v);
+    }
+  }
+}
+
 template <int DT, int OP, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(GroupedArgs a, int n_tiles) {
   constexpr int T = WM * WN * kWave;
@@ -203,40 +225,75 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
   constexpr int K = kStepK, GA = 4, GB = 4 * NF;
   using OA = Operand<A_ALONG, BM, GA, T, DIRECT>;
   using OB = Operand<B_ALONG, BN, GB, T, DIRECT>;
-  __shared__ __align__(16) uint16_t sa[2][OA::kElems], sb[2][OB::kElems];
+  constexpr int kBytes = 2 * 2 * (OA::kElems + OB::kElems);
+  __shared__ __align__(16) char lds[kBytes];
+  uint16_t* const sa[2] = {reinterpret_cast<uint16_t*>(lds), reinterpret_cast<uint16_t*>(lds) + OA::kElems};
+  uint16_t* const sb[2] = {sa[1] + OA::kElems, sa[1] + OA::kElems + OB::kElems};
   OA A;
   OB B;
   const int64_t io = static_cast<int64_t>(a.inner) * a.outer;
-  int expert;
-  int64_t row = 0, m0 = 0, n0;
-  if constexpr (OP == kBackwardWeight) {
-    const int m_tiles = (a.outer + BM - 1) / BM, tiles = n_tiles * m_tiles;
-    expert = blockIdx.x / tiles;
-    // experts differ in their rows: each one's tiles are shared among the chiplets
-    const int t = chiplet_order(blockIdx.x % tiles, tiles);
-    m0 = static_cast<int64_t>(t % m_tiles) * BM;
-    n0 = static_cast<int64_t>(t / m_tiles) * BN;
-    const RowRange r = rows_of(a, expert);
-    A.init(static_cast<const uint16_t*>(a.gy) + r.lo * a.gy_stride + m0, a.gy_stride, a.outer - m0, r.hi - r.lo);
-    B.init(static_cast<const uint16_t*>(a.x) + r.lo * a.x_stride + n0, a.x_stride, a.inner - n0, r.hi - r.lo);
-  } else {
-    constexpr bool fwd = OP == kForward;
-    const unsigned id = chiplet_order(blockIdx.x, gridDim.x);
-    RowTile t;
-    if (!find_row_tile(a, BM, id / n_tiles, t)) return;
-    expert = t.expert;
-    row = t.row;
-    n0 = static_cast<int64_t>(id % n_tiles) * BN;
-    const int64_t lda = fwd ? a.x_stride : a.gy_stride;
-    const int64_t ks = expert < a.experts ? (fwd ? a.inner : a.outer) : 0;
-    A.init(static_cast<const uint16_t*>(fwd ? a.x : a.gy) + row * lda, lda, t.hi - t.row, ks);
-    B.init(static_cast<const uint16_t*>(a.w) + expert * io + (fwd ? n0 * a.inner : n0), a.inner, (fwd ? a.outer : a.inner) - n0, ks);
-  }
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
   const int wm = (w / WN) * (MF * 16), wn = (w % WN) * (NF * 16);
+
+  // the tile: its expert, rows, place in C and what of it lies inside, steps of k
+  int expert, row, m0 = 0, n0, m_left, n_left, steps;
+  float* part = nullptr;  // backward by weight: the unit's partial sums
+  if constexpr (OP == kBackwardWeight) {
+    // one tile of one expert's rows, or with a.split of one unit of at most a.split of them; the
+    // experts with the most rows come first, so that the workgroups still to come are the short ones
+    const int m_tiles = (a.outer + BM - 1) / BM, each = n_tiles * m_tiles;
+    const int unit = blockIdx.x / each;
+    // experts differ in their rows: each one's tiles are shared among the chiplets
+    const int k = chiplet_order(blockIdx.x % each, each);
+    m0 = (k % m_tiles) * BM;
+    n0 = (k / m_tiles) * BN;
+    m_left = a.outer - m0;
+    n_left = a.inner - n0;
+    int rows;
+    if (a.split) {
+      RowTiles tiles;
+      RowTile t;
+      if (!tiles.find(a, a.split, unit, false, t) || t.expert >= a.experts) return;
+      expert = t.expert;
+      row = static_cast<int>(t.row);
+      rows = static_cast<int>(min(t.hi - t.row, static_cast<int64_t>(a.split)));
+      const RowRange all = rows_of(a, expert);
+      if (all.hi - all.lo > a.split) part = static_cast<float*>(a.workspace) + unit * (io + a.outer);
+    } else {
+      expert = expert_by_rows(a, unit);
+      const RowRange r = rows_of(a, expert);
+      row = static_cast<int>(r.lo);
+      rows = static_cast<int>(r.hi - r.lo);
+    }
+    steps = (rows + K - 1) / K;
+    A.init(static_cast<const uint16_t*>(a.gy) + row * a.gy_stride + m0, a.gy_stride, m_left, rows);
+    B.init(static_cast<const uint16_t*>(a.x) + row * a.x_stride + n0, a.x_stride, n_left, rows);
+  } else {
+    // a chiplet's tiles are neighbours: a contiguous share of all, of which there are fewer than
+    // workgroups where experts' last tiles are not all there
+    constexpr bool fwd = OP == kForward;
+    RowTiles tiles;
+    RowTile t;
+    const int64_t total = static_cast<int64_t>(tiles.total(a, BM)) * n_tiles;
+    const unsigned x = blockIdx.x % 8;
+    const int id = static_cast<int>(total * x / 8 + blockIdx.x / 8);
+    if (id >= total * (x + 1) / 8 || !tiles.find(a, BM, id / n_tiles, true, t)) return;
+    expert = t.expert;
+    row = static_cast<int>(t.row);
+    n0 = (id % n_tiles) * BN;
+    m_left = static_cast<int>(t.hi - t.row);
+    n_left = (fwd ? a.outer : a.inner) - n0;
+    const int64_t lda = fwd ? a.x_stride : a.gy_stride;
+    const int ks = fwd ? a.inner : a.outer;
+    steps = expert < a.experts ? (ks + K - 1) / K : 0;
+    A.init(static_cast<const uint16_t*>(fwd ? a.x : a.gy) + row * lda, lda, m_left, ks);
+    B.init(static_cast<const uint16_t*>(a.w) + expert * io + (fwd ? static_cast<int64_t>(n0) * a.inner : n0), a.inner, n_left, ks);
+  }
+
   // this lane's place in a product's 16 m and 16 n
   const int a_place = OA::read_place(wm + (A_ALONG ? l & 15 : 4 * (l & 3)));
   const int b_place = OB::read_place(wn + (B_ALONG ? ((l & 15) >> 2) * (4 * NF) + (l & 3) : 4 * (l & 3)));
+  const int a_half[2] = {a_place, OA::second_half(a_place)}, b_half[2] = {b_place, OB::second_half(b_place)};
   constexpr int kNext = B_ALONG ? 4 : 16;  // n from one product to the next
   const bool sums = OP == kBackwardWeight && a.grad_bias && n0 == 0 && wn == 0;
   f32x4 acc[MF][NF];
@@ -253,12 +310,10 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
   // waves, the loads of it + 2 start there, also between the products, and have the products of 64
   // k to arrive.  Loads are started past the end too, with nothing in range.
   constexpr int kLoads = OA::kEach + OB::kEach;
-  const int steps = static_cast<int>((A.ks + K - 1) / K);
   u16x8_t fa[2][MF], fb[2][NF];
-  const int a_half[2] = {a_place, OA::second_half(a_place)}, b_half[2] = {b_place, OB::second_half(b_place)};
   auto load = [&](int i, int step, uint16_t* pa, uint16_t* pb) {
-    if (i < OA::kEach) A.load(i, static_cast<int64_t>(step) * K, pa);
-    else B.load(i - OA::kEach, static_cast<int64_t>(step) * K, pb);
+    if (i < OA::kEach) A.load(i, step * K, pa);
+    else B.load(i - OA::kEach, step * K, pb);
   };
   if (steps > 0) {
 #pragma unroll
@@ -290,11 +345,11 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if constexpr (!DIRECT) {
-          A.store(sa[cur]);
-          B.store(sb[cur]);
+          A.store(sa[0] + cur * OA::kElems);
+          B.store(sb[0] + cur * OB::kElems);
         }
       }
-      const uint16_t *ra = sa[from] + a_half[Q], *rb = sb[from] + b_half[Q];
+      const uint16_t *ra = sa[0] + from * OA::kElems + a_half[Q], *rb = sb[0] + from * OB::kElems + b_half[Q];
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
         fa[Q][i] = OA::read(ra, 16 * i);
@@ -304,7 +359,8 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
         for (int j = 0; j < NF; ++j) acc[i][j] = mfma16<DT>(fb[P][j], fa[P][i], acc[i][j]);
         if (P == 1) {
 #pragma unroll
-          for (int k = i * kLoads / MF; k < (i + 1) * kLoads / MF; ++k) load(k, it + (DIRECT ? 2 : 3), sa[cur], sb[cur]);
+          for (int k = i * kLoads / MF; k < (i + 1) * kLoads / MF; ++k)
+            load(k, it + (DIRECT ? 2 : 3), sa[0] + cur * OA::kElems, sb[0] + cur * OB::kElems);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -312,48 +368,50 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
         if (sums) {
 #pragma unroll
           for (int i = 0; i < MF; ++i) {
-            float t[8];
+            float u[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = Fmt<DT>::to_f(fa[P][i][e]);
-            sum[i] += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+            for (int e = 0; e < 8; ++e) u[e] = Fmt<DT>::to_f(fa[P][i][e]);
+            sum[i] += ((u[0] + u[1]) + (u[2] + u[3])) + ((u[4] + u[5]) + (u[6] + u[7]));
           }
         }
       }
     }
   }
-  wait_loads<0>();  // LDS stays this workgroup's until the last load is done
+  wait_loads<0>();  // no load is under way when LDS takes the results
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 
-  // this lane: m = wm + 16 i + l % 16; RUNS runs of LEN adjacent n from wn + LEN (l / 16) on
-  constexpr int LEN = B_ALONG ? 4 * NF : 4, RUNS = 4 * NF / LEN;
-  const int n = wn + (l >> 4) * LEN;
+  constexpr int LEN = B_ALONG ? 4 * NF : 4;  // adjacent n of a lane
   float bias[OP == kForward ? LEN : 1];
   if constexpr (OP == kForward) {
-    static_assert(RUNS == 1, "one run");
+    const int n = wn + (l >> 4) * LEN;
     const uint16_t* p = static_cast<const uint16_t*>(a.bias) + static_cast<int64_t>(expert) * a.outer + n0 + n;
     const bool with = a.bias && expert < a.experts;
 #pragma unroll
-    for (int i = 0; i < LEN; ++i) bias[i] = with && i < B.ms - n ? Fmt<DT>::to_f(p[i]) : 0.0f;
+    for (int i = 0; i < LEN; ++i) bias[i] = with && i < n_left - n ? Fmt<DT>::to_f(p[i]) : 0.0f;
   }
+  auto value = [&](int i, int j, int e) { return OP == kForward ? acc[i][j][e] + bias[4 * j + e] : acc[i][j][e]; };
+  constexpr int kWaveBytes = kBytes / (WM * WN) / 16 * 16;
+  char* s = lds + w * kWaveBytes;
+  const int64_t pitch = OP == kBackwardWeight ? a.inner : a.out_stride;
+  const int64_t at = OP == kBackwardWeight ? (part ? 0 : expert * io) + (m0 + wm) * pitch + n0 + wn : (row + wm) * pitch + n0 + wn;
+  const int ml = m_left - wm, nl = n_left - wn;
+  if (part || a.out_dt == 0)
+    store_tile<float, MF, NF, LEN, kWaveBytes>((part ? part : static_cast<float*>(a.out)) + at, pitch, ml, nl, s, value);
+  else
+    store_tile<uint16_t, MF, NF, LEN, kWaveBytes>(static_cast<uint16_t*>(a.out) + at, pitch, ml, nl, s,
+                                                  [&](int i, int j, int e) { return tower_from_f<DT>(value(i, j, e)); });
+  if constexpr (OP == kBackwardWeight) {
+    if (sums) {  // the 4 lanes of an m have its rows 8 at a time
 #pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const int m = wm + 16 * i + (l & 15);
-    if (m >= A.ms) continue;
-    const int64_t at = (OP == kBackwardWeight ? expert * io + (m0 + m) * a.inner : (row + m) * a.out_stride) + n0 + n;
-#pragma unroll
-    for (int u = 0; u < RUNS; ++u) {
-      float v[LEN];
-#pragma unroll
-      for (int e = 0; e < LEN; ++e) {
-        v[e] = acc[i][u * (LEN / 4) + e / 4][e % 4];
-        if constexpr (OP == kForward) v[e] += bias[e];
-      }
-      store_out<LEN>(a.out, a.out_dt, at + 16 * u, B.ms - n - 16 * u, v);
-    }
-    if constexpr (OP == kBackwardWeight) {
-      if (sums) {  // the 4 lanes of an m have its rows 8 at a time
-        float t = sum[i] + __shfl_xor(sum[i], 16);
-        t += __shfl_xor(t, 32);
-        if (l < 16) store_any(a.grad_bias, a.out_dt, static_cast<int64_t>(expert) * a.outer + m0 + m, t);
+      for (int i = 0; i < MF; ++i) {
+        float u = sum[i] + __shfl_xor(sum[i], 16);
+        u += __shfl_xor(u, 32);
+        const int m = wm + 16 * i + (l & 15);
+        if (l < 16 && m < m_left) {
+          if (part) part[io + m0 + m] = u;
+          else store_any(a.grad_bias, a.out_dt, static_cast<int64_t>(expert) * a.outer + m0 + m, u);
+        }
       }
     }
   }
