@@ -183,9 +183,11 @@ __device__ __forceinline__ unsigned chiplet_order(unsigned id, unsigned n) {
 }
 
 // A wave's results, MF x NF products, to rows `out` + m * pitch, of type S: through LDS, a few rows at a
-// time, so that each row's bytes leave in whole cache lines (16 lanes' 4 adjacent values each reach
-// memory as 32-byte pieces: 1.07 GB of them took 0.34 ms of 1.23).  `s`: this wave's part of LDS.
-template <typename S, int MF, int NF, int LEN, int BYTES, typename Value>
+// time, so that each row's bytes leave in whole cache lines.  STREAM: past the caches, where they would
+// take the operands' place (1.07 GB of results of 131072 rows, inner 4096, outer 1024: backward by
+// input 1.21 ms without, 1.03 ms with it, 0.96 ms with no results stored; streaming pieces of 32
+// bytes straight from the registers, 1.40 ms).  `s`: this wave's part of LDS.
+template <typename S, bool STREAM, int MF, int NF, int LEN, int BYTES, typename Value>
 __device__ __forceinline__ void store_tile(S* out, int64_t pitch, int m_left, int n_left, char* s, Value value) {
   constexpr int kRow = NF * 16 * static_cast<int>(sizeof(S)), kPitch = kRow + 16;  // 16: the rows of a write in different banks
   constexpr int kFit = BYTES / (16 * kPitch);
@@ -212,7 +214,10 @@ __device__ __forceinline__ void store_tile(S* out, int64_t pitch, int m_left, in
       const int m = k * (kWave / kLanes) + l / kLanes, n = (l % kLanes) * kPer;
       Vec<S, kPer> v;
       __builtin_memcpy(v.e, s + m * kPitch + n * sizeof(S), 16);
-      if (16 * i0 + m < m_left) store_vec_part<S, kPer>(out + (16 * i0 + m) * pitch + n, n_left - n, v);
+      if (16 * i0 + m >= m_left) continue;
+      S* p = out + (16 * i0 + m) * pitch + n;
+      if (STREAM && n_left - n >= kPer) store_vec_stream<S, kPer>(p, v);
+      else store_vec_part<S, kPer>(p, n_left - n, v);
     }
   }
 }
@@ -396,11 +401,13 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(Groupe
   const int64_t pitch = OP == kBackwardWeight ? a.inner : a.out_stride;
   const int64_t at = OP == kBackwardWeight ? (part ? 0 : expert * io) + (m0 + wm) * pitch + n0 + wn : (row + wm) * pitch + n0 + wn;
   const int ml = m_left - wm, nl = n_left - wn;
-  if (part || a.out_dt == 0)
-    store_tile<float, MF, NF, LEN, kWaveBytes>((part ? part : static_cast<float*>(a.out)) + at, pitch, ml, nl, s, value);
+  if (OP == kBackwardWeight && part)  // read back soon
+    store_tile<float, false, MF, NF, LEN, kWaveBytes>(part + at, pitch, ml, nl, s, value);
+  else if (a.out_dt == 0)
+    store_tile<float, true, MF, NF, LEN, kWaveBytes>(static_cast<float*>(a.out) + at, pitch, ml, nl, s, value);
   else
-    store_tile<uint16_t, MF, NF, LEN, kWaveBytes>(static_cast<uint16_t*>(a.out) + at, pitch, ml, nl, s,
-                                                  [&](int i, int j, int e) { return tower_from_f<DT>(value(i, j, e)); });
+    store_tile<uint16_t, true, MF, NF, LEN, kWaveBytes>(static_cast<uint16_t*>(a.out) + at, pitch, ml, nl, s,
+                                                        [&](int i, int j, int e) { return tower_from_f<DT>(value(i, j, e)); });
   if constexpr (OP == kBackwardWeight) {
     if (sums) {  // the 4 lanes of an m have its rows 8 at a time
 #pragma unroll

@@ -32,6 +32,18 @@ __device__ __forceinline__ void store_vec_any(S* p, const Vec<S, N>& v) {
 #pragma unroll
   for (int i = 0; i < N; i += kPart) __builtin_memcpy(p + i, &v.e[i], kPart * sizeof(S));
 }
+// Same with the streaming cache policy, 16 bytes at a time: for results that nothing reads back soon.
+template <typename S, int N>
+__device__ __forceinline__ void store_vec_stream(S* p, const Vec<S, N>& v) {
+  typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+  static_assert(N * sizeof(S) % 16 == 0, "whole 16 bytes");
+#pragma unroll
+  for (int i = 0; i < N; i += 16 / static_cast<int>(sizeof(S))) {
+    u32x4_any x;
+    __builtin_memcpy(&x, &v.e[i], 16);
+    __builtin_nontemporal_store(x, reinterpret_cast<u32x4_any*>(p + i));
+  }
+}
 // The first `left` of N elements (all of them where left >= N); the others are zero.
 template <typename S, int N>
 __device__ __forceinline__ void load_vec_part(const S* p, int64_t left, Vec<S, N>& v) {
