@@ -12,7 +12,7 @@ from typing import Optional, Sequence, Union
 
 import torch
 
-from . import _I_DTYPE, _W_DTYPE, TbeError, _check, _ptr, _stream, lib
+from . import _I_DTYPE, _W_DTYPE, TbeError, _check, lib
 
 TBE_LAYER_NORM_MAX_WIDTH = 1 << 24
 TBE_STATE_F32, TBE_STATE_8BIT = 0, 1
@@ -29,76 +29,96 @@ class tbe_adamw_tensor(ctypes.Structure):
                 ("state", ctypes.c_int32)]
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise TbeError(what)
+# The checks build their messages only when they refuse: a call of a small kernel takes a few
+# microseconds in all.
+def _device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
 
 
-def _on_gpu(name: str, t: torch.Tensor):
-    _need(t.is_cuda and t.device.index == torch.cuda.current_device(),
-          f"{name} is on {t.device}, not on the current GPU")
+def _current(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _refuse(what: str):
+    raise TbeError(what)
+
+
+def _off_gpu(name: str, t: torch.Tensor):
+    _refuse(f"{name} is on {t.device}, not on the current GPU")
 
 
 def _dtype(name: str, t: torch.Tensor) -> int:
-    _need(t.dtype in _W_DTYPE, f"{name} is {t.dtype}: float32, float16 or bfloat16 are supported")
-    return _W_DTYPE[t.dtype]
+    d = _W_DTYPE.get(t.dtype)
+    if d is None:
+        _refuse(f"{name} is {t.dtype}: float32, float16 or bfloat16 are supported")
+    return d
 
 
-def _rows(name: str, t: torch.Tensor, shape=None) -> int:
+def _rows(name: str, t: torch.Tensor, dev: int, shape=None) -> int:
     """The row stride of a matrix whose rows are contiguous."""
-    _on_gpu(name, t)
-    _need(t.dim() == 2 and (shape is None or tuple(t.shape) == tuple(shape)),
-          f"{name} has shape {tuple(t.shape)}" + ("" if shape is None else f", not {tuple(shape)}"))
-    _need(t.shape[1] <= 1 or t.shape[0] == 0 or t.stride(1) == 1, f"{name}: rows have to be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.get_device() != dev:
+        _off_gpu(name, t)
+    s = t.shape
+    if len(s) != 2 or (shape is not None and s != shape):
+        _refuse(f"{name} has shape {tuple(s)}" + ("" if shape is None else f", not {tuple(shape)}"))
+    ld, one = t.stride()
+    if one != 1 and s[1] > 1 and s[0] > 0:
+        _refuse(f"{name}: rows have to be contiguous")
+    return ld if s[0] > 1 else s[1]
 
 
-def _whole(name: str, t: torch.Tensor, shape, dtype=None):
+def _whole(name: str, t: torch.Tensor, dev: int, shape, dtype=None):
     """A contiguous tensor of this shape (and type)."""
-    _on_gpu(name, t)
-    _need(tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-          f"{name} has shape {tuple(t.shape)} and strides {tuple(t.stride())}: contiguous {tuple(shape)} is needed")
-    _need(dtype is None or t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}")
+    if t.get_device() != dev:
+        _off_gpu(name, t)
+    if t.shape != shape or not t.is_contiguous():
+        _refuse(f"{name} has shape {tuple(t.shape)} and strides {tuple(t.stride())}: contiguous {tuple(shape)} is needed")
+    if dtype is not None and t.dtype != dtype:
+        _refuse(f"{name} is {t.dtype}, not {dtype}")
 
 
-def _bytes(workspace: Optional[torch.Tensor]) -> int:
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _bytes(workspace: Optional[torch.Tensor], dev: int) -> int:
     if workspace is None:
         return 0
-    _on_gpu("workspace", workspace)
+    if workspace.get_device() != dev:
+        _off_gpu("workspace", workspace)
     return workspace.numel() * workspace.element_size()
 
 
 # ---------------------------------------------------------------------------
 # layer norm
 # ---------------------------------------------------------------------------
+def _vectors(dev: int, width: int, *named) -> int:
+    """The one type of the vectors that are given."""
+    wd, dtype, shape = 0, None, (width,)
+    for name, t in named:
+        if t is not None:
+            _whole(name, t, dev, shape, dtype)
+            if dtype is None:
+                dtype, wd = t.dtype, _dtype(name, t)
+    return wd
+
+
 def tbe_layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor],
                            eps: float, y: torch.Tensor, mean: Optional[torch.Tensor] = None,
                            rstd: Optional[torch.Tensor] = None, stream=None):
     """y = (x - mean) * rstd * weight + bias for each row of x [rows, width]."""
-    xs = _rows("x", x)
-    rows, width = x.shape
-    ys = _rows("y", y, x.shape)
-    vectors = [("weight", weight), ("bias", bias)]
-    wd = _vectors(vectors, width)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t is not None:
-            _whole(name, t, (rows,), torch.float32)
-    st = lib().tbe_layer_norm_forward(rows, width, _ptr(x), xs, _dtype("x", x), _ptr(weight), _ptr(bias), wd,
-                                      float(eps), _ptr(y), ys, _dtype("y", y), _ptr(mean), _ptr(rstd),
-                                      _stream(stream))
+    dev = _device()
+    xs = _rows("x", x, dev)
+    rows, width = shape = x.shape
+    ys = _rows("y", y, dev, shape)
+    wd = _vectors(dev, width, ("weight", weight), ("bias", bias))
+    if mean is not None:
+        _whole("mean", mean, dev, (rows,), torch.float32)
+    if rstd is not None:
+        _whole("rstd", rstd, dev, (rows,), torch.float32)
+    st = lib().tbe_layer_norm_forward(rows, width, x.data_ptr(), xs, _dtype("x", x), _at(weight), _at(bias), wd, eps,
+                                      y.data_ptr(), ys, _dtype("y", y), _at(mean), _at(rstd), _current(stream, dev))
     _check(st, "tbe_layer_norm_forward")
-
-
-def _vectors(named, width: int) -> int:
-    """The one type of the vectors that are given."""
-    wd, first = 0, None
-    for name, t in named:
-        if t is None:
-            continue
-        first = t if first is None else first
-        _whole(name, t, (width,), first.dtype)
-        wd = _dtype(name, t)
-    return wd
 
 
 def tbe_layer_norm_backward_workspace_bytes(rows: int, width: int) -> int:
@@ -109,68 +129,76 @@ def tbe_layer_norm_backward(x: torch.Tensor, grad_y: torch.Tensor, mean: torch.T
                             weight: Optional[torch.Tensor], grad_x: Optional[torch.Tensor],
                             grad_weight: Optional[torch.Tensor], grad_bias: Optional[torch.Tensor],
                             workspace: Optional[torch.Tensor], stream=None):
-    xs = _rows("x", x)
-    rows, width = x.shape
-    gs = _rows("grad_y", grad_y, x.shape)
+    """The gradients of tbe_layer_norm_forward; each of the three may be left out (None)."""
+    dev = _device()
+    xs = _rows("x", x, dev)
+    rows, width = shape = x.shape
+    gs = _rows("grad_y", grad_y, dev, shape)
     os = 0
     if grad_x is not None:
-        os = _rows("grad_x", grad_x, x.shape)
-        _need(grad_x.dtype == x.dtype, f"grad_x is {grad_x.dtype}, not {x.dtype}")
-    wd = _vectors([("weight", weight), ("grad_weight", grad_weight), ("grad_bias", grad_bias)], width)
-    _whole("mean", mean, (rows,), torch.float32)
-    _whole("rstd", rstd, (rows,), torch.float32)
-    st = lib().tbe_layer_norm_backward(rows, width, _ptr(x), xs, _dtype("x", x), _ptr(grad_y), gs,
-                                       _dtype("grad_y", grad_y), _ptr(mean), _ptr(rstd), _ptr(weight), wd,
-                                       _ptr(grad_x), os, _ptr(grad_weight), _ptr(grad_bias), _ptr(workspace),
-                                       _bytes(workspace), _stream(stream))
+        os = _rows("grad_x", grad_x, dev, shape)
+        if grad_x.dtype != x.dtype:
+            _refuse(f"grad_x is {grad_x.dtype}, not {x.dtype}")
+    wd = _vectors(dev, width, ("weight", weight), ("grad_weight", grad_weight), ("grad_bias", grad_bias))
+    _whole("mean", mean, dev, (rows,), torch.float32)
+    _whole("rstd", rstd, dev, (rows,), torch.float32)
+    st = lib().tbe_layer_norm_backward(rows, width, x.data_ptr(), xs, _dtype("x", x), grad_y.data_ptr(), gs,
+                                       _dtype("grad_y", grad_y), mean.data_ptr(), rstd.data_ptr(), _at(weight), wd,
+                                       _at(grad_x), os, _at(grad_weight), _at(grad_bias), _at(workspace),
+                                       _bytes(workspace, dev), _current(stream, dev))
     _check(st, "tbe_layer_norm_backward")
 
 
 # ---------------------------------------------------------------------------
 # linear layers on rows grouped by expert
 # ---------------------------------------------------------------------------
-def _grouped(weight_shape, offsets: torch.Tensor):
-    _need(len(weight_shape) == 3, f"weights have shape {tuple(weight_shape)}, not (experts, outer, inner)")
-    experts, outer, inner = weight_shape
-    _need(offsets.dtype in _I_DTYPE, f"offsets are {offsets.dtype}: int32 or int64 are supported")
-    _whole("offsets", offsets, (experts + 1,))
-    return experts, outer, inner
+def _grouped(shape, offsets: torch.Tensor, dev: int):
+    if len(shape) != 3:
+        _refuse(f"weights have shape {tuple(shape)}, not (experts, outer, inner)")
+    ot = _I_DTYPE.get(offsets.dtype)
+    if ot is None:
+        _refuse(f"offsets are {offsets.dtype}: int32 or int64 are supported")
+    _whole("offsets", offsets, dev, (shape[0] + 1,))
+    return ot
 
 
-def _same(named):
-    first = named[0]
-    for name, t in named[1:]:
-        _need(t is None or t.dtype == first[1].dtype, f"{name} is not of {first[0]}'s type")
+def _same(name: str, t: torch.Tensor, first: str, dtype):
+    if t.dtype != dtype:
+        _refuse(f"{name} is not of {first}'s type")
 
 
 def tbe_grouped_linear_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
                                offsets: torch.Tensor, y: torch.Tensor, stream=None):
     """y[i] = weight[e] @ x[i] + bias[e] for offsets[e] <= i < offsets[e + 1]; zero behind the last."""
-    experts, outer, inner = _grouped(weight.shape, offsets)
+    dev = _device()
+    ot = _grouped(weight.shape, offsets, dev)
+    experts, outer, inner = weight.shape
     rows = x.shape[0]
-    xs, ys = _rows("x", x, (rows, inner)), _rows("y", y, (rows, outer))
-    _whole("weight", weight, weight.shape)
+    xs, ys = _rows("x", x, dev, (rows, inner)), _rows("y", y, dev, (rows, outer))
+    _whole("weight", weight, dev, weight.shape)
+    _same("weight", weight, "x", x.dtype)
     if bias is not None:
-        _whole("bias", bias, (experts, outer))
-    _same([("x", x), ("weight", weight), ("bias", bias)])
-    st = lib().tbe_grouped_linear_forward(rows, experts, inner, outer, _ptr(x), xs, _ptr(weight), _ptr(bias),
-                                          _dtype("x", x), _ptr(offsets), _I_DTYPE[offsets.dtype], _ptr(y), ys,
-                                          _dtype("y", y), _stream(stream))
+        _whole("bias", bias, dev, (experts, outer))
+        _same("bias", bias, "x", x.dtype)
+    st = lib().tbe_grouped_linear_forward(rows, experts, inner, outer, x.data_ptr(), xs, weight.data_ptr(), _at(bias),
+                                          _dtype("x", x), offsets.data_ptr(), ot, y.data_ptr(), ys, _dtype("y", y),
+                                          _current(stream, dev))
     _check(st, "tbe_grouped_linear_forward")
 
 
 def tbe_grouped_linear_backward_input(grad_y: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
                                       grad_x: torch.Tensor, stream=None):
     """grad_x[i] = grad_y[i] @ weight[e]."""
-    experts, outer, inner = _grouped(weight.shape, offsets)
+    dev = _device()
+    ot = _grouped(weight.shape, offsets, dev)
+    experts, outer, inner = weight.shape
     rows = grad_y.shape[0]
-    gs, xs = _rows("grad_y", grad_y, (rows, outer)), _rows("grad_x", grad_x, (rows, inner))
-    _whole("weight", weight, weight.shape)
-    _same([("grad_y", grad_y), ("weight", weight)])
-    st = lib().tbe_grouped_linear_backward_input(rows, experts, inner, outer, _ptr(grad_y), gs, _ptr(weight),
-                                                 _dtype("grad_y", grad_y), _ptr(offsets),
-                                                 _I_DTYPE[offsets.dtype], _ptr(grad_x), xs,
-                                                 _dtype("grad_x", grad_x), _stream(stream))
+    gs, xs = _rows("grad_y", grad_y, dev, (rows, outer)), _rows("grad_x", grad_x, dev, (rows, inner))
+    _whole("weight", weight, dev, weight.shape)
+    _same("weight", weight, "grad_y", grad_y.dtype)
+    st = lib().tbe_grouped_linear_backward_input(rows, experts, inner, outer, grad_y.data_ptr(), gs, weight.data_ptr(),
+                                                 _dtype("grad_y", grad_y), offsets.data_ptr(), ot, grad_x.data_ptr(), xs,
+                                                 _dtype("grad_x", grad_x), _current(stream, dev))
     _check(st, "tbe_grouped_linear_backward_input")
 
 
@@ -183,18 +211,19 @@ def tbe_grouped_linear_backward_weight(x: torch.Tensor, grad_y: torch.Tensor, of
                                        grad_weight: torch.Tensor, grad_bias: Optional[torch.Tensor],
                                        workspace: Optional[torch.Tensor], stream=None):
     """grad_weight[e] = the sum of outer products of expert e's rows, grad_bias[e] their grad_y's sum."""
-    experts, outer, inner = _grouped(grad_weight.shape, offsets)
+    dev = _device()
+    ot = _grouped(grad_weight.shape, offsets, dev)
+    experts, outer, inner = grad_weight.shape
     rows = x.shape[0]
-    xs, gs = _rows("x", x, (rows, inner)), _rows("grad_y", grad_y, (rows, outer))
-    _whole("grad_weight", grad_weight, grad_weight.shape)
+    xs, gs = _rows("x", x, dev, (rows, inner)), _rows("grad_y", grad_y, dev, (rows, outer))
+    _whole("grad_weight", grad_weight, dev, grad_weight.shape)
+    _same("grad_y", grad_y, "x", x.dtype)
     if grad_bias is not None:
-        _whole("grad_bias", grad_bias, (experts, outer), grad_weight.dtype)
-    _same([("x", x), ("grad_y", grad_y)])
-    st = lib().tbe_grouped_linear_backward_weight(rows, experts, inner, outer, _ptr(x), xs, _ptr(grad_y), gs,
-                                                  _dtype("x", x), _ptr(offsets), _I_DTYPE[offsets.dtype],
-                                                  _ptr(grad_weight), _ptr(grad_bias),
-                                                  _dtype("grad_weight", grad_weight), _ptr(workspace),
-                                                  _bytes(workspace), _stream(stream))
+        _whole("grad_bias", grad_bias, dev, (experts, outer), grad_weight.dtype)
+    st = lib().tbe_grouped_linear_backward_weight(rows, experts, inner, outer, x.data_ptr(), xs, grad_y.data_ptr(), gs,
+                                                  _dtype("x", x), offsets.data_ptr(), ot, grad_weight.data_ptr(),
+                                                  _at(grad_bias), _dtype("grad_weight", grad_weight), _at(workspace),
+                                                  _bytes(workspace, dev), _current(stream, dev))
     _check(st, "tbe_grouped_linear_backward_weight")
 
 
@@ -212,31 +241,33 @@ class AdamWTensors:
                  masters: Optional[Sequence[Optional[torch.Tensor]]] = None,
                  exp_avg_scales: Optional[Sequence[Optional[torch.Tensor]]] = None,
                  exp_avg_sq_scales: Optional[Sequence[Optional[torch.Tensor]]] = None):
-        n = len(params)
+        n, dev = len(params), _device()
         none = [None] * n
         decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
         self.tensors = [list(x) if x is not None else none for x in
                         (params, grads, exp_avg, exp_avg_sq, masters, exp_avg_scales, exp_avg_sq_scales)]
-        _need(all(len(x) == n for x in self.tensors) and len(decay) == n,
-              f"{n} params need as many gradients, states and weight decays")
+        if any(len(x) != n for x in self.tensors) or len(decay) != n:
+            _refuse(f"{n} params need as many gradients, states and weight decays")
         self.c = (tbe_adamw_tensor * max(1, n))()
         self.count = n
         for i, (p, g, m, v, w, ms, vs) in enumerate(zip(*self.tensors)):
             numel = p.numel()
             eight = m.dtype == torch.uint8
             st = torch.uint8 if eight else torch.float32
+            blocks = -(-numel // TBE_ADAMW_BLOCK)
             for name, t, size, dt in (("param", p, numel, None), ("gradient", g, numel, None),
                                       ("exp_avg", m, numel, st), ("exp_avg_sq", v, numel, st),
-                                      ("master", w, numel, torch.float32),
-                                      ("exp_avg_scale", ms, -(-numel // TBE_ADAMW_BLOCK), torch.uint8),
-                                      ("exp_avg_sq_scale", vs, -(-numel // TBE_ADAMW_BLOCK), torch.uint8)):
+                                      ("master", w, numel, torch.float32), ("exp_avg_scale", ms, blocks, torch.uint8),
+                                      ("exp_avg_sq_scale", vs, blocks, torch.uint8)):
                 if t is None:
-                    _need("scale" not in name or not eight, f"tensor {i}: states of 8 bits need scales")
+                    if eight and "scale" in name:
+                        _refuse(f"tensor {i}: states of 8 bits need scales")
                     continue
-                _on_gpu(f"tensor {i}: {name}", t)
-                _need(t.is_contiguous() and t.numel() == size and (dt is None or t.dtype == dt),
-                      f"tensor {i}: {name} is {t.dtype} of {t.numel()} with strides {tuple(t.stride())}: "
-                      f"contiguous {'' if dt is None else dt} of {size} is needed")
+                if t.get_device() != dev:
+                    _off_gpu(f"tensor {i}: {name}", t)
+                if not t.is_contiguous() or t.numel() != size or (dt is not None and t.dtype != dt):
+                    _refuse(f"tensor {i}: {name} is {t.dtype} of {t.numel()} with strides {tuple(t.stride())}: "
+                            f"contiguous {'' if dt is None else dt} of {size} is needed")
             self.c[i] = tbe_adamw_tensor(
                 p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), None if w is None else w.data_ptr(),
                 ms.data_ptr() if eight else None, vs.data_ptr() if eight else None, numel, decay[i],
@@ -248,26 +279,28 @@ def tbe_adamw_step(tensors: AdamWTensors, step: int, lr: float, beta1: float = 0
                    eps: float = 1e-8, control: Optional[torch.Tensor] = None, stream=None):
     """One AdamW step on every tensor.  control (float64, on the GPU): step, lr factor, gradient
     factor, skip; its step takes the place of `step`."""
+    dev = _device()
     if control is not None:
-        _whole("control", control, (TBE_ADAMW_CONTROL,), torch.float64)
-    st = lib().tbe_adamw_step(tensors.c, tensors.count, int(step), float(lr), float(beta1), float(beta2),
-                              float(eps), _ptr(control), _stream(stream))
+        _whole("control", control, dev, (TBE_ADAMW_CONTROL,), torch.float64)
+    st = lib().tbe_adamw_step(tensors.c, tensors.count, step, lr, beta1, beta2, eps, _at(control), _current(stream, dev))
     _check(st, "tbe_adamw_step")
 
 
 def tbe_adamw_state_read(tensors: AdamWTensors, exp_avg_out: Sequence[torch.Tensor],
                          exp_avg_sq_out: Sequence[torch.Tensor], stream=None):
     """The values of states of 8 bits, into float32 or bfloat16 tensors (both hold them exactly)."""
-    n = tensors.count
-    _need(len(exp_avg_out) == n and len(exp_avg_sq_out) == n, f"{n} tensors need as many outputs of each state")
-    outs = list(exp_avg_out) + list(exp_avg_sq_out)
-    dtype = outs[0].dtype if outs else torch.float32
-    for k, t in enumerate(outs):
-        _on_gpu(f"output {k % n}", t)
-        _need(t.is_contiguous() and t.numel() == tensors.c[k % n].numel and t.dtype == dtype,
-              f"output {k % n} is {t.dtype} of {t.numel()}: contiguous {dtype} of {tensors.c[k % n].numel} is needed")
+    n, dev, c = tensors.count, _device(), tensors.c
+    if len(exp_avg_out) != n or len(exp_avg_sq_out) != n:
+        _refuse(f"{n} tensors need as many outputs of each state")
+    dtype = exp_avg_out[0].dtype if n else torch.float32
     array = ctypes.c_void_p * max(1, n)
-    st = lib().tbe_adamw_state_read(tensors.c, n, array(*[t.data_ptr() for t in exp_avg_out]),
-                                    array(*[t.data_ptr() for t in exp_avg_sq_out]),
-                                    _dtype("outputs", outs[0]) if outs else 0, _stream(stream))
+    arrays = array(), array()
+    for outs, at in zip((exp_avg_out, exp_avg_sq_out), arrays):
+        for i, t in enumerate(outs):
+            if t.get_device() != dev:
+                _off_gpu(f"output {i}", t)
+            if t.numel() != c[i].numel or t.dtype != dtype or not t.is_contiguous():
+                _refuse(f"output {i} is {t.dtype} of {t.numel()}: contiguous {dtype} of {c[i].numel} is needed")
+            at[i] = t.data_ptr()
+    st = lib().tbe_adamw_state_read(c, n, *arrays, _dtype("output 0", exp_avg_out[0]) if n else 0, _current(stream, dev))
     _check(st, "tbe_adamw_state_read")
