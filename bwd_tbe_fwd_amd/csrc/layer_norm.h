@@ -5,10 +5,10 @@
 // it is read once, its mean and then the sum of squared deviations are taken from registers
 // (two passes over registers lose nothing where the mean is large against the deviations, as
 // sum x^2 - mean^2 would), and it is written once.  Both directions are bound by memory.  The
-// lanes that own a row are 16, 64, 256 or 1024 by its width, so that a lane holds 4 to 32
-// elements: enough bytes in flight to cover the latency, few enough registers for 2 or more
-// waves per SIMD next to the scale, the shift and (backward) their gradients' sums, which stay
-// in registers while a workgroup walks its rows.
+// lanes that own a row are 16 to 1024 by its width, so that a lane holds 4 to 32 elements: enough
+// bytes in flight to cover the latency, few enough registers for several waves a SIMD next to the
+// scale, the shift and (backward) their gradients' sums, which stay in registers while a workgroup
+// walks its rows.
 #pragma once
 
 #include "tbe_internal.h"
@@ -43,6 +43,8 @@ struct NormArgs {
 template <int XT> constexpr int kNormVec = XT == 0 ? 4 : 8;
 
 constexpr int kNormBlock = 256;
+// Threads of a workgroup whose rows are owned by G lanes each.
+constexpr int norm_block(int G) { return G > kWave ? G : kNormBlock; }
 
 // Sum over the G threads that own a row, with one barrier where they are several waves.  s_red:
 // a float for each wave.  A kernel uses two of them in turn: who writes one again has passed the
@@ -88,16 +90,34 @@ __device__ __forceinline__ void row_sum2(float& u, float& v, float* s_red) {
   }
 }
 
-// VEC elements of the shared vector p from column c on (`left` of them valid), as floats.
+// VEC elements of the shared vector p from column c on (`left` of them valid), as floats; `none` where
+// there is no vector.
 template <int VEC>
 __device__ __forceinline__ void load_shared(const void* p, int dt, int64_t c, int64_t left, float none, float (&v)[VEC]) {
+  if (!p || left <= 0) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) v[i] = p && i < left ? load_any(p, dt, c + i) : none;
+    for (int i = 0; i < VEC; ++i) v[i] = none;
+  } else if (dt == 0) {
+    Vec<float, VEC> f;
+    load_vec_part<float, VEC>(static_cast<const float*>(p) + c, left, f);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = f.e[i];
+  } else {
+    Vec<uint16_t, VEC> h;
+    load_vec_part<uint16_t, VEC>(static_cast<const uint16_t*>(p) + c, left, h);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = dt == 1 ? Fmt<1>::to_f(h.e[i]) : Fmt<2>::to_f(h.e[i]);
+  }
 }
 
+// Whether a kernel loads its next row before it works on this one: where a lane has at most 32 bytes of
+// a row in flight.  (More cost the registers that the other waves' loads need: fp32 rows of 4096
+// reach the memory's rate without.)
+template <int XT, int NV> constexpr bool kNormAhead = NV * kNormVec<XT> * (XT == 0 ? 4 : 2) <= 32;
+
 template <int XT, int YT, int G, int NV>
-__global__ __launch_bounds__(G > kNormBlock ? G : kNormBlock) void norm_forward_kernel(NormArgs a) {
-  constexpr int VEC = kNormVec<XT>, B = G > kNormBlock ? G : kNormBlock, R = B / G;
+__global__ __launch_bounds__(norm_block(G)) void norm_forward_kernel(NormArgs a) {
+  constexpr int VEC = kNormVec<XT>, B = norm_block(G), R = B / G;
   constexpr bool KEEP = NV * VEC <= 16;  // the scale and the shift stay in registers
   using XS = typename Fmt<XT>::S;
   using YS = typename Fmt<YT>::S;
@@ -116,17 +136,26 @@ __global__ __launch_bounds__(G > kNormBlock ? G : kNormBlock) void norm_forward_
     }
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * R;
-  // every thread of a workgroup makes the same number of steps (the barriers in row_sum)
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * R; r0 < a.rows; r0 += step) {
-    const int64_t r = r0 + threadIdx.x / G;
-    const bool live = r < a.rows;
-    const int64_t row = live ? r : a.rows - 1;
-    const XS* xr = x + row * a.x_stride;
-    Vec<XS, VEC> raw[NV];
+  auto fetch = [&](int64_t r, Vec<XS, VEC>(&to)[NV]) {
+    const XS* xr = x + min(r, a.rows - 1) * a.x_stride;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int64_t c = static_cast<int64_t>(v * G + g) * VEC;
-      load_vec_part<XS, VEC>(xr + c, a.width - c, raw[v]);
+      load_vec_part<XS, VEC>(xr + c, a.width - c, to[v]);
+    }
+  };
+  Vec<XS, VEC> raw[NV], ahead[kNormAhead<XT, NV> ? NV : 1];
+  if constexpr (kNormAhead<XT, NV>) fetch(static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G, ahead);
+  // every thread of a workgroup makes the same number of steps (the barriers in row_sum)
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * R; r0 < a.rows; r0 += step) {
+    const int64_t row = r0 + threadIdx.x / G;
+    const bool live = row < a.rows;
+    if constexpr (kNormAhead<XT, NV>) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) raw[v] = ahead[v];
+      if (r0 + step < a.rows) fetch(row + step, ahead);
+    } else {
+      fetch(row, raw);
     }
     float sum = 0.0f;
 #pragma unroll
@@ -220,8 +249,8 @@ __global__ __launch_bounds__(kNormWide) void norm_forward_wide_kernel(NormArgs a
 // of grad_y * h and grad_y in registers; at the end the lane groups that share columns add up
 // through LDS in their order and the workgroup writes one partial row pair.
 template <int XT, int YT, int G, int NV>
-__global__ __launch_bounds__(G > kNormBlock ? G : kNormBlock) void norm_backward_kernel(NormArgs a) {
-  constexpr int VEC = kNormVec<XT>, B = G > kNormBlock ? G : kNormBlock, R = B / G;
+__global__ __launch_bounds__(norm_block(G)) void norm_backward_kernel(NormArgs a) {
+  constexpr int VEC = kNormVec<XT>, B = norm_block(G), R = B / G;
   using XS = typename Fmt<XT>::S;
   using YS = typename Fmt<YT>::S;
   __shared__ float s_red[2][2 * B / kWave];
@@ -237,27 +266,49 @@ __global__ __launch_bounds__(G > kNormBlock ? G : kNormBlock) void norm_backward
     for (int i = 0; i < VEC; ++i) gw[v][i] = gb[v][i] = 0.0f;
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * R;
-  int turn = 0;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * R; r0 < a.rows; r0 += step, turn ^= 1) {
-    const int64_t r = r0 + threadIdx.x / G;
+  // A wave that owns whole rows of 16 bits loads its next row before it works on this one: 10007 rows of
+  // 1001, where a wave has two or three, 27.1 -> 22.2 us.  Wider rows lose more by the registers
+  // (65536 rows of 4096: 0.41 -> 0.52 ms).
+  constexpr bool AHEAD = G == 64 && XT != 0;
+  auto fetch = [&](int64_t r, Vec<XS, VEC>(&xs)[NV], Vec<YS, VEC>(&gs)[NV], float& mean, float& rstd) {
     const bool live = r < a.rows;
     const int64_t row = live ? r : a.rows - 1;
     const XS* xr = static_cast<const XS*>(a.x) + row * a.x_stride;
     const YS* gr = static_cast<const YS*>(a.gy) + row * a.gy_stride;
-    Vec<XS, VEC> raw[NV];
-    Vec<YS, VEC> gin[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int64_t c = static_cast<int64_t>(v * G + g) * VEC;
       // a group without a row reads the last row and adds zeros
-      load_vec_part<XS, VEC>(xr + c, a.width - c, raw[v]);
-      load_vec_part<YS, VEC>(gr + c, live ? a.width - c : 0, gin[v]);
+      load_vec_part<XS, VEC>(xr + c, a.width - c, xs[v]);
+      load_vec_part<YS, VEC>(gr + c, live ? a.width - c : 0, gs[v]);
     }
-    const float mean = a.mean[row], rstd = a.rstd[row];
+    mean = a.mean[row];
+    rstd = a.rstd[row];
+  };
+  Vec<XS, VEC> raw[NV], raw_ahead[AHEAD ? NV : 1];
+  Vec<YS, VEC> gin[NV], gin_ahead[AHEAD ? NV : 1];
+  float mean, rstd, mean_ahead, rstd_ahead;
+  if constexpr (AHEAD) fetch(static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G, raw_ahead, gin_ahead, mean_ahead, rstd_ahead);
+  int turn = 0;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * R; r0 < a.rows; r0 += step, turn ^= 1) {
+    const int64_t row = r0 + threadIdx.x / G;
+    const bool live = row < a.rows;
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        raw[v] = raw_ahead[v];
+        gin[v] = gin_ahead[v];
+      }
+      mean = mean_ahead;
+      rstd = rstd_ahead;
+      if (r0 + step < a.rows) fetch(row + step, raw_ahead, gin_ahead, mean_ahead, rstd_ahead);
+    } else {
+      fetch(row, raw, gin, mean, rstd);
+    }
     float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t left = live ? a.width - static_cast<int64_t>(v * G + g) * VEC : 0;
+      const int64_t c = static_cast<int64_t>(v * G + g) * VEC, left = live ? a.width - c : 0;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         // columns past the row have no h (mean * rstd there could be infinite)
@@ -294,12 +345,14 @@ __global__ __launch_bounds__(G > kNormBlock ? G : kNormBlock) void norm_backward
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int64_t c = static_cast<int64_t>(v * G + g) * VEC;
+      Vec<float, VEC> o, p;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        if (c + i < a.width) {
-          out[c + i] = gw[v][i];
-          out[a.width + c + i] = gb[v][i];
-        }
+      for (int i = 0; i < VEC; ++i) {
+        o.e[i] = gw[v][i];
+        p.e[i] = gb[v][i];
+      }
+      store_vec_part<float, VEC>(out + c, a.width - c, o);
+      store_vec_part<float, VEC>(out + a.width + c, a.width - c, p);
     }
   } else {
 #pragma unroll
@@ -322,8 +375,12 @@ __global__ __launch_bounds__(G > kNormBlock ? G : kNormBlock) void norm_backward
 // below takes the partial sums, a slice of rows and 256 columns a workgroup.
 template <int XT, int YT>
 __global__ __launch_bounds__(kNormWide) void norm_backward_wide_kernel(NormArgs a) {
+  constexpr int VEC = kNormVec<XT>;
+  constexpr int64_t kStep = static_cast<int64_t>(kNormWide) * VEC;
   using XS = typename Fmt<XT>::S;
   using YS = typename Fmt<YT>::S;
+  Vec<XS, VEC> raw;
+  Vec<YS, VEC> gin;
   __shared__ float s_red[2][2 * kNormWide / kWave];
   const float width = static_cast<float>(a.width);
   int turn = 0;
@@ -333,17 +390,31 @@ __global__ __launch_bounds__(kNormWide) void norm_backward_wide_kernel(NormArgs 
     XS* xo = static_cast<XS*>(a.gx) + row * a.gx_stride;
     const float mean = a.mean[row], rstd = a.rstd[row];
     float c1 = 0.0f, c2 = 0.0f;
-    for (int64_t c = threadIdx.x; c < a.width; c += kNormWide) {
-      const float d = Fmt<YT>::to_f(gr[c]) * (a.w ? load_any(a.w, a.w_dt, c) : 1.0f);
-      c1 += d;
-      c2 += d * (Fmt<XT>::to_f(xr[c]) - mean) * rstd;
+    for (int64_t c = threadIdx.x * VEC; c < a.width; c += kStep) {
+      float w[VEC];
+      load_vec_part<XS, VEC>(xr + c, a.width - c, raw);
+      load_vec_part<YS, VEC>(gr + c, a.width - c, gin);  // zeros past the row
+      load_shared<VEC>(a.w, a.w_dt, c, a.width - c, 1.0f, w);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float d = Fmt<YT>::to_f(gin.e[i]) * w[i];
+        c1 += d;
+        c2 += i < a.width - c ? d * ((Fmt<XT>::to_f(raw.e[i]) - mean) * rstd) : 0.0f;
+      }
     }
     row_sum2<kNormWide>(c1, c2, s_red[turn]);
     c1 /= width;
     c2 /= width;
-    for (int64_t c = threadIdx.x; c < a.width; c += kNormWide) {
-      const float d = Fmt<YT>::to_f(gr[c]) * (a.w ? load_any(a.w, a.w_dt, c) : 1.0f);
-      xo[c] = tower_from_f<XT>((d - c1 - (Fmt<XT>::to_f(xr[c]) - mean) * rstd * c2) * rstd);
+    for (int64_t c = threadIdx.x * VEC; c < a.width; c += kStep) {
+      float w[VEC];
+      load_vec_part<XS, VEC>(xr + c, a.width - c, raw);
+      load_vec_part<YS, VEC>(gr + c, a.width - c, gin);
+      load_shared<VEC>(a.w, a.w_dt, c, a.width - c, 1.0f, w);
+      Vec<XS, VEC> o;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        o.e[i] = tower_from_f<XT>((Fmt<YT>::to_f(gin.e[i]) * w[i] - c1 - (Fmt<XT>::to_f(raw.e[i]) - mean) * rstd * c2) * rstd);
+      store_vec_part<XS, VEC>(xo + c, a.width - c, o);
     }
   }
 }
@@ -383,48 +454,58 @@ tbe_status norm_launch(const char* what, K* kernel, int64_t work, int threads, i
 
 template <int XT, int YT, int G, int NV>
 tbe_status norm_forward_as(const NormArgs& a, hipStream_t s) {
-  constexpr int B = G > kNormBlock ? G : kNormBlock;
+  constexpr int B = norm_block(G);
   constexpr int64_t R = B / G;
   return norm_launch("norm_forward", norm_forward_kernel<XT, YT, G, NV>, (a.rows + R - 1) / R, B, 0x7fffffff, a, s, nullptr);
 }
 template <int XT, int YT, int G, int NV>
 tbe_status norm_backward_as(const NormArgs& a, hipStream_t s, int* grid) {
-  constexpr int B = G > kNormBlock ? G : kNormBlock;
+  constexpr int B = norm_block(G);
   constexpr int64_t R = B / G;
-  return norm_launch("norm_backward", norm_backward_kernel<XT, YT, G, NV>, (a.rows + R - 1) / R, B, norm_partials(a.width), a,
-                     s, grid);
+  // at least two rows a lane group: a workgroup's partial rows are as many bytes as one or two rows
+  return norm_launch("norm_backward", norm_backward_kernel<XT, YT, G, NV>, (a.rows + 2 * R - 1) / (2 * R), B,
+                     norm_partials(a.width), a, s, grid);
 }
 
+// Up to 16 elements a lane (32 for the widest rows), by as few lanes as that takes.
 template <int XT, int YT>
 tbe_status norm_forward_types(const NormArgs& a, hipStream_t s) {
+  constexpr int F = XT == 0 ? 2 : 1;  // vectors of 8 elements
   const int64_t n = (a.width + kNormVec<XT> - 1) / kNormVec<XT>;  // vectors of a row
   if (n <= 16) return norm_forward_as<XT, YT, 16, 1>(a, s);
   if (n <= 32) return norm_forward_as<XT, YT, 16, 2>(a, s);
   if (n <= 64) return norm_forward_as<XT, YT, 64, 1>(a, s);
-  if (n <= 128) return norm_forward_as<XT, YT, 64, 2>(a, s);
-  if (n <= 256) return norm_forward_as<XT, YT, 64, 4>(a, s);
-  if (n <= 512) return norm_forward_as<XT, YT, 256, 2>(a, s);
-  if (n <= 1024) return norm_forward_as<XT, YT, 256, 4>(a, s);
-  if (n <= 2048) return norm_forward_as<XT, YT, 256, 8>(a, s);
-  if (n <= 4096) return norm_forward_as<XT, YT, 1024, 4>(a, s);
+  if (n <= 64 * 2 * F) return norm_forward_as<XT, YT, 64, 2 * F>(a, s);
+  if (n <= 256 * F) return norm_forward_as<XT, YT, 256, F>(a, s);
+  if (n <= 256 * 2 * F) return norm_forward_as<XT, YT, 256, 2 * F>(a, s);
+  if (n <= 512 * 2 * F) return norm_forward_as<XT, YT, 512, 2 * F>(a, s);
+  if (n <= 1024 * 2 * F) return norm_forward_as<XT, YT, 1024, 2 * F>(a, s);
+  if (n <= 1024 * 4 * F) return norm_forward_as<XT, YT, 1024, 4 * F>(a, s);
   return norm_launch("norm_forward", norm_forward_wide_kernel<XT, YT>, a.rows, kNormWide, 0x7fffffff, a, s, nullptr);
 }
 
+// 16 elements a lane for x of fp32, 8 where several waves own a row of 16 bits: more waves a row, fewer
+// registers (65536 rows of 4096: 256 lanes 0.41 ms, 512 lanes 0.36 ms).
 template <int XT, int YT>
 tbe_status norm_backward_types(const NormArgs& a, hipStream_t s, int* grid) {
   const int64_t n = (a.width + kNormVec<XT> - 1) / kNormVec<XT>;
-  constexpr int kMost = XT == 0 ? 4 : 2;  // vectors of a lane: at most 16 elements
   if (n <= 16) return norm_backward_as<XT, YT, 16, 1>(a, s, grid);
   if (n <= 32) return norm_backward_as<XT, YT, 16, 2>(a, s, grid);
   if (n <= 64) return norm_backward_as<XT, YT, 64, 1>(a, s, grid);
-  if (n <= 128) return norm_backward_as<XT, YT, 64, 2>(a, s, grid);
-  if (n <= 64 * kMost) return norm_backward_as<XT, YT, 64, kMost>(a, s, grid);
-  if (n <= 256) return norm_backward_as<XT, YT, 256, 1>(a, s, grid);
-  if (n <= 512) return norm_backward_as<XT, YT, 256, 2>(a, s, grid);
-  if (n <= 256 * kMost) return norm_backward_as<XT, YT, 256, kMost>(a, s, grid);
-  if (n <= 1024) return norm_backward_as<XT, YT, 1024, 1>(a, s, grid);
-  if (n <= 2048) return norm_backward_as<XT, YT, 1024, 2>(a, s, grid);
-  if (n <= 1024 * kMost) return norm_backward_as<XT, YT, 1024, kMost>(a, s, grid);
+  if constexpr (XT == 0) {
+    if (n <= 128) return norm_backward_as<XT, YT, 64, 2>(a, s, grid);
+    if (n <= 256) return norm_backward_as<XT, YT, 64, 4>(a, s, grid);
+    if (n <= 512) return norm_backward_as<XT, YT, 256, 2>(a, s, grid);
+    if (n <= 1024) return norm_backward_as<XT, YT, 256, 4>(a, s, grid);
+    if (n <= 2048) return norm_backward_as<XT, YT, 512, 4>(a, s, grid);
+    if (n <= 4096) return norm_backward_as<XT, YT, 1024, 4>(a, s, grid);
+  } else {
+    if (n <= 128) return norm_backward_as<XT, YT, 64, 2>(a, s, grid);
+    if (n <= 256) return norm_backward_as<XT, YT, 256, 1>(a, s, grid);
+    if (n <= 512) return norm_backward_as<XT, YT, 512, 1>(a, s, grid);
+    if (n <= 1024) return norm_backward_as<XT, YT, 1024, 1>(a, s, grid);
+    if (n <= 2048) return norm_backward_as<XT, YT, 1024, 2>(a, s, grid);
+  }
   tbe_status st = TBE_OK;
   if (a.gx) st = norm_launch("norm_backward", norm_backward_wide_kernel<XT, YT>, a.rows, kNormWide, 0x7fffffff, a, s, nullptr);
   if (st != TBE_OK || !a.partial) return st;

@@ -10,22 +10,28 @@
 namespace tbe {
 namespace {
 
-// Final sum of the partial rows [P][2][width], in the order of the workgroups: 16 waves take the
-// rows w, w + 16, ... of 64 columns, then wave 0's lanes add the 16 sums in their order.
-constexpr int kSumWaves = 16;
-__global__ __launch_bounds__(kSumWaves * kWave) void norm_partials_kernel(const float* __restrict__ partial, int P,
-                                                                         int64_t width, void* gw, void* gb, int dt) {
-  __shared__ float s[kSumWaves][kWave];
-  const int w = threadIdx.x >> 6, l = lane_id();
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kWave + l;
+// Final sum of the partial rows [P][2][width], in a fixed order: a workgroup takes 16 columns, its 64
+// groups of 16 lanes the rows g, g + 64, ..., 4 of them in flight, then 16 lanes add the 64 sums.  64
+// columns and 16 groups left 1024 rows of 1001 columns to 32 workgroups that waited for one row
+// after the other.
+constexpr int kSumCols = 16, kSumGroups = 64;
+__global__ __launch_bounds__(kSumCols * kSumGroups) void norm_partials_kernel(const float* __restrict__ partial, int P,
+                                                                             int64_t width, void* gw, void* gb, int dt) {
+  __shared__ float s[kSumGroups][kSumCols + 1];
+  const int g = threadIdx.x / kSumCols, l = threadIdx.x % kSumCols;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kSumCols + l;
   float sum = 0.0f;
-  if (c < 2 * width)
-    for (int p = w; p < P; p += kSumWaves) sum += partial[static_cast<int64_t>(p) * 2 * width + c];
-  s[w][l] = sum;
+  if (c < 2 * width) {
+    const float* p = partial + c;
+#pragma unroll 4
+    for (int r = g; r < P; r += kSumGroups) sum += p[static_cast<int64_t>(r) * 2 * width];
+  }
+  s[g][l] = sum;
   __syncthreads();
-  if (w || c >= 2 * width) return;
+  if (g || c >= 2 * width) return;
   sum = 0.0f;
-  for (int k = 0; k < kSumWaves; ++k) sum += s[k][l];
+#pragma unroll 8
+  for (int k = 0; k < kSumGroups; ++k) sum += s[k][l];
   if (c < width) {
     if (gw) store_any(gw, dt, c, sum);
   } else if (gb) {
@@ -155,7 +161,7 @@ extern "C" tbe_status tbe_layer_norm_backward(int64_t rows, int64_t width, const
   }
   if (!sums) return TBE_OK;
   ProfScope ps("norm_partials", s);
-  hipLaunchKernelGGL(norm_partials_kernel, dim3((2 * width + kWave - 1) / kWave), dim3(kSumWaves * kWave), 0, s, a.partial, grid,
+  hipLaunchKernelGGL(norm_partials_kernel, dim3((2 * width + kSumCols - 1) / kSumCols), dim3(kSumCols * kSumGroups), 0, s, a.partial, grid,
                      width, grad_weight, grad_bias, w_dtype);
   return check_launch("norm_partials");
 }
