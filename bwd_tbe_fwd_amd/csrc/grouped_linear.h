@@ -45,6 +45,7 @@ struct GroupedArgs {
   void* grad_bias;      // backward by weight; NULL: none
   void* workspace;
   int32_t split;        // backward by weight: rows of a unit, 0: an expert's rows are one
+  int32_t tile;         // backward by weight: which of kTileSide, host only
 };
 
 // Rows [lo, hi) of expert e < experts, inside [0, rows]; e = experts: the rows of no expert.
@@ -128,6 +129,35 @@ __device__ __forceinline__ int expert_by_rows(const GroupedArgs& a, int k) {
 // Row tiles at most: a partly filled one for every expert and the rows of no expert.
 inline int64_t row_tiles_bound(const GroupedArgs& a, int BM) { return a.rows / BM + a.experts + 1; }
 
+// ---------------------------------------------------------------------------
+// the tile, on the host
+// ---------------------------------------------------------------------------
+// Three tiles of C: 256 x 256 by 8 waves, 128 x 128 and 64 x 64 by 4; as many run at once as
+// kTileSlots on 256 CUs.  Time of a round of them in us: a fixed part and one for each 64 of k, fitted
+// to 65536 rows, 16 experts, 1024 x 1024 (139 / 148 / 218 us) and to 1024 and 4096 rows (27 / 18 /
+// 14 and 27 / 21 / 27 us).  The larger tile moves fewer operand bytes for each product, the smaller one
+// leaves fewer CUs idle: 8192 rows, 8 experts, 2048 x 2048 take 93 / 88 / 122 us, 400 rows, 8 experts,
+// 1024 x 512 take 24 / 13 / 10 us.
+constexpr int kTileSide[3] = {256, 128, 64};
+constexpr double kTileSlots[3] = {256, 512, 1024}, kTileFixed[3] = {6.0, 4.0, 3.0}, kTileStep[3] = {1.37, 0.78, 0.61};
+// Of the weight gradient, whose k are many: its 64 x 64 tiles wait for L2.
+constexpr double kWeightStep[3] = {1.45, 0.85, 0.90};
+inline double round_us(int tile, double k, const double (&step)[3] = kTileStep) { return kTileFixed[tile] + (k + 63) / 64 * step[tile]; }
+// Row tiles of `bm` rows that are expected of rows spread over experts.
+inline double row_tiles_expected(int64_t rows, int64_t experts, int bm) {
+  if (experts == 1) return static_cast<double>((rows + bm - 1) / bm);
+  return static_cast<double>(rows) / bm + 0.5 * static_cast<double>(hmin(experts, rows));
+}
+inline double rounds_of(double tiles, double slots) {
+  const double r = tiles / slots;
+  const int64_t whole = static_cast<int64_t>(r);
+  return r > static_cast<double>(whole) ? static_cast<double>(whole + 1) : static_cast<double>(hmax(1, whole));
+}
+
 enum { kForward = 0, kBackwardInput = 1, kBackwardWeight = 2 };
+
+// Defined in grouped_launch.h, in a translation unit for each product and type.
+template <int DT, int OP>
+tbe_status grouped_launch(const GroupedArgs& a, hipStream_t s);
 
 }  // namespace tbe

@@ -40,13 +40,13 @@ __device__ __forceinline__ int along_pattern(int r) {
   return ((r >> 1) & 1) | ((r / GAP) & 3) << 1;
 }
 // Place of an across row k in LDS, in elements.  A load instruction fills 1024 bytes: rows k = 8 g + 4 h
-// + r of one r together (h = 0, 1, and g & 1 where a row has 256 bytes), 32 bytes before those of
-// the next r: the 4 rows of a read, and those of the next 16 lanes' read, lie in different banks.
+// + r of one r together (h = 0, 1, and as many g as fit), 32 bytes before those of the next r: the 4
+// rows of a read lie in different banks.
+template <int SIDE> constexpr int kTogether = 256 / SIDE;  // g
 template <int SIDE>
 __device__ __forceinline__ int across_place(int k) {
   const int r = k & 3, h = (k >> 2) & 1, g = k >> 3;
-  if constexpr (SIDE == 256) return (4 * g + r) * (512 + 16) + h * SIDE;
-  else return (4 * (g >> 1) + r) * (512 + 16) + ((g & 1) * 2 + h) * SIDE;
+  return (4 * (g / kTogether<SIDE>) + r) * (512 + 16) + (g % kTogether<SIDE> * 2 + h) * SIDE;
 }
 
 // 16 bytes a lane from offset `o` of the buffer to LDS, lane l's at lds + 16 l.  Written as an
@@ -65,7 +65,7 @@ struct Operand {
   static constexpr int kEach = kChunks / THREADS;
   static constexpr int kElems = ALONG ? SIDE * K : SIDE * K / 512 * (512 + 16);  // of an LDS buffer
   static_assert(kChunks % THREADS == 0, "whole chunks a thread");
-  static_assert(ALONG || SIDE == 256 || SIDE == 128, "1024 bytes a load instruction");
+  static_assert(ALONG || SIDE == 256 || SIDE == 128 || SIDE == 64, "whole rows a load instruction");
 
   const uint16_t* base;  // (m0, k = 0)
   int64_t ld;
@@ -81,9 +81,9 @@ struct Operand {
       chunk = q % (K / 8) ^ along_pattern<GAP>(row);
     } else {
       const int u = q / 64, v = q % 64;  // load instruction, lane
+      const int sub = v / (SIDE / 8);    // 2 g + h
       chunk = v % (SIDE / 8);
-      if constexpr (SIDE == 256) row = 8 * (u >> 2) + (u & 3) + 4 * (v >> 5);
-      else row = 16 * (u >> 2) + (u & 3) + 4 * (v >> 4);
+      row = 8 * ((u >> 2) * kTogether<SIDE> + (sub >> 1)) + 4 * (sub & 1) + (u & 3);
     }
   }
   // where a thread's i-th chunk lies in LDS, in elements: lane l's 8 l after lane 0's
@@ -223,7 +223,7 @@ __device__ __forceinline__ void store_tile(S* out, int64_t pitch, int m_left, in
 }
 
 template <int DT, int OP, int BM, int BN, int WM, int WN, bool DIRECT>
-__global__ __launch_bounds__(WM * WN * kWave, 2) void grouped_tile_kernel(GroupedArgs a, int n_tiles) {
+__global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void grouped_tile_kernel(GroupedArgs a, int n_tiles) {
   constexpr int T = WM * WN * kWave;
   constexpr int MF = BM / WM / 16, NF = BN / WN / 16;  // products of 16 x 16 a wave
   constexpr bool A_ALONG = OP != kBackwardWeight, B_ALONG = OP == kForward;
