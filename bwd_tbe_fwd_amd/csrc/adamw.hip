@@ -80,14 +80,27 @@ __device__ __forceinline__ double power(double beta, int64_t n) {
 }
 
 // Bits of a finite magnitude; an infinity or a NaN does not scale its block (it becomes a NaN code).
-__device__ __forceinline__ uint32_t finite_bits(float x) {
-  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
-  return u < 0x7f800000u ? u : 0u;
-}
+__device__ __forceinline__ uint32_t finite_bits(uint32_t u) { return u < 0x7f800000u ? u : 0u; }
 // Scale byte of a block from the bits of its largest finite magnitude.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t top) { return min(max(top >> 23, 24u), 250u); }
 __device__ __forceinline__ float unit_of(uint32_t e) { return __uint_as_float(e << 23); }            // 2^(e - 127)
 __device__ __forceinline__ float inverse_unit(uint32_t e) { return __uint_as_float((254u - e) << 23); }
+
+// The scale byte of 16 lanes' values x, and whether one of them is an infinity or a NaN.
+__device__ __forceinline__ uint32_t block_scale(const float (&x)[kVals], bool& odd) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  top = lanes16_max(top);
+  odd = top >= 0x7f800000u;
+  if (odd) {  // rare
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) top = max(top, finite_bits(__float_as_uint(x[i]) & 0x7fffffffu));
+    top = lanes16_max(top);
+  }
+  return scale_byte(top);
+}
 
 __device__ __forceinline__ void open_m(const uint32_t (&c)[2], uint32_t e, float (&m)[kVals]) {
   const float unit = unit_of(e) * 0.0078125f;  // 2^(e - 134): exact, e >= 24 (0 for zeroed bytes)
@@ -106,9 +119,19 @@ __device__ __forceinline__ void open_v(const uint32_t (&c)[2], uint32_t e, float
 #pragma unroll
   for (int i = 0; i < kVals; ++i) {
     const uint32_t k = (c[i / 4] >> (8 * (i % 4))) & 0xffu;
-    v[i] = k == 0 ? 0.0f : k == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((k + 776u) << 20) * unit;
+    v[i] = k == 0 ? 0.0f : __uint_as_float((k << 20) + (776u << 20)) * unit;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t t = ~c[i];  // a byte of 255 is a zero byte here
+    if ((t - 0x01010101u) & ~t & 0x80808080u) {  // rare: a NaN
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (((c[i] >> (8 * k)) & 0xffu) == 255u) v[4 * i + k] = __uint_as_float(0x7fc00000u);
+    }
   }
 }
+// The conversion makes an infinity a NaN.
 __device__ __forceinline__ void pack_m(const float (&m)[kVals], uint32_t e, uint32_t (&c)[2]) {
   const float inverse = inverse_unit(e) * 128.0f;  // a power of two: the products are exact, below 256
 #pragma unroll
@@ -118,19 +141,30 @@ __device__ __forceinline__ void pack_m(const float (&m)[kVals], uint32_t e, uint
     c[i] = static_cast<uint32_t>(k);
   }
 }
-__device__ __forceinline__ uint32_t code_v(float v, float inverse) {
-  const uint32_t u = __float_as_uint(v * inverse);
-  if (u == 0) return 0;
-  if (u >= 0x7f800000u) return 255;  // NaN, infinity
-  const int k = static_cast<int>((u + 0x7ffffu + ((u >> 20) & 1u)) >> 20) - 776;
-  return static_cast<uint32_t>(min(max(k, 1), 254));
-}
-__device__ __forceinline__ void pack_v(const float (&v)[kVals], uint32_t e, uint32_t (&c)[2]) {
+__device__ __forceinline__ void pack_v(const float (&v)[kVals], uint32_t e, bool odd, uint32_t (&c)[2]) {
   const float inverse = inverse_unit(e);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    c[i] = code_v(v[4 * i], inverse) | code_v(v[4 * i + 1], inverse) << 8 | code_v(v[4 * i + 2], inverse) << 16 |
-           code_v(v[4 * i + 3], inverse) << 24;
+  for (int i = 0; i < 2; ++i) {
+    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u = __float_as_uint(v[4 * i + j] * inverse);
+      // to three mantissa bits, ties to even, then the exponent counted from 2^-30 / unit on
+      const int k = static_cast<int>(u + ((u >> 20) & 1u) + (0x7ffffu - (776u << 20))) >> 20;
+      uint32_t code = u ? static_cast<uint32_t>(min(max(k, 1), 254)) : 0u;
+      if (odd && u >= 0x7f800000u) code = 255u;
+      word |= code << (8 * j);
+    }
+    c[i] = word;
+  }
+}
+
+// sqrt and 1 / x to one unit in the last place: the step's own products and sums round as much.  (The
+// correctly rounded ones are 25 more instructions a value, which 8-bit states, 10 bytes a value,
+// leave no time for.)  The square root instruction takes numbers below 2^-126 for zero.
+__device__ __forceinline__ float root_of(float v) {
+  const bool small = v < 0x1.0p-96f;
+  return __builtin_amdgcn_sqrtf(small ? v * 0x1.0p+32f : v) * (small ? 0x1.0p-16f : 1.0f);
 }
 
 __device__ __forceinline__ void load_codes(const uint8_t* p, int64_t left, uint32_t (&c)[2]) {
@@ -204,20 +238,14 @@ __global__ __launch_bounds__(kBlock) void adamw_kernel(AdamArgs a) {
       const float g = Fmt<GT>::to_f(gr.e[i]) * factor;
       m[i] = m[i] * a.beta1 + g * a.om1;
       v[i] = v[i] * a.beta2 + g * g * a.om2;
-      w.e[i] = w.e[i] * keep - size * m[i] / (sqrtf(v[i]) * root + a.eps);
+      w.e[i] = w.e[i] * keep - size * m[i] * __builtin_amdgcn_rcpf(root_of(v[i]) * root + a.eps);
     }
     if constexpr (S8) {
       // values past the tensor's end are zeros here: zero moments, gradients and weights
-      uint32_t mt = 0, vt = 0;
-#pragma unroll
-      for (int i = 0; i < kVals; ++i) {
-        mt = max(mt, finite_bits(m[i]));
-        vt = max(vt, finite_bits(v[i]));
-      }
-      mt = scale_byte(lanes16_max(mt));
-      vt = scale_byte(lanes16_max(vt));
+      bool m_odd, v_odd;
+      const uint32_t mt = block_scale(m, m_odd), vt = block_scale(v, v_odd);
       pack_m(m, mt, mc);
-      pack_v(v, vt, vc);
+      pack_v(v, vt, v_odd, vc);
       if (left > 0) {
         store_codes(static_cast<uint8_t*>(t.m) + at, left, mc);
         store_codes(static_cast<uint8_t*>(t.v) + at, left, vc);
@@ -248,16 +276,23 @@ __global__ __launch_bounds__(kBlock) void adamw_read_kernel(ReadArgs a) {
   const int which = __builtin_amdgcn_readfirstlane(tensor_of(a, blockIdx.x));
   const ReadTensor& t = a.t[which];
   const int64_t at0 = static_cast<int64_t>(static_cast<int>(blockIdx.x) - a.first[which]) * kChunk + threadIdx.x * kVals;
+  // every load of the chunk is on its way before the first value is stored: 16 bytes a lane and step
+  uint32_t mc[kChunkSteps][2], vc[kChunkSteps][2], me[kChunkSteps], ve[kChunkSteps];
+#pragma unroll
+  for (int k = 0; k < kChunkSteps; ++k) {
+    const int64_t at = at0 + static_cast<int64_t>(k) * kStepVals, left = t.n - at;
+    load_codes(t.m + at, left, mc[k]);
+    load_codes(t.v + at, left, vc[k]);
+    me[k] = left > 0 ? t.ms[at / TBE_ADAMW_BLOCK] : 0;
+    ve[k] = left > 0 ? t.vs[at / TBE_ADAMW_BLOCK] : 0;
+  }
 #pragma unroll
   for (int k = 0; k < kChunkSteps; ++k) {
     const int64_t at = at0 + static_cast<int64_t>(k) * kStepVals, left = t.n - at;
     if (left <= 0) return;
-    uint32_t mc[2], vc[2];
     float m[kVals], v[kVals];
-    load_codes(t.m + at, left, mc);
-    load_codes(t.v + at, left, vc);
-    open_m(mc, t.ms[at / TBE_ADAMW_BLOCK], m);
-    open_v(vc, t.vs[at / TBE_ADAMW_BLOCK], v);
+    open_m(mc[k], me[k], m);
+    open_v(vc[k], ve[k], v);
     Vec<OS, kVals> mo, vo;
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
