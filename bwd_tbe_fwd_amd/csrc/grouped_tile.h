@@ -194,6 +194,8 @@ __device__ __forceinline__ void store_tile(S* out, int64_t pitch, int m_left, in
   constexpr int R = kFit >= MF ? MF : kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;           // products of m at a time
   static_assert(kFit >= 1 && MF % R == 0, "16 rows fit");
   constexpr int kPer = 16 / static_cast<int>(sizeof(S)), kLanes = kRow / 16;       // values of 16 bytes, lanes of a row
+  // rows that start on 16 bytes only: the pieces of others share their lines' ends
+  const bool on_16 = pitch * static_cast<int64_t>(sizeof(S)) % 16 == 0 && !(reinterpret_cast<uintptr_t>(out) & 15);
   const int l = lane_id(), g = l >> 4;
 #pragma unroll
   for (int i0 = 0; i0 < MF; i0 += R) {
@@ -216,7 +218,7 @@ __device__ __forceinline__ void store_tile(S* out, int64_t pitch, int m_left, in
       __builtin_memcpy(v.e, s + m * kPitch + n * sizeof(S), 16);
       if (16 * i0 + m >= m_left) continue;
       S* p = out + (16 * i0 + m) * pitch + n;
-      if (STREAM && n_left - n >= kPer) store_vec_stream<S, kPer>(p, v);
+      if (STREAM && on_16 && n_left - n >= kPer) store_vec_stream<S, kPer>(p, v);
       else store_vec_part<S, kPer>(p, n_left - n, v);
     }
   }

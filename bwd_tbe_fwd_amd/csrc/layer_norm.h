@@ -33,6 +33,7 @@ struct NormArgs {
   int64_t gy_stride;
   void* gx;
   int64_t gx_stride;
+  int stream;      // the rows written start on 16 bytes
   float* partial;  // [grid][2][width] sums of grad_y * h and of grad_y, or NULL
 };
 
@@ -108,6 +109,20 @@ __device__ __forceinline__ void load_shared(const void* p, int dt, int64_t c, in
 #pragma unroll
     for (int i = 0; i < VEC; ++i) v[i] = dt == 1 ? Fmt<1>::to_f(h.e[i]) : Fmt<2>::to_f(h.e[i]);
   }
+}
+
+// A result vector: with the streaming policy where it is whole 16 bytes of a row that starts on 16.
+// 65536 x 4096 in bf16: forward 252 -> 197 us, backward 349 -> 343 us; not for fp32 rows' gradients (131072
+// x 4096: 1000 -> 1026 us).
+template <typename S, int VEC>
+__device__ __forceinline__ void store_row(S* p, int64_t left, bool stream, const Vec<S, VEC>& v) {
+  if constexpr (VEC * sizeof(S) % 16 == 0) {
+    if (stream && left >= VEC) {
+      store_vec_stream<S, VEC>(p, v);
+      return;
+    }
+  }
+  store_vec_part<S, VEC>(p, left, v);
 }
 
 // Whether a kernel loads its next row before it works on this one: where a lane has at most 32 bytes of
@@ -191,7 +206,7 @@ __global__ __launch_bounds__(norm_block(G)) void norm_forward_kernel(NormArgs a)
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
           o.e[i] = tower_from_f<YT>((Fmt<XT>::to_f(raw[v].e[i]) - mean) * rstd * w[KEEP ? v : 0][i] + b[KEEP ? v : 0][i]);
-        store_vec_part<YS, VEC>(yr + c, a.width - c, o);
+        store_row<YS, VEC>(yr + c, a.width - c, a.stream, o);
       }
     }
   }
@@ -240,7 +255,7 @@ __global__ __launch_bounds__(kNormWide) void norm_forward_wide_kernel(NormArgs a
       Vec<YS, VEC> o;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) o.e[i] = tower_from_f<YT>((Fmt<XT>::to_f(raw.e[i]) - mean) * rstd * w[i] + b[i]);
-      store_vec_part<YS, VEC>(yr + c, a.width - c, o);
+      store_row<YS, VEC>(yr + c, a.width - c, a.stream, o);
     }
   }
 }
@@ -335,7 +350,7 @@ __global__ __launch_bounds__(norm_block(G)) void norm_backward_kernel(NormArgs a
           const float h = (Fmt<XT>::to_f(raw[v].e[i]) - mean) * rstd;
           o.e[i] = tower_from_f<XT>((Fmt<YT>::to_f(gin[v].e[i]) * w[v][i] - c1 - h * c2) * rstd);
         }
-        store_vec_part<XS, VEC>(xo + c, a.width - c, o);
+        store_row<XS, VEC>(xo + c, a.width - c, XT != 0 && a.stream, o);
       }
     }
   }
@@ -414,7 +429,7 @@ __global__ __launch_bounds__(kNormWide) void norm_backward_wide_kernel(NormArgs 
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
         o.e[i] = tower_from_f<XT>((Fmt<YT>::to_f(gin.e[i]) * w[i] - c1 - (Fmt<XT>::to_f(raw.e[i]) - mean) * rstd * c2) * rstd);
-      store_vec_part<XS, VEC>(xo + c, a.width - c, o);
+      store_row<XS, VEC>(xo + c, a.width - c, XT != 0 && a.stream, o);
     }
   }
 }

@@ -42,6 +42,11 @@ __global__ __launch_bounds__(kSumCols * kSumGroups) void norm_partials_kernel(co
 bool dtype_ok(int dt) { return dt == TBE_F32 || dt == TBE_F16 || dt == TBE_BF16; }
 bool aligned_to(const void* p, int dt) { return !(reinterpret_cast<uintptr_t>(p) & (dt == TBE_F32 ? 3u : 1u)); }
 
+// Whether every row starts on 16 bytes.
+bool rows_on_16(const void* p, int64_t stride, int dt) {
+  return !(reinterpret_cast<uintptr_t>(p) & 15) && stride * (dt == TBE_F32 ? 4 : 2) % 16 == 0;
+}
+
 // What both directions ask of a row matrix.
 tbe_status check_rows(const char* what, const void* p, int64_t stride, int dt, int64_t rows, int64_t width) {
   if (!dtype_ok(dt)) {
@@ -112,6 +117,7 @@ extern "C" tbe_status tbe_layer_norm_forward(int64_t rows, int64_t width, const 
   a.rows = rows; a.width = width; a.x = x; a.x_stride = x_stride;
   a.w = weight; a.b = bias; a.w_dt = w_dtype; a.eps = eps;
   a.y = y; a.y_stride = y_stride; a.mean = mean; a.rstd = rstd;
+  a.stream = rows_on_16(y, rows > 1 ? y_stride : 0, y_dtype);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return x_dtype == TBE_F32 ? norm_forward_x<0>(a, y_dtype, s)
                             : x_dtype == TBE_F16 ? norm_forward_x<1>(a, y_dtype, s) : norm_forward_x<2>(a, y_dtype, s);
@@ -151,6 +157,7 @@ extern "C" tbe_status tbe_layer_norm_backward(int64_t rows, int64_t width, const
   a.w = weight; a.w_dt = w_dtype;
   a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
   a.gy = grad_y; a.gy_stride = grad_y_stride; a.gx = grad_x; a.gx_stride = grad_x_stride;
+  a.stream = rows_on_16(grad_x, rows > 1 ? grad_x_stride : 0, x_dtype);
   a.partial = sums ? static_cast<float*>(workspace) : nullptr;
   int grid = 0;  // partial rows
   if (rows > 0 && (sums || grad_x)) {

@@ -140,7 +140,7 @@ typedef struct {
                               copy; NULL: the step is taken on param itself */
   uint8_t* exp_avg_scale;  /* ceil(numel / TBE_ADAMW_BLOCK) bytes with states of 8 bits, else unused */
   uint8_t* exp_avg_sq_scale;
-  int64_t numel;           /* may be 0, at most 2^36 */
+  int64_t numel;           /* may be 0, at most 2^34 */
   float weight_decay;      /* of this tensor */
   int32_t param_dtype, grad_dtype; /* tbe_dtype */
   int32_t state;           /* tbe_adamw_state */

@@ -111,7 +111,7 @@ def test_adamw_refusals():
                          (dict(lr=float("inf")), ARG, b"lr"), (dict(control=P(4100)), ARG, b"control"),
                          (dict(param_dtype=4), UNSUPPORTED, b"type"), (dict(grad_dtype=-1), UNSUPPORTED, b"type"),
                          (dict(state=2), UNSUPPORTED, b"state"), (dict(master=4096), UNSUPPORTED, b"master"),
-                         (dict(n=-1), ARG, b"numel"), (dict(n=(1 << 36) + 1), ARG, b"numel"), (dict(param=None), ARG, b"NULL"),
+                         (dict(n=-1), ARG, b"numel"), (dict(n=(1 << 34) + 1), ARG, b"numel"), (dict(param=None), ARG, b"NULL"),
                          (dict(grad=None), ARG, b"NULL"), (dict(exp_avg=None), ARG, b"NULL"), (dict(exp_avg_sq=None), ARG, b"NULL"),
                          (dict(state=1), ARG, b"NULL"), (dict(param=4098), ARG, b"aligned"), (dict(exp_avg=4097), ARG, b"aligned"),
                          (dict(grad=4097, grad_dtype=2), ARG, b"aligned")):
