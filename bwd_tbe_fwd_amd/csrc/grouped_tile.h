@@ -70,7 +70,7 @@ struct Operand {
   const uint16_t* base;  // (m0, k = 0)
   int64_t ld;
   int ms, ks;            // that lie inside from there on
-  uint32_t at[kEach];    // DIRECT: byte offset of a chunk, or kOutside
+  uint32_t at[kEach];    // byte offset of a chunk, or kOutside
   u16x8_t reg[DIRECT ? 1 : kEach];
 
   // row of the matrix (m or k within the tile) and its chunk that a thread's i-th chunk holds
@@ -96,18 +96,13 @@ struct Operand {
     ld = stride;
     ms = m_left;
     ks = k_left;
-    if constexpr (DIRECT) {
-      // computed anew for each tile: kept from one to the next they would cost registers in the loop
-      uint32_t pitch = static_cast<uint32_t>(stride) * 2;
-      int tid = threadIdx.x;
-      asm volatile("" : "+s"(pitch), "+v"(tid));
+    const uint32_t pitch = static_cast<uint32_t>(stride) * 2;
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        int row, chunk;
-        place(i, tid, row, chunk);
-        const bool in = ALONG ? row < ms : chunk * 8 < ms;
-        at[i] = in ? row * pitch + chunk * 16 : kOutside;
-      }
+    for (int i = 0; i < kEach; ++i) {
+      int row, chunk;
+      place(i, threadIdx.x, row, chunk);
+      const bool in = ALONG ? row < ms : chunk * 8 < ms;
+      at[i] = in ? row * pitch + chunk * 16 : kOutside;
     }
   }
   // Starts the i-th load of step k0 (of kEach).
@@ -116,6 +111,7 @@ struct Operand {
     const int left = ks - k0;
     int row, chunk;
     place(i, threadIdx.x, row, chunk);
+    const bool near = ld < (int64_t{1} << 21);  // a tile's byte offsets stay below 2^31
     if constexpr (DIRECT) {
       const uint64_t u = reinterpret_cast<uint64_t>(p);
       const u32x4 r = {static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32) & 0xffffu, 0x7fffffffu, 0x00027000u};
@@ -124,6 +120,11 @@ struct Operand {
       uint32_t o = at[i];
       if (left < K && (ALONG ? chunk * 8 : row) >= left) o = kOutside;
       load_to_lds(r, o, static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)(s + to))));
+    } else if (near && (ALONG ? left >= K : left > K)) {
+      // Whole 16 bytes at any alignment.  An across chunk at the edge reads on into the next row (there
+      // is one): m that are not stored.
+      const __amdgpu_buffer_rsrc_t whole = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, 0x7fffffff, 0x00027000);
+      reg[i] = __builtin_bit_cast(u16x8_t, __builtin_amdgcn_raw_buffer_load_b128(whole, at[i], 0, 0));
     } else {
       Vec<uint16_t, 8> v;
       const int n = (ALONG ? row < ms : row < left) ? (ALONG ? left : ms) - chunk * 8 : 0;
