@@ -140,9 +140,7 @@ inline int64_t row_tiles_bound(const GroupedArgs& a, int BM) { return a.rows / B
 // 1024 x 512 take 24 / 13 / 10 us.
 constexpr int kTileSide[3] = {256, 128, 64};
 constexpr double kTileSlots[3] = {256, 512, 1024}, kTileFixed[3] = {6.0, 4.0, 3.0}, kTileStep[3] = {1.37, 0.78, 0.61};
-// Of the weight gradient, whose k are many: its 64 x 64 tiles wait for L2.
-constexpr double kWeightStep[3] = {1.45, 0.85, 0.90};
-inline double round_us(int tile, double k, const double (&step)[3] = kTileStep) { return kTileFixed[tile] + (k + 63) / 64 * step[tile]; }
+inline double round_us(int tile, double k) { return kTileFixed[tile] + (k + 63) / 64 * kTileStep[tile]; }
 // Row tiles of `bm` rows that are expected of rows spread over experts.
 inline double row_tiles_expected(int64_t rows, int64_t experts, int bm) {
   if (experts == 1) return static_cast<double>((rows + bm - 1) / bm);

@@ -42,8 +42,12 @@ __global__ __launch_bounds__(kBlock) void grouped_reduce_kernel(GroupedArgs a) {
 // are shared among workgroups, and a second kernel adds their partial sums: units of 512, 1024, ...
 // rows (0: an expert's rows are one).  The least of the expected times: rounds of tiles, the last of
 // them by an expert of twice the average rows where rows are not shared, and 4 TB/s for the partial
-// sums' way to memory and back.  16384 rows of one expert, 4096 x 1024: units of 8192 rows; 4096
-// rows, 4 experts, 1024 x 1024: 64 x 64 and no sharing.
+// sums' way to memory and back.  A step of 64 rows takes longer the more workgroups read their rows
+// from memory at once: kWeightStep where all slots are taken, kWeightAlone where few are.  Measured with
+// tile and unit as given: 16384 rows, 1 expert, 4096 x 1024: 256, 4096 rows 156 us; 256, all 398; 128,
+// all 207; 64, all 227.  65536 rows, 16 experts, 1024 x 1024: 256, all 137 us (the experts' rows
+// unequal, 370); 256, 4096 rows 257 (205); 128, all 187 (238); 64, all 279 (263).
+constexpr double kWeightStep[3] = {1.85, 1.36, 0.95}, kWeightAlone[3] = {1.5, 0.75, 0.6};
 struct WeightPlan {
   int tile, split;
 };
@@ -54,16 +58,21 @@ WeightPlan weight_plan(int64_t rows, int64_t experts, int64_t inner, int64_t out
   for (int t = 0; t < 3; ++t) {
     const int side = kTileSide[t];
     const double each = static_cast<double>((outer + side - 1) / side) * static_cast<double>((inner + side - 1) / side);
-    double us = (rounds_of(used * each, kTileSlots[t]) - 1.0) * round_us(t, average, kWeightStep) +
-                round_us(t, experts > 1 ? 2.0 * average : average, kWeightStep);
+    // rounds of `tiles` over k rows, the last one over `last`
+    auto time = [&](double tiles, double k, double last) {
+      const double r = rounds_of(tiles, kTileSlots[t]);
+      const double step = kWeightAlone[t] + (kWeightStep[t] - kWeightAlone[t]) * tiles / (r * kTileSlots[t]);
+      return r * kTileFixed[t] + ((r - 1.0) * k + last) / 64 * step;
+    };
+    double us = time(used * each, average, experts > 1 ? 2.0 * average : average);
     if (best < 0.0 || us < best) {
       best = us;
       p = WeightPlan{t, 0};
     }
     for (int64_t c = 512; c < rows && c <= (1 << 20); c *= 2) {
-      const double units = static_cast<double>(rows) / static_cast<double>(c) + 0.5 * used;
+      const double units = row_tiles_expected(rows, experts, static_cast<int>(c)), k = static_cast<double>(c);
       const double bytes = 4.0 * static_cast<double>(rows / c) * static_cast<double>(inner + 1) * static_cast<double>(outer);
-      us = rounds_of(units * each, kTileSlots[t]) * round_us(t, static_cast<double>(c), kWeightStep) + 5.0 + 2.0 * bytes / 4e6;
+      us = time(units * each, k, k) + 5.0 + 2.0 * bytes / 4e6;
       if (us < best) {
         best = us;
         p = WeightPlan{t, static_cast<int>(c)};

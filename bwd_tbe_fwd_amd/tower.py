@@ -250,6 +250,7 @@ class AdamWTensors:
             _refuse(f"{n} params need as many gradients, states and weight decays")
         self.c = (tbe_adamw_tensor * max(1, n))()
         self.count = n
+        self.numels = [p.numel() for p in params]
         for i, (p, g, m, v, w, ms, vs) in enumerate(zip(*self.tensors)):
             numel = p.numel()
             eight = m.dtype == torch.uint8
@@ -294,13 +295,15 @@ def tbe_adamw_state_read(tensors: AdamWTensors, exp_avg_out: Sequence[torch.Tens
         _refuse(f"{n} tensors need as many outputs of each state")
     dtype = exp_avg_out[0].dtype if n else torch.float32
     array = ctypes.c_void_p * max(1, n)
-    arrays = array(), array()
-    for outs, at in zip((exp_avg_out, exp_avg_sq_out), arrays):
-        for i, t in enumerate(outs):
-            if t.get_device() != dev:
-                _off_gpu(f"output {i}", t)
-            if t.numel() != c[i].numel or t.dtype != dtype or not t.is_contiguous():
-                _refuse(f"output {i} is {t.dtype} of {t.numel()}: contiguous {dtype} of {c[i].numel} is needed")
-            at[i] = t.data_ptr()
+    arrays = []
+    for outs in (exp_avg_out, exp_avg_sq_out):
+        if [t.numel() for t in outs] != tensors.numels or any(t.dtype is not dtype or t.get_device() != dev for t in outs) \
+                or not all([t.is_contiguous() for t in outs]):
+            for i, t in enumerate(outs):
+                if t.get_device() != dev:
+                    _off_gpu(f"output {i}", t)
+                if t.numel() != c[i].numel or t.dtype != dtype or not t.is_contiguous():
+                    _refuse(f"output {i} is {t.dtype} of {t.numel()}: contiguous {dtype} of {c[i].numel} is needed")
+        arrays.append(array(*[t.data_ptr() for t in outs]))
     st = lib().tbe_adamw_state_read(c, n, *arrays, _dtype("output 0", exp_avg_out[0]) if n else 0, _current(stream, dev))
     _check(st, "tbe_adamw_state_read")
