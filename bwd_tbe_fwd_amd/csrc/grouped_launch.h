@@ -6,7 +6,6 @@
 
 namespace tbe {
 
-constexpr int64_t kMaxGroups = int64_t{1} << 22;  // a launch has fewer than 2^32 threads
 
 template <int DT, int OP, int BM, int BN, int WM, int WN, bool DIRECT>
 tbe_status launch_tile(const GroupedArgs& a, hipStream_t s) {
@@ -15,10 +14,10 @@ tbe_status launch_tile(const GroupedArgs& a, hipStream_t s) {
   const char* what = OP == kForward ? "grouped_forward" : OP == kBackwardInput ? "grouped_input" : "grouped_weight";
   const int n = OP == kForward ? a.outer : a.inner;
   const int n_tiles = (n + BN - 1) / BN;
-  const int64_t units = OP != kBackwardWeight ? row_tiles_bound(a, BM) : a.split ? row_tiles_bound(a, a.split) : a.experts;
+  const int64_t units = OP != kBackwardWeight ? row_tiles_bound(a, BM) : a.split ? a.units : a.experts;
   // rows: a multiple of 8, for the chiplets' shares
   const int64_t groups = OP == kBackwardWeight ? units * ((a.outer + BM - 1) / BM) * n_tiles : (units * n_tiles + 7) / 8 * 8;
-  if (groups > kMaxGroups) {
+  if (groups * kThreads >= (int64_t{1} << 32)) {
     set_error("grouped linear: %lld tiles are more than a launch takes", static_cast<long long>(groups));
     return TBE_ERR_UNSUPPORTED;
   }

@@ -45,6 +45,7 @@ struct GroupedArgs {
   void* grad_bias;      // backward by weight; NULL: none
   void* workspace;
   int32_t split;        // backward by weight: rows of a unit, 0: an expert's rows are one
+  int32_t units;        // units at most: partial sums that the workspace holds
   int32_t tile;         // backward by weight: which of kTileSide, host only
 };
 
@@ -64,7 +65,8 @@ __device__ __forceinline__ RowRange rows_of(const GroupedArgs& a, int e) {
 }
 
 // Tiles of BM rows are counted over the experts in order and then the rows of no expert.  Every wave
-// counts them by itself, 64 experts a step, a lane each.
+// counts them by itself, 64 experts a step, a lane each.  Offsets that are not in order may count some
+// rows twice, but a tile's rows lie inside [0, rows] whatever they are.
 struct RowTile {
   int expert;
   int64_t row, hi;   // first row, and where its expert's end
@@ -85,16 +87,11 @@ struct RowTiles {
     }
     return read_lane(upto, kWave - 1);
   }
-  // All tiles.
-  __device__ __forceinline__ int total(const GroupedArgs& a, int BM) {
-    int all = 0;
-    for (int base = 0; base <= a.experts; base += kWave) all += count(a, BM, base);
-    return all;
-  }
-  // Tile `tile`; false past the last one.  After total(), with up to 63 experts the lanes still hold them.
+  // Tile `tile` (>= 0); false past the last one.  counted: count(a, BM, 0) was called, and all experts are
+  // in it.
   __device__ __forceinline__ bool find(const GroupedArgs& a, int BM, int tile, bool counted, RowTile& t) {
     for (int base = 0; base <= a.experts; base += kWave) {
-      const int here = counted && a.experts < kWave ? read_lane(upto, kWave - 1) : count(a, BM, base);
+      const int here = counted ? read_lane(upto, kWave - 1) : count(a, BM, base);
       if (tile < here) {
         const int src = __ffsll(static_cast<unsigned long long>(__ballot(upto > tile))) - 1;
         t.expert = base + src;

@@ -16,11 +16,12 @@ __global__ __launch_bounds__(kBlock) void grouped_reduce_kernel(GroupedArgs a) {
     const RowRange r = rows_of(a, k);
     return (r.hi - r.lo + a.split - 1) / a.split;
   };
-  const int64_t n = units_of(e);
+  int64_t n = units_of(e);
   if (n == 1) return;
   int64_t first = 0;  // units of the experts before
   for (int k = lane_id(); k < e; k += kWave) first += units_of(k);
   for (int d = 1; d < kWave; d <<= 1) first += __shfl_xor(first, d);
+  n = min(n, max(a.units - first, static_cast<int64_t>(0)));  // offsets that are not in order: inside the workspace
   const float* p = static_cast<const float*>(a.workspace) + first * each;
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x) * 4; i < each; i += static_cast<int64_t>(gridDim.x) * kBlock * 4) {
     Vec<float, 4> sum = {};
@@ -213,6 +214,7 @@ extern "C" tbe_status tbe_grouped_linear_backward_weight(int64_t rows, int32_t e
   a.out = grad_weight; a.out_dt = out_dtype; a.grad_bias = grad_bias; a.workspace = workspace;
   const WeightPlan plan = weight_plan(rows, experts, inner, outer);
   a.split = plan.split;
+  a.units = plan.split ? static_cast<int>(row_tiles_bound(a, plan.split)) : 0;
   a.tile = plan.tile;
   return launch<kBackwardWeight>(a, dtype, static_cast<hipStream_t>(stream));
 }

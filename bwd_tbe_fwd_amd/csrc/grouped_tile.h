@@ -278,14 +278,20 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void g
     B.init(static_cast<const uint16_t*>(a.x) + row * a.x_stride + n0, a.x_stride, n_left, rows);
   } else {
     // a chiplet's tiles are neighbours: a contiguous share of all, of which there are fewer than
-    // workgroups where experts' last tiles are not all there
+    // workgroups where experts' last tiles are not all there; with 64 experts and more, whose counting
+    // takes several steps, the tiles are taken as they come
     constexpr bool fwd = OP == kForward;
     RowTiles tiles;
     RowTile t;
-    const int64_t total = static_cast<int64_t>(tiles.total(a, BM)) * n_tiles;
-    const unsigned x = blockIdx.x % 8;
-    const int id = static_cast<int>(total * x / 8 + blockIdx.x / 8);
-    if (id >= total * (x + 1) / 8 || !tiles.find(a, BM, id / n_tiles, true, t)) return;
+    const bool counted = a.experts < kWave;
+    int id = blockIdx.x;
+    if (counted) {
+      const int64_t total = min(static_cast<int64_t>(tiles.count(a, BM, 0)) * n_tiles, static_cast<int64_t>(gridDim.x));
+      const unsigned x = blockIdx.x % 8;
+      id = static_cast<int>(total * x / 8 + blockIdx.x / 8);
+      if (id >= total * (x + 1) / 8) return;
+    }
+    if (!tiles.find(a, BM, id / n_tiles, counted, t)) return;
     expert = t.expert;
     row = static_cast<int>(t.row);
     n0 = (id % n_tiles) * BN;

@@ -58,7 +58,7 @@ tbe_status check_rows(const char* what, const void* p, int64_t stride, int dt, i
     return TBE_ERR_ARG;
   }
   // the last element's index stays within 64 bits
-  if (rows > 1 && (stride < width || stride > (int64_t{1} << 40))) {
+  if (rows > 1 && (stride < width || stride > (int64_t{1} << 31))) {
     set_error("%s: rows of %lld elements cannot be %lld apart", what, static_cast<long long>(width),
               static_cast<long long>(stride));
     return TBE_ERR_ARG;

@@ -130,10 +130,26 @@ def test_larger_sides():
         Case(groups, inner, outer, BF16, pad_rows=3).all()
 
 
+@pytest.mark.parametrize("groups,inner,outer,dtype", [
+    ([7600, 7400], 2040, 1000, BF16),                          # forward and by input: 256 x 256
+    ([1100, 0, 900, 2001], 1016, 1032, F16),                   # 128 x 128
+    ([4000 + 13 * e for e in range(16)], 1024, 1000, BF16),    # by weight: 256 x 256
+    ([16000], 4088, 1000, BF16),                               # by weight: 256 x 256, rows shared
+    ([5000, 9000, 6000], 1001, 515, F16),                      # odd: 256 x 128
+    ([700, 20, 0, 3000], 515, 1001, BF16),                     # odd: 64 x 64
+])
+def test_each_tile(groups, inner, outer, dtype):
+    """Sizes at which each tile is the one expected to be fastest, with edges inside it."""
+    flush_print("grouped", groups, inner, outer)
+    Case(groups, inner, outer, dtype, pad_rows=7).all()
+
+
 def test_many_experts():
     g = torch.Generator().manual_seed(3)
     groups = [int(n) for n in torch.randint(0, 9, (200,), generator=g)]
     Case(groups, 48, 40, BF16, pad_rows=2).all()
+    for n in (63, 64, 65):  # around the experts that one wave counts at a time
+        Case(groups[:n], 40, 72, BF16, pad_rows=70).all()
 
 
 def test_long_group():
