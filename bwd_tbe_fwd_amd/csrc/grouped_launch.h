@@ -69,7 +69,7 @@ tbe_status grouped_launch(const GroupedArgs& a, hipStream_t s) {
     const double t = rounds_of(row_tiles_expected(a.rows, a.experts, 64) * static_cast<double>((n + 63) / 64), 1024) * (3.0 + steps * 1.44);
     large = l <= t;
   }
-  return large ? launch_tile<DT, OP, 256, 128, 2, 4, false>(a, s) : launch_tile<DT, OP, 64, 64, 2, 2, false>(a, s);
+  return large ? launch_tile<DT, OP, 256, 128, 4, 2, false>(a, s) : launch_tile<DT, OP, 64, 64, 2, 2, false>(a, s);
 }
 
 #define TBE_GROUPED(DT, OP)                                                                  \
