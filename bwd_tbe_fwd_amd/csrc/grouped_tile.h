@@ -19,6 +19,8 @@
 //    products give 4 NF adjacent n (an across read of such n would meet in the same banks).
 #pragma once
 
+#include <type_traits>
+
 #include "grouped_linear.h"
 
 namespace tbe {
@@ -70,6 +72,7 @@ struct Operand {
   const uint16_t* base;  // (m0, k = 0)
   int64_t ld;
   int ms, ks;            // that lie inside from there on
+  bool at_least_8;       // values in a row of the matrix
   uint32_t at[kEach];    // byte offset of a chunk, or kOutside
   u16x8_t reg[DIRECT ? 1 : kEach];
 
@@ -91,11 +94,12 @@ struct Operand {
     const int q = i * THREADS + threadIdx.x;
     return ALONG ? q * 8 : q / 64 * (512 + 16) + q % 64 * 8;
   }
-  __device__ __forceinline__ void init(const uint16_t* p, int64_t stride, int m_left, int k_left) {
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t stride, int m_left, int k_left, int row) {
     base = p;
     ld = stride;
     ms = m_left;
     ks = k_left;
+    at_least_8 = row >= 8;
     const uint32_t pitch = static_cast<uint32_t>(stride) * 2;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -105,7 +109,13 @@ struct Operand {
       at[i] = in ? row * pitch + chunk * 16 : kOutside;
     }
   }
-  // Starts the i-th load of step k0 (of kEach).
+  // Steps whose loads need no look at the matrix's end: those with kFurther more k behind them (across,
+  // a chunk at the edge reads up to 7 values on, of rows that are there, one value wide as they may be),
+  // and none where a tile's byte offsets pass 2^31.
+  static constexpr int kFurther = ALONG || DIRECT ? 0 : 7;
+  __device__ __forceinline__ int whole_steps() const { return DIRECT || ld < (int64_t{1} << 21) ? max(ks - kFurther, 0) / K : 0; }
+  // Starts the i-th load of step k0 (of kEach).  WHOLE: one of whole_steps().
+  template <bool WHOLE>
   __device__ __forceinline__ void load(int i, int k0, uint16_t* s) {
     const uint16_t* p = base + (ALONG ? k0 : k0 * ld);
     const int left = ks - k0;
@@ -118,13 +128,41 @@ struct Operand {
       const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
       const int to = ALONG ? (i * THREADS + w * kWave) * 8 : (i * (THREADS / kWave) + w) * (512 + 16);
       uint32_t o = at[i];
-      if (left < K && (ALONG ? chunk * 8 : row) >= left) o = kOutside;
+      if (!WHOLE && left < K && (ALONG ? chunk * 8 : row) >= left) o = kOutside;
       load_to_lds(r, o, static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)(s + to))));
-    } else if (near && (ALONG ? left >= K : left > K)) {
-      // Whole 16 bytes at any alignment.  An across chunk at the edge reads on into the next row (there
-      // is one): m that are not stored.
-      const __amdgpu_buffer_rsrc_t whole = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, 0x7fffffff, 0x00027000);
-      reg[i] = __builtin_bit_cast(u16x8_t, __builtin_amdgcn_raw_buffer_load_b128(whole, at[i], 0, 0));
+    } else if (WHOLE || left <= 0 || near) {
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, 0x7fffffff, 0x00027000);
+      if (WHOLE || (near && left >= K + kFurther)) {
+        // 16 bytes at any alignment; an across chunk at the edge brings m that are not stored
+        reg[i] = __builtin_bit_cast(u16x8_t, __builtin_amdgcn_raw_buffer_load_b128(r, at[i], 0, 0));
+      } else if (left <= 0) {
+        reg[i] = u16x8_t{};
+      } else {
+        const int n = (ALONG ? row < ms : row < left) ? (ALONG ? left : ms) - chunk * 8 : 0;
+        if (at_least_8) {
+          // A row's last n < 8 values: its last 8, moved down.  Offsets count from 16 bytes before p, so that
+          // a load may start there.
+          const __amdgpu_buffer_rsrc_t before = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p - 8), 0, 0x7fffffff, 0x00027000);
+          const int back = min(max(8 - n, 0), 7);  // values
+          const uint32_t o = n > 0 ? at[i] + 16 - 2 * back : kOutside;
+          const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(before, o, 0, 0));
+          uint64_t lo = x.x | static_cast<uint64_t>(x.y) << 32, hi = x.z | static_cast<uint64_t>(x.w) << 32;
+          if (back >= 4) {
+            lo = hi;
+            hi = 0;
+          }
+          const int bits = 16 * (back & 3);
+          lo = bits ? lo >> bits | hi << (64 - bits) : lo;
+          hi >>= bits;
+          const u32x4 y = {static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
+          reg[i] = __builtin_bit_cast(u16x8_t, y);
+        } else {
+          // rows of fewer than 8 values: one by one, what lies outside from an offset past the range
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            reg[i][e] = __builtin_amdgcn_raw_buffer_load_b16(r, e < n ? at[i] + 2 * e : kOutside, 0, 0);
+        }
+      }
     } else {
       Vec<uint16_t, 8> v;
       const int n = (ALONG ? row < ms : row < left) ? (ALONG ? left : ms) - chunk * 8 : 0;
@@ -274,8 +312,8 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void g
       rows = static_cast<int>(r.hi - r.lo);
     }
     steps = (rows + K - 1) / K;
-    A.init(static_cast<const uint16_t*>(a.gy) + row * a.gy_stride + m0, a.gy_stride, m_left, rows);
-    B.init(static_cast<const uint16_t*>(a.x) + row * a.x_stride + n0, a.x_stride, n_left, rows);
+    A.init(static_cast<const uint16_t*>(a.gy) + row * a.gy_stride + m0, a.gy_stride, m_left, rows, a.outer);
+    B.init(static_cast<const uint16_t*>(a.x) + row * a.x_stride + n0, a.x_stride, n_left, rows, a.inner);
   } else {
     // a chiplet's tiles are neighbours: a contiguous share of all, of which there are fewer than
     // workgroups where experts' last tiles are not all there; with 64 experts and more, whose counting
@@ -300,8 +338,8 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void g
     const int64_t lda = fwd ? a.x_stride : a.gy_stride;
     const int ks = fwd ? a.inner : a.outer;
     steps = expert < a.experts ? (ks + K - 1) / K : 0;
-    A.init(static_cast<const uint16_t*>(fwd ? a.x : a.gy) + row * lda, lda, m_left, ks);
-    B.init(static_cast<const uint16_t*>(a.w) + expert * io + (fwd ? static_cast<int64_t>(n0) * a.inner : n0), a.inner, n_left, ks);
+    A.init(static_cast<const uint16_t*>(fwd ? a.x : a.gy) + row * lda, lda, m_left, ks, ks);
+    B.init(static_cast<const uint16_t*>(a.w) + expert * io + (fwd ? static_cast<int64_t>(n0) * a.inner : n0), a.inner, n_left, ks, a.inner);
   }
 
   // this lane's place in a product's 16 m and 16 n
@@ -325,21 +363,23 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void g
   // k to arrive.  Loads are started past the end too, with nothing in range.
   constexpr int kLoads = OA::kEach + OB::kEach;
   u16x8_t fa[2][MF], fb[2][NF];
-  auto load = [&](int i, int step, uint16_t* pa, uint16_t* pb) {
-    if (i < OA::kEach) A.load(i, step * K, pa);
-    else B.load(i - OA::kEach, step * K, pb);
+  auto load = [&](int i, int step, uint16_t* pa, uint16_t* pb, auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    if (i < OA::kEach) A.template load<WHOLE>(i, step * K, pa);
+    else B.template load<WHOLE>(i - OA::kEach, step * K, pb);
   };
+  constexpr std::false_type any{};
   if (steps > 0) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) load(i, k, sa[k], sb[k]);
+      for (int i = 0; i < kLoads; ++i) load(i, k, sa[k], sb[k], any);
       A.store(sa[k]);
       B.store(sb[k]);
     }
     if constexpr (!DIRECT) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) load(i, 2, nullptr, nullptr);
+      for (int i = 0; i < kLoads; ++i) load(i, 2, nullptr, nullptr, any);
     }
     wait_loads<DIRECT ? kLoads : 63>();
     __builtin_amdgcn_s_barrier();
@@ -349,7 +389,8 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void g
 #pragma unroll
     for (int i = 0; i < MF; ++i) fa[0][i] = OA::read(sa[0] + a_place, 16 * i);
   }
-  for (int it = 0; it < steps; ++it) {
+  constexpr int kAhead = DIRECT ? 2 : 3;  // the step whose loads start at a step
+  auto step = [&](int it, auto whole) {
     const int cur = it & 1;
 #pragma unroll
     for (int P = 0; P < 2; ++P) {  // the half in registers
@@ -374,7 +415,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void g
         if (P == 1) {
 #pragma unroll
           for (int k = i * kLoads / MF; k < (i + 1) * kLoads / MF; ++k)
-            load(k, it + (DIRECT ? 2 : 3), sa[0] + cur * OA::kElems, sb[0] + cur * OB::kElems);
+            load(k, it + kAhead, sa[0] + cur * OA::kElems, sb[0] + cur * OB::kElems, whole);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -390,7 +431,12 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void g
         }
       }
     }
-  }
+  };
+  // the steps whose loads are whole, without a look at the end or a branch; then the last ones
+  const int whole_steps = min(min(A.whole_steps(), B.whole_steps()) - kAhead, steps);
+  int it = 0;
+  for (; it < whole_steps; ++it) step(it, std::true_type{});
+  for (; it < steps; ++it) step(it, any);
   wait_loads<0>();  // no load is under way when LDS takes the results
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
