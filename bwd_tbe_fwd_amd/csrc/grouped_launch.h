@@ -38,38 +38,35 @@ inline bool chunked(const GroupedArgs& a, int op) {
   return whole(a.gy, gs, a.outer) && whole(a.x, xs, a.inner);
 }
 
+// The tile of least expected time.  (The weight gradient's comes with its plan.)
+inline int row_tile(const GroupedArgs& a, const TileCost (&tiles)[3], int64_t n, int64_t k) {
+  int tile = 0;
+  double best = 0.0;
+  for (int t = 0; t < 3; ++t) {
+    const TileCost& c = tiles[t];
+    const double us = tiles_us(c, row_tiles_expected(a.rows, a.experts, c.bm) * static_cast<double>((n + c.bn - 1) / c.bn),
+                               static_cast<double>((k + 63) / 64 * 64), static_cast<double>((k + 63) / 64 * 64));
+    if (t == 0 || us < best) {
+      best = us;
+      tile = t;
+    }
+  }
+  return tile;
+}
+
 template <int DT, int OP>
 tbe_status grouped_launch(const GroupedArgs& a, hipStream_t s) {
   const int64_t n = OP == kForward ? a.outer : a.inner, k = OP == kForward ? a.inner : a.outer;
   if (chunked(a, OP)) {
-    int tile = a.tile;
-    if (OP != kBackwardWeight) {
-      double best = 0.0;
-      for (int t = 0; t < 3; ++t) {
-        const int side = kTileSide[t];
-        const double tiles = row_tiles_expected(a.rows, a.experts, side) * static_cast<double>((n + side - 1) / side);
-        const double us = rounds_of(tiles, kTileSlots[t]) * round_us(t, static_cast<double>(k));
-        if (t == 0 || us < best) {
-          best = us;
-          tile = t;
-        }
-      }
-    }
+    const int tile = OP == kBackwardWeight ? a.tile : row_tile(a, kDirectTiles, n, k);
     return tile == 0 ? launch_tile<DT, OP, 256, 256, 2, 4, true>(a, s)
                      : tile == 1 ? launch_tile<DT, OP, 128, 128, 2, 2, true>(a, s) : launch_tile<DT, OP, 64, 64, 2, 2, true>(a, s);
   }
-  // Through registers: 256 x 128 (the registers of 256 x 256 do not suffice) or 64 x 64; 128 x 128 was
-  // never the fastest.  20000 rows, 8 experts, 1001 x 515: 68 / 80 / 78 us; 2000 rows: 36 / 45 / 26 us.
-  bool large;
-  if (OP == kBackwardWeight) {
-    large = a.tile == 0;
-  } else {
-    const double steps = static_cast<double>((k + 63) / 64);
-    const double l = rounds_of(row_tiles_expected(a.rows, a.experts, 256) * static_cast<double>((n + 127) / 128), 256) * (6.0 + steps * 1.75);
-    const double t = rounds_of(row_tiles_expected(a.rows, a.experts, 64) * static_cast<double>((n + 63) / 64), 1024) * (3.0 + steps * 1.44);
-    large = l <= t;
-  }
-  return large ? launch_tile<DT, OP, 256, 128, 4, 2, false>(a, s) : launch_tile<DT, OP, 64, 64, 2, 2, false>(a, s);
+  const int tile = OP == kBackwardWeight ? a.tile : row_tile(a, kRegisterTiles, n, k);
+  if (tile == 0) return launch_tile<DT, OP, 256, 256, 2, 4, false>(a, s);
+  if (tile == 2) return launch_tile<DT, OP, 64, 64, 2, 2, false>(a, s);
+  if constexpr (OP == kBackwardWeight) return launch_tile<DT, OP, 128, 128, 2, 2, false>(a, s);
+  else return launch_tile<DT, OP, 256, 128, 4, 2, false>(a, s);
 }
 
 #define TBE_GROUPED(DT, OP)                                                                  \

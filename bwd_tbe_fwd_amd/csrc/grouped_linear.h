@@ -46,7 +46,7 @@ struct GroupedArgs {
   void* workspace;
   int32_t split;        // backward by weight: rows of a unit, 0: an expert's rows are one
   int32_t units;        // units at most: partial sums that the workspace holds
-  int32_t tile;         // backward by weight: which of kTileSide, host only
+  int32_t tile;         // backward by weight: which of the three, host only
 };
 
 // Rows [lo, hi) of expert e < experts, inside [0, rows]; e = experts: the rows of no expert.
@@ -129,24 +129,39 @@ inline int64_t row_tiles_bound(const GroupedArgs& a, int BM) { return a.rows / B
 // ---------------------------------------------------------------------------
 // the tile, on the host
 // ---------------------------------------------------------------------------
-// Three tiles of C: 256 x 256 by 8 waves, 128 x 128 and 64 x 64 by 4; as many run at once as
-// kTileSlots on 256 CUs.  Time of a round of them in us: a fixed part and one for each 64 of k, fitted
-// to 65536 rows, 16 experts, 1024 x 1024 (139 / 148 / 218 us) and to 1024 and 4096 rows (27 / 18 /
-// 14 and 27 / 21 / 27 us).  The larger tile moves fewer operand bytes for each product, the smaller one
-// leaves fewer CUs idle: 8192 rows, 8 experts, 2048 x 2048 take 93 / 88 / 122 us, 400 rows, 8 experts,
-// 1024 x 512 take 24 / 13 / 10 us.
-constexpr int kTileSide[3] = {256, 128, 64};
-constexpr double kTileSlots[3] = {256, 512, 1024}, kTileFixed[3] = {6.0, 4.0, 3.0}, kTileStep[3] = {1.37, 0.78, 0.61};
-inline double round_us(int tile, double k) { return kTileFixed[tile] + (k + 63) / 64 * kTileStep[tile]; }
-// Row tiles of `bm` rows that are expected of rows spread over experts.
-inline double row_tiles_expected(int64_t rows, int64_t experts, int bm) {
-  if (experts == 1) return static_cast<double>((rows + bm - 1) / bm);
-  return static_cast<double>(rows) / bm + 0.5 * static_cast<double>(hmin(experts, rows));
-}
 inline double rounds_of(double tiles, double slots) {
   const double r = tiles / slots;
   const int64_t whole = static_cast<int64_t>(r);
   return r > static_cast<double>(whole) ? static_cast<double>(whole + 1) : static_cast<double>(hmax(1, whole));
+}
+// Three tiles of C for a product: the larger one moves fewer operand bytes for each product, the smaller
+// one leaves fewer CUs idle.  As many run at once as `slots` on 256 CUs; a round of them takes a fixed
+// time and one for each 64 of k, `alone` where few of the slots are taken and `full` where all are (us,
+// fitted to times with the tile as given).
+struct TileCost {
+  int bm, bn;
+  double slots, fixed, alone, full;
+};
+// Operands straight to LDS, forward, the three tiles in turn: 65536 rows, 16 experts, 1024 x 1024: 137 / 143 /
+// 213 us; 8192 rows, 8 experts, 2048 x 2048: 91 / 84 / 119; 4096 rows, 4 experts, 1024 x 1024: 26 / 21 /
+// 26; 400 rows, 8 experts, 1024 x 512: 24 / 12 / 10.
+constexpr TileCost kDirectTiles[3] = {{256, 256, 256, 6.0, 1.37, 1.37}, {128, 128, 512, 4.0, 0.78, 0.78}, {64, 64, 1024, 3.0, 0.61, 0.61}};
+// Operands through registers: 60000 rows, 8 experts, 1777 x 1201, forward: 334 / 419 / 746 us; 3000 rows, 4
+// experts, 2047 x 901, by input: 37 / 30 / 40; 1000 rows, 1 expert, 2047 x 901, by input: 34 / 23 / 18.
+constexpr TileCost kRegisterTiles[3] = {{256, 256, 256, 6.0, 1.3, 2.05}, {256, 128, 256, 6.0, 1.0, 1.3}, {64, 64, 1024, 3.0, 0.55, 1.35}};
+// The weight gradient, both ways; times of the direct loads are at its plan (grouped_linear.hip).  Through
+// registers: 60000 rows, 8 experts, 1777 x 1201: 365 / 465 / 862 us; 3000 rows, 4 experts, 2047 x 901: 39 /
+// 29 / 44; 5003 rows, 13 experts, 1000 x 515: 33 / 33 / 30.
+constexpr TileCost kWeightTiles[3] = {{256, 256, 256, 6.0, 1.5, 1.85}, {128, 128, 512, 4.0, 0.75, 1.36}, {64, 64, 1024, 3.0, 0.6, 0.95}};
+// Tiles of k each, those of the last round of `last`.
+inline double tiles_us(const TileCost& c, double tiles, double k, double last) {
+  const double r = rounds_of(tiles, c.slots);
+  return r * c.fixed + ((r - 1.0) * k + last) / 64 * (c.alone + (c.full - c.alone) * tiles / (r * c.slots));
+}
+// Row tiles of `bm` rows that are expected of rows spread over experts.
+inline double row_tiles_expected(int64_t rows, int64_t experts, int bm) {
+  if (experts == 1) return static_cast<double>((rows + bm - 1) / bm);
+  return static_cast<double>(rows) / bm + 0.5 * static_cast<double>(hmin(experts, rows));
 }
 
 enum { kForward = 0, kBackwardInput = 1, kBackwardWeight = 2 };

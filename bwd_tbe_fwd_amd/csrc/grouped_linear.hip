@@ -44,11 +44,9 @@ __global__ __launch_bounds__(kBlock) void grouped_reduce_kernel(GroupedArgs a) {
 // rows (0: an expert's rows are one).  The least of the expected times: rounds of tiles, the last of
 // them by an expert of twice the average rows where rows are not shared, and 4 TB/s for the partial
 // sums' way to memory and back.  A step of 64 rows takes longer the more workgroups read their rows
-// from memory at once: kWeightStep where all slots are taken, kWeightAlone where few are.  Measured with
-// tile and unit as given: 16384 rows, 1 expert, 4096 x 1024: 256, 4096 rows 156 us; 256, all 398; 128,
-// all 207; 64, all 227.  65536 rows, 16 experts, 1024 x 1024: 256, all 137 us (the experts' rows
-// unequal, 370); 256, 4096 rows 257 (205); 128, all 187 (238); 64, all 279 (263).
-constexpr double kWeightStep[3] = {1.85, 1.36, 0.95}, kWeightAlone[3] = {1.5, 0.75, 0.6};
+// from memory at once.  Measured with tile and unit as given: 16384 rows, 1 expert, 4096 x 1024: 256, 4096
+// rows 139 us; 256, all 398; 128, all 207; 64, all 227.  65536 rows, 16 experts, 1024 x 1024: 256, all 130
+// us (the experts' rows unequal, 370); 256, 4096 rows 257 (205); 128, all 186 (238); 64, all 279 (263).
 struct WeightPlan {
   int tile, split;
 };
@@ -57,26 +55,20 @@ WeightPlan weight_plan(int64_t rows, int64_t experts, int64_t inner, int64_t out
   double best = -1.0;
   const double used = static_cast<double>(hmax(1, hmin(experts, rows))), average = static_cast<double>(rows) / used;
   for (int t = 0; t < 3; ++t) {
-    const int side = kTileSide[t];
-    const double each = static_cast<double>((outer + side - 1) / side) * static_cast<double>((inner + side - 1) / side);
-    // rounds of `tiles` over k rows, the last one over `last`
-    auto time = [&](double tiles, double k, double last) {
-      const double r = rounds_of(tiles, kTileSlots[t]);
-      const double step = kWeightAlone[t] + (kWeightStep[t] - kWeightAlone[t]) * tiles / (r * kTileSlots[t]);
-      return r * kTileFixed[t] + ((r - 1.0) * k + last) / 64 * step;
-    };
-    double us = time(used * each, average, experts > 1 ? 2.0 * average : average);
+    const TileCost& c = kWeightTiles[t];
+    const double each = static_cast<double>((outer + c.bm - 1) / c.bm) * static_cast<double>((inner + c.bn - 1) / c.bn);
+    double us = tiles_us(c, used * each, average, experts > 1 ? 2.0 * average : average);
     if (best < 0.0 || us < best) {
       best = us;
       p = WeightPlan{t, 0};
     }
-    for (int64_t c = 512; c < rows && c <= (1 << 20); c *= 2) {
-      const double units = row_tiles_expected(rows, experts, static_cast<int>(c)), k = static_cast<double>(c);
-      const double bytes = 4.0 * static_cast<double>(rows / c) * static_cast<double>(inner + 1) * static_cast<double>(outer);
-      us = time(units * each, k, k) + 5.0 + 2.0 * bytes / 4e6;
+    for (int64_t split = 512; split < rows && split <= (1 << 20); split *= 2) {
+      const double units = row_tiles_expected(rows, experts, static_cast<int>(split)), k = static_cast<double>(split);
+      const double bytes = 4.0 * static_cast<double>(rows / split) * static_cast<double>(inner + 1) * static_cast<double>(outer);
+      us = tiles_us(c, units * each, k, k) + 5.0 + 2.0 * bytes / 4e6;
       if (us < best) {
         best = us;
-        p = WeightPlan{t, static_cast<int>(c)};
+        p = WeightPlan{t, static_cast<int>(split)};
       }
     }
   }

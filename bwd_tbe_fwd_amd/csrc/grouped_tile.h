@@ -7,13 +7,16 @@
 //    bytes a lane), one step ahead of the products, with one barrier a step.  Lanes past the
 //    matrix's edge get an offset past the buffer's range and so write zeros: the edges of the
 //    groups cost no branch in the loop.  Rows that do not start on 16 bytes (or k or n that are not
-//    whole 16 bytes) go through registers instead, with the same LDS layout.
+//    whole 16 bytes) go through registers instead, with the same LDS layout: 60000 rows, 8 experts, 1777 x
+//    1201 forward take 340 us where 1776 x 1200 take 242.
 //  * LDS holds an operand as it lies in memory, along: [m][64 k], across: [64 k][m].  The 16-byte
 //    columns of an along row are exchanged by a pattern of the row, and the across rows are put in an
 //    order with gaps, so that what a read takes lies in different banks.  A lane's place in a read
 //    is a base that never changes plus a constant: no address arithmetic between the products.
 //  * An across operand is turned on the way from LDS to the registers (ds_read_b64_tr_b16: 16 lanes
 //    read 4 k x 16 m and each gets 4 k of one m).
+//  * Only the last steps look at the matrix's end: the others' loads have no compare and no branch
+//    (131072 rows, 16 experts, 4096 x 1024: forward 978 -> 955 us).
 //  * The products are taken as C^T: a lane then holds adjacent n of one m, 4 of each product.  Where B
 //    lies along, the 16 n of one product are 4 at a time from 4 blocks of 4 NF, so that a lane's NF
 //    products give 4 NF adjacent n (an across read of such n would meet in the same banks).
@@ -170,12 +173,11 @@ struct Operand {
       __builtin_memcpy(&reg[i], v.e, 16);
     }
   }
-  // Registers to LDS, where the loads went there.
+  // Registers to LDS, where the loads went there: a thread's i-th chunk, or all of them.
+  __device__ __forceinline__ void store(int i, uint16_t* s) { *reinterpret_cast<u16x8_t*>(s + lds_place(i)) = reg[i]; }
   __device__ __forceinline__ void store(uint16_t* s) {
-    if constexpr (!DIRECT) {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) *reinterpret_cast<u16x8_t*>(s + lds_place(i)) = reg[i];
-    }
+    for (int i = 0; i < kEach; ++i) store(i, s);
   }
   // This lane's place in a read of the 8 k from 8 (lane / 16) on of one m.  Along: of m itself.  Across:
   // m is the first of the 4 adjacent m that this lane reads for its 16 lanes; it gets the (lane %
@@ -357,86 +359,138 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void g
     if constexpr (OP == kBackwardWeight) sum[i] = 0.0f;
   }
 
-  // The operands of 32 k are in registers while those of the next 32 k are read from LDS, between the
-  // products.  Two LDS buffers of 64 k each: when the second half of buffer `it` has been read by all
-  // waves, the loads of it + 2 start there, also between the products, and have the products of 64
-  // k to arrive.  Loads are started past the end too, with nothing in range.
   constexpr int kLoads = OA::kEach + OB::kEach;
-  u16x8_t fa[2][MF], fb[2][NF];
   auto load = [&](int i, int step, uint16_t* pa, uint16_t* pb, auto whole) {
     constexpr bool WHOLE = decltype(whole)::value;
     if (i < OA::kEach) A.template load<WHOLE>(i, step * K, pa);
     else B.template load<WHOLE>(i - OA::kEach, step * K, pb);
   };
-  constexpr std::false_type any{};
-  if (steps > 0) {
+  auto add_up = [&](int i, u16x8_t v) {
+    if constexpr (OP == kBackwardWeight) {
+      if (sums) {
+        float u[8];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) load(i, k, sa[k], sb[k], any);
-      A.store(sa[k]);
-      B.store(sb[k]);
-    }
-    if constexpr (!DIRECT) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) load(i, 2, nullptr, nullptr, any);
-    }
-    wait_loads<DIRECT ? kLoads : 63>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-#pragma unroll
-    for (int j = 0; j < NF; ++j) fb[0][j] = OB::read(sb[0] + b_place, kNext * j);
-#pragma unroll
-    for (int i = 0; i < MF; ++i) fa[0][i] = OA::read(sa[0] + a_place, 16 * i);
-  }
-  constexpr int kAhead = DIRECT ? 2 : 3;  // the step whose loads start at a step
-  auto step = [&](int it, auto whole) {
-    const int cur = it & 1;
-#pragma unroll
-    for (int P = 0; P < 2; ++P) {  // the half in registers
-      const int Q = 1 - P, from = P == 0 ? cur : cur ^ 1;
-      if (P == 1) {
-        wait_loads<DIRECT ? 0 : 63>();
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if constexpr (!DIRECT) {
-          A.store(sa[0] + cur * OA::kElems);
-          B.store(sb[0] + cur * OB::kElems);
-        }
-      }
-      const uint16_t *ra = sa[0] + from * OA::kElems + a_half[Q], *rb = sb[0] + from * OB::kElems + b_half[Q];
-#pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        fa[Q][i] = OA::read(ra, 16 * i);
-#pragma unroll
-        for (int j = i * NF / MF; j < (i + 1) * NF / MF; ++j) fb[Q][j] = OB::read(rb, kNext * j);
-#pragma unroll
-        for (int j = 0; j < NF; ++j) acc[i][j] = mfma16<DT>(fb[P][j], fa[P][i], acc[i][j]);
-        if (P == 1) {
-#pragma unroll
-          for (int k = i * kLoads / MF; k < (i + 1) * kLoads / MF; ++k)
-            load(k, it + kAhead, sa[0] + cur * OA::kElems, sb[0] + cur * OB::kElems, whole);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if constexpr (OP == kBackwardWeight) {
-        if (sums) {
-#pragma unroll
-          for (int i = 0; i < MF; ++i) {
-            float u[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = Fmt<DT>::to_f(fa[P][i][e]);
-            sum[i] += ((u[0] + u[1]) + (u[2] + u[3])) + ((u[4] + u[5]) + (u[6] + u[7]));
-          }
-        }
+        for (int e = 0; e < 8; ++e) u[e] = Fmt<DT>::to_f(v[e]);
+        sum[i] += ((u[0] + u[1]) + (u[2] + u[3])) + ((u[4] + u[5]) + (u[6] + u[7]));
       }
     }
   };
-  // the steps whose loads are whole, without a look at the end or a branch; then the last ones
-  const int whole_steps = min(min(A.whole_steps(), B.whole_steps()) - kAhead, steps);
-  int it = 0;
-  for (; it < whole_steps; ++it) step(it, std::true_type{});
-  for (; it < steps; ++it) step(it, any);
+  constexpr std::false_type any{};
+  // whole_steps: those whose loads are whole, without a look at the end or a branch; then the last ones
+  auto walk = [&](auto step, int ahead) {
+    const int whole_steps = min(min(A.whole_steps(), B.whole_steps()) - ahead, steps);
+    int it = 0;
+    for (; it < whole_steps; ++it) step(it, std::true_type{});
+    for (; it < steps; ++it) step(it, any);
+  };
+  if constexpr (DIRECT) {
+    // The operands of 32 k are in registers while those of the next 32 k are read from LDS, between the
+    // products.  Two LDS buffers of 64 k each: when the second half of buffer `it` has been read by all
+    // waves, the loads of it + 2 start there, also between the products, and have the products of 64
+    // k to arrive.  Loads are started past the end too, with nothing in range.
+    u16x8_t fa[2][MF], fb[2][NF];
+    if (steps > 0) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) load(i, k, sa[k], sb[k], any);
+      }
+      wait_loads<kLoads>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < NF; ++j) fb[0][j] = OB::read(sb[0] + b_place, kNext * j);
+#pragma unroll
+      for (int i = 0; i < MF; ++i) fa[0][i] = OA::read(sa[0] + a_place, 16 * i);
+    }
+    walk([&](int it, auto whole) {
+      const int cur = it & 1;
+#pragma unroll
+      for (int P = 0; P < 2; ++P) {  // the half in registers
+        const int Q = 1 - P, from = P == 0 ? cur : cur ^ 1;
+        if (P == 1) {
+          wait_loads<0>();
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        }
+        const uint16_t *ra = sa[0] + from * OA::kElems + a_half[Q], *rb = sb[0] + from * OB::kElems + b_half[Q];
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          fa[Q][i] = OA::read(ra, 16 * i);
+#pragma unroll
+          for (int j = i * NF / MF; j < (i + 1) * NF / MF; ++j) fb[Q][j] = OB::read(rb, kNext * j);
+#pragma unroll
+          for (int j = 0; j < NF; ++j) acc[i][j] = mfma16<DT>(fb[P][j], fa[P][i], acc[i][j]);
+          if (P == 1) {
+#pragma unroll
+            for (int k = i * kLoads / MF; k < (i + 1) * kLoads / MF; ++k)
+              load(k, it + 2, sa[0] + cur * OA::kElems, sb[0] + cur * OB::kElems, whole);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < MF; ++i) add_up(i, fa[P][i]);
+      }
+    }, 2);
+  } else {
+    // The registers that loads pass through are paid for by those of the operands: 16 m of A are read
+    // two ahead of their products.  While the products of buffer `it` are taken, what was loaded for
+    // it + 1 goes to the other buffer and the loads of it + 2 start.  One barrier a step, two products of m
+    // before its end: what is left of buffer `it` is then in registers, and the next one is there.  (The
+    // fragments of 32 k twice, as above, leave no room for 256 x 256: 60000 rows, 8 experts, 1777 x 1201
+    // forward took 432 us with 256 x 128.  Here a few registers spill around the loop, none inside it.)
+    constexpr int T2 = 2 * MF;
+    u16x8_t fa[4], fb[2][NF];
+    if (steps > 0) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load(i, 0, nullptr, nullptr, any);
+      A.store(sa[0]);
+      B.store(sb[0]);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load(i, 1, nullptr, nullptr, any);
+      wait_loads<63>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < NF; ++j) fb[0][j] = OB::read(sb[0] + b_place, kNext * j);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) fa[i] = OA::read(sa[0] + a_place, 16 * i);
+    }
+    walk([&](int it, auto whole) {
+      const int cur = it & 1;
+      uint16_t *ca = sa[0] + cur * OA::kElems, *cb = sb[0] + cur * OB::kElems;
+      uint16_t *na = sa[0] + (cur ^ 1) * OA::kElems, *nb = sb[0] + (cur ^ 1) * OB::kElems;
+#pragma unroll
+      for (int t = 0; t < T2; ++t) {
+        const int P = t / MF, i = t % MF, u = (t + 2) % T2;
+        if (t == T2 - 2) {
+          wait_loads<63>();
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        }
+        fa[(t + 2) % 4] = OA::read((t < T2 - 2 ? ca : na) + a_half[u / MF], 16 * (u % MF));
+        if (P == 0) {
+#pragma unroll
+          for (int j = i * NF / MF; j < (i + 1) * NF / MF; ++j) fb[1][j] = OB::read(cb + b_half[1], kNext * j);
+        } else if (t >= T2 - 2) {
+#pragma unroll
+          for (int j = (t - T2 + 2) * NF / 2; j < (t - T2 + 3) * NF / 2; ++j) fb[0][j] = OB::read(nb + b_half[0], kNext * j);
+        }
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[i][j] = mfma16<DT>(fb[P][j], fa[t % 4], acc[i][j]);
+        add_up(i, fa[t % 4]);
+        if (t < T2 - 2) {
+#pragma unroll
+          for (int k = t * kLoads / (T2 - 2); k < (t + 1) * kLoads / (T2 - 2); ++k) {
+            if (k < OA::kEach) A.store(k, na);
+            else B.store(k - OA::kEach, nb);
+            load(k, it + 2, nullptr, nullptr, whole);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }, 2);
+  }
   wait_loads<0>();  // no load is under way when LDS takes the results
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");

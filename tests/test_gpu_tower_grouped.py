@@ -144,6 +144,27 @@ def test_each_tile(groups, inner, outer, dtype):
     Case(groups, inner, outer, dtype, pad_rows=7).all()
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("groups,inner,outer", [
+    ([9000, 4100, 1900], 2041, 1001),      # forward, by input and by weight: 256 x 256, rows shared
+    ([2500, 0, 1400, 2100], 1001, 1201),   # forward and by input: 256 x 128
+    ([900, 1, 700, 1399], 2047, 901),      # by weight: 128 x 128
+    ([300, 0, 7, 393], 515, 77),           # 64 x 64
+])
+def test_each_tile_at_any_alignment(groups, inner, outer, dtype):
+    """As test_each_tile, where rows do not start on 16 bytes or do not end on them."""
+    flush_print("grouped", groups, inner, outer)
+    Case(groups, inner, outer, dtype, pad_rows=7).all()
+
+
+@pytest.mark.parametrize("pad", [0, 1, 8])
+@pytest.mark.parametrize("inner,outer", [(1, 1), (3, 8), (7, 2), (8, 5), (9, 15), (71, 7), (129, 9), (64, 63)])
+def test_narrow_sides(inner, outer, pad):
+    """Sides around the 8 values of one load, over several steps of 64 rows; the last group ends the buffers."""
+    flush_print("grouped", inner, outer, pad)
+    Case([65, 130, 0, 257], inner, outer, BF16, pad=pad).all()
+
+
 def test_many_experts():
     g = torch.Generator().manual_seed(3)
     groups = [int(n) for n in torch.randint(0, 9, (200,), generator=g)]
