@@ -56,10 +56,9 @@ __device__ __forceinline__ int across_place(int k) {
 
 // 16 bytes a lane from offset `o` of the buffer to LDS, lane l's at lds + 16 l.  Written as an
 // instruction because the compiler, which cannot tell the LDS buffers apart, would wait for every
-// load under way before each LDS read; it writes no register but m0, which the compiler uses for
-// nothing here, and wait_loads is its wait.
+// load under way before each LDS read; it writes no register but m0, and wait_loads is its wait.
 __device__ __forceinline__ void load_to_lds(u32x4 r, uint32_t o, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(o), "s"(r) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(o), "s"(r) : "memory", "m0");
 }
 
 // One operand's tile of SIDE m by kStepK k, THREADS threads.

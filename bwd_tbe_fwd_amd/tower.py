@@ -296,14 +296,15 @@ def tbe_adamw_state_read(tensors: AdamWTensors, exp_avg_out: Sequence[torch.Tens
     dtype = exp_avg_out[0].dtype if n else torch.float32
     array = ctypes.c_void_p * max(1, n)
     arrays = []
+    T = torch.Tensor
     for outs in (exp_avg_out, exp_avg_sq_out):
-        if [t.numel() for t in outs] != tensors.numels or any(t.dtype is not dtype or t.get_device() != dev for t in outs) \
-                or not all([t.is_contiguous() for t in outs]):
+        if list(map(T.numel, outs)) != tensors.numels or set(map(T.get_device, outs)) - {dev} \
+                or set(map(T.dtype.__get__, outs)) - {dtype} or not all(map(T.is_contiguous, outs)):
             for i, t in enumerate(outs):
                 if t.get_device() != dev:
                     _off_gpu(f"output {i}", t)
                 if t.numel() != c[i].numel or t.dtype != dtype or not t.is_contiguous():
                     _refuse(f"output {i} is {t.dtype} of {t.numel()}: contiguous {dtype} of {c[i].numel} is needed")
-        arrays.append(array(*[t.data_ptr() for t in outs]))
+        arrays.append(array(*map(T.data_ptr, outs)))
     st = lib().tbe_adamw_state_read(c, n, *arrays, _dtype("output 0", exp_avg_out[0]) if n else 0, _current(stream, dev))
     _check(st, "tbe_adamw_state_read")
