@@ -111,9 +111,82 @@ __device__ __forceinline__ void load_shared(const void* p, int dt, int64_t c, in
   }
 }
 
-// A result vector: with the streaming policy where it is whole 16 bytes of a row that starts on 16.
-// 65536 x 4096 in bf16: forward 252 -> 197 us, backward 349 -> 343 us; not for fp32 rows' gradients (131072
-// x 4096: 1000 -> 1026 us).
+// Where a lane's v-th vector of a row lies.  EDGE kFull: every lane's vectors lie inside the row; kWhole: some
+// lie past it (skip = VEC); kRagged: the width is no multiple of VEC.  The row's last vector then ends at its
+// last column: it starts earlier, and `skip` of its elements are the vector's before it too, which both
+// compute and store alike and only the first adds to sums.  So every access is a whole vector, and no lane
+// walks through a vector's elements (67 M values of bf16, backward: rows of 900 131 -> 83 us, of 361 162 ->
+// 86; rows of 4096 92 -> 80 by the packed zeros below).
+enum { kFull = 0, kWhole = 1, kRagged = 2 };
+inline int norm_edge(int64_t width, int G, int vec, int nv) { return width % vec ? kRagged : width == static_cast<int64_t>(G) * vec * nv ? kFull : kWhole; }
+template <int G, int VEC, int EDGE>
+struct Place {
+  static constexpr bool RAGGED = EDGE == kRagged;
+  int64_t c;  // first column; negative for rows narrower than a vector
+  int skip;
+  __device__ __forceinline__ Place(int v, int64_t width) {
+    c = static_cast<int64_t>(v * G + threadIdx.x % G) * VEC;
+    skip = EDGE == kFull ? 0 : c >= width ? VEC : RAGGED ? static_cast<int>(max(c + VEC - width, static_cast<int64_t>(0))) : 0;
+    if (RAGGED) c -= skip;
+  }
+  __device__ __forceinline__ bool in() const { return EDGE == kFull || skip < VEC; }
+  // A row narrower than a vector goes element by element; it is one of the 16-lane kernels'.
+  __device__ __forceinline__ static bool narrow(int64_t width) { return RAGGED && G == 16 && width < VEC; }
+  __device__ __forceinline__ bool has(int i) const { return !RAGGED || i >= skip; }
+  template <typename S>
+  __device__ __forceinline__ void load(const S* p, int64_t width, bool live, Vec<S, VEC>& v) const {
+    // Packed until it is used: the compiler otherwise takes a vector apart where the zeros and the loaded
+    // values meet, and waits there for one load before it starts the next.
+    constexpr int kBytes = VEC * static_cast<int>(sizeof(S)), kPart = kBytes < 16 ? kBytes : 16;
+    typedef uint32_t Part __attribute__((ext_vector_type(kPart / 4)));
+    Part x[kBytes / kPart] = {};
+    if (live && in()) {
+      if (!narrow(width)) {
+#pragma unroll
+        for (int k = 0; k < kBytes / kPart; ++k) __builtin_memcpy(&x[k], reinterpret_cast<const char*>(p + c) + k * kPart, kPart);
+      } else {
+        Vec<S, VEC> e;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) e.e[i] = i >= skip ? p[c + i] : S(0);
+        __builtin_memcpy(x, e.e, kBytes);
+      }
+    }
+    __builtin_memcpy(v.e, x, kBytes);
+  }
+  // stream: the rows start on 16 bytes, and results go past the caches (65536 rows of 4096 in bf16: forward 252 ->
+  // 197 us, backward 349 -> 343 us; not fp32 rows' gradients: 131072 rows of 4096 1000 -> 1026 us)
+  template <typename S>
+  __device__ __forceinline__ void store(S* p, int64_t width, bool stream, const Vec<S, VEC>& v) const {
+    if (!in()) return;
+    if (narrow(width)) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (i >= skip) p[c + i] = v.e[i];
+      return;
+    }
+    if constexpr (VEC * sizeof(S) % 16 == 0) {
+      if (stream && (!RAGGED || skip == 0)) {
+        store_vec_stream<S, VEC>(p + c, v);
+        return;
+      }
+    }
+    store_vec_any<S, VEC>(p + c, v);
+  }
+  // of a vector that every row shares, as floats; `none` where there is none
+  __device__ __forceinline__ void shared(const void* p, int dt, int64_t width, float none, float (&v)[VEC]) const {
+    if (!p || !in()) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = none;
+    } else if (narrow(width)) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = i >= skip ? load_any(p, dt, c + i) : none;
+    } else {
+      load_shared<VEC>(p, dt, c, VEC, none, v);
+    }
+  }
+};
+
+// A result vector of a wider row: with the streaming policy where it is whole 16 bytes of a row that starts on 16.
 template <typename S, int VEC>
 __device__ __forceinline__ void store_row(S* p, int64_t left, bool stream, const Vec<S, VEC>& v) {
   if constexpr (VEC * sizeof(S) % 16 == 0) {
@@ -125,15 +198,16 @@ __device__ __forceinline__ void store_row(S* p, int64_t left, bool stream, const
   store_vec_part<S, VEC>(p, left, v);
 }
 
-// Whether a kernel loads its next row before it works on this one: where a lane has at most 32 bytes of
+// Whether the forward loads its next row before it works on this one: where a lane has at most 32 bytes of
 // a row in flight.  (More cost the registers that the other waves' loads need: fp32 rows of 4096
 // reach the memory's rate without.)
 template <int XT, int NV> constexpr bool kNormAhead = NV * kNormVec<XT> * (XT == 0 ? 4 : 2) <= 32;
 
-template <int XT, int YT, int G, int NV>
+template <int XT, int YT, int G, int NV, int EDGE>
 __global__ __launch_bounds__(norm_block(G)) void norm_forward_kernel(NormArgs a) {
   constexpr int VEC = kNormVec<XT>, B = norm_block(G), R = B / G;
   constexpr bool KEEP = NV * VEC <= 16;  // the scale and the shift stay in registers
+  using At = Place<G, VEC, EDGE>;
   using XS = typename Fmt<XT>::S;
   using YS = typename Fmt<YT>::S;
   __shared__ float s_red[2][B / kWave];
@@ -145,19 +219,16 @@ __global__ __launch_bounds__(norm_block(G)) void norm_forward_kernel(NormArgs a)
   if constexpr (KEEP) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t c = static_cast<int64_t>(v * G + g) * VEC;
-      load_shared<VEC>(a.w, a.w_dt, c, a.width - c, 1.0f, w[v]);
-      load_shared<VEC>(a.b, a.w_dt, c, a.width - c, 0.0f, b[v]);
+      const At at(v, a.width);
+      at.shared(a.w, a.w_dt, a.width, 1.0f, w[v]);
+      at.shared(a.b, a.w_dt, a.width, 0.0f, b[v]);
     }
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * R;
   auto fetch = [&](int64_t r, Vec<XS, VEC>(&to)[NV]) {
     const XS* xr = x + min(r, a.rows - 1) * a.x_stride;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int64_t c = static_cast<int64_t>(v * G + g) * VEC;
-      load_vec_part<XS, VEC>(xr + c, a.width - c, to[v]);
-    }
+    for (int v = 0; v < NV; ++v) At(v, a.width).load(xr, a.width, true, to[v]);
   };
   Vec<XS, VEC> raw[NV], ahead[kNormAhead<XT, NV> ? NV : 1];
   if constexpr (kNormAhead<XT, NV>) fetch(static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G, ahead);
@@ -174,18 +245,21 @@ __global__ __launch_bounds__(norm_block(G)) void norm_forward_kernel(NormArgs a)
     }
     float sum = 0.0f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+      const At at(v, a.width);  // zeros past the row
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) sum += Fmt<XT>::to_f(raw[v].e[i]);
+      for (int i = 0; i < VEC; ++i) sum += at.has(i) ? Fmt<XT>::to_f(raw[v].e[i]) : 0.0f;
+    }
     const float mean = row_sum<G>(sum, s_red[0]) / width;
     float sq = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t left = a.width - static_cast<int64_t>(v * G + g) * VEC;
+      const At at(v, a.width);
+      const float middle = at.in() ? mean : 0.0f;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float d = Fmt<XT>::to_f(raw[v].e[i]) - mean;
-        sq += i < left ? d * d : 0.0f;
+        const float d = Fmt<XT>::to_f(raw[v].e[i]) - middle;
+        sq += at.has(i) ? d * d : 0.0f;
       }
     }
     const float rstd = 1.0f / sqrtf(row_sum<G>(sq, s_red[1]) / width + a.eps);
@@ -197,21 +271,20 @@ __global__ __launch_bounds__(norm_block(G)) void norm_forward_kernel(NormArgs a)
       YS* yr = y + row * a.y_stride;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int64_t c = static_cast<int64_t>(v * G + g) * VEC;
+        const At at(v, a.width);
         if constexpr (!KEEP) {
-          load_shared<VEC>(a.w, a.w_dt, c, a.width - c, 1.0f, w[0]);
-          load_shared<VEC>(a.b, a.w_dt, c, a.width - c, 0.0f, b[0]);
+          at.shared(a.w, a.w_dt, a.width, 1.0f, w[0]);
+          at.shared(a.b, a.w_dt, a.width, 0.0f, b[0]);
         }
         Vec<YS, VEC> o;
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
           o.e[i] = tower_from_f<YT>((Fmt<XT>::to_f(raw[v].e[i]) - mean) * rstd * w[KEEP ? v : 0][i] + b[KEEP ? v : 0][i]);
-        store_row<YS, VEC>(yr + c, a.width - c, a.stream, o);
+        at.store(yr, a.width, a.stream, o);
       }
     }
   }
 }
-
 // Rows wider than registers hold: one workgroup of 1024 a row, which reads it three times (from
 // the caches after the first).
 constexpr int kNormWide = 1024;
@@ -263,9 +336,10 @@ __global__ __launch_bounds__(kNormWide) void norm_forward_wide_kernel(NormArgs a
 // Backward.  Each workgroup walks rows blockIdx.x, + gridDim.x, ... and keeps its columns' sums
 // of grad_y * h and grad_y in registers; at the end the lane groups that share columns add up
 // through LDS in their order and the workgroup writes one partial row pair.
-template <int XT, int YT, int G, int NV>
+template <int XT, int YT, int G, int NV, int EDGE>
 __global__ __launch_bounds__(norm_block(G)) void norm_backward_kernel(NormArgs a) {
   constexpr int VEC = kNormVec<XT>, B = norm_block(G), R = B / G;
+  using At = Place<G, VEC, EDGE>;
   using XS = typename Fmt<XT>::S;
   using YS = typename Fmt<YT>::S;
   __shared__ float s_red[2][2 * B / kWave];
@@ -275,27 +349,25 @@ __global__ __launch_bounds__(norm_block(G)) void norm_backward_kernel(NormArgs a
   float w[NV][VEC], gw[NV][VEC], gb[NV][VEC];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int64_t c = static_cast<int64_t>(v * G + g) * VEC;
-    load_shared<VEC>(a.w, a.w_dt, c, a.width - c, 1.0f, w[v]);
+    At(v, a.width).shared(a.w, a.w_dt, a.width, 1.0f, w[v]);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) gw[v][i] = gb[v][i] = 0.0f;
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * R;
   // A wave that owns whole rows of 16 bits loads its next row before it works on this one: 10007 rows of
-  // 1001, where a wave has two or three, 27.1 -> 22.2 us.  Wider rows lose more by the registers
-  // (65536 rows of 4096: 0.41 -> 0.52 ms).
+  // 1001, where a wave has five, 20.7 -> 19.1 us.  Wider rows have several waves to wait for each other (65536
+  // rows of 4096: 297 us with and without).
   constexpr bool AHEAD = G == 64 && XT != 0;
   auto fetch = [&](int64_t r, Vec<XS, VEC>(&xs)[NV], Vec<YS, VEC>(&gs)[NV], float& mean, float& rstd) {
     const bool live = r < a.rows;
-    const int64_t row = live ? r : a.rows - 1;
+    const int64_t row = live ? r : a.rows - 1;  // a group without a row reads the last one's x and adds zeros
     const XS* xr = static_cast<const XS*>(a.x) + row * a.x_stride;
     const YS* gr = static_cast<const YS*>(a.gy) + row * a.gy_stride;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t c = static_cast<int64_t>(v * G + g) * VEC;
-      // a group without a row reads the last row and adds zeros
-      load_vec_part<XS, VEC>(xr + c, a.width - c, xs[v]);
-      load_vec_part<YS, VEC>(gr + c, live ? a.width - c : 0, gs[v]);
+      const At at(v, a.width);
+      at.load(xr, a.width, true, xs[v]);
+      at.load(gr, a.width, live, gs[v]);
     }
     mean = a.mean[row];
     rstd = a.rstd[row];
@@ -323,12 +395,12 @@ __global__ __launch_bounds__(norm_block(G)) void norm_backward_kernel(NormArgs a
     float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t c = static_cast<int64_t>(v * G + g) * VEC, left = live ? a.width - c : 0;
+      const At at(v, a.width);
+      const float scale = at.in() ? rstd : 0.0f;  // columns past the row have no h (mean * rstd there could be infinite)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        // columns past the row have no h (mean * rstd there could be infinite)
-        const float h = i < left ? (Fmt<XT>::to_f(raw[v].e[i]) - mean) * rstd : 0.0f;
-        const float gy = Fmt<YT>::to_f(gin[v].e[i]);
+        const float h = at.has(i) ? (Fmt<XT>::to_f(raw[v].e[i]) - mean) * scale : 0.0f;
+        const float gy = at.has(i) ? Fmt<YT>::to_f(gin[v].e[i]) : 0.0f;
         const float d = gy * w[v][i];
         c1 += d;
         c2 += d * h;
@@ -343,14 +415,13 @@ __global__ __launch_bounds__(norm_block(G)) void norm_backward_kernel(NormArgs a
       XS* xo = static_cast<XS*>(a.gx) + row * a.gx_stride;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int64_t c = static_cast<int64_t>(v * G + g) * VEC;
         Vec<XS, VEC> o;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           const float h = (Fmt<XT>::to_f(raw[v].e[i]) - mean) * rstd;
           o.e[i] = tower_from_f<XT>((Fmt<YT>::to_f(gin[v].e[i]) * w[v][i] - c1 - h * c2) * rstd);
         }
-        store_row<XS, VEC>(xo + c, a.width - c, XT != 0 && a.stream, o);
+        At(v, a.width).store(xo, a.width, XT != 0 && a.stream, o);
       }
     }
   }
@@ -359,22 +430,34 @@ __global__ __launch_bounds__(norm_block(G)) void norm_backward_kernel(NormArgs a
   if constexpr (R == 1) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t c = static_cast<int64_t>(v * G + g) * VEC;
+      const At at(v, a.width);
+      if (!at.in()) continue;
       Vec<float, VEC> o, p;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         o.e[i] = gw[v][i];
         p.e[i] = gb[v][i];
       }
-      store_vec_part<float, VEC>(out + c, a.width - c, o);
-      store_vec_part<float, VEC>(out + a.width + c, a.width - c, p);
+      if (at.skip == 0) {
+        store_vec_any<float, VEC>(out + at.c, o);
+        store_vec_any<float, VEC>(out + a.width + at.c, p);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          if (i >= at.skip) {
+            out[at.c + i] = o.e[i];
+            out[a.width + at.c + i] = p.e[i];
+          }
+      }
     }
   } else {
 #pragma unroll
     for (int v = 0; v < 2 * NV; ++v) {
       __syncthreads();
+      const At at(v % NV, a.width);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) s_part[threadIdx.x * VEC + i] = v < NV ? gw[v % NV][i] : gb[v % NV][i];
+      for (int i = 0; i < VEC; ++i)
+        if (i >= at.skip) s_part[threadIdx.x * VEC + i - at.skip] = v < NV ? gw[v % NV][i] : gb[v % NV][i];
       __syncthreads();
       for (int e = threadIdx.x; e < G * VEC; e += B) {
         float sum = 0.0f;
@@ -471,15 +554,31 @@ template <int XT, int YT, int G, int NV>
 tbe_status norm_forward_as(const NormArgs& a, hipStream_t s) {
   constexpr int B = norm_block(G);
   constexpr int64_t R = B / G;
-  return norm_launch("norm_forward", norm_forward_kernel<XT, YT, G, NV>, (a.rows + R - 1) / R, B, 0x7fffffff, a, s, nullptr);
+  const int edge = norm_edge(a.width, G, kNormVec<XT>, NV);
+  auto kernel = edge == kFull ? norm_forward_kernel<XT, YT, G, NV, kFull>
+                              : edge == kWhole ? norm_forward_kernel<XT, YT, G, NV, kWhole> : norm_forward_kernel<XT, YT, G, NV, kRagged>;
+  // No more workgroups than keep the memory busy, by the bytes that each reads at a time, as in the backward.
+  // 512 / 768 / 1024 / all resident: 131072 rows of 4096 fp32, 16 KB: 569 / 597 / 649 / 618 us; 400000 rows of 1001 of 16
+  // bits, 8 KB: - / 302 / 333 / 339; 200000 rows of 2048, 4 KB: - / 325 / 289 / 331; 67 M values in rows of 200 fp32, 3 KB: - /
+  // - / 111 / 95.
+  const int64_t bytes = R * a.width * static_cast<int64_t>(sizeof(typename Fmt<XT>::S));
+  const int64_t cap = bytes >= 12000 ? 512 : bytes >= 6500 ? 768 : bytes >= 3800 ? 1024 : 0x7fffffff;
+  return norm_launch("norm_forward", kernel, (a.rows + R - 1) / R, B, cap, a, s, nullptr);
 }
 template <int XT, int YT, int G, int NV>
 tbe_status norm_backward_as(const NormArgs& a, hipStream_t s, int* grid) {
   constexpr int B = norm_block(G);
   constexpr int64_t R = B / G;
-  // at least two rows a lane group: a workgroup's partial rows are as many bytes as one or two rows
-  return norm_launch("norm_backward", norm_backward_kernel<XT, YT, G, NV>, (a.rows + 2 * R - 1) / (2 * R), B,
-                     norm_partials(a.width), a, s, grid);
+  // At least two rows a lane group: a workgroup's partial rows are as many bytes as one or two rows.  And no more
+  // workgroups than keep the memory busy, two to four a CU by the bytes that each reads at a time: more make reads
+  // and writes meet.  512 / 768 / 1024 workgroups: 131072 rows of 4096, fp32 and bf16, 24 KB: 991 / 1034 / 1149 us; 67 M
+  // values of bf16 in rows of 2048, 8 KB: 92 / 77 / 81; of 1501, 6 KB: - / 104 / 91.
+  const int64_t bytes = R * a.width * static_cast<int64_t>(sizeof(typename Fmt<XT>::S) + sizeof(typename Fmt<YT>::S));
+  const int edge = norm_edge(a.width, G, kNormVec<XT>, NV);
+  auto kernel = edge == kFull ? norm_backward_kernel<XT, YT, G, NV, kFull>
+                              : edge == kWhole ? norm_backward_kernel<XT, YT, G, NV, kWhole> : norm_backward_kernel<XT, YT, G, NV, kRagged>;
+  return norm_launch("norm_backward", kernel, (a.rows + 2 * R - 1) / (2 * R), B,
+                     hmin(bytes >= 12000 ? 512 : bytes >= 6500 ? 768 : 1024, norm_partials(a.width)), a, s, grid);
 }
 
 // Up to 16 elements a lane (32 for the widest rows), by as few lanes as that takes.
@@ -491,6 +590,11 @@ tbe_status norm_forward_types(const NormArgs& a, hipStream_t s) {
   if (n <= 32) return norm_forward_as<XT, YT, 16, 2>(a, s);
   if (n <= 64) return norm_forward_as<XT, YT, 64, 1>(a, s);
   if (n <= 64 * 2 * F) return norm_forward_as<XT, YT, 64, 2 * F>(a, s);
+  if constexpr (XT != 0) {
+    if (n <= 192) return norm_forward_as<XT, YT, 192, 1>(a, s);
+    if (n > 256 && n <= 384) return norm_forward_as<XT, YT, 192, 2>(a, s);
+    if (n > 1024 && n <= 1536) return norm_forward_as<XT, YT, 768, 2>(a, s);
+  }
   if (n <= 256 * F) return norm_forward_as<XT, YT, 256, F>(a, s);
   if (n <= 256 * 2 * F) return norm_forward_as<XT, YT, 256, 2 * F>(a, s);
   if (n <= 512 * 2 * F) return norm_forward_as<XT, YT, 512, 2 * F>(a, s);
@@ -499,8 +603,8 @@ tbe_status norm_forward_types(const NormArgs& a, hipStream_t s) {
   return norm_launch("norm_forward", norm_forward_wide_kernel<XT, YT>, a.rows, kNormWide, 0x7fffffff, a, s, nullptr);
 }
 
-// 16 elements a lane for x of fp32, 8 where several waves own a row of 16 bits: more waves a row, fewer
-// registers (65536 rows of 4096: 256 lanes 0.41 ms, 512 lanes 0.36 ms).
+// 16 elements a lane for x of fp32; 8 or 16 where several waves own a row of 16 bits (65536 rows of 4096: 512 lanes
+// of one vector 297 us, 256 lanes of two 284).
 template <int XT, int YT>
 tbe_status norm_backward_types(const NormArgs& a, hipStream_t s, int* grid) {
   const int64_t n = (a.width + kNormVec<XT> - 1) / kNormVec<XT>;
@@ -513,13 +617,16 @@ tbe_status norm_backward_types(const NormArgs& a, hipStream_t s, int* grid) {
     if (n <= 512) return norm_backward_as<XT, YT, 256, 2>(a, s, grid);
     if (n <= 1024) return norm_backward_as<XT, YT, 256, 4>(a, s, grid);
     if (n <= 2048) return norm_backward_as<XT, YT, 512, 4>(a, s, grid);
+    if (n <= 3072) return norm_backward_as<XT, YT, 1024, 3>(a, s, grid);
+    // 67 M values, 1024 lanes of 4 vectors or 512 of 8: rows of 16384 167 / 205 us, of 14001 295 / 192
+    if (n <= 4096 && a.width % kNormVec<XT>) return norm_backward_as<XT, YT, 512, 8>(a, s, grid);
     if (n <= 4096) return norm_backward_as<XT, YT, 1024, 4>(a, s, grid);
   } else {
     if (n <= 128) return norm_backward_as<XT, YT, 64, 2>(a, s, grid);
     if (n <= 256) return norm_backward_as<XT, YT, 256, 1>(a, s, grid);
-    if (n <= 512) return norm_backward_as<XT, YT, 512, 1>(a, s, grid);
+    if (n <= 512) return norm_backward_as<XT, YT, 256, 2>(a, s, grid);
     if (n <= 1024) return norm_backward_as<XT, YT, 1024, 1>(a, s, grid);
-    if (n <= 2048) return norm_backward_as<XT, YT, 1024, 2>(a, s, grid);
+    if (n <= 2048) return norm_backward_as<XT, YT, 512, 4>(a, s, grid);
   }
   tbe_status st = TBE_OK;
   if (a.gx) st = norm_launch("norm_backward", norm_backward_wide_kernel<XT, YT>, a.rows, kNormWide, 0x7fffffff, a, s, nullptr);

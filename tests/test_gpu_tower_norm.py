@@ -106,6 +106,26 @@ def test_forward_rows_and_options():
     run_forward(40, 512, F32, F32, shift=3000.0)
 
 
+# rows whose last vector overlaps the one before it, for each number of lanes and vectors
+@pytest.mark.parametrize("xt,yt", [(F32, BF16), (BF16, BF16), (F16, F32), (F32, F32)])
+@pytest.mark.parametrize("width", [3, 5, 9, 100, 361, 1100, 1535, 2100, 3071, 5001, 9001, 12287, 14001])
+def test_ragged_widths(xt, yt, width):
+    flush_print("norm ragged", xt, yt, width)
+    run_forward(37, width, xt, yt, stride=width + 8 - width % 8, seed=width)
+    run_backward(37, width, xt, yt, seed=width)
+
+
+@pytest.mark.parametrize("width", [7, 131, 1001, 2047, 9001])
+def test_ragged_in_place(width):
+    for xt in (F32, BF16):
+        x = rows_of(1100, width, xt, 3)
+        w, b = vector(width, F32, 4, 1.0), vector(width, F32, 5, 0.0)
+        y = torch.empty_like(x)
+        tbe.tbe_layer_norm_forward(x, w, b, 1e-5, y)
+        tbe.tbe_layer_norm_forward(x, w, b, 1e-5, x)
+        assert torch.equal(x, y)
+
+
 def test_no_rows_and_in_place():
     e = torch.empty(0, 64, device="cuda")
     tbe.tbe_layer_norm_forward(e, None, None, 1e-5, e, torch.empty(0, device="cuda"), torch.empty(0, device="cuda"))
