@@ -36,7 +36,8 @@ extern "C" {
  * have different types (fp32 pooled rows into a bf16 tower), and y may be x
  * when they have one type and stride.  mean = sum x / width and
  * rstd = 1 / sqrt(sum (x - mean)^2 / width + eps) are taken in fp32, the
- * squares after the mean is known.  weight and bias [width] of type w_dtype
+ * squares after the mean is known; the mean is corrected by the deviations'
+ * sum, so a row of equal values gives exactly its bias (eps > 0).  weight and bias [width] of type w_dtype
  * may each be NULL (1 and 0).  mean and rstd [rows] fp32 may be NULL where no
  * backward follows.  A row with an infinity or a NaN gives NaN in that row
  * only.  eps >= 0.  1 <= width <= TBE_LAYER_NORM_MAX_WIDTH; rows may be 0.
