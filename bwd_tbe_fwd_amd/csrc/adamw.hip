@@ -154,7 +154,8 @@ __device__ __forceinline__ void pack_v(const float (&v)[kVals], uint32_t e, bool
       const uint32_t u = __float_as_uint(v[4 * i + j] * inverse);
       // to three mantissa bits, ties to even, then the exponent counted from 2^-30 / unit on
       const int k = static_cast<int>(u + ((u >> 20) & 1u) + (0x7ffffu - (776u << 20))) >> 20;
-      uint32_t code = u ? static_cast<uint32_t>(min(max(k, 1), 254)) : 0u;
+      // v itself tells zero: far below its block's largest value (by 2^149), the product is zero too
+      uint32_t code = v[4 * i + j] != 0.0f ? static_cast<uint32_t>(min(max(k, 1), 254)) : 0u;
       if (odd && u >= 0x7f800000u) code = 255u;
       word |= code << (8 * j);
     }
