@@ -134,9 +134,16 @@ __device__ __forceinline__ void open_v(const uint32_t (&c)[2], uint32_t e, float
     }
   }
 }
-// The conversion makes an infinity a NaN.
-__device__ __forceinline__ void pack_m(const float (&m)[kVals], uint32_t e, uint32_t (&c)[2]) {
-  const float inverse = inverse_unit(e) * 128.0f;  // a power of two: the products are exact, below 256
+// The conversion makes an infinity a NaN, and a finite value beyond 448 too.  Such are there only where the scale
+// byte is at its end: they take the largest code.
+__device__ __forceinline__ void pack_m(float (&m)[kVals], uint32_t e, uint32_t (&c)[2]) {
+  const float inverse = inverse_unit(e) * 128.0f;  // a power of two: the products are exact, below 256 with e < 250
+  if (e == 250u) {  // rare
+    constexpr float kMost = 448.0f * 0x1.0p+116f;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i)
+      if (fabsf(m[i]) > kMost && fabsf(m[i]) < __builtin_inff()) m[i] = copysignf(kMost, m[i]);
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     int k = __builtin_amdgcn_cvt_pk_fp8_f32(m[4 * i] * inverse, m[4 * i + 1] * inverse, 0, false);

@@ -124,11 +124,12 @@ tbe_status tbe_grouped_linear_backward_weight(int64_t rows, int32_t experts, int
  * and at most 250.  A first moment is an e4m3 number times 2^(s - 134).  A second
  * moment c is an unsigned number of 5 exponent and 3 mantissa bits: 0 for
  * c = 0, NaN for c = 255, else the fp32 number with bits (c + 776) << 20,
- * times 2^(s - 127): 30 powers of two below the block's largest.  Both round
- * to nearest, ties to even; a second moment above zero never becomes zero, so
- * that no later step divides by eps alone.  An infinity or a NaN becomes a
- * NaN and leaves its block's other values as they are.  Zeroed bytes are zero
- * states.
+ * times 2^(s - 127): 30 powers of two below the block's largest.  Finite
+ * values beyond the largest code's at s = 250, 448 * 2^116 and 3.5 * 2^123,
+ * take that code.  Both round to nearest, ties to even; a second moment
+ * above zero never becomes zero, so that no later step divides by eps alone.
+ * An infinity or a NaN becomes a NaN and leaves its block's other values as
+ * they are.  Zeroed bytes are zero states.
  */
 #define TBE_ADAMW_BLOCK 128
 typedef enum { TBE_STATE_F32 = 0, TBE_STATE_8BIT = 1 } tbe_adamw_state;

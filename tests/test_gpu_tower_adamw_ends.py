@@ -36,3 +36,21 @@ def test_second_moments_of_a_wide_block_stay_above_zero():
     assert (t.v[[0, 1, 2]] > 0).all()
     assert torch.equal(t.dve.cpu(), e) and torch.equal(t.dv.cpu(), code)
     assert (t.dv.cpu()[t.v > 0] > 0).all() and not t.dv.cpu()[t.v == 0].any()
+
+
+def test_finite_moments_beyond_the_codes_range_take_its_ends():
+    """The scale byte stops at 250: larger finite moments take the largest code, and do not become NaN."""
+    g = torch.zeros(3 * BLOCK)
+    g[:8] = torch.tensor([3e38, -3e38, 1e38, -5e37, 2.5e37, 3.7e37, 3.75e37, 1.0])
+    g[BLOCK:BLOCK + 4] = torch.tensor([1.8e19, 1.6e19, 4e18, -1e10])
+    t = stepped(g, 0.0, 0.0)
+    for got, scale, x, second in ((t.dm, t.dme, t.m, False), (t.dv, t.dve, t.v, True)):
+        code, e = pack(torch.where(x.isfinite(), x, 0.0), second)
+        assert torch.equal(scale.cpu(), e)
+        keep = x.isfinite()
+        assert torch.equal(got.cpu()[keep], code[keep])
+    m = torch.empty(3 * BLOCK, device="cuda")
+    v = torch.empty(3 * BLOCK, device="cuda")
+    tbe.tbe_adamw_state_read(plan_of([t]), [m], [v])
+    assert m.isfinite().all() and torch.equal(v.isfinite().cpu(), t.v.isfinite())
+    assert float(m[0]) == 448 * 2.0 ** 116 and float(m[1]) == -448 * 2.0 ** 116 and float(v[BLOCK]) == 3.5 * 2.0 ** 123
