@@ -150,8 +150,9 @@ typedef struct {
 
 /*
  * One step on every tensor of tensors [host, count entries]; tensors must
- * not overlap.  In fp32, each product and sum rounded by itself for the
- * moments (so that their codes are the same on any machine):
+ * not overlap.  In fp32, each operation rounded by itself (so that the moments
+ * and their codes are the same on any machine), but with states of 8 bits the
+ * weight's square root and division are good to one unit in the last place:
  *   m = beta1 * m + (1 - beta1) * g
  *   v = beta2 * v + (1 - beta2) * (g * g)
  *   p = p * (1 - lr * weight_decay)

@@ -1,13 +1,16 @@
-"""AdamW's states of 8 bits at the ends of their range, on the GPU: bit for bit against a quantiser in
-64 bits."""
+"""AdamW's states of 8 bits at the ends of their range, and the roundings of a step with states of 32 bits,
+on the GPU: bit for bit against a quantiser in 64 bits and fp32 operations on the CPU."""
+import math
+
 import pytest
 import torch
 
 import bwd_tbe_fwd_amd as tbe
+from gpu_util import flush_print
 from test_gpu_tower_adamw import BLOCK, Tensor, pack, plan_of
 
 pytestmark = pytest.mark.gpu
-F32 = torch.float32
+F32, BF16 = torch.float32, torch.bfloat16
 
 
 def stepped(g, b1, b2, **kw):
@@ -54,3 +57,30 @@ def test_finite_moments_beyond_the_codes_range_take_its_ends():
     tbe.tbe_adamw_state_read(plan_of([t]), [m], [v])
     assert m.isfinite().all() and torch.equal(v.isfinite().cpu(), t.v.isfinite())
     assert float(m[0]) == 448 * 2.0 ** 116 and float(m[1]) == -448 * 2.0 ** 116 and float(v[BLOCK]) == 3.5 * 2.0 ** 123
+
+
+@pytest.mark.parametrize("p,g", [(F32, F32), (BF16, F32), (BF16, BF16)])
+def test_each_operation_of_a_32_bit_step_is_rounded_by_itself(p, g):
+    """Weights bit for bit against fp32 operations on the CPU, one rounding each (fp32 weights or masters)."""
+    flush_print("adamw rounding", p, g)
+    n, step, lr, b1, b2, eps = 20011, 17, 3e-3, 0.9, 0.99, 1e-8
+    f = lambda x: torch.tensor(x, dtype=torch.float32)  # noqa: E731
+    for decay in (0.0, 0.1):
+        t = Tensor(n, p, g, False, p != F32, decay, 700)
+        p0, m0, v0 = t.p0.clone(), t.m.clone(), t.v.clone()
+        v0[:4000] *= 1e-42  # among them roots of subnormal numbers
+        t.dv[:4000] = v0[:4000].cuda()
+        t.dg[:2000] = 0
+        gr = t.dg.cpu().float()
+        tbe.tbe_adamw_step(plan_of([t]), step, lr, b1, b2, eps)
+        torch.cuda.synchronize()
+        m = m0 * f(b1) + gr * f(1 - b1)
+        v = v0 * f(b2) + gr * gr * f(1 - b2)
+        keep = f(1.0) - f(lr) * f(decay)
+        size, root = f(lr / (1 - b1 ** step)), f(1 / math.sqrt(1 - b2 ** step))
+        # (the root through 64 bits, which rounds to the nearest fp32; torch's fp32 one on the CPU does not always)
+        w = p0 * keep - size * m / (v.double().sqrt().float() * root + f(eps))
+        assert torch.equal(t.dm.cpu(), m) and torch.equal(t.dv.cpu(), v)
+        got = t.dp if t.dw is None else t.dw
+        assert torch.equal(got.cpu(), w)
+        assert torch.equal(t.dp.cpu(), w.to(p))
