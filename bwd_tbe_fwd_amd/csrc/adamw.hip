@@ -477,7 +477,7 @@ extern "C" tbe_status tbe_adamw_state_read(const tbe_adamw_tensor* tensors, int3
     return TBE_ERR_ARG;
   }
   if (out_dtype != TBE_F32 && out_dtype != TBE_BF16) {
-    set_error("adamw state read: values are exact in fp32 and bf16 only (type %d)", out_dtype);
+    set_error("adamw state read: values go to fp32, where they are exact, or to bf16 (type %d)", out_dtype);
     return TBE_ERR_UNSUPPORTED;
   }
   for (int i = 0; i < count; ++i) {

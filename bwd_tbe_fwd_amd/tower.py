@@ -289,7 +289,7 @@ def tbe_adamw_step(tensors: AdamWTensors, step: int, lr: float, beta1: float = 0
 
 def tbe_adamw_state_read(tensors: AdamWTensors, exp_avg_out: Sequence[torch.Tensor],
                          exp_avg_sq_out: Sequence[torch.Tensor], stream=None):
-    """The values of states of 8 bits, into float32 or bfloat16 tensors (both hold them exactly)."""
+    """The values of states of 8 bits, into float32 tensors or bfloat16 ones (exact from 2^-126 on)."""
     n, dev, c = tensors.count, _device(), tensors.c
     if len(exp_avg_out) != n or len(exp_avg_sq_out) != n:
         _refuse(f"{n} tensors need as many outputs of each state")

@@ -172,8 +172,10 @@ tbe_status tbe_adamw_step(const tbe_adamw_tensor* tensors, int32_t count, int64_
 
 /*
  * The values of states of 8 bits: exp_avg_out[i] and exp_avg_sq_out[i]
- * [host arrays of count device pointers, out_dtype fp32 or bf16: both hold
- * them exactly] receive tensor i's numel values.  Every tensor must have
+ * [host arrays of count device pointers, out_dtype fp32 or bf16] receive
+ * tensor i's numel values.  fp32 holds them exactly, bf16 from 2^-126 on;
+ * smaller second moments (of blocks with s below 31) are rounded to bf16's
+ * nearest, and none above zero becomes zero.  Every tensor must have
  * states of 8 bits.
  */
 tbe_status tbe_adamw_state_read(const tbe_adamw_tensor* tensors, int32_t count,

@@ -7,7 +7,7 @@ import torch
 
 import bwd_tbe_fwd_amd as tbe
 from gpu_util import flush_print
-from test_gpu_tower_adamw import BLOCK, Tensor, pack, plan_of
+from test_gpu_tower_adamw import BLOCK, Tensor, opened, pack, plan_of
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -57,6 +57,25 @@ def test_finite_moments_beyond_the_codes_range_take_its_ends():
     tbe.tbe_adamw_state_read(plan_of([t]), [m], [v])
     assert m.isfinite().all() and torch.equal(v.isfinite().cpu(), t.v.isfinite())
     assert float(m[0]) == 448 * 2.0 ** 116 and float(m[1]) == -448 * 2.0 ** 116 and float(v[BLOCK]) == 3.5 * 2.0 ** 123
+
+
+def test_reading_every_code_in_16_bits():
+    """bf16 holds every value from 2^-126 on; smaller second moments are rounded to nearest, above zero all."""
+    code = torch.arange(256, dtype=torch.uint8).repeat(6)
+    e = torch.tensor([24, 24, 25, 25, 26, 26, 27, 27, 40, 40, 250, 250], dtype=torch.uint8)
+    n = code.numel()
+    flat = torch.zeros(n, device="cuda")
+    plan = tbe.AdamWTensors([flat], [flat], [code.cuda()], [code.cuda()], exp_avg_scales=[e.cuda()], exp_avg_sq_scales=[e.cuda()])
+    m, v = (torch.empty(n, dtype=BF16, device="cuda") for _ in range(2))
+    tbe.tbe_adamw_state_read(plan, [m], [v])
+    for got, second in ((m.cpu(), False), (v.cpu(), True)):
+        exp = opened(code, e, second)
+        assert torch.equal(got.isnan(), exp.isnan())
+        ok = ~exp.isnan()
+        assert torch.equal(got[ok], exp[ok].bfloat16())
+        held = ok & (exp.abs() >= 2.0 ** -126)
+        assert torch.equal(got[held].float(), exp[held])
+        assert ((got != 0) == (exp != 0))[ok].all()
 
 
 @pytest.mark.parametrize("p,g", [(F32, F32), (BF16, F32), (BF16, BF16)])
