@@ -45,7 +45,8 @@ struct GroupedArgs {
   void* grad_bias;      // backward by weight; NULL: none
   void* workspace;
   int32_t split;        // backward by weight: rows of a unit, 0: an expert's rows are one
-  int32_t units;        // units at most: partial sums that the workspace holds
+  int32_t units;        // units at most
+  int32_t slots;        // partial sums that the workspace holds
   int32_t tile;         // backward by weight: which of the three, host only
 };
 
@@ -70,6 +71,7 @@ __device__ __forceinline__ RowRange rows_of(const GroupedArgs& a, int e) {
 struct RowTile {
   int expert;
   int64_t row, hi;   // first row, and where its expert's end
+  int singles;       // experts before it that have one tile
 };
 struct RowTiles {
   RowRange r;        // of this lane's expert, and its tiles: how many, and with those of the lanes before
@@ -90,16 +92,20 @@ struct RowTiles {
   // Tile `tile` (>= 0); false past the last one.  counted: count(a, BM, 0) was called, and all experts are
   // in it.
   __device__ __forceinline__ bool find(const GroupedArgs& a, int BM, int tile, bool counted, RowTile& t) {
+    t.singles = 0;
     for (int base = 0; base <= a.experts; base += kWave) {
       const int here = counted ? read_lane(upto, kWave - 1) : count(a, BM, base);
+      const unsigned long long singles = __ballot(n == 1);
       if (tile < here) {
         const int src = __ffsll(static_cast<unsigned long long>(__ballot(upto > tile))) - 1;
         t.expert = base + src;
+        t.singles += __popcll(singles & ((1ull << src) - 1));
         t.row = read_lane64(r.lo + static_cast<int64_t>(tile - (upto - n)) * BM, src);
         t.hi = read_lane64(r.hi, src);
         return true;
       }
       tile -= here;
+      t.singles += __popcll(singles);
     }
     return false;
   }

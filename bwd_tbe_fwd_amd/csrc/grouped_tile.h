@@ -305,7 +305,11 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void g
       row = static_cast<int>(t.row);
       rows = static_cast<int>(min(t.hi - t.row, static_cast<int64_t>(a.split)));
       const RowRange all = rows_of(a, expert);
-      if (all.hi - all.lo > a.split) part = static_cast<float*>(a.workspace) + unit * (io + a.outer);
+      if (all.hi - all.lo > a.split) {
+        const int slot = unit - t.singles;  // units of experts that have several, in order
+        if (slot >= a.slots) return;        // offsets that are not in order: inside the workspace
+        part = static_cast<float*>(a.workspace) + slot * (io + a.outer);
+      }
     } else {
       expert = expert_by_rows(a, unit);
       const RowRange r = rows_of(a, expert);
