@@ -192,8 +192,10 @@ extern "C" size_t tbe_grouped_linear_backward_weight_workspace_bytes(int64_t row
   if (rows < 0 || rows > kMaxRows || experts < 1 || experts > kMaxExperts || inner < 1 || inner > kMaxSide || outer < 1 ||
       outer > kMaxSide)
     return 0;
-  const int64_t split = weight_plan(rows, experts, inner, outer).split;
-  return split ? static_cast<size_t>(weight_slots(rows, experts, split) * slot_bytes(inner, outer)) : 0;
+  // What any plan for up to so many rows may need, the one for these rows or not: a workspace sized for the
+  // largest batch serves every smaller one.  Both terms grow with the rows.
+  const int64_t each = slot_bytes(inner, outer);
+  return static_cast<size_t>(hmin(weight_slots(rows, experts, kLeastSplit), most_partials(rows, inner, outer) / each) * each);
 }
 
 extern "C" tbe_status tbe_grouped_linear_backward_weight(int64_t rows, int32_t experts, int64_t inner, int64_t outer,

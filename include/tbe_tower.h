@@ -102,7 +102,9 @@ tbe_status tbe_grouped_linear_backward_input(int64_t rows, int32_t experts, int6
  * and grad_bias_e [outer] = sum of grad_y_i (NULL: not computed), both
  * overwritten, zero for an expert without rows, in out_dtype.  workspace: at
  * least tbe_grouped_linear_backward_weight_workspace_bytes bytes, 256-byte
- * aligned (may be 0: then workspace may be NULL).
+ * aligned (0 below 512 rows: then workspace may be NULL).  The bytes grow with
+ * the rows, so a workspace for the largest batch serves every smaller one, and
+ * are at most 1 GiB, or an eighth of x and grad_y where that is more.
  */
 size_t tbe_grouped_linear_backward_weight_workspace_bytes(int64_t rows, int32_t experts,
                                                           int64_t inner, int64_t outer);

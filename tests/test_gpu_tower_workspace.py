@@ -41,3 +41,14 @@ def test_shared_rows_next_to_whole_experts(groups, inner, outer, dtype):
     n = tbe.tbe_grouped_linear_backward_weight_workspace_bytes(c.rows, c.E, inner, outer)
     assert n > 0, "sizes whose rows are shared"
     weight_gradient(c, n)
+
+
+def test_one_workspace_for_every_smaller_batch():
+    """Sized for the largest batch, as a training program does."""
+    inner, outer, largest = 520, 264, 20000
+    for experts in (1, 4):
+        n = tbe.tbe_grouped_linear_backward_weight_workspace_bytes(largest, experts, inner, outer)
+        for rows in (largest, 19999, 13000, 8192, 4160, 4032, 1025, 513, 512, 40, 1):
+            groups = [rows] if experts == 1 else [rows // 2, rows // 8, 0, rows - rows // 2 - rows // 8]
+            flush_print("weight gradient", groups)
+            weight_gradient(Case(groups, inner, outer, BF16), n)
