@@ -222,6 +222,13 @@ __device__ __forceinline__ unsigned chiplet_order(unsigned id, unsigned n) {
   return x * q + min(x, r) + id / 8;
 }
 
+// Between a wave's LDS writes and its other lanes' reads of them, and before those places are written again: the LDS
+// serves a wave's instructions in order, so nothing has to wait, but no access may move across.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // A wave's results, MF x NF products, to rows `out` + m * pitch, of type S: through LDS, a few rows at a
 // time, so that each row's bytes leave in whole cache lines.  STREAM: past the caches, where they would
 // take the operands' place (1.07 GB of results of 131072 rows, inner 4096, outer 1024: backward by
@@ -251,6 +258,7 @@ __device__ __forceinline__ void store_tile(S* out, int64_t pitch, int m_left, in
         __builtin_memcpy(p + (LEN > 4 ? g * LEN + 4 * j : 16 * j + 4 * g) * sizeof(S), v.e, 4 * sizeof(S));
       }
     }
+    wave_order();
 #pragma unroll
     for (int k = 0; k < 16 * R * kLanes / kWave; ++k) {
       const int m = k * (kWave / kLanes) + l / kLanes, n = (l % kLanes) * kPer;
@@ -261,6 +269,7 @@ __device__ __forceinline__ void store_tile(S* out, int64_t pitch, int m_left, in
       if (STREAM && on_16 && n_left - n >= kPer) store_vec_stream<S, kPer>(p, v);
       else store_vec_part<S, kPer>(p, n_left - n, v);
     }
+    wave_order();
   }
 }
 
