@@ -414,6 +414,7 @@ using namespace tbe;
 
 extern "C" tbe_status tbe_adamw_step(const tbe_adamw_tensor* tensors, int32_t count, int64_t step, double lr, double beta1,
                                      double beta2, double eps, const double* control, tbe_stream_t stream) {
+  clear_error();
   if (count < 0 || (count > 0 && !tensors)) {
     set_error("adamw: %d tensors at %p", count, static_cast<const void*>(tensors));
     return TBE_ERR_ARG;
@@ -472,6 +473,7 @@ extern "C" tbe_status tbe_adamw_step(const tbe_adamw_tensor* tensors, int32_t co
 
 extern "C" tbe_status tbe_adamw_state_read(const tbe_adamw_tensor* tensors, int32_t count, void* const* exp_avg_out,
                                            void* const* exp_avg_sq_out, int32_t out_dtype, tbe_stream_t stream) {
+  clear_error();
   if (count < 0 || (count > 0 && (!tensors || !exp_avg_out || !exp_avg_sq_out))) {
     set_error("adamw state read: %d tensors, a NULL array", count);
     return TBE_ERR_ARG;

@@ -20,6 +20,8 @@ namespace tbe {
 // ---------------------------------------------------------------------------
 static thread_local char g_error[512] = "";
 
+void clear_error() { g_error[0] = 0; }
+
 void set_error(const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);

@@ -155,6 +155,7 @@ extern "C" tbe_status tbe_grouped_linear_forward(int64_t rows, int32_t experts, 
                                                  int64_t x_stride, const void* weight, const void* bias, int32_t dtype,
                                                  const void* offsets, int32_t offset_type, void* y, int64_t y_stride,
                                                  int32_t out_dtype, tbe_stream_t stream) {
+  clear_error();
   tbe_status st = check_sizes(rows, experts, inner, outer, dtype, out_dtype, offsets, offset_type);
   if (st == TBE_OK) st = check_matrix("x", x, dtype, rows, inner, x_stride);
   if (st == TBE_OK) st = check_matrix("weight", weight, dtype, 1, inner, inner);
@@ -174,6 +175,7 @@ extern "C" tbe_status tbe_grouped_linear_backward_input(int64_t rows, int32_t ex
                                                         int32_t dtype, const void* offsets, int32_t offset_type,
                                                         void* grad_x, int64_t grad_x_stride, int32_t out_dtype,
                                                         tbe_stream_t stream) {
+  clear_error();
   tbe_status st = check_sizes(rows, experts, inner, outer, dtype, out_dtype, offsets, offset_type);
   if (st == TBE_OK) st = check_matrix("grad_y", grad_y, dtype, rows, outer, grad_y_stride);
   if (st == TBE_OK) st = check_matrix("weight", weight, dtype, 1, inner, inner);
@@ -204,6 +206,7 @@ extern "C" tbe_status tbe_grouped_linear_backward_weight(int64_t rows, int32_t e
                                                          int32_t offset_type, void* grad_weight, void* grad_bias,
                                                          int32_t out_dtype, void* workspace, size_t workspace_bytes,
                                                          tbe_stream_t stream) {
+  clear_error();
   tbe_status st = check_sizes(rows, experts, inner, outer, dtype, out_dtype, offsets, offset_type);
   if (st == TBE_OK) st = check_matrix("x", x, dtype, rows, inner, x_stride);
   if (st == TBE_OK) st = check_matrix("grad_y", grad_y, dtype, rows, outer, grad_y_stride);

@@ -99,6 +99,7 @@ extern "C" tbe_status tbe_layer_norm_forward(int64_t rows, int64_t width, const 
                                              const void* weight, const void* bias, int32_t w_dtype, float eps, void* y,
                                              int64_t y_stride, int32_t y_dtype, float* mean, float* rstd,
                                              tbe_stream_t stream) {
+  clear_error();
   tbe_status st = check_sizes(rows, width);
   if (st == TBE_OK) st = check_rows("x", x, x_stride, x_dtype, rows, width);
   if (st == TBE_OK) st = check_rows("y", y, y_stride, y_dtype, rows, width);
@@ -133,6 +134,7 @@ extern "C" tbe_status tbe_layer_norm_backward(int64_t rows, int64_t width, const
                                               const float* rstd, const void* weight, int32_t w_dtype, void* grad_x,
                                               int64_t grad_x_stride, void* grad_weight, void* grad_bias, void* workspace,
                                               size_t workspace_bytes, tbe_stream_t stream) {
+  clear_error();
   tbe_status st = check_sizes(rows, width);
   if (st == TBE_OK) st = check_rows("x", x, x_stride, x_dtype, rows, width);
   if (st == TBE_OK) st = check_rows("grad_y", grad_y, grad_y_stride, y_dtype, rows, width);

@@ -14,6 +14,7 @@ namespace tbe {
 // errors and kernel timing
 // ---------------------------------------------------------------------------
 void set_error(const char* fmt, ...);
+void clear_error();  // at the start of an entry point
 tbe_status check_launch(const char* what);
 
 // Records a pair of events around a launch when the kernel is the one
