@@ -242,6 +242,7 @@ class AdamWTensors:
                  exp_avg_scales: Optional[Sequence[Optional[torch.Tensor]]] = None,
                  exp_avg_sq_scales: Optional[Sequence[Optional[torch.Tensor]]] = None):
         n, dev = len(params), _device()
+        self.device = dev
         none = [None] * n
         decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
         self.tensors = [list(x) if x is not None else none for x in
@@ -276,11 +277,17 @@ class AdamWTensors:
                 TBE_STATE_8BIT if eight else TBE_STATE_F32)
 
 
+def _same_device(tensors: AdamWTensors, dev: int):
+    if tensors.device != dev:
+        _refuse(f"the tensors are on GPU {tensors.device}, the current one is {dev}")
+
+
 def tbe_adamw_step(tensors: AdamWTensors, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999,
                    eps: float = 1e-8, control: Optional[torch.Tensor] = None, stream=None):
     """One AdamW step on every tensor.  control (float64, on the GPU): step, lr factor, gradient
     factor, skip; its step takes the place of `step`."""
     dev = _device()
+    _same_device(tensors, dev)
     if control is not None:
         _whole("control", control, dev, (TBE_ADAMW_CONTROL,), torch.float64)
     st = lib().tbe_adamw_step(tensors.c, tensors.count, step, lr, beta1, beta2, eps, _at(control), _current(stream, dev))
@@ -291,6 +298,7 @@ def tbe_adamw_state_read(tensors: AdamWTensors, exp_avg_out: Sequence[torch.Tens
                          exp_avg_sq_out: Sequence[torch.Tensor], stream=None):
     """The values of states of 8 bits, into float32 tensors or bfloat16 ones (exact from 2^-126 on)."""
     n, dev, c = tensors.count, _device(), tensors.c
+    _same_device(tensors, dev)
     if len(exp_avg_out) != n or len(exp_avg_sq_out) != n:
         _refuse(f"{n} tensors need as many outputs of each state")
     dtype = exp_avg_out[0].dtype if n else torch.float32

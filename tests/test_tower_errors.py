@@ -1,7 +1,10 @@
 """The error text of the tower's entry points, and what the binding refuses before a call.  No GPU needed."""
 import ctypes
 
+import pytest
+
 import bwd_tbe_fwd_amd as tbe
+from bwd_tbe_fwd_amd import tower
 
 P = ctypes.c_void_p
 A = P(4096)
@@ -21,3 +24,16 @@ def test_a_call_that_succeeds_leaves_no_error_text():
         assert L.tbe_last_error() != b""
         assert call() == 0
         assert L.tbe_last_error() == b""
+
+
+def test_steps_are_taken_on_the_tensors_gpu(monkeypatch):
+    """A plan made on one GPU is refused where another one is current: its kernels would run there."""
+    monkeypatch.setattr(tower, "_device", lambda: 0)
+    monkeypatch.setattr(tower, "_current", lambda stream, dev: None)
+    plan = tbe.AdamWTensors([], [], [], [])
+    tbe.tbe_adamw_step(plan, 1, 1e-3)
+    tbe.tbe_adamw_state_read(plan, [], [])
+    monkeypatch.setattr(tower, "_device", lambda: 1)
+    for call in (lambda: tbe.tbe_adamw_step(plan, 1, 1e-3), lambda: tbe.tbe_adamw_state_read(plan, [], [])):
+        with pytest.raises(tbe.TbeError, match="GPU 0"):
+            call()
