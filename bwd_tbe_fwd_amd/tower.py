@@ -233,7 +233,8 @@ def tbe_grouped_linear_backward_weight(x: torch.Tensor, grad_y: torch.Tensor, of
 class AdamWTensors:
     """The tensors of a step, as an array of tbe_adamw_tensor on the host (the tensors are kept alive
     here).  States are float32, or uint8 codes with uint8 scales of ceil(numel / TBE_ADAMW_BLOCK)
-    bytes; gradients are read from the same buffers at every step."""
+    bytes.  A step reads the gradients from the buffers given here; a program whose gradients are new
+    tensors at every step hands them over with set_gradients before it."""
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                  exp_avg: Sequence[torch.Tensor], exp_avg_sq: Sequence[torch.Tensor],
@@ -265,16 +266,33 @@ class AdamWTensors:
                     if eight and "scale" in name:
                         _refuse(f"tensor {i}: states of 8 bits need scales")
                     continue
-                if t.get_device() != dev:
-                    _off_gpu(f"tensor {i}: {name}", t)
-                if not t.is_contiguous() or t.numel() != size or (dt is not None and t.dtype != dt):
-                    _refuse(f"tensor {i}: {name} is {t.dtype} of {t.numel()} with strides {tuple(t.stride())}: "
-                            f"contiguous {'' if dt is None else dt} of {size} is needed")
+                if t.get_device() != dev or not t.is_contiguous() or t.numel() != size or (dt is not None and t.dtype != dt):
+                    self._refuse_tensor(i, name, t, size, dt)
             self.c[i] = tbe_adamw_tensor(
                 p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), None if w is None else w.data_ptr(),
                 ms.data_ptr() if eight else None, vs.data_ptr() if eight else None, numel, decay[i],
                 _dtype(f"tensor {i}: param", p), _dtype(f"tensor {i}: gradient", g),
                 TBE_STATE_8BIT if eight else TBE_STATE_F32)
+
+    def _refuse_tensor(self, i, name, t, size, dtype):
+        if t.get_device() != self.device:
+            _off_gpu(f"tensor {i}: {name}", t)
+        _refuse(f"tensor {i}: {name} is {t.dtype} of {t.numel()} with strides {tuple(t.stride())}: "
+                f"contiguous {'' if dtype is None else dtype} of {size} is needed")
+
+    def set_gradients(self, grads: Sequence[torch.Tensor]):
+        """Takes these gradients in place of the ones before, all or none of them."""
+        grads = list(grads)
+        if len(grads) != self.count:
+            _refuse(f"{self.count} params need as many gradients")
+        types = []
+        for i, (g, numel) in enumerate(zip(grads, self.numels)):
+            if g.get_device() != self.device or not g.is_contiguous() or g.numel() != numel:
+                self._refuse_tensor(i, "gradient", g, numel, None)
+            types.append(_dtype(f"tensor {i}: gradient", g))
+        for c, g, dtype in zip(self.c, grads, types):
+            c.grad, c.grad_dtype = g.data_ptr(), dtype
+        self.tensors[1] = grads
 
 
 def _same_device(tensors: AdamWTensors, dev: int):
