@@ -14,10 +14,10 @@ tbe_status launch_tile(const GroupedArgs& a, hipStream_t s) {
   const char* what = OP == kForward ? "grouped_forward" : OP == kBackwardInput ? "grouped_input" : "grouped_weight";
   const int n = OP == kForward ? a.outer : a.inner;
   const int n_tiles = (n + BN - 1) / BN;
-  const int64_t units = OP != kBackwardWeight ? row_tiles_bound(a, BM) : a.split ? a.units : a.experts;
+  const int64_t units = OP != kBackwardWeight ? row_tiles_bound(a.rows, a.experts, BM) : a.split ? a.units : a.experts;
   // rows: a multiple of 8, for the chiplets' shares
   const int64_t groups = OP == kBackwardWeight ? units * ((a.outer + BM - 1) / BM) * n_tiles : (units * n_tiles + 7) / 8 * 8;
-  if (groups * kThreads >= (int64_t{1} << 32)) {
+  if (!launch_takes(groups, kThreads)) {
     set_error("grouped linear: %lld tiles are more than a launch takes", static_cast<long long>(groups));
     return TBE_ERR_UNSUPPORTED;
   }
@@ -38,13 +38,15 @@ inline bool chunked(const GroupedArgs& a, int op) {
   return whole(a.gy, gs, a.outer) && whole(a.x, xs, a.inner);
 }
 
-// The tile of least expected time.  (The weight gradient's comes with its plan.)
+// The tile of least expected time among those that a launch takes.  (The weight gradient's comes with its plan.)
 inline int row_tile(const GroupedArgs& a, const TileCost (&tiles)[3], int64_t n, int64_t k) {
   int tile = 0;
   double best = 0.0;
   for (int t = 0; t < 3; ++t) {
     const TileCost& c = tiles[t];
-    const double us = tiles_us(c, row_tiles_expected(a.rows, a.experts, c.bm) * static_cast<double>((n + c.bn - 1) / c.bn),
+    const int64_t n_tiles = (n + c.bn - 1) / c.bn;
+    if (t > 0 && !launch_takes(row_tiles_bound(a.rows, a.experts, c.bm) * n_tiles + 7, c.threads)) continue;
+    const double us = tiles_us(c, row_tiles_expected(a.rows, a.experts, c.bm) * static_cast<double>(n_tiles),
                                static_cast<double>((k + 63) / 64 * 64), static_cast<double>((k + 63) / 64 * 64));
     if (t == 0 || us < best) {
       best = us;

@@ -129,8 +129,10 @@ __device__ __forceinline__ int expert_by_rows(const GroupedArgs& a, int k) {
   return __ffsll(static_cast<unsigned long long>(__ballot(l < a.experts && rank == k))) - 1;
 }
 
-// Row tiles at most: a partly filled one for every expert and the rows of no expert.
-inline int64_t row_tiles_bound(const GroupedArgs& a, int BM) { return a.rows / BM + a.experts + 1; }
+// Row tiles at most: a partly filled one for every expert that has rows and for the rows of no expert.
+inline int64_t row_tiles_bound(int64_t rows, int64_t experts, int64_t bm) { return rows / bm + hmin(experts, rows) + 1; }
+// A launch has fewer than 2^32 threads.
+inline bool launch_takes(int64_t groups, int threads) { return groups * threads < (int64_t{1} << 32); }
 
 // ---------------------------------------------------------------------------
 // the tile, on the host
@@ -145,20 +147,20 @@ inline double rounds_of(double tiles, double slots) {
 // time and one for each 64 of k, `alone` where few of the slots are taken and `full` where all are (us,
 // fitted to times with the tile as given).
 struct TileCost {
-  int bm, bn;
+  int bm, bn, threads;
   double slots, fixed, alone, full;
 };
 // Operands straight to LDS, forward, the three tiles in turn: 65536 rows, 16 experts, 1024 x 1024: 137 / 143 /
 // 213 us; 8192 rows, 8 experts, 2048 x 2048: 91 / 84 / 119; 4096 rows, 4 experts, 1024 x 1024: 26 / 21 /
 // 26; 400 rows, 8 experts, 1024 x 512: 24 / 12 / 10.
-constexpr TileCost kDirectTiles[3] = {{256, 256, 256, 6.0, 1.37, 1.37}, {128, 128, 512, 4.0, 0.78, 0.78}, {64, 64, 1024, 3.0, 0.61, 0.61}};
+constexpr TileCost kDirectTiles[3] = {{256, 256, 512, 256, 6.0, 1.37, 1.37}, {128, 128, 256, 512, 4.0, 0.78, 0.78}, {64, 64, 256, 1024, 3.0, 0.61, 0.61}};
 // Operands through registers: 60000 rows, 8 experts, 1777 x 1201, forward: 334 / 419 / 746 us; 3000 rows, 4
 // experts, 2047 x 901, by input: 37 / 30 / 40; 1000 rows, 1 expert, 2047 x 901, by input: 34 / 23 / 18.
-constexpr TileCost kRegisterTiles[3] = {{256, 256, 256, 6.0, 1.3, 2.05}, {256, 128, 256, 6.0, 1.0, 1.3}, {64, 64, 1024, 3.0, 0.55, 1.35}};
+constexpr TileCost kRegisterTiles[3] = {{256, 256, 512, 256, 6.0, 1.3, 2.05}, {256, 128, 512, 256, 6.0, 1.0, 1.3}, {64, 64, 256, 1024, 3.0, 0.55, 1.35}};
 // The weight gradient, both ways; times of the direct loads are at its plan (grouped_linear.hip).  Through
 // registers: 60000 rows, 8 experts, 1777 x 1201: 365 / 465 / 862 us; 3000 rows, 4 experts, 2047 x 901: 39 /
 // 29 / 44; 5003 rows, 13 experts, 1000 x 515: 33 / 33 / 30.
-constexpr TileCost kWeightTiles[3] = {{256, 256, 256, 6.0, 1.5, 1.85}, {128, 128, 512, 4.0, 0.75, 1.36}, {64, 64, 1024, 3.0, 0.6, 0.95}};
+constexpr TileCost kWeightTiles[3] = {{256, 256, 512, 256, 6.0, 1.5, 1.85}, {128, 128, 256, 512, 4.0, 0.75, 1.36}, {64, 64, 256, 1024, 3.0, 0.6, 0.95}};
 // Tiles of k each, those of the last round of `last`.
 inline double tiles_us(const TileCost& c, double tiles, double k, double last) {
   const double r = rounds_of(tiles, c.slots);

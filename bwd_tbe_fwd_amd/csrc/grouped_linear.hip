@@ -70,13 +70,15 @@ WeightPlan weight_plan(int64_t rows, int64_t experts, int64_t inner, int64_t out
   const double used = static_cast<double>(hmax(1, hmin(experts, rows))), average = static_cast<double>(rows) / used;
   for (int t = 0; t < 3; ++t) {
     const TileCost& c = kWeightTiles[t];
-    const double each = static_cast<double>((outer + c.bm - 1) / c.bm) * static_cast<double>((inner + c.bn - 1) / c.bn);
+    const int64_t tiles = ((outer + c.bm - 1) / c.bm) * ((inner + c.bn - 1) / c.bn);
+    const double each = static_cast<double>(tiles);
     double us = tiles_us(c, used * each, average, experts > 1 ? 2.0 * average : average);
-    if (best < 0.0 || us < best) {
+    if (best < 0.0 || (us < best && launch_takes(experts * tiles, c.threads))) {
       best = us;
       p = WeightPlan{t, 0};
     }
     for (int64_t split = kLeastSplit; split < rows && split <= (1 << 20); split *= 2) {
+      if (!launch_takes(row_tiles_bound(rows, experts, split) * tiles, c.threads)) continue;
       if (weight_slots(rows, experts, split) > most_partials(rows, inner, outer) / slot_bytes(inner, outer)) continue;
       const double units = row_tiles_expected(rows, experts, static_cast<int>(split)), k = static_cast<double>(split);
       const double bytes = 4.0 * static_cast<double>(rows / split) * static_cast<double>(inner + 1) * static_cast<double>(outer);
@@ -226,7 +228,7 @@ extern "C" tbe_status tbe_grouped_linear_backward_weight(int64_t rows, int32_t e
   a.out = grad_weight; a.out_dt = out_dtype; a.grad_bias = grad_bias; a.workspace = workspace;
   const WeightPlan plan = weight_plan(rows, experts, inner, outer);
   a.split = plan.split;
-  a.units = plan.split ? static_cast<int>(row_tiles_bound(a, plan.split)) : 0;
+  a.units = plan.split ? static_cast<int>(row_tiles_bound(rows, experts, plan.split)) : 0;
   a.slots = plan.split ? static_cast<int>(weight_slots(rows, experts, plan.split)) : 0;
   a.tile = plan.tile;
   return launch<kBackwardWeight>(a, dtype, static_cast<hipStream_t>(stream));

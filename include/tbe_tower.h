@@ -40,7 +40,8 @@ extern "C" {
  * sum, so a row of equal values gives exactly its bias (eps > 0).  weight and bias [width] of type w_dtype
  * may each be NULL (1 and 0).  mean and rstd [rows] fp32 may be NULL where no
  * backward follows.  A row with an infinity or a NaN gives NaN in that row
- * only.  eps >= 0.  1 <= width <= TBE_LAYER_NORM_MAX_WIDTH; rows may be 0.
+ * only.  eps >= 0.  1 <= width <= TBE_LAYER_NORM_MAX_WIDTH; rows may be 0 and
+ * at most 2^31 - 1, at most 2^31 elements apart.
  */
 #define TBE_LAYER_NORM_MAX_WIDTH (1 << 24)
 tbe_status tbe_layer_norm_forward(int64_t rows, int64_t width, const void* x, int64_t x_stride,
@@ -80,7 +81,10 @@ tbe_status tbe_layer_norm_backward(int64_t rows, int64_t width, const void* x, i
  * inside the buffers.  x, weight, bias and grad_y have one type, dtype: fp16
  * or bf16; y and the gradients are of out_dtype: dtype or fp32.  Products are
  * summed in fp32 and rounded once.  E, inner, outer >= 1; rows may be 0 and
- * at most 2^29; inner and outer at most 2^20, E at most 65535.
+ * at most 2^29; inner and outer at most 2^20, E at most 65535, rows at most
+ * 2^31 elements apart.  Sizes whose 256 x 256 tiles (by weight: of every
+ * expert, elsewhere of those that have rows) are 2^23 and more are refused
+ * with TBE_ERR_UNSUPPORTED.
  */
 tbe_status tbe_grouped_linear_forward(int64_t rows, int32_t experts, int64_t inner, int64_t outer,
                                       const void* x, int64_t x_stride, const void* weight,
