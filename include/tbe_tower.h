@@ -36,12 +36,14 @@ extern "C" {
  * have different types (fp32 pooled rows into a bf16 tower), and y may be x
  * when they have one type and stride.  mean = sum x / width and
  * rstd = 1 / sqrt(sum (x - mean)^2 / width + eps) are taken in fp32, the
- * squares after the mean is known; the mean is corrected by the deviations'
- * sum, so a row of equal values gives exactly its bias (eps > 0).  weight and bias [width] of type w_dtype
- * may each be NULL (1 and 0).  mean and rstd [rows] fp32 may be NULL where no
- * backward follows.  A row with an infinity or a NaN gives NaN in that row
- * only.  eps >= 0.  1 <= width <= TBE_LAYER_NORM_MAX_WIDTH; rows may be 0 and
- * at most 2^31 - 1, at most 2^31 elements apart.
+ * squares after the mean is known; a mean far from zero is corrected by the
+ * deviations' sum, so a row of equal values gives exactly its bias (eps > 0,
+ * up to 2^22 wide; beyond, to a unit of the mean's last place).  weight and
+ * bias [width] of type w_dtype may each be NULL (1 and 0).  mean and rstd
+ * [rows] fp32 may be NULL where no backward follows.  A row with an infinity
+ * or a NaN gives NaN in that row only.  eps >= 0.  1 <= width <=
+ * TBE_LAYER_NORM_MAX_WIDTH; rows may be 0 and at most 2^31 - 1, at most 2^31
+ * elements apart.
  */
 #define TBE_LAYER_NORM_MAX_WIDTH (1 << 24)
 tbe_status tbe_layer_norm_forward(int64_t rows, int64_t width, const void* x, int64_t x_stride,

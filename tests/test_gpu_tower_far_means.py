@@ -39,6 +39,17 @@ def test_constant_rows_give_the_shift(dtype, width):
         assert (rstd.double() >= (1 - 4 * U) / (eps + 264 * U * c * c).sqrt()).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("width", [131072, 1 << 20, 1 << 22])
+def test_very_wide_constant_rows_give_the_shift(dtype, width):
+    flush_print("norm of wide constant rows", dtype, width)
+    x = torch.tensor([0.1, 1000.1, -12345.6], device="cuda").to(dtype)[:, None].expand(-1, width).contiguous()
+    b = vector(width, F32, 2, 0.0)
+    y = torch.empty(x.shape, device="cuda")
+    tbe.tbe_layer_norm_forward(x, None, b, 1e-12, y)
+    assert torch.equal(y, b.expand_as(y))
+
+
 @pytest.mark.parametrize("yt", [F32, BF16])
 @pytest.mark.parametrize("width", WIDTHS)
 def test_means_far_above_the_deviations(yt, width):
