@@ -25,40 +25,40 @@ ITYPE = {32: torch.int32, 64: torch.int64}
 def listed():
     return [
         # one request's items at serving time: latency alone
-        {"name": "lookup forward, one request", "op": "lookup_forward", "ids": 64, "items": 131072, "width": 1024,
+        {"name": "lookup forward: one request", "op": "lookup_forward", "ids": 64, "items": 131072, "width": 1024,
          "table": "bf16", "y": "bf16", "itype": 32, "pad": 0.0, "skew": 1.0},
         # all positions of a training batch from one of the benchmark's tables of 2M rows, into the tower's type
-        {"name": "lookup forward, training batch", "op": "lookup_forward", "ids": 1048576, "items": 2000000, "width": 128,
+        {"name": "lookup forward: training batch", "op": "lookup_forward", "ids": 1048576, "items": 2000000, "width": 128,
          "table": "f16", "y": "bf16", "itype": 64, "pad": 0.1, "skew": 0.91},
         # an odd width in fp32: rows start at any alignment
-        {"name": "lookup forward, odd width", "op": "lookup_forward", "ids": 20011, "items": 50021, "width": 1001,
+        {"name": "lookup forward: odd width", "op": "lookup_forward", "ids": 20011, "items": 50021, "width": 1001,
          "table": "f32", "y": "f32", "itype": 64, "pad": 0.05, "skew": 1.0},
         # the dense gradient of a vocabulary's table: a few ids have a good part of the positions
-        {"name": "lookup backward, training batch", "op": "lookup_backward", "ids": 131072, "items": 131072, "width": 1024,
+        {"name": "lookup backward: training batch", "op": "lookup_backward", "ids": 131072, "items": 131072, "width": 1024,
          "table": "bf16", "y": "bf16", "itype": 64, "pad": 0.1, "skew": 1.0, "add": False},
         # tied weights: the positions' gradient on top of the loss's, in the 16 bits in which that one came
-        {"name": "lookup backward, tied weights", "op": "lookup_backward", "ids": 1048576, "items": 2000000, "width": 128,
+        {"name": "lookup backward: tied weights", "op": "lookup_backward", "ids": 1048576, "items": 2000000, "width": 128,
          "table": "f16", "y": "f16", "itype": 64, "pad": 0.1, "skew": 0.91, "add": True},
         # a small batch of odd sizes, gradients kept in fp32
-        {"name": "lookup backward, odd sizes", "op": "lookup_backward", "ids": 517, "items": 3001, "width": 515,
+        {"name": "lookup backward: odd sizes", "op": "lookup_backward", "ids": 517, "items": 3001, "width": 515,
          "table": "f32", "y": "bf16", "itype": 32, "pad": 0.0, "skew": 1.0, "add": False},
         # the scores of one request's continuations: the weights' bytes decide
-        {"name": "loss forward, one request", "op": "loss_forward", "rows": 8, "items": 131072, "width": 1024, "type": "bf16",
+        {"name": "loss forward: one request", "op": "loss_forward", "rows": 8, "items": 131072, "width": 1024, "type": "bf16",
          "bias": False, "itype": 64, "pad": 0.0, "skew": 1.0},
         # a training batch over a vocabulary
-        {"name": "loss forward, training batch", "op": "loss_forward", "rows": 8192, "items": 131072, "width": 1024,
+        {"name": "loss forward: training batch", "op": "loss_forward", "rows": 8192, "items": 131072, "width": 1024,
          "type": "bf16", "bias": False, "itype": 64, "pad": 0.1, "skew": 1.0},
         # retrieval: two million items of width 128, popularity corrected by a bias
-        {"name": "loss forward, items of a table", "op": "loss_forward", "rows": 2048, "items": 2000000, "width": 128,
+        {"name": "loss forward: items of a table", "op": "loss_forward", "rows": 2048, "items": 2000000, "width": 128,
          "type": "f16", "bias": True, "itype": 64, "pad": 0.0, "skew": 0.91},
         # the training batch's backward: gradients of the rows and of the vocabulary's weights
-        {"name": "loss backward, training batch", "op": "loss_backward", "rows": 8192, "items": 131072, "width": 1024,
+        {"name": "loss backward: training batch", "op": "loss_backward", "rows": 8192, "items": 131072, "width": 1024,
          "type": "bf16", "bias": False, "itype": 64, "pad": 0.1, "skew": 1.0, "weights": False},
         # retrieval's backward, a weight for each sample
-        {"name": "loss backward, items of a table", "op": "loss_backward", "rows": 2048, "items": 500000, "width": 128,
+        {"name": "loss backward: items of a table", "op": "loss_backward", "rows": 2048, "items": 500000, "width": 128,
          "type": "f16", "bias": True, "itype": 64, "pad": 0.0, "skew": 0.91, "weights": True},
         # odd sizes: rows that start at any alignment, a bias, many positions without a target
-        {"name": "loss backward, odd sizes", "op": "loss_backward", "rows": 517, "items": 10007, "width": 515, "type": "bf16",
+        {"name": "loss backward: odd sizes", "op": "loss_backward", "rows": 517, "items": 10007, "width": 515, "type": "bf16",
          "bias": True, "itype": 32, "pad": 0.4, "skew": 1.0, "weights": True},
     ]
 
