@@ -160,7 +160,6 @@ struct Carver {
 };
 constexpr int kDefaultSortBlocks = 4096;
 constexpr int kClsBlocks = 4096;  // classification workgroups at most (the scan takes up to 4096)
-constexpr int kMaxSortBlocks = 4096;
 }  // namespace
 
 // sort / RLE block segments and classification blocks for n keys
@@ -182,6 +181,24 @@ static void sort_geometry(int64_t n, const Config& cfg, int T, bool all_keys, in
   *seg = per * kRadixTile;
   *nblocks = static_cast<int>((n1 + *seg - 1) / *seg);
   *cls_blocks = static_cast<int>(hmax(1, hmin(kClsBlocks, (n1 + kBlock - 1) / kBlock)));
+}
+
+void sort_segments(int64_t n, int64_t* seg, int* nblocks) {
+  int cls_blocks;
+  sort_geometry(n, resolve_config(nullptr), 1, true, seg, nblocks, &cls_blocks);
+}
+
+RadixPlan radix_plan(int bits_total) {
+  RadixPlan R = {};
+  R.passes = (bits_total + kRadixMaxBits - 1) / kRadixMaxBits;
+  int shift = 0;
+  for (int p = 0; p < R.passes; ++p) {
+    const int bits = bits_total / R.passes + (p < bits_total % R.passes ? 1 : 0);
+    R.shift[p] = shift;
+    R.bits[p] = bits;
+    shift += bits;
+  }
+  return R;
 }
 
 BwdLayout bwd_layout(const tbe_tables* tb, int64_t N, int weighted, const Config& cfg) {
@@ -288,14 +305,7 @@ BwdLayout bwd_layout(const tbe_tables* tb, int64_t N, int weighted, const Config
   while (kb < 32 && (maxkey >> kb) != 0) ++kb;
   L.key_bits = kb;
   auto plan = [](int bits_total, int by_table, RadixPlan& R) {
-    R.passes = (bits_total + kRadixMaxBits - 1) / kRadixMaxBits;
-    int shift = 0;
-    for (int p = 0; p < R.passes; ++p) {
-      const int bits = bits_total / R.passes + (p < bits_total % R.passes ? 1 : 0);
-      R.shift[p] = shift;
-      R.bits[p] = bits;
-      shift += bits;
-    }
+    R = radix_plan(bits_total);
     R.by_table = by_table;
   };
   plan(kb, 0, L.sample_radix);

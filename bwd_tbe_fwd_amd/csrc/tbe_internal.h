@@ -178,6 +178,18 @@ tbe_status launch_transpose(const tbe_tables* tb, const IndexArgs& ia, int weigh
                             char* ws, const BwdLayout& L, const Config& cfg, int skip_table,
                             int invalid_as_row0, int dense, int* final_buf, hipStream_t s);
 
+// Stable sort of N pairs (key, payload) by the key's R bits; not by table.  keys[0] and pay[0] hold the input, keys[*final_buf]
+// and pay[*final_buf] (known on the host at once) the result, *n_sorted (device) how many keys differ from `drop`: the others
+// are left out.  nblocks segments of seg keys (a multiple of kRadixTile) cover N, at most 4096; hist: kRadixDigits *
+// (nblocks + 1) words.
+tbe_status launch_radix_sort(int64_t N, int64_t seg, int nblocks, const RadixPlan& R, uint32_t* const (&keys)[2],
+                             uint32_t* const (&pay)[2], uint32_t* hist, int32_t* n_sorted, uint32_t drop, int* final_buf,
+                             hipStream_t s);
+// Segments of whole tiles for n keys, kMaxSortBlocks at most, and the passes for keys of so many bits.
+constexpr int kMaxSortBlocks = 4096;
+void sort_segments(int64_t n, int64_t* seg, int* nblocks);
+RadixPlan radix_plan(int bits_total);
+
 // histogram backward of the small table (counts x gradient on MFMA, then the optimizer)
 constexpr int kHistBwdBlocks = 512;  // max partials (workgroups) of the histogram backward
 // dense hot rows of large tables (counts x gradient on MFMA).  With dense_presort, before the

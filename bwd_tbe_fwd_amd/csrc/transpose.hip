@@ -963,21 +963,15 @@ struct RouteNames {
 constexpr RouteNames kMainNames = {"radix_upsweep", "radix_scan", "radix_downsweep", "rle", "classify"};
 constexpr RouteNames kQuietNames = {"-", "-", "-", "-", "-"};
 
-// R.by_table: tstart holds the first pass's table starts (table_starts_kernel) and room for
-// the next pass's
-tbe_status sort_route(const tbe_tables* tb, char* ws, const SortPlan& P, const RadixPlan& R, int32_t* tstart,
-                      const int32_t* n_in, uint32_t drop, int threshold, int chunk, const ShortLists& lists,
-                      const RouteNames& nm, int* final_buf, hipStream_t s) {
-  const int64_t N = P.N;
-  int32_t* counters = reinterpret_cast<int32_t*>(ws + P.counters);
-  uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + P.keys[0]), reinterpret_cast<uint32_t*>(ws + P.keys[1])};
-  uint32_t* pay[2] = {reinterpret_cast<uint32_t*>(ws + P.pay[0]), reinterpret_cast<uint32_t*>(ws + P.pay[1])};
-  uint32_t* hist = reinterpret_cast<uint32_t*>(ws + P.sort_hist);
-  uint32_t* tot = hist + static_cast<int64_t>(kRadixDigits) * P.nblocks;
-  int32_t* n_sorted = counters + kSorted;
+// The radix passes alone: sorts keys[0] with pay[0] into keys[*final_buf], pay[*final_buf]; *n_sorted (device) receives
+// the keys kept.  R.by_table: tstart holds the first pass's table starts (table_starts_kernel) and room for
+// the next pass's.
+tbe_status radix_passes(int64_t N, int64_t seg, int nblocks, const RadixPlan& R, uint32_t* const (&keys)[2],
+                        uint32_t* const (&pay)[2], uint32_t* hist, int32_t* n_sorted, const int32_t* n_in, uint32_t drop,
+                        int T, const int64_t* meta, int32_t* tstart, const RouteNames& nm, int* final_buf, hipStream_t s) {
+  uint32_t* tot = hist + static_cast<int64_t>(kRadixDigits) * nblocks;
   tbe_status st;
   int cur = 0;
-  const int T = tb->T;
   for (int pass = 0; pass < R.passes; ++pass) {
     const int ndig = 1 << R.bits[pass];
     const int32_t* n_p = pass == 0 ? n_in : n_sorted;
@@ -988,24 +982,24 @@ tbe_status sort_route(const tbe_tables* tb, char* ws, const SortPlan& P, const R
     {
       ProfScope ps(nm.up, s);
       if (R.by_table)
-        hipLaunchKernelGGL(radix_upsweep<true>, dim3(P.nblocks), dim3(kBlock), 0, s, keys[cur], N, n_p, P.seg,
-                           R.shift[pass], R.bits[pass], d, hist, P.nblocks, ts_in, tb->meta, T);
+        hipLaunchKernelGGL(radix_upsweep<true>, dim3(nblocks), dim3(kBlock), 0, s, keys[cur], N, n_p, seg,
+                           R.shift[pass], R.bits[pass], d, hist, nblocks, ts_in, meta, T);
       else
-        hipLaunchKernelGGL(radix_upsweep<false>, dim3(P.nblocks), dim3(kBlock), 0, s, keys[cur], N, n_p, P.seg,
-                           R.shift[pass], R.bits[pass], d, hist, P.nblocks, ts_in, tb->meta, T);
+        hipLaunchKernelGGL(radix_upsweep<false>, dim3(nblocks), dim3(kBlock), 0, s, keys[cur], N, n_p, seg,
+                           R.shift[pass], R.bits[pass], d, hist, nblocks, ts_in, meta, T);
     }
     if ((st = check_launch("radix_upsweep"))) return st;
     {
       ProfScope ps(nm.scan, s);
-      hipLaunchKernelGGL(radix_scan, dim3(ndig), dim3(kBlock), 0, s, hist, P.nblocks, tot);
+      hipLaunchKernelGGL(radix_scan, dim3(ndig), dim3(kBlock), 0, s, hist, nblocks, tot);
     }
     if ((st = check_launch("radix_scan"))) return st;
     {
       ProfScope ps(nm.down, s);
 #define TBE_DOWN(BT, DG)                                                                             \
-  hipLaunchKernelGGL((radix_downsweep<BT, DG>), dim3(P.nblocks), dim3(kBlock), 0, s, keys[cur], pay[cur], \
-                     keys[cur ^ 1], pay[cur ^ 1], N, n_p, P.seg, R.shift[pass], R.bits[pass], d, hist, tot, \
-                     P.nblocks, pass == 0 ? n_sorted : nullptr, ts_in, ts_out, tb->meta, T)
+  hipLaunchKernelGGL((radix_downsweep<BT, DG>), dim3(nblocks), dim3(kBlock), 0, s, keys[cur], pay[cur], \
+                     keys[cur ^ 1], pay[cur ^ 1], N, n_p, seg, R.shift[pass], R.bits[pass], d, hist, tot, \
+                     nblocks, pass == 0 ? n_sorted : nullptr, ts_in, ts_out, meta, T)
       if (R.by_table) {
         if (ndig <= 128) TBE_DOWN(true, 128);
         else TBE_DOWN(true, kRadixDigits);
@@ -1019,6 +1013,21 @@ tbe_status sort_route(const tbe_tables* tb, char* ws, const SortPlan& P, const R
     cur ^= 1;
   }
   *final_buf = cur;
+  return TBE_OK;
+}
+
+tbe_status sort_route(const tbe_tables* tb, char* ws, const SortPlan& P, const RadixPlan& R, int32_t* tstart,
+                      const int32_t* n_in, uint32_t drop, int threshold, int chunk, const ShortLists& lists,
+                      const RouteNames& nm, int* final_buf, hipStream_t s) {
+  const int64_t N = P.N;
+  int32_t* counters = reinterpret_cast<int32_t*>(ws + P.counters);
+  uint32_t* const keys[2] = {reinterpret_cast<uint32_t*>(ws + P.keys[0]), reinterpret_cast<uint32_t*>(ws + P.keys[1])};
+  uint32_t* const pay[2] = {reinterpret_cast<uint32_t*>(ws + P.pay[0]), reinterpret_cast<uint32_t*>(ws + P.pay[1])};
+  int32_t* n_sorted = counters + kSorted;
+  tbe_status st = radix_passes(N, P.seg, P.nblocks, R, keys, pay, reinterpret_cast<uint32_t*>(ws + P.sort_hist), n_sorted,
+                               n_in, drop, tb->T, tb->meta, tstart, nm, final_buf, s);
+  if (st) return st;
+  const int cur = *final_buf;
   uint32_t* run_key = reinterpret_cast<uint32_t*>(ws + P.run_key);
   uint32_t* run_start = reinterpret_cast<uint32_t*>(ws + P.run_start);
   uint32_t* seg_cnt = reinterpret_cast<uint32_t*>(ws + P.seg_cnt);
@@ -1059,6 +1068,12 @@ tbe_status launch_fill_i32(int32_t* p, int32_t v, int64_t n, hipStream_t s) {
   ProfScope ps("init", s);
   hipLaunchKernelGGL(fill_i32_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, p, v, n);
   return check_launch("init");
+}
+
+tbe_status launch_radix_sort(int64_t N, int64_t seg, int nblocks, const RadixPlan& R, uint32_t* const (&keys)[2],
+                             uint32_t* const (&pay)[2], uint32_t* hist, int32_t* n_sorted, uint32_t drop, int* final_buf,
+                             hipStream_t s) {
+  return radix_passes(N, seg, nblocks, R, keys, pay, hist, n_sorted, nullptr, drop, 1, nullptr, nullptr, kMainNames, final_buf, s);
 }
 
 tbe_status launch_transpose(const tbe_tables* tb, const IndexArgs& ia, int weighted, char* ws,
