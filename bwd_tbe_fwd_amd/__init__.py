@@ -2,7 +2,7 @@
 
 Argument marshalling only: every function here turns torch tensors into device
 pointers and calls the C entry point of the same name declared in
-``include/tbe.h`` or ``include/tbe_tower.h`` (tower.py); all computation happens in the library's HIP kernels.
+``include/tbe.h``, ``include/tbe_tower.h`` (tower.py) or ``include/tbe_items.h`` (items.py); all computation happens in the library's HIP kernels.
 PyTorch provides device memory and the current stream.  There is no fallback:
 if the library is missing or a call fails, an exception is raised.
 """
@@ -110,6 +110,12 @@ _SIGS = {
     "tbe_adamw_step": ([_P, _I32, _I64, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                         ctypes.c_double, _P, _P], ctypes.c_int),
     "tbe_adamw_state_read": ([_P, _I32, _P, _P, _I32, _P], ctypes.c_int),
+    # the item table's two ends (include/tbe_items.h)
+    "tbe_lookup_forward": ([_I64, _I64, _I64, _P, _I64, _I32, _P, _I32, ctypes.c_float, _P, _I64, _I32, _P],
+                           ctypes.c_int),
+    "tbe_lookup_backward_workspace_bytes": ([_I64, _I64, _I64], ctypes.c_size_t),
+    "tbe_lookup_backward": ([_I64, _I64, _I64, _P, _I32, _P, _I64, _I32, ctypes.c_float, _P, _I64, _I32, _I32,
+                             _P, ctypes.c_size_t, _P], ctypes.c_int),
     # measurement hooks (include/tbe_measure.h)
     "tbe_profile_select": ([ctypes.c_char_p], ctypes.c_int),
     "tbe_profile_read": ([_P, _P], ctypes.c_int),
@@ -344,3 +350,5 @@ from .tower import (AdamWTensors, TBE_ADAMW_BLOCK, TBE_ADAMW_CONTROL, TBE_LAYER_
                     tbe_grouped_linear_backward_weight_workspace_bytes, tbe_grouped_linear_forward,
                     tbe_layer_norm_backward, tbe_layer_norm_backward_workspace_bytes,
                     tbe_layer_norm_forward)
+from .items import (TBE_ITEMS_MAX_WIDTH, tbe_lookup_backward, tbe_lookup_backward_workspace_bytes,  # noqa: E402,F401
+                    tbe_lookup_forward)

@@ -1,0 +1,546 @@
+// Scaled lookup of single rows and the table's dense gradient.  Declarations and the meaning of every argument are in
+// include/tbe_items.h.
+//
+//   forward    y_i = s W[id_i]
+//   backward   dW_v = s sum_{i: id_i = v} dy_i
+//
+// Both are bound by memory: the forward by n rows read and written, the backward by n rows read and the table's rows
+// written (or, added to a gradient that is there, the touched rows read and written).
+//
+// The backward sorts the positions by id, stably, and walks the sorted positions once.  Overwriting, it walks the merged
+// sequence of positions and of the rows' ends (row v's end follows its last position), so that one pass writes the sums and
+// the zeros between them; adding, the positions alone.  That sequence is cut into shares of equal length, whatever the
+// ids' popularity; a share finds its start by a search of d = i + key_i.  A row that a cut would split within its last 64
+// positions stays with the share before, so most rows are summed and rounded where they are read; of the others each share
+// leaves its sum in the workspace, and the share in which the row ends has them joined, in order.
+#include "items.h"
+
+#include "tower_device.h"
+
+namespace tbe {
+namespace {
+
+constexpr int kVec = 8;        // columns of a lane
+constexpr int kFlight = 4;     // forward: rows of a group of lanes whose loads are under way together
+constexpr int kWalk = 8;       // backward: the same
+constexpr int kKeep = 64;      // positions of a row at most that a share takes over from the next one
+constexpr int kRankMost = 4096;  // ids that are sorted by counting, in one launch
+
+template <int DT>
+struct RowVec {
+  Vec<typename Fmt<DT>::S, kVec> v;
+  // the columns [0, left) at p
+  __device__ __forceinline__ void load(const typename Fmt<DT>::S* p, int left) { load_vec_part<typename Fmt<DT>::S, kVec>(p, left, v); }
+  __device__ __forceinline__ float at(int e) const { return Fmt<DT>::to_f(v.e[e]); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) v.e[e] = 0;
+  }
+};
+template <int DT>
+__device__ __forceinline__ void store_row(typename Fmt<DT>::S* p, int left, const float (&x)[kVec], bool stream) {
+  Vec<typename Fmt<DT>::S, kVec> v;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) v.e[e] = tower_from_f<DT>(x[e]);
+  if (stream && left >= kVec) store_vec_stream<typename Fmt<DT>::S, kVec>(p, v);
+  else store_vec_part<typename Fmt<DT>::S, kVec>(p, left, v);
+}
+
+// A launch's columns: blockIdx.y takes `cols` of them (a multiple of kVec), a group of G lanes a row of these.
+struct Columns {
+  int64_t width;
+  int cols;
+};
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+struct LookupArgs {
+  int64_t n, items;
+  const void* table;
+  int64_t table_stride;
+  const void* ids;
+  int32_t id64;
+  float scale;
+  void* y;
+  int64_t y_stride;
+  int32_t stream;  // y's rows start on 16 bytes
+  Columns c;
+};
+__device__ __forceinline__ int64_t id_at(const void* ids, int id64, int64_t i) {
+  return id64 ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
+}
+
+// A group of G lanes takes kFlight rows, a workgroup consecutive ones.
+template <int WT, int YT, int G>
+__global__ __launch_bounds__(kBlock) void lookup_forward_kernel(LookupArgs a) {
+  using S = typename Fmt<WT>::S;
+  constexpr int kGroups = kBlock / G;
+  const int g = threadIdx.x / G, l = threadIdx.x % G;
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * a.c.cols + l * kVec;
+  const int left = l * kVec < a.c.cols ? static_cast<int>(min(a.c.width - c, static_cast<int64_t>(kVec))) : 0;
+  if (left <= 0) return;
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kGroups * kFlight) + g; i0 < a.n; i0 += static_cast<int64_t>(gridDim.x) * (kGroups * kFlight)) {
+    int64_t id[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int64_t i = i0 + u * kGroups;
+      id[u] = i < a.n ? id_at(a.ids, a.id64, i) : -1;
+    }
+    RowVec<WT> r[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      if (static_cast<uint64_t>(id[u]) < static_cast<uint64_t>(a.items))
+        r[u].load(static_cast<const S*>(a.table) + id[u] * a.table_stride + c, left);
+      else
+        r[u].zero();
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int64_t i = i0 + u * kGroups;
+      if (i >= a.n) break;
+      const bool there = static_cast<uint64_t>(id[u]) < static_cast<uint64_t>(a.items);
+      float x[kVec];
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) x[e] = there ? r[u].at(e) * a.scale : 0.0f;  // 0, whatever the scale
+      store_row<YT>(static_cast<typename Fmt<YT>::S*>(a.y) + i * a.y_stride + c, left, x, a.stream);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// backward: positions by id
+// ---------------------------------------------------------------------------
+// Keys of all ids (items: outside the table) and their positions, for the radix sort.
+__global__ __launch_bounds__(kBlock) void lookup_keys_kernel(const void* ids, int id64, int64_t n, int64_t items,
+                                                             uint32_t* __restrict__ keys, uint32_t* __restrict__ pay) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+  if (i >= n) return;
+  const int64_t id = id_at(ids, id64, i);
+  keys[i] = static_cast<uint32_t>(static_cast<uint64_t>(id) < static_cast<uint64_t>(items) ? id : items);
+  pay[i] = static_cast<uint32_t>(i);
+}
+
+// Up to kRankMost ids: an id's place is the number of smaller ones and of equal ones before it.  A workgroup places 64
+// ids, each of its 4 waves counts a quarter of all of them.  One launch of a few microseconds, where the radix sort takes
+// ten launches.  (512 ids.)
+__global__ __launch_bounds__(kBlock) void lookup_rank_kernel(const void* ids, int id64, int n, int64_t items,
+                                                             uint32_t* __restrict__ keys, uint32_t* __restrict__ pay,
+                                                             int32_t* __restrict__ n_sorted) {
+  __shared__ __align__(16) uint32_t s_key[kRankMost];
+  __shared__ int s_rank[kWavesPerBlock][kWave];
+  const int n4 = (n + 15) / 16 * 16;  // a whole number of fours for each wave
+  int valid = 0;
+  for (int i = threadIdx.x; i < n4; i += kBlock) {
+    const int64_t id = i < n ? id_at(ids, id64, i) : -1;
+    const bool in = static_cast<uint64_t>(id) < static_cast<uint64_t>(items);
+    s_key[i] = i < n ? static_cast<uint32_t>(in ? id : items) : ~0u;  // behind all others
+    valid += in ? 1 : 0;
+  }
+  __syncthreads();
+  const int w = threadIdx.x / kWave, l = lane_id();
+  const int mine = blockIdx.x * kWave + l;
+  const uint32_t k = mine < n ? s_key[mine] : ~0u;
+  int rank = 0;
+  const int part = n4 / kWavesPerBlock;
+  for (int j = w * part; j < (w + 1) * part; j += 4) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(s_key + j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) rank += v[e] < k || (v[e] == k && j + e < mine) ? 1 : 0;
+  }
+  s_rank[w][l] = rank;
+  __syncthreads();
+  if (w == 0 && mine < n) {
+    rank = s_rank[0][l] + s_rank[1][l] + s_rank[2][l] + s_rank[3][l];
+    keys[rank] = k;
+    pay[rank] = static_cast<uint32_t>(mine);
+  }
+  if (blockIdx.x) return;
+  __syncthreads();
+  for (int d = 1; d < kWave; d <<= 1) valid += __shfl_xor(valid, d);
+  if (l == 0) s_rank[0][w] = valid;
+  __syncthreads();
+  if (threadIdx.x == 0) *n_sorted = s_rank[0][0] + s_rank[0][1] + s_rank[0][2] + s_rank[0][3];
+}
+
+// ---------------------------------------------------------------------------
+// backward: sums
+// ---------------------------------------------------------------------------
+struct LookupGradArgs {
+  int64_t items;
+  const uint32_t* keys;      // sorted
+  const uint32_t* pay;       // their positions
+  const int32_t* n_sorted;
+  const void* gy;
+  int64_t gy_stride;
+  float scale;
+  void* grad;
+  int64_t grad_stride;
+  int32_t add;
+  int32_t stream;            // overwriting, grad's rows start on 16 bytes
+  int32_t share;             // length of a share
+  int32_t shares;
+  float* part;               // [shares][2][width]: the sum of a row that began before the share and ends in it, of one that
+                             // goes on behind it
+  Columns c;
+};
+
+// Lanes of this lane's group of G whose predicate holds, as bits 0 .. G - 1.
+template <int G>
+__device__ __forceinline__ uint64_t group_ballot(bool p) {
+  const uint64_t b = __ballot(p);
+  if constexpr (G == kWave) return b;
+  else return (b >> (lane_id() / G * G)) & ((uint64_t{1} << G) - 1);
+}
+
+// First i of [lo, hi] with value(i) >= d for i < hi (value does not decrease): a group of lanes probes G places at a time.
+template <int G, typename F>
+__device__ __forceinline__ int64_t first_at_least(int64_t lo, int64_t hi, int64_t d, F value) {
+  const int l = lane_id() % G;
+  while (lo < hi) {
+    const int64_t step = (hi - lo + G) / (G + 1);  // >= 1
+    const int64_t i = lo + (l + 1) * step - 1;     // probes at lo + step - 1, lo + 2 step - 1, ...
+    const bool below = i < hi && value(i) < d;
+    const int n = __popcll(group_ballot<G>(below));  // the first n probes are below
+    const int64_t from = lo + n * step;              // at most hi: probe n - 1 lies before hi
+    if (n < G) hi = min(hi, from + step - 1);
+    lo = from;
+  }
+  return lo;
+}
+
+// A cut of the merged sequence: positions before i and the ends of the rows before row lie before it.
+struct Cut {
+  int64_t i, row;
+  bool split;  // row has positions on both sides
+};
+template <int G>
+__device__ __forceinline__ Cut cut_at(const LookupGradArgs& a, int64_t n, int64_t d) {
+  Cut c;
+  const int64_t all = a.add ? n : n + a.items;
+  if (d >= all) return Cut{n, a.items, false};
+  if (a.add) {
+    c.i = d;
+    c.row = a.keys[d];
+  } else {
+    c.i = first_at_least<G>(max(int64_t{0}, d - a.items), min(n, d), d, [&](int64_t i) { return i + static_cast<int64_t>(a.keys[i]); });
+    c.row = d - c.i;
+  }
+  c.split = false;
+  if (c.i > 0 && a.keys[c.i - 1] == c.row) {
+    // the row has begun: what is left of it, up to kKeep positions
+    int more = 0;
+    const int l = lane_id() % G;
+#pragma unroll
+    for (int k = 0; k < kKeep; k += G) {
+      const int64_t i = c.i + k + l;
+      more += __popcll(group_ballot<G>(i < n && a.keys[i] == c.row));
+    }
+    if (more == kKeep) {
+      c.split = true;
+    } else {
+      c.i += more;
+      c.row += 1;
+    }
+  }
+  return c;
+}
+
+template <int YT, int WT, int G>
+__global__ __launch_bounds__(kBlock) void lookup_sum_kernel(LookupGradArgs a) {
+  using SY = typename Fmt<YT>::S;
+  using SW = typename Fmt<WT>::S;
+  constexpr int kGroups = kBlock / G;
+  const int l = threadIdx.x % G;
+  const int64_t share = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / G;
+  const int64_t n = *a.n_sorted;
+  const int64_t d = share * a.share;
+  // all lanes take part in the searches
+  const Cut from = cut_at<G>(a, n, d), to = cut_at<G>(a, n, share + 1 < a.shares ? d + a.share : n + a.items);
+  if (share >= a.shares) return;
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * a.c.cols + l * kVec;
+  const int left = l * kVec < a.c.cols ? static_cast<int>(min(a.c.width - c, static_cast<int64_t>(kVec))) : 0;
+  if (left <= 0) return;
+  float acc[kVec];
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) acc[e] = 0.0f;
+  bool open = from.split;  // the row began in an earlier share
+  auto keep = [&](int which) {
+    Vec<float, kVec> v;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) v.e[e] = acc[e];
+    store_vec_part<float, kVec>(a.part + (share * 2 + which) * a.c.width + c, left, v);
+  };
+  auto finish = [&](int64_t row) {  // the row's sum is whole, or its last part
+    if (open) {
+      keep(0);
+      open = false;
+    } else {
+      SW* p = static_cast<SW*>(a.grad) + row * a.grad_stride + c;
+      float x[kVec];
+      if (a.add) {
+        RowVec<WT> old;
+        old.load(p, left);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) x[e] = old.at(e) + acc[e] * a.scale;
+      } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) x[e] = acc[e] * a.scale;
+      }
+      store_row<WT>(p, left, x, a.stream);
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) acc[e] = 0.0f;
+  };
+  auto zeros = [&](int64_t row, int64_t end) {
+    const float x[kVec] = {};
+    for (; row < end; ++row) store_row<WT>(static_cast<SW*>(a.grad) + row * a.grad_stride + c, left, x, a.stream);
+  };
+  int64_t row = from.row;      // the row whose end comes next
+  bool begun = from.split;     // it has positions already
+  uint32_t at[kWalk];          // the next positions, loaded ahead of their rows
+#pragma unroll
+  for (int u = 0; u < kWalk; ++u) at[u] = from.i + u < to.i ? a.pay[from.i + u] : 0;
+  for (int64_t i = from.i; i < to.i; i += kWalk) {
+    RowVec<YT> r[kWalk];
+    uint32_t key[kWalk];
+#pragma unroll
+    for (int u = 0; u < kWalk; ++u) {
+      if (i + u < to.i) {
+        r[u].load(static_cast<const SY*>(a.gy) + at[u] * a.gy_stride + c, left);
+        key[u] = a.keys[i + u];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kWalk; ++u) at[u] = i + kWalk + u < to.i ? a.pay[i + kWalk + u] : 0;
+#pragma unroll
+    for (int u = 0; u < kWalk; ++u) {
+      if (i + u < to.i) {
+        const int64_t k = key[u];
+        if (k != row) {
+          if (begun) {
+            finish(row);
+            ++row;
+          }
+          if (!a.add) zeros(row, k);
+          row = k;
+        }
+        begun = true;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] += r[u].at(e);
+      }
+    }
+  }
+  if (begun) {
+    if (to.split && to.row == row) {
+      keep(1);
+      return;
+    }
+    finish(row);
+    ++row;
+  }
+  if (!a.add) zeros(row, to.row);
+}
+
+// Joins the sums of a row that several shares have parts of: a workgroup for each share (blockIdx.x, from 1 on) that
+// finds one ending in it, 256 columns each.  16 waves add the shares' sums, each wave a contiguous part of them, then the
+// waves' sums are added in order.
+template <int WT>
+__global__ __launch_bounds__(1024) void lookup_join_kernel(LookupGradArgs a) {
+  using SW = typename Fmt<WT>::S;
+  constexpr int kWaves = 16, kCols = 4 * kWave;
+  __shared__ __align__(16) float s_sum[kWaves][kCols];
+  const int64_t share = blockIdx.x + 1;
+  const int64_t n = *a.n_sorted, d = share * a.share;
+  const Cut from = cut_at<kWave>(a, n, d);
+  if (!from.split) return;
+  const Cut to = cut_at<kWave>(a, n, share + 1 < a.shares ? d + a.share : n + a.items);
+  if (to.split && to.row == from.row) return;  // the row goes on
+  // the share that has the row's first position: its place in the sequence is i + row, or i; a share whose end was moved
+  // behind that place does not split the row, so the row is in that share
+  const int64_t i0 = first_at_least<kWave>(0, n, from.row, [&](int64_t i) { return static_cast<int64_t>(a.keys[i]); });
+  const int64_t first = (a.add ? i0 : i0 + from.row) / a.share;
+  const int w = threadIdx.x / kWave, l = lane_id();
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + 4 * l;
+  const int left = static_cast<int>(min(max(a.c.width - c, int64_t{0}), int64_t{4}));
+  // parts: the shares' from `first` to the one before, then this one's
+  const int64_t parts = share - first + 1, each = (parts + kWaves - 1) / kWaves;
+  f32x4 sum = {0, 0, 0, 0};
+  if (left > 0) {
+#pragma unroll 8
+    for (int64_t k = w * each; k < min(parts, (w + 1) * each); ++k) {
+      Vec<float, 4> v;
+      load_vec_part<float, 4>(a.part + ((first + k) * 2 + (k + 1 < parts ? 1 : 0)) * a.c.width + c, left, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += v.e[e];
+    }
+  }
+  *reinterpret_cast<f32x4*>(&s_sum[w][4 * l]) = sum;
+  __syncthreads();
+  if (w > 0 || left <= 0) return;
+  for (int k = 1; k < kWaves; ++k) sum += *reinterpret_cast<const f32x4*>(&s_sum[k][4 * l]);
+  SW* p = static_cast<SW*>(a.grad) + from.row * a.grad_stride + c;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (e < left) p[e] = tower_from_f<WT>(a.add ? Fmt<WT>::to_f(p[e]) + sum[e] * a.scale : sum[e] * a.scale);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+// Groups of 8 to 64 lanes, the fewest that hold a row; wider rows in equal parts.
+struct Split {
+  int lanes, parts;
+  Columns c;
+};
+Split split_of(int64_t width) {
+  Split s;
+  s.lanes = width <= 8 * kVec ? 8 : width <= 16 * kVec ? 16 : width <= 32 * kVec ? 32 : 64;
+  s.parts = static_cast<int>((width + kWave * kVec - 1) / (kWave * kVec));
+  const int64_t vecs = (width + kVec - 1) / kVec;
+  s.c = Columns{width, static_cast<int>((vecs + s.parts - 1) / s.parts) * kVec};
+  return s;
+}
+
+template <typename F>
+tbe_status by_type(int dt, F f) {
+  if (dt == TBE_F32) return f(std::integral_constant<int, 0>{});
+  if (dt == TBE_F16) return f(std::integral_constant<int, 1>{});
+  return f(std::integral_constant<int, 2>{});
+}
+template <typename F>
+tbe_status by_lanes(int lanes, F f) {
+  if (lanes == 8) return f(std::integral_constant<int, 8>{});
+  if (lanes == 16) return f(std::integral_constant<int, 16>{});
+  if (lanes == 32) return f(std::integral_constant<int, 32>{});
+  return f(std::integral_constant<int, 64>{});
+}
+
+// Shares: of 128, shorter ones where that leaves fewer than 4096, longer ones from 65536 shares on.  And how many there are
+// at most for any sequence up to this length: a workspace serves every smaller batch.
+constexpr int kLeastShare = 16, kShare = 128, kFewShares = 4096, kMostShares = 65536;
+int share_of(int64_t all) {
+  return static_cast<int>(hmax((all + kMostShares - 1) / kMostShares, hmin(kShare, hmax(kLeastShare, all / kFewShares))));
+}
+int64_t shares_bound(int64_t all) {
+  const int64_t least = (all + kLeastShare - 1) / kLeastShare, few = kFewShares + kFewShares / kLeastShare;
+  return hmin(least, hmax(few, hmin(kMostShares, (all + kShare - 1) / kShare)));
+}
+
+// The workspace: sorted pairs twice, the sort's counts, the shares' sums.
+struct LookupPlan {
+  int64_t seg, shares;
+  int nblocks, share;
+  size_t keys[2], pay[2], hist, n_sorted, part, total;
+};
+LookupPlan lookup_plan(int64_t n, int64_t items, int64_t width, bool add) {
+  LookupPlan p = {};
+  sort_segments(n, &p.seg, &p.nblocks);
+  const int64_t all = add ? n : n + items, tiles = (n + kRadixTile - 1) / kRadixTile;
+  p.share = share_of(all);
+  p.shares = (all + p.share - 1) / p.share;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  for (int i = 0; i < 2; ++i) {
+    p.keys[i] = take(n * 4);
+    p.pay[i] = take(n * 4);
+  }
+  p.hist = take(static_cast<size_t>(kRadixDigits) * (hmin(tiles, kMaxSortBlocks) + 1) * 4);
+  p.n_sorted = take(4);
+  p.part = take(static_cast<size_t>(shares_bound(n + items)) * 2 * width * 4);
+  p.total = at;
+  return p;
+}
+
+}  // namespace
+
+tbe_status launch_lookup_forward(int64_t n, int64_t items, int64_t width, const void* table, int64_t table_stride, int table_dtype,
+                                 const void* ids, int id_type, float scale, void* y, int64_t y_stride, int y_dtype, hipStream_t s) {
+  const Split sp = split_of(width);
+  LookupArgs a = {};
+  a.n = n; a.items = items; a.table = table; a.table_stride = table_stride; a.ids = ids; a.id64 = id_type == TBE_I64;
+  a.scale = scale; a.y = y; a.y_stride = y_stride; a.c = sp.c;
+  a.stream = rows_on_16(y, y_stride, y_dtype);
+  return by_type(table_dtype, [&](auto wt) {
+    return by_type(y_dtype, [&](auto yt) {
+      return by_lanes(sp.lanes, [&](auto g) {
+        constexpr int G = decltype(g)::value;
+        // a launch has fewer than 2^32 threads
+        const int64_t groups = hmin((n + kBlock / G * kFlight - 1) / (kBlock / G * kFlight), int64_t{1} << 23);
+        ProfScope ps("lookup_forward", s);
+        hipLaunchKernelGGL((lookup_forward_kernel<decltype(wt)::value, decltype(yt)::value, G>),
+                           dim3(static_cast<unsigned>(groups), sp.parts), dim3(kBlock), 0, s, a);
+        return check_launch("lookup_forward");
+      });
+    });
+  });
+}
+
+size_t lookup_backward_workspace(int64_t n, int64_t items, int64_t width) {
+  return lookup_plan(n, items, width, false).total;
+}
+
+tbe_status launch_lookup_backward(int64_t n, int64_t items, int64_t width, const void* ids, int id_type, const void* gy,
+                                  int64_t gy_stride, int y_dtype, float scale, void* grad, int64_t grad_stride, int table_dtype,
+                                  bool add, void* workspace, hipStream_t s) {
+  const LookupPlan p = lookup_plan(n, items, width, add);
+  char* ws = static_cast<char*>(workspace);
+  uint32_t* const keys[2] = {reinterpret_cast<uint32_t*>(ws + p.keys[0]), reinterpret_cast<uint32_t*>(ws + p.keys[1])};
+  uint32_t* const pay[2] = {reinterpret_cast<uint32_t*>(ws + p.pay[0]), reinterpret_cast<uint32_t*>(ws + p.pay[1])};
+  int32_t* n_sorted = reinterpret_cast<int32_t*>(ws + p.n_sorted);
+  const int id64 = id_type == TBE_I64;
+  int sorted = 0;
+  tbe_status st;
+  if (n == 0) {
+    if ((st = launch_fill_i32(n_sorted, 0, 1, s))) return st;
+  } else if (n <= kRankMost) {
+    ProfScope ps("lookup_rank", s);
+    hipLaunchKernelGGL(lookup_rank_kernel, dim3(static_cast<unsigned>((n + kWave - 1) / kWave)), dim3(kBlock), 0, s, ids, id64,
+                       static_cast<int>(n), items, keys[0], pay[0], n_sorted);
+    if ((st = check_launch("lookup_rank"))) return st;
+  } else {
+    {
+      ProfScope ps("lookup_keys", s);
+      hipLaunchKernelGGL(lookup_keys_kernel, dim3(static_cast<unsigned>((n + kBlock - 1) / kBlock)), dim3(kBlock), 0, s, ids, id64,
+                         n, items, keys[0], pay[0]);
+      if ((st = check_launch("lookup_keys"))) return st;
+    }
+    int bits = 1;  // of the largest id, items - 1: what is outside is left out before its digits count
+    while (bits < 31 && ((items - 1) >> bits) != 0) ++bits;
+    if ((st = launch_radix_sort(n, p.seg, p.nblocks, radix_plan(bits), keys, pay, reinterpret_cast<uint32_t*>(ws + p.hist), n_sorted,
+                                static_cast<uint32_t>(items), &sorted, s)))
+      return st;
+  }
+  const Split sp = split_of(width);
+  LookupGradArgs a = {};
+  a.items = items; a.keys = keys[sorted]; a.pay = pay[sorted]; a.n_sorted = n_sorted; a.gy = gy; a.gy_stride = gy_stride;
+  a.scale = scale; a.grad = grad; a.grad_stride = grad_stride; a.add = add;
+  a.stream = !add && rows_on_16(grad, grad_stride, table_dtype);
+  a.share = p.share; a.shares = static_cast<int32_t>(p.shares); a.part = reinterpret_cast<float*>(ws + p.part); a.c = sp.c;
+  st = by_type(y_dtype, [&](auto yt) {
+    return by_type(table_dtype, [&](auto wt) {
+      return by_lanes(sp.lanes, [&](auto g) {
+        constexpr int G = decltype(g)::value;
+        ProfScope ps("lookup_sum", s);
+        hipLaunchKernelGGL((lookup_sum_kernel<decltype(yt)::value, decltype(wt)::value, G>),
+                           dim3(static_cast<unsigned>((p.shares + kBlock / G - 1) / (kBlock / G)), sp.parts), dim3(kBlock), 0, s, a);
+        return check_launch("lookup_sum");
+      });
+    });
+  });
+  // a row has more than kKeep positions on the far side of a cut that splits it
+  if (st != TBE_OK || p.shares < 2 || n <= kKeep) return st;
+  return by_type(table_dtype, [&](auto wt) {
+    ProfScope ps("lookup_join", s);
+    hipLaunchKernelGGL((lookup_join_kernel<decltype(wt)::value>),
+                       dim3(static_cast<unsigned>(p.shares - 1), static_cast<unsigned>((width + 4 * kWave - 1) / (4 * kWave))), dim3(1024), 0, s, a);
+    return check_launch("lookup_join");
+  });
+}
+
+}  // namespace tbe

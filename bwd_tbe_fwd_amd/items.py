@@ -1,0 +1,65 @@
+"""The two ends of a model that reads and predicts the rows of one table (``include/tbe_items.h``): scaled
+lookup of single rows with the table's dense gradient.
+
+Argument marshalling as in tower.py: torch tensors in, the C entry point of the same name called on the
+current stream, TbeError where it refuses.  What the C interface cannot see, a tensor's shape, strides,
+type and device, is checked here.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import _I_DTYPE, _check, lib
+from .tower import _at, _bytes, _current, _device, _dtype, _off_gpu, _refuse, _rows
+
+TBE_ITEMS_MAX_WIDTH = 1 << 20
+
+
+def _ids(name: str, t: torch.Tensor, dev: int, n: Optional[int] = None) -> int:
+    """The type of a contiguous vector of ids."""
+    if t.get_device() != dev:
+        _off_gpu(name, t)
+    it = _I_DTYPE.get(t.dtype)
+    if it is None:
+        _refuse(f"{name} are {t.dtype}: int32 or int64 are supported")
+    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        _refuse(f"{name} have shape {tuple(t.shape)} and strides {tuple(t.stride())}: contiguous "
+                f"{'(n,)' if n is None else (n,)} is needed")
+    return it
+
+
+# ---------------------------------------------------------------------------
+# lookup
+# ---------------------------------------------------------------------------
+def tbe_lookup_forward(table: torch.Tensor, ids: torch.Tensor, scale: float, y: torch.Tensor, stream=None):
+    """y[i] = scale * table[ids[i]]; zero for an id outside the table."""
+    dev = _device()
+    ts = _rows("table", table, dev)
+    items, width = table.shape
+    it = _ids("ids", ids, dev)
+    n = ids.shape[0]
+    ys = _rows("y", y, dev, (n, width))
+    st = lib().tbe_lookup_forward(n, items, width, table.data_ptr(), ts, _dtype("table", table), ids.data_ptr(), it, scale,
+                                  y.data_ptr(), ys, _dtype("y", y), _current(stream, dev))
+    _check(st, "tbe_lookup_forward")
+
+
+def tbe_lookup_backward_workspace_bytes(num_ids: int, items: int, width: int) -> int:
+    return int(lib().tbe_lookup_backward_workspace_bytes(int(num_ids), int(items), int(width)))
+
+
+def tbe_lookup_backward(ids: torch.Tensor, grad_y: torch.Tensor, scale: float, grad_table: torch.Tensor,
+                        workspace: Optional[torch.Tensor], accumulate: bool = False, stream=None):
+    """grad_table[v] = scale * the sum of grad_y[i] over ids[i] = v, or (accumulate) has it added."""
+    dev = _device()
+    ts = _rows("grad_table", grad_table, dev)
+    items, width = grad_table.shape
+    it = _ids("ids", ids, dev)
+    n = ids.shape[0]
+    gs = _rows("grad_y", grad_y, dev, (n, width))
+    st = lib().tbe_lookup_backward(n, items, width, ids.data_ptr(), it, grad_y.data_ptr(), gs, _dtype("grad_y", grad_y), scale,
+                                   grad_table.data_ptr(), ts, _dtype("grad_table", grad_table), int(bool(accumulate)),
+                                   _at(workspace), _bytes(workspace, dev), _current(stream, dev))
+    _check(st, "tbe_lookup_backward")

@@ -1,0 +1,69 @@
+/*
+ * tbe_items.h - the two ends of a model that reads and predicts the rows of
+ * one table (next item, retrieval, language).
+ *
+ *   lookup           y_i = scale * table[id_i], one row for each id, and the
+ *                    table's dense gradient;
+ *   cross entropy    softmax cross entropy of each row over all items of a
+ *                    table, without the logits ever being kept, and its
+ *                    gradients.
+ *
+ * Between them stand the operators of tbe_tower.h.  With tied weights the same
+ * table is at both ends: the lookup's gradient is then added to the loss's.
+ * They follow the conventions of tbe.h and tbe_tower.h: device pointers,
+ * caller-owned buffers and workspaces, no allocation, no synchronization, no
+ * copy to the host, every kernel on the caller's stream, errors found on the
+ * host before anything is launched.  Every result is computed in a fixed
+ * order: the same inputs give the same bits.  Sizes and strides are in
+ * elements.  Element pointers need the alignment of their element type only;
+ * larger alignment (16 bytes, rows that start on it) is faster.  A workspace
+ * may be used by any number of calls that follow each other on one stream, and
+ * holds nothing between calls; calls that may run at the same time (two
+ * streams, two captured graphs) need one each.  Outputs must not overlap
+ * inputs or each other.
+ */
+#ifndef TBE_ITEMS_H_
+#define TBE_ITEMS_H_
+
+#include "tbe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * y [ids][width] with rows y_stride apart: y_i = scale * table[id_i], rounded
+ * once to y's type; zero for an id outside [0, items) (padding).  table is
+ * [items][width] with rows table_stride apart; table and y may have different
+ * types.  0 <= num_ids <= TBE_MAX_LOOKUPS, 1 <= items < 2^31 - 1,
+ * 1 <= width <= TBE_ITEMS_MAX_WIDTH, rows at most 2^31 elements apart.
+ */
+#define TBE_ITEMS_MAX_WIDTH (1 << 20)
+tbe_status tbe_lookup_forward(int64_t num_ids, int64_t items, int64_t width, const void* table,
+                              int64_t table_stride, int32_t table_dtype, const void* ids,
+                              int32_t id_type, float scale, void* y, int64_t y_stride,
+                              int32_t y_dtype, tbe_stream_t stream);
+
+/*
+ * The table's gradient: row v of grad_table [items][width] becomes
+ * scale * (sum of grad_y_i over the i with id_i = v), zero where there is none
+ * (accumulate = 0), or has it added (accumulate = 1: rows that no id names are
+ * neither read nor written).  The sum is kept in fp32 over the positions in
+ * their order, with the row that it is added to, and rounded once.  ids
+ * outside [0, items) contribute nothing, whatever their grad_y holds.
+ * grad_y, grad_table and the table may have different types.  workspace: at
+ * least tbe_lookup_backward_workspace_bytes bytes, 256-byte aligned; the bytes
+ * grow with the ids, so one for the largest batch serves every smaller one.
+ */
+size_t tbe_lookup_backward_workspace_bytes(int64_t num_ids, int64_t items, int64_t width);
+tbe_status tbe_lookup_backward(int64_t num_ids, int64_t items, int64_t width, const void* ids,
+                               int32_t id_type, const void* grad_y, int64_t grad_y_stride,
+                               int32_t y_dtype, float scale, void* grad_table,
+                               int64_t grad_table_stride, int32_t table_dtype, int32_t accumulate,
+                               void* workspace, size_t workspace_bytes, tbe_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* TBE_ITEMS_H_ */
