@@ -116,6 +116,12 @@ _SIGS = {
     "tbe_lookup_backward_workspace_bytes": ([_I64, _I64, _I64], ctypes.c_size_t),
     "tbe_lookup_backward": ([_I64, _I64, _I64, _P, _I32, _P, _I64, _I32, ctypes.c_float, _P, _I64, _I32, _I32,
                              _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "tbe_cross_entropy_forward_workspace_bytes": ([_I64, _I64, _I64], ctypes.c_size_t),
+    "tbe_cross_entropy_forward": ([_I64, _I64, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _I32, ctypes.c_float, _P, _P, _P,
+                                   ctypes.c_size_t, _P], ctypes.c_int),
+    "tbe_cross_entropy_backward_workspace_bytes": ([_I64, _I64, _I64], ctypes.c_size_t),
+    "tbe_cross_entropy_backward": ([_I64, _I64, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _I32, ctypes.c_float, _P, _P, _P,
+                                    _I64, _P, _I64, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
     # measurement hooks (include/tbe_measure.h)
     "tbe_profile_select": ([ctypes.c_char_p], ctypes.c_int),
     "tbe_profile_read": ([_P, _P], ctypes.c_int),
@@ -350,5 +356,7 @@ from .tower import (AdamWTensors, TBE_ADAMW_BLOCK, TBE_ADAMW_CONTROL, TBE_LAYER_
                     tbe_grouped_linear_backward_weight_workspace_bytes, tbe_grouped_linear_forward,
                     tbe_layer_norm_backward, tbe_layer_norm_backward_workspace_bytes,
                     tbe_layer_norm_forward)
-from .items import (TBE_ITEMS_MAX_WIDTH, tbe_lookup_backward, tbe_lookup_backward_workspace_bytes,  # noqa: E402,F401
-                    tbe_lookup_forward)
+from .items import (TBE_CROSS_ENTROPY_MAX_ROWS, TBE_CROSS_ENTROPY_MAX_WIDTH, TBE_ITEMS_MAX_WIDTH,  # noqa: E402,F401
+                    tbe_cross_entropy_backward, tbe_cross_entropy_backward_workspace_bytes,
+                    tbe_cross_entropy_forward, tbe_cross_entropy_forward_workspace_bytes, tbe_lookup_backward,
+                    tbe_lookup_backward_workspace_bytes, tbe_lookup_forward)

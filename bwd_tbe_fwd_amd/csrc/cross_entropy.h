@@ -1,0 +1,65 @@
+// Softmax cross entropy over all items of a table: what its kernels share.  Declarations and the meaning of every argument
+// are in include/tbe_items.h.
+//
+// The rows that have a target are copied side by side first (their count stays on the device): a batch's padding costs no
+// products, and every row starts on 16 bytes.  Then, C(m, n) = sum_k A(m, k) B(n, k) as in tile_products.h:
+//   logits            m = row,  n = item,   k = column: A = x, B = weight, both along
+//   gradient of x     m = row,  n = column, k = item:   A = z along, B = weight across
+//   of the weights    m = item, n = column, k = row:    A = z across, B = x * grad_loss across
+// Forward, the logits' tile ends in each row's maximum and sum of exponentials over the tile's items.  Backward, it ends in
+// z, 16 bits each, for a piece of the items: small enough for the Infinity Cache, large enough for its two products.
+#pragma once
+
+#include "items.h"
+
+namespace tbe {
+
+// Rows that have a target, in order, and what the kernels need of each.
+struct CeRows {
+  const int32_t* count;    // of them
+  const int32_t* row;      // in the caller's arrays
+  const int32_t* target;
+  const float* lse;        // backward
+  const float* grad;       // backward: grad_loss
+  const float* largest;    // backward: of |grad_loss|
+};
+
+struct CeArgs {
+  int64_t rows;            // of the caller's batch: at least as many as have a target
+  int32_t width;
+  const void* x;           // [count][x_stride], 16 bits
+  int64_t x_stride;
+  const void* w;           // the piece's first item
+  int64_t w_stride;
+  const float* bias;       // the piece's; NULL: none
+  float scale;
+  CeRows r;
+  int32_t first, items;    // of the piece
+  float2* part;            // forward: [tiles of items][rows] maximum and sum
+  float* picked;           // forward: [rows] the target's logit
+  uint16_t* z;             // backward: [rows][z_stride]
+  int64_t z_stride;
+  float* bias_part;        // backward: [tiles of rows][items of a piece at most]; NULL: none
+  int64_t bias_stride;
+  // products of z
+  const void* xg;          // x * grad_loss / largest, like x
+  float* sum;              // [splits][rows or items][width] fp32 sums
+  int32_t splits;
+  int32_t add;             // to what is there
+  void* out;               // gradient of the weights, the piece's first item, with one split
+  int64_t out_stride;
+};
+
+// z is stored times this, so that fp16 holds probabilities down to 2^-29 as normal numbers.
+template <int DT> constexpr float kUnit = DT == 1 ? 32768.0f : 1.0f;
+
+// A tile of C and how it is walked, as for the grouped layers.
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
+
+// Defined in translation units of their own (cross_entropy_forward_f16.hip and its siblings).
+template <int DT> tbe_status ce_launch_forward(const CeArgs& a, int tile, bool direct, hipStream_t s);
+template <int DT> tbe_status ce_launch_z(const CeArgs& a, int tile, bool direct, hipStream_t s);
+template <int DT> tbe_status ce_launch_grad_x(const CeArgs& a, int tile, bool direct, hipStream_t s);
+template <int DT> tbe_status ce_launch_grad_w(const CeArgs& a, int tile, hipStream_t s);
+
+}  // namespace tbe

@@ -1,0 +1,459 @@
+// Softmax cross entropy over all items of a table: the rows that have a target, the joins of partial results, and the plan
+// of a call.  The products are in cross_entropy_tile.h, a translation unit each.
+#include "cross_entropy.h"
+
+#include "grouped_linear.h"
+#include "sort_common.h"
+
+namespace tbe {
+namespace {
+
+constexpr float kInf = __builtin_huge_valf();
+
+// ---------------------------------------------------------------------------
+// the rows that have a target
+// ---------------------------------------------------------------------------
+struct CeBatch {
+  int64_t rows, items;
+  const void* targets;
+  int32_t target64;
+  const float* grad_loss;  // backward, else NULL
+  const float* lse_in;     // backward
+  float* loss;             // forward: 0 for the rows without a target
+  float* lse_out;
+  int32_t* counts;         // per kBlock rows: of those with a target
+  float* tops;             // and their largest |grad_loss|
+  int32_t* count;
+  float* largest;
+  int32_t* row;
+  int32_t* target;
+  int32_t* slot;           // backward: of every row, -1: none
+  float* lse;
+  float* grad;
+};
+__device__ __forceinline__ int target_of(const CeBatch& b, int64_t i) {
+  if (i >= b.rows) return -1;
+  const int64_t t = b.target64 ? static_cast<const int64_t*>(b.targets)[i] : static_cast<const int32_t*>(b.targets)[i];
+  return static_cast<uint64_t>(t) < static_cast<uint64_t>(b.items) ? static_cast<int>(t) : -1;
+}
+__device__ __forceinline__ float block_max(float v, float* s_tmp) {
+  for (int m = 1; m < kWave; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
+  __syncthreads();
+  if (lane_id() == 0) s_tmp[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(s_tmp[0], s_tmp[1]), fmaxf(s_tmp[2], s_tmp[3]));
+}
+
+__global__ __launch_bounds__(kBlock) void ce_count_kernel(CeBatch b) {
+  __shared__ uint32_t s_n[kWavesPerBlock];
+  __shared__ float s_top[kWavesPerBlock];
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+  const bool has = target_of(b, i) >= 0;
+  const uint32_t n = block_sum(has ? 1u : 0u, s_n);
+  const float top = block_max(has && b.grad_loss ? fabsf(b.grad_loss[i]) : 0.0f, s_top);
+  if (threadIdx.x == 0) {
+    b.counts[blockIdx.x] = static_cast<int32_t>(n);
+    b.tops[blockIdx.x] = top;
+  }
+}
+
+__global__ __launch_bounds__(kBlock) void ce_list_kernel(CeBatch b) {
+  __shared__ uint32_t s_n[kWavesPerBlock];
+  __shared__ float s_top[kWavesPerBlock];
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+  const int t = target_of(b, i);
+  uint32_t before = 0, here;
+  for (unsigned k = threadIdx.x; k < blockIdx.x; k += kBlock) before += b.counts[k];
+  before = block_sum(before, s_n);
+  const uint32_t at = before + block_exclusive_sum(t >= 0 ? 1u : 0u, s_n, &here);
+  if (t >= 0) {
+    b.row[at] = static_cast<int32_t>(i);
+    b.target[at] = t;
+    if (b.grad_loss) {
+      b.lse[at] = b.lse_in[i];
+      b.grad[at] = b.grad_loss[i];
+    }
+  } else if (i < b.rows && b.loss) {
+    b.loss[i] = 0.0f;
+    b.lse_out[i] = 0.0f;
+  }
+  if (b.slot && i < b.rows) b.slot[i] = t >= 0 ? static_cast<int32_t>(at) : -1;
+  if (blockIdx.x + 1 < gridDim.x) return;
+  float top = 0.0f;
+  for (unsigned k = threadIdx.x; k < gridDim.x; k += kBlock) top = fmaxf(top, b.tops[k]);
+  top = block_max(top, s_top);
+  if (threadIdx.x == 0) {
+    *b.count = static_cast<int32_t>(before + here);
+    *b.largest = top;
+  }
+}
+
+// Their x side by side, rows of `pitch` (whole 16 bytes, zeros behind the width), and x times grad_loss over the largest.  A
+// wave a row.
+template <int DT>
+__global__ __launch_bounds__(kBlock) void ce_copy_kernel(const CeBatch b, const uint16_t* __restrict__ x, int64_t stride, int width,
+                                                         int pitch, uint16_t* __restrict__ xc, uint16_t* __restrict__ xg) {
+  const int count = *b.count, l = lane_id();
+  for (int64_t c = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6); c < count;
+       c += static_cast<int64_t>(gridDim.x) * kWavesPerBlock) {
+    const uint16_t* p = x + b.row[c] * stride;
+    const float g = xg ? (*b.largest > 0.0f ? b.grad[c] / *b.largest : 0.0f * b.grad[c]) : 1.0f;
+    for (int d = l * 8; d < pitch; d += kWave * 8) {
+      Vec<uint16_t, 8> v;
+      load_vec_part<uint16_t, 8>(p + d, width - d, v);
+      if (xc) store_vec_any<uint16_t, 8>(xc + c * pitch + d, v);
+      if (xg) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.e[e] = tower_from_f<DT>(Fmt<DT>::to_f(v.e[e]) * g);
+        store_vec_any<uint16_t, 8>(xg + c * pitch + d, v);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// joins
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float top = fmaxf(a.x, b.x), from = top == -kInf ? 0.0f : top;
+  return make_float2(top, a.y * expf(a.x - from) + b.y * expf(b.x - from));
+}
+
+// A piece's maxima and sums of each row, its tiles in a fixed order, joined with the pieces before: 16 rows a workgroup, 64
+// groups of 16 lanes.  The last piece's ends in the loss.
+constexpr int kJoinRows = 16, kJoinGroups = 64;
+__global__ __launch_bounds__(kJoinRows * kJoinGroups) void ce_join_kernel(const float2* __restrict__ part, int64_t rows, int tiles,
+                                                                         float2* __restrict__ all, int first, int last,
+                                                                         const float* __restrict__ picked, CeBatch b) {
+  __shared__ float2 s_all[kJoinGroups][kJoinRows + 1];
+  const int q = threadIdx.x / kJoinRows, k = threadIdx.x % kJoinRows, count = *b.count;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kJoinRows + k;
+  float2 sum = make_float2(-kInf, 0.0f);
+  if (c < count) {
+#pragma unroll 4
+    for (int t = q; t < tiles; t += kJoinGroups) sum = join(sum, part[t * rows + c]);
+  }
+  s_all[q][k] = sum;
+  __syncthreads();
+  for (int n = kJoinGroups / 2; n > 0; n /= 2) {
+    if (q < n) s_all[q][k] = join(s_all[q][k], s_all[q + n][k]);
+    __syncthreads();
+  }
+  if (q || c >= count) return;
+  sum = s_all[0][k];
+  if (!first) sum = join(all[c], sum);
+  if (!last) {
+    all[c] = sum;
+    return;
+  }
+  const float lse = sum.x + logf(sum.y), at = picked[c];  // every item masked: -inf + log 0
+  b.lse_out[b.row[c]] = lse;
+  b.loss[b.row[c]] = at == -kInf && !(lse != lse) ? kInf : lse - at;
+}
+
+// The rows' gradients: the parts' sums times scale * grad_loss; zero for a row without a target.
+template <int DT>
+__global__ __launch_bounds__(kBlock) void ce_grad_x_kernel(const CeBatch b, const float* __restrict__ sum, int splits, int width, float factor,
+                                                           uint16_t* __restrict__ gx, int64_t stride) {
+  const int l = lane_id();
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6); i < b.rows;
+       i += static_cast<int64_t>(gridDim.x) * kWavesPerBlock) {
+    const int64_t c = b.slot[i];
+    const float g = c >= 0 ? b.grad[c] * factor : 0.0f;
+    for (int d = l * 4; d < width; d += kWave * 4) {
+      Vec<float, 4> all = {};
+      if (c >= 0) {
+        for (int k = 0; k < splits; ++k) {
+          Vec<float, 4> v;
+          load_vec_part<float, 4>(sum + (k * b.rows + c) * width + d, width - d, v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) all.e[e] += v.e[e];
+        }
+      }
+      Vec<uint16_t, 4> out;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out.e[e] = c >= 0 ? tower_from_f<DT>(all.e[e] * g) : static_cast<uint16_t>(0);
+      store_vec_part<uint16_t, 4>(gx + i * stride + d, width - d, out);
+    }
+  }
+}
+
+// The weights' gradients of a piece whose rows were shared.
+template <int DT>
+__global__ __launch_bounds__(kBlock) void ce_grad_w_kernel(const float* __restrict__ sum, int splits, int items, int width, float scale,
+                                                           const float* __restrict__ largest, uint16_t* __restrict__ gw, int64_t stride) {
+  const float factor = scale * *largest;
+  const int l = lane_id();
+  for (int64_t v = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6); v < items;
+       v += static_cast<int64_t>(gridDim.x) * kWavesPerBlock) {
+    for (int d = l * 4; d < width; d += kWave * 4) {
+      Vec<float, 4> all = {};
+      for (int k = 0; k < splits; ++k) {
+        Vec<float, 4> p;
+        load_vec_part<float, 4>(sum + (static_cast<int64_t>(k) * items + v) * width + d, width - d, p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) all.e[e] += p.e[e];
+      }
+      Vec<uint16_t, 4> out;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out.e[e] = tower_from_f<DT>(all.e[e] * factor);
+      store_vec_part<uint16_t, 4>(gw + v * stride + d, width - d, out);
+    }
+  }
+}
+
+// A piece's bias gradients: the sums over the tiles of rows (bm rows each), in order.  64 items a workgroup, 16 groups.
+__global__ __launch_bounds__(1024) void ce_grad_bias_kernel(const float* __restrict__ part, int64_t stride, const int32_t* __restrict__ count,
+                                                            int bm, int items, float* __restrict__ gb) {
+  __shared__ float s_sum[16][kWave];
+  const int q = threadIdx.x / kWave, l = lane_id();
+  const int v = blockIdx.x * kWave + l, tiles = (*count + bm - 1) / bm;
+  float sum = 0.0f;
+  if (v < items) {
+#pragma unroll 4
+    for (int t = q; t < tiles; t += 16) sum += part[t * stride + v];
+  }
+  s_sum[q][l] = sum;
+  __syncthreads();
+  if (q || v >= items) return;
+  for (int k = 1; k < 16; ++k) sum += s_sum[k][l];
+  gb[v] = sum;
+}
+
+// ---------------------------------------------------------------------------
+// the plan, from sizes alone
+// ---------------------------------------------------------------------------
+// Bytes below never shrink with the rows, so a workspace for the largest batch serves every smaller one.
+constexpr int64_t kPartBytes = int64_t{64} << 20;    // forward: of the rows' maxima and sums over a piece's tiles
+constexpr int64_t kZElems = int64_t{1} << 27;        // backward: of z
+constexpr int64_t kLeastPiece = 1024, kMostPiece = 131072;  // items of a piece, backward
+constexpr int64_t kSumBytes = int64_t{128} << 20;    // of the sums over shares of k, beyond one share of x's gradient
+constexpr int kMostSplits = 16;
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+struct Carve {
+  size_t at = 0;
+  size_t take(int64_t bytes) {
+    const size_t here = at;
+    at += static_cast<size_t>(up(hmax(bytes, 1), 256));
+    return here;
+  }
+};
+struct CeLayout {
+  int64_t pitch, piece;
+  size_t counts, tops, count, largest, row, target, slot, lse, grad, xc;
+  size_t part, picked, all;                 // forward
+  size_t xg, z, sum_x, sum_w, bias_part;    // backward
+  size_t total;
+};
+void carve_rows(CeLayout& L, Carve& c, int64_t rows, int64_t width) {
+  const int64_t blocks = (rows + kBlock - 1) / kBlock;
+  L.pitch = up(width, 8);
+  L.counts = c.take(blocks * 4);
+  L.tops = c.take(blocks * 4);
+  L.count = c.take(4);
+  L.largest = c.take(4);
+  L.row = c.take(rows * 4);
+  L.target = c.take(rows * 4);
+  L.xc = c.take(rows * L.pitch * 2);
+}
+CeLayout forward_layout(int64_t rows, int64_t items, int64_t width) {
+  CeLayout L = {};
+  Carve c;
+  carve_rows(L, c, rows, width);
+  // pieces of whole 256s; the smallest tile has 64 items
+  L.piece = hmin(up(items, 256), hmax(1, kPartBytes / (8 * hmax(rows, 1)) / 4) * 256);
+  L.part = c.take(hmin(rows * (up(items, 256) / 64) * 8, hmax(kPartBytes, rows * 4 * 8)));
+  L.picked = c.take(rows * 4);
+  L.all = c.take(rows * 8);
+  L.total = c.at;
+  return L;
+}
+CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
+  CeLayout L = {};
+  Carve c;
+  carve_rows(L, c, rows, width);
+  L.slot = c.take(rows * 4);
+  L.lse = c.take(rows * 4);
+  L.grad = c.take(rows * 4);
+  L.xg = c.take(rows * L.pitch * 2);
+  const int64_t all = up(items, 256), most = hmin(all, kMostPiece);
+  L.piece = hmin(most, hmax(kLeastPiece, kZElems / hmax(rows, 1) / 256 * 256));
+  const int64_t z = hmin(rows * most, hmax(kZElems, rows * kLeastPiece));
+  L.z = c.take(z * 2);
+  L.sum_x = c.take(hmax(rows * width * 4, hmin(kSumBytes, kMostSplits * rows * width * 4)));
+  L.sum_w = c.take(kSumBytes);
+  L.bias_part = c.take(z / 64 * 4 + most * 4);
+  L.total = c.at;
+  return L;
+}
+
+// The tile of least expected time for m x n of C, k deep, and into how many shares k goes where few tiles leave CUs idle.
+struct TilePick {
+  int tile, splits;
+};
+TilePick pick_tile(const TileCost (&costs)[3], int64_t m, int64_t n, int64_t k, int most_splits, int64_t most_bytes) {
+  TilePick best = {0, 1};
+  double least = -1.0;
+  for (int t = 0; t < 3; ++t) {
+    const TileCost& c = costs[t];
+    const double tiles = static_cast<double>(((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn));
+    for (int split = 1; split <= most_splits; split *= 2) {
+      if (split > 1 && (k / split < 256 || split * m * n * 4 > most_bytes)) break;
+      const double kk = static_cast<double>(up((k + split - 1) / split, 64));
+      const double us = tiles_us(c, tiles * split, kk, kk) + (split > 1 ? 4.0 + 2.0 * split * static_cast<double>(m * n) * 4 / 4e6 : 0.0);
+      if (least < 0.0 || us < least) {
+        least = us;
+        best = TilePick{t, split};
+      }
+    }
+  }
+  return best;
+}
+// Costs of the kernels here: grouped_linear.h's, with square tiles through registers as well.
+constexpr TileCost kAlongRegisters[3] = {{256, 256, 512, 256, 6.0, 1.3, 2.05}, {128, 128, 256, 512, 5.0, 0.8, 1.5}, {64, 64, 256, 1024, 3.0, 0.55, 1.35}};
+
+bool whole_16(const void* p, int64_t stride, int64_t width) {
+  return !(reinterpret_cast<uintptr_t>(p) & 15) && stride % 8 == 0 && width % 8 == 0 && stride < (int64_t{1} << 21);
+}
+
+CeBatch batch_of(char* ws, const CeLayout& L, int64_t rows, int64_t items, const void* targets, int target_type) {
+  CeBatch b = {};
+  b.rows = rows; b.items = items; b.targets = targets; b.target64 = target_type == TBE_I64;
+  b.counts = reinterpret_cast<int32_t*>(ws + L.counts);
+  b.tops = reinterpret_cast<float*>(ws + L.tops);
+  b.count = reinterpret_cast<int32_t*>(ws + L.count);
+  b.largest = reinterpret_cast<float*>(ws + L.largest);
+  b.row = reinterpret_cast<int32_t*>(ws + L.row);
+  b.target = reinterpret_cast<int32_t*>(ws + L.target);
+  return b;
+}
+tbe_status launch_rows(const CeBatch& b, const void* x, int64_t x_stride, int64_t width, int64_t pitch, int dtype, void* xc, void* xg,
+                       hipStream_t s) {
+  const unsigned blocks = static_cast<unsigned>(hmax(1, (b.rows + kBlock - 1) / kBlock));  // no rows: their count, 0
+  ProfScope ps("ce_rows", s);
+  hipLaunchKernelGGL(ce_count_kernel, dim3(blocks), dim3(kBlock), 0, s, b);
+  hipLaunchKernelGGL(ce_list_kernel, dim3(blocks), dim3(kBlock), 0, s, b);
+  const unsigned groups = static_cast<unsigned>(hmax(1, hmin((b.rows + kWavesPerBlock - 1) / kWavesPerBlock, 8192)));
+  auto kernel = dtype == TBE_F16 ? ce_copy_kernel<1> : ce_copy_kernel<2>;
+  hipLaunchKernelGGL(kernel, dim3(groups), dim3(kBlock), 0, s, b, static_cast<const uint16_t*>(x), x_stride, static_cast<int>(width),
+                     static_cast<int>(pitch), static_cast<uint16_t*>(xc), static_cast<uint16_t*>(xg));
+  return check_launch("ce_rows");
+}
+CeRows rows_of(const CeBatch& b) { return CeRows{b.count, b.row, b.target, b.lse, b.grad, b.largest}; }
+
+}  // namespace
+
+size_t cross_entropy_forward_workspace(int64_t rows, int64_t items, int64_t width) { return forward_layout(rows, items, width).total; }
+size_t cross_entropy_backward_workspace(int64_t rows, int64_t items, int64_t width) { return backward_layout(rows, items, width).total; }
+
+tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t width, const void* x, int64_t x_stride, const void* weight,
+                                        int64_t weight_stride, int dtype, const float* bias, const void* targets, int target_type,
+                                        float scale, float* loss, float* lse, void* workspace, hipStream_t s) {
+  const CeLayout L = forward_layout(rows, items, width);
+  char* ws = static_cast<char*>(workspace);
+  CeBatch b = batch_of(ws, L, rows, items, targets, target_type);
+  b.loss = loss;
+  b.lse_out = lse;
+  tbe_status st = launch_rows(b, x, x_stride, width, L.pitch, dtype, ws + L.xc, nullptr, s);
+  const bool direct = whole_16(weight, weight_stride, width);
+  CeArgs a = {};
+  a.rows = rows; a.width = static_cast<int>(width);
+  a.x = ws + L.xc; a.x_stride = L.pitch;
+  a.w_stride = weight_stride; a.scale = scale; a.r = rows_of(b);
+  a.part = reinterpret_cast<float2*>(ws + L.part);
+  a.picked = reinterpret_cast<float*>(ws + L.picked);
+  for (int64_t first = 0; st == TBE_OK && first < items; first += L.piece) {
+    a.first = static_cast<int>(first);
+    a.items = static_cast<int>(hmin(L.piece, items - first));
+    a.w = static_cast<const uint16_t*>(weight) + first * weight_stride;
+    a.bias = bias ? bias + first : nullptr;
+    const TileCost(&costs)[3] = direct ? kDirectTiles : kAlongRegisters;
+    const int tile = pick_tile(costs, rows, a.items, width, 1, 0).tile;
+    st = dtype == TBE_F16 ? ce_launch_forward<1>(a, tile, direct, s) : ce_launch_forward<2>(a, tile, direct, s);
+    if (st != TBE_OK) break;
+    ProfScope ps("ce_join", s);
+    const int bn = costs[tile].bn;
+    hipLaunchKernelGGL(ce_join_kernel, dim3(static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows)), dim3(kJoinRows * kJoinGroups), 0, s,
+                       a.part, rows, (a.items + bn - 1) / bn, reinterpret_cast<float2*>(ws + L.all), first == 0 ? 1 : 0,
+                       first + L.piece >= items ? 1 : 0, a.picked, b);
+    st = check_launch("ce_join");
+  }
+  return st;
+}
+
+tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t width, const void* x, int64_t x_stride, const void* weight,
+                                         int64_t weight_stride, int dtype, const float* bias, const void* targets, int target_type,
+                                         float scale, const float* lse, const float* grad_loss, void* grad_x, int64_t grad_x_stride,
+                                         void* grad_weight, int64_t grad_weight_stride, float* grad_bias, void* workspace, hipStream_t s) {
+  const CeLayout L = backward_layout(rows, items, width);
+  char* ws = static_cast<char*>(workspace);
+  CeBatch b = batch_of(ws, L, rows, items, targets, target_type);
+  b.grad_loss = grad_loss;
+  b.lse_in = lse;
+  b.slot = reinterpret_cast<int32_t*>(ws + L.slot);
+  b.lse = reinterpret_cast<float*>(ws + L.lse);
+  b.grad = reinterpret_cast<float*>(ws + L.grad);
+  tbe_status st = launch_rows(b, x, x_stride, width, L.pitch, dtype, ws + L.xc, grad_weight ? ws + L.xg : nullptr, s);
+  const bool direct = whole_16(weight, weight_stride, width);
+  const bool f16 = dtype == TBE_F16;
+  CeArgs a = {};
+  a.rows = rows; a.width = static_cast<int>(width);
+  a.x = ws + L.xc; a.x_stride = L.pitch; a.xg = ws + L.xg;
+  a.w_stride = weight_stride; a.scale = scale; a.r = rows_of(b);
+  a.z = reinterpret_cast<uint16_t*>(ws + L.z); a.z_stride = L.piece;
+  a.bias_part = grad_bias ? reinterpret_cast<float*>(ws + L.bias_part) : nullptr;
+  a.bias_stride = L.piece;
+  const TileCost(&costs)[3] = direct ? kDirectTiles : kAlongRegisters;
+  const int64_t sum_x_bytes = hmax(rows * width * 4, hmin(kSumBytes, kMostSplits * rows * width * 4));
+  TilePick x_pick = {0, 1};
+  if (rows == 0) grad_x = nullptr;  // the gradients of the weights and biases are zeros
+  for (int64_t first = 0; st == TBE_OK && first < items; first += L.piece) {
+    a.first = static_cast<int>(first);
+    a.items = static_cast<int>(hmin(L.piece, items - first));
+    a.w = static_cast<const uint16_t*>(weight) + first * weight_stride;
+    a.bias = bias ? bias + first : nullptr;
+    const int tile = pick_tile(costs, rows, a.items, width, 1, 0).tile;
+    if (rows > 0) st = f16 ? ce_launch_z<1>(a, tile, direct, s) : ce_launch_z<2>(a, tile, direct, s);
+    if (st == TBE_OK && grad_bias) {
+      ProfScope ps("ce_grad_bias", s);
+      hipLaunchKernelGGL(ce_grad_bias_kernel, dim3(static_cast<unsigned>((a.items + kWave - 1) / kWave)), dim3(1024), 0, s, a.bias_part,
+                         a.bias_stride, b.count, costs[tile].bm, a.items, grad_bias + first);
+      st = check_launch("ce_grad_bias");
+    }
+    if (st == TBE_OK && grad_x) {
+      // the same shares for every piece: their sums go on
+      if (first == 0) x_pick = pick_tile(costs, rows, width, a.items, kMostSplits, sum_x_bytes);
+      a.sum = reinterpret_cast<float*>(ws + L.sum_x);
+      a.splits = x_pick.splits;
+      a.add = first > 0;
+      st = f16 ? ce_launch_grad_x<1>(a, x_pick.tile, direct, s) : ce_launch_grad_x<2>(a, x_pick.tile, direct, s);
+    }
+    if (st == TBE_OK && grad_weight) {
+      const TilePick p = pick_tile(kWeightTiles, a.items, width, rows, kMostSplits, kSumBytes);
+      a.sum = reinterpret_cast<float*>(ws + L.sum_w);
+      a.splits = p.splits;
+      a.add = 0;
+      a.out = static_cast<uint16_t*>(grad_weight) + first * grad_weight_stride;
+      a.out_stride = grad_weight_stride;
+      st = f16 ? ce_launch_grad_w<1>(a, p.tile, s) : ce_launch_grad_w<2>(a, p.tile, s);
+      if (st == TBE_OK && p.splits > 1) {
+        ProfScope ps("ce_grad_w_sum", s);
+        auto kernel = f16 ? ce_grad_w_kernel<1> : ce_grad_w_kernel<2>;
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((a.items + 3) / 4, 8192))), dim3(kBlock), 0, s, a.sum, p.splits, a.items,
+                           a.width, scale / (f16 ? kUnit<1> : kUnit<2>), b.largest, static_cast<uint16_t*>(a.out), grad_weight_stride);
+        st = check_launch("ce_grad_w_sum");
+      }
+    }
+  }
+  if (st != TBE_OK || !grad_x) return st;
+  ProfScope ps("ce_grad_x_sum", s);
+  auto kernel = f16 ? ce_grad_x_kernel<1> : ce_grad_x_kernel<2>;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((rows + 3) / 4, 8192))), dim3(kBlock), 0, s, b,
+                     reinterpret_cast<const float*>(ws + L.sum_x), x_pick.splits, static_cast<int>(width),
+                     scale / (f16 ? kUnit<1> : kUnit<2>), static_cast<uint16_t*>(grad_x), grad_x_stride);
+  return check_launch("ce_grad_x_sum");
+}
+
+}  // namespace tbe

@@ -1,0 +1,9 @@
+// Cross entropy, the weights' gradient, bf16.
+#include "cross_entropy_tile.h"
+
+namespace tbe {
+template <>
+tbe_status ce_launch_grad_w<2>(const CeArgs& a, int tile, hipStream_t s) {
+  return ce_grad<2, false, true>(a, tile, s);
+}
+}  // namespace tbe

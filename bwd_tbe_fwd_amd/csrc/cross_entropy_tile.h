@@ -1,0 +1,234 @@
+// The tiled kernels of the cross entropy (cross_entropy.h says what m, n and k are).
+#pragma once
+
+#include "cross_entropy.h"
+#include "tile_products.h"
+
+namespace tbe {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kInfinity = __builtin_huge_valf();
+
+// Workgroup blockIdx.x's place among m_tiles x n_tiles: a contiguous share for each chiplet, and in it bands of 8 tiles of m
+// walked along n, so that the 32 workgroups that a chiplet runs at once read 8 + 4 tiles of operands and not 1 + 32.  False:
+// none.
+struct TilePlace {
+  int m, n;
+};
+__device__ __forceinline__ bool tile_place(int64_t m_tiles, int64_t n_tiles, TilePlace& t) {
+  const int64_t total = m_tiles * n_tiles, x = blockIdx.x % 8;
+  const int64_t id = total * x / 8 + blockIdx.x / 8;
+  if (id >= total * (x + 1) / 8) return false;
+  const int64_t band = id / (8 * n_tiles);
+  const int r = static_cast<int>(id - band * 8 * n_tiles);
+  const int high = static_cast<int>(m_tiles - band * 8 < 8 ? m_tiles - band * 8 : 8);
+  t.m = static_cast<int>(band) * 8 + r % high;
+  t.n = r / high;
+  return true;
+}
+
+// Logits of BM rows and BN items, and what becomes of them.
+template <int DT, bool BACK, int BM, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void ce_logits_kernel(CeArgs a) {
+  constexpr int T = WM * WN * kWave;
+  constexpr int MF = BM / WM / 16, NF = BN / WN / 16, LEN = 4 * NF;  // LEN adjacent items of a lane
+  using OA = Operand<true, BM, 4, T, DIRECT>;
+  using OB = Operand<true, BN, 4 * NF, T, DIRECT>;
+  constexpr int kBytes = 2 * 2 * (OA::kElems + OB::kElems);
+  __shared__ __align__(16) char lds[kBytes];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
+  const int wm = (w / WN) * (MF * 16), wn = (w % WN) * (NF * 16);
+  const int count = *a.r.count;
+  TilePlace t;
+  if (!tile_place((count + BM - 1) / BM, (a.items + BN - 1) / BN, t)) return;
+  const int m0 = t.m * BM, n0 = t.n * BN;
+  const int m_left = count - m0, n_left = a.items - n0;
+  OA A;
+  OB B;
+  A.init(static_cast<const uint16_t*>(a.x) + m0 * a.x_stride, a.x_stride, m_left, a.width, a.width);
+  B.init(static_cast<const uint16_t*>(a.w) + n0 * a.w_stride, a.w_stride, n_left, a.width, a.width);
+  f32x4 acc[MF][NF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  tile_products<DT, true, true, DIRECT>(A, B, lds, wm, wn, (a.width + kStepK - 1) / kStepK, acc, [](int, u16x8_t) {});
+
+  // this lane's items: n .. n + LEN of the tile
+  const int n = wn + (l >> 4) * LEN;
+  float bias[LEN];
+#pragma unroll
+  for (int c = 0; c < LEN; ++c) bias[c] = a.bias && n + c < n_left ? a.bias[n0 + n + c] : 0.0f;
+  auto logit = [&](int i, int c) { return fmaf(acc[i][c / 4][c % 4], a.scale, bias[c]); };
+  if constexpr (!BACK) {
+    float2* stat = reinterpret_cast<float2*>(lds);  // [WN][BM]
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      const int m = wm + 16 * i + (l & 15);
+      float v[LEN], top = -kInfinity;
+#pragma unroll
+      for (int c = 0; c < LEN; ++c) {
+        v[c] = n + c < n_left ? logit(i, c) : -kInfinity;
+        top = fmaxf(top, v[c]);
+      }
+      const int at = m < m_left ? a.r.target[m0 + m] - a.first - n0 - n : -1;
+      if (at >= 0 && at < LEN) {
+#pragma unroll
+        for (int c = 0; c < LEN; ++c)
+          if (c == at) a.picked[m0 + m] = v[c];
+      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float from = top == -kInfinity ? 0.0f : top;  // no item that is not masked: the sum is 0
+      float sum = 0.0f;
+#pragma unroll
+      for (int c = 0; c < LEN; ++c) sum += __builtin_amdgcn_exp2f((v[c] - from) * kLog2e);
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (l < 16) stat[(w % WN) * BM + m] = make_float2(top, sum);
+    }
+    __syncthreads();
+    for (int m = threadIdx.x; m < BM; m += T) {
+      float2 all = stat[m];
+      for (int k = 1; k < WN; ++k) {
+        const float2 s = stat[k * BM + m];
+        const float top = fmaxf(all.x, s.x), from = top == -kInfinity ? 0.0f : top;
+        all = make_float2(top, all.y * __builtin_amdgcn_exp2f((all.x - from) * kLog2e) + s.y * __builtin_amdgcn_exp2f((s.x - from) * kLog2e));
+      }
+      if (m < m_left) a.part[t.n * a.rows + m0 + m] = all;
+    }
+  } else {
+    // z in place of the logits
+    float columns[LEN];
+#pragma unroll
+    for (int c = 0; c < LEN; ++c) columns[c] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      const int m = wm + 16 * i + (l & 15);
+      const bool in = m < m_left;
+      float lse = in ? a.r.lse[m0 + m] : kInfinity;
+      if (lse == -kInfinity) lse = kInfinity;  // every item is masked: no probability
+      const int at = in ? a.r.target[m0 + m] - a.first - n0 - n : -1;
+      const float g = in && a.bias_part ? a.r.grad[m0 + m] : 0.0f;
+#pragma unroll
+      for (int c = 0; c < LEN; ++c) {
+        float p = __builtin_amdgcn_exp2f((logit(i, c) - lse) * kLog2e);
+        if (c == at) p -= 1.0f;
+        if (n_left < BN && n + c >= n_left) p = 0.0f;  // z's columns up to a whole 16 bytes are read
+        acc[i][c / 4][c % 4] = p;
+        if (in) columns[c] = fmaf(p, g, columns[c]);
+      }
+    }
+    if (a.bias_part) {
+      float* sums = reinterpret_cast<float*>(lds);  // [WM][BN]
+#pragma unroll
+      for (int c = 0; c < LEN; ++c) {
+        const float s = lanes_sum<16>(columns[c]);
+        if ((l & 15) == 0) sums[(w / WN) * BN + n + c] = s;
+      }
+      __syncthreads();
+      for (int k = threadIdx.x; k < BN; k += T) {
+        float s = sums[k];
+        for (int q = 1; q < WM; ++q) s += sums[q * BN + k];
+        if (k < n_left) a.bias_part[t.m * a.bias_stride + n0 + k] = s;
+      }
+      __syncthreads();
+    }
+    constexpr int kWaveBytes = kBytes / (WM * WN) / 16 * 16;
+    store_tile<uint16_t, false, MF, NF, LEN, kWaveBytes>(a.z + (m0 + wm) * a.z_stride + n0 + wn, a.z_stride, m_left - wm, (n_left + 7) / 8 * 8 - wn,
+                                                         lds + w * kWaveBytes,
+                                                         [&](int i, int j, int e) { return tower_from_f<DT>(acc[i][j][e] * kUnit<DT>); });
+  }
+}
+
+// The two products of z.  X: the gradient of x, else of the weights.  blockIdx.y: the part of k.
+template <int DT, bool X, int BM, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void ce_grad_kernel(CeArgs a) {
+  constexpr int T = WM * WN * kWave;
+  constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
+  using OA = Operand<X, BM, 4, T, DIRECT>;
+  using OB = Operand<false, BN, 4 * NF, T, DIRECT>;
+  constexpr int kBytes = 2 * 2 * (OA::kElems + OB::kElems);
+  __shared__ __align__(16) char lds[kBytes];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
+  const int wm = (w / WN) * (MF * 16), wn = (w % WN) * (NF * 16);
+  const int count = *a.r.count, ms = X ? count : a.items, ks = X ? a.items : count;
+  TilePlace t;
+  if (!tile_place((ms + BM - 1) / BM, (a.width + BN - 1) / BN, t)) return;
+  const int m0 = t.m * BM, n0 = t.n * BN;
+  const int m_left = ms - m0, n_left = a.width - n0;
+  // parts of whole steps
+  const int each = ((ks + a.splits - 1) / a.splits + kStepK - 1) / kStepK * kStepK;
+  const int64_t k0 = min(static_cast<int64_t>(blockIdx.y) * each, static_cast<int64_t>(ks));
+  const int k = min(each, static_cast<int>(ks - k0));
+  OA A;
+  OB B;
+  if constexpr (X) {
+    A.init(a.z + m0 * a.z_stride + k0, a.z_stride, m_left, k, k);
+    B.init(static_cast<const uint16_t*>(a.w) + k0 * a.w_stride + n0, a.w_stride, n_left, k, a.width);
+  } else {
+    A.init(a.z + k0 * a.z_stride + m0, a.z_stride, m_left, k, a.items);
+    B.init(static_cast<const uint16_t*>(a.xg) + k0 * a.x_stride + n0, a.x_stride, n_left, k, a.width);
+  }
+  const int64_t pitch = a.width;
+  float* const sum = a.sum + (static_cast<int64_t>(blockIdx.y) * (X ? a.rows : a.items) + m0 + wm) * pitch + n0 + wn;
+  f32x4 acc[MF][NF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i) {
+    const int m = 16 * i + (l & 15);
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      const int n = 16 * j + 4 * (l >> 4);
+      acc[i][j] = f32x4{0, 0, 0, 0};
+      if (X && a.add && m < m_left - wm) {
+        Vec<float, 4> v;
+        load_vec_part<float, 4>(sum + m * pitch + n, n_left - wn - n, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = v.e[e];
+      }
+    }
+  }
+  tile_products<DT, X, false, DIRECT>(A, B, lds, wm, wn, (k + kStepK - 1) / kStepK, acc, [](int, u16x8_t) {});
+  constexpr int kWaveBytes = kBytes / (WM * WN) / 16 * 16;
+  char* s = lds + w * kWaveBytes;
+  if (!X && a.splits == 1) {
+    const float factor = a.scale * *a.r.largest / kUnit<DT>;
+    store_tile<uint16_t, true, MF, NF, 4, kWaveBytes>(static_cast<uint16_t*>(a.out) + (m0 + wm) * a.out_stride + n0 + wn, a.out_stride,
+                                                      m_left - wm, n_left - wn, s,
+                                                      [&](int i, int j, int e) { return tower_from_f<DT>(acc[i][j][e] * factor); });
+  } else {
+    store_tile<float, false, MF, NF, 4, kWaveBytes>(sum, pitch, m_left - wm, n_left - wn, s,
+                                                    [&](int i, int j, int e) { return acc[i][j][e]; });
+  }
+}
+
+template <typename K>
+tbe_status ce_launch(K* kernel, const char* what, int threads, int64_t tiles, int splits, const CeArgs& a, hipStream_t s) {
+  const int64_t groups = (tiles + 7) / 8 * 8;  // for the chiplets' shares
+  if (groups * threads >= (int64_t{1} << 32)) {
+    set_error("cross entropy: %lld tiles are more than a launch takes", static_cast<long long>(groups));
+    return TBE_ERR_UNSUPPORTED;
+  }
+  ProfScope ps(what, s);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups), splits), dim3(threads), 0, s, a);
+  return check_launch(what);
+}
+inline int64_t ce_tiles(int64_t m, int bm, int64_t n, int bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
+
+template <int DT, bool BACK, bool DIRECT>
+tbe_status ce_logits(const CeArgs& a, int tile, hipStream_t s) {
+  const char* what = BACK ? "ce_z" : "ce_logits";
+  if (tile == kTile256) return ce_launch(ce_logits_kernel<DT, BACK, 256, 256, 2, 4, DIRECT>, what, 512, ce_tiles(a.rows, 256, a.items, 256), 1, a, s);
+  if (tile == kTile128) return ce_launch(ce_logits_kernel<DT, BACK, 128, 128, 2, 2, DIRECT>, what, 256, ce_tiles(a.rows, 128, a.items, 128), 1, a, s);
+  return ce_launch(ce_logits_kernel<DT, BACK, 64, 64, 2, 2, DIRECT>, what, 256, ce_tiles(a.rows, 64, a.items, 64), 1, a, s);
+}
+template <int DT, bool X, bool DIRECT>
+tbe_status ce_grad(const CeArgs& a, int tile, hipStream_t s) {
+  const char* what = X ? "ce_grad_x" : "ce_grad_w";
+  const int64_t m = X ? a.rows : a.items;
+  if (tile == kTile256) return ce_launch(ce_grad_kernel<DT, X, 256, 256, 2, 4, DIRECT>, what, 512, ce_tiles(m, 256, a.width, 256), a.splits, a, s);
+  if (tile == kTile128) return ce_launch(ce_grad_kernel<DT, X, 128, 128, 2, 2, DIRECT>, what, 256, ce_tiles(m, 128, a.width, 128), a.splits, a, s);
+  return ce_launch(ce_grad_kernel<DT, X, 64, 64, 2, 2, DIRECT>, what, 256, ce_tiles(m, 64, a.width, 64), a.splits, a, s);
+}
+
+}  // namespace tbe

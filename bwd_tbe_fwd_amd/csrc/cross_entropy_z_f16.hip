@@ -1,0 +1,9 @@
+// Cross entropy, the logits backward, fp16.
+#include "cross_entropy_tile.h"
+
+namespace tbe {
+template <>
+tbe_status ce_launch_z<1>(const CeArgs& a, int tile, bool direct, hipStream_t s) {
+  return direct ? ce_logits<1, true, true>(a, tile, s) : ce_logits<1, true, false>(a, tile, s);
+}
+}  // namespace tbe

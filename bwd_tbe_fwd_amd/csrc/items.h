@@ -20,4 +20,15 @@ tbe_status launch_lookup_backward(int64_t n, int64_t items, int64_t width, const
                                   int64_t gy_stride, int y_dtype, float scale, void* grad, int64_t grad_stride, int table_dtype,
                                   bool add, void* workspace, hipStream_t s);
 
+
+size_t cross_entropy_forward_workspace(int64_t rows, int64_t items, int64_t width);
+size_t cross_entropy_backward_workspace(int64_t rows, int64_t items, int64_t width);
+tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t width, const void* x, int64_t x_stride, const void* weight,
+                                        int64_t weight_stride, int dtype, const float* bias, const void* targets, int target_type,
+                                        float scale, float* loss, float* lse, void* workspace, hipStream_t s);
+tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t width, const void* x, int64_t x_stride, const void* weight,
+                                         int64_t weight_stride, int dtype, const float* bias, const void* targets, int target_type,
+                                         float scale, const float* lse, const float* grad_loss, void* grad_x, int64_t grad_x_stride,
+                                         void* grad_weight, int64_t grad_weight_stride, float* grad_bias, void* workspace, hipStream_t s);
+
 }  // namespace tbe

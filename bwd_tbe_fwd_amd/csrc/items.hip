@@ -53,7 +53,78 @@ tbe_status check_lookup(int64_t n, int64_t items, int64_t width) {
   return n < 0 || items < 1 || width < 1 ? TBE_ERR_ARG : TBE_ERR_UNSUPPORTED;
 }
 
+bool loss_sizes_ok(int64_t rows, int64_t items, int64_t width) {
+  return rows >= 0 && rows <= TBE_CROSS_ENTROPY_MAX_ROWS && items >= 1 && items <= kMaxItems && width >= 1 &&
+         width <= TBE_CROSS_ENTROPY_MAX_WIDTH;
+}
+// What both directions ask.
+tbe_status check_loss(int64_t rows, int64_t items, int64_t width, const void* x, int64_t x_stride, const void* weight,
+                      int64_t weight_stride, int dtype, const float* bias, const void* targets, int target_type, float scale) {
+  if (!loss_sizes_ok(rows, items, width)) {
+    set_error("cross entropy: %lld rows, %lld items of width %lld (0 <= rows <= %d, 1 <= items < 2^31 - 1, 1 <= width <= %d)",
+              static_cast<long long>(rows), static_cast<long long>(items), static_cast<long long>(width), TBE_CROSS_ENTROPY_MAX_ROWS,
+              TBE_CROSS_ENTROPY_MAX_WIDTH);
+    return rows < 0 || items < 1 || width < 1 ? TBE_ERR_ARG : TBE_ERR_UNSUPPORTED;
+  }
+  if (dtype != TBE_F16 && dtype != TBE_BF16) {
+    set_error("cross entropy: type %d (fp16 or bf16)", dtype);
+    return TBE_ERR_UNSUPPORTED;
+  }
+  if (!(scale - scale == 0.0f)) {
+    set_error("cross entropy: scale is not finite");
+    return TBE_ERR_ARG;
+  }
+  tbe_status st = check_matrix("x", x, dtype, rows, width, x_stride);
+  if (st == TBE_OK) st = check_matrix("weight", weight, dtype, items, width, weight_stride);
+  if (st == TBE_OK && bias) st = check_matrix("bias", bias, TBE_F32, 1, items, items);
+  if (st == TBE_OK) st = check_ids("targets", targets, target_type, rows);
+  return st;
+}
+
 }  // namespace
+
+extern "C" size_t tbe_cross_entropy_forward_workspace_bytes(int64_t rows, int64_t items, int64_t width) {
+  return loss_sizes_ok(rows, items, width) ? cross_entropy_forward_workspace(rows, items, width) : 0;
+}
+extern "C" size_t tbe_cross_entropy_backward_workspace_bytes(int64_t rows, int64_t items, int64_t width) {
+  return loss_sizes_ok(rows, items, width) ? cross_entropy_backward_workspace(rows, items, width) : 0;
+}
+
+extern "C" tbe_status tbe_cross_entropy_forward(int64_t rows, int64_t items, int64_t width, const void* x, int64_t x_stride,
+                                                const void* weight, int64_t weight_stride, int32_t dtype, const float* bias,
+                                                const void* targets, int32_t target_type, float scale, float* loss, float* lse,
+                                                void* workspace, size_t workspace_bytes, tbe_stream_t stream) {
+  clear_error();
+  tbe_status st = check_loss(rows, items, width, x, x_stride, weight, weight_stride, dtype, bias, targets, target_type, scale);
+  if (st == TBE_OK) st = check_matrix("loss", loss, TBE_F32, rows, 1, 1);
+  if (st == TBE_OK) st = check_matrix("lse", lse, TBE_F32, rows, 1, 1);
+  if (st != TBE_OK || rows == 0) return st;
+  st = check_workspace("cross entropy", workspace, workspace_bytes, cross_entropy_forward_workspace(rows, items, width));
+  if (st != TBE_OK) return st;
+  return launch_cross_entropy_forward(rows, items, width, x, x_stride, weight, weight_stride, dtype, bias, targets, target_type, scale,
+                                      loss, lse, workspace, static_cast<hipStream_t>(stream));
+}
+
+extern "C" tbe_status tbe_cross_entropy_backward(int64_t rows, int64_t items, int64_t width, const void* x, int64_t x_stride,
+                                                 const void* weight, int64_t weight_stride, int32_t dtype, const float* bias,
+                                                 const void* targets, int32_t target_type, float scale, const float* lse,
+                                                 const float* grad_loss, void* grad_x, int64_t grad_x_stride, void* grad_weight,
+                                                 int64_t grad_weight_stride, float* grad_bias, void* workspace, size_t workspace_bytes,
+                                                 tbe_stream_t stream) {
+  clear_error();
+  tbe_status st = check_loss(rows, items, width, x, x_stride, weight, weight_stride, dtype, bias, targets, target_type, scale);
+  if (st == TBE_OK) st = check_matrix("lse", lse, TBE_F32, rows, 1, 1);
+  if (st == TBE_OK) st = check_matrix("grad_loss", grad_loss, TBE_F32, rows, 1, 1);
+  if (st == TBE_OK && grad_x) st = check_matrix("grad_x", grad_x, dtype, rows, width, grad_x_stride);
+  if (st == TBE_OK && grad_weight) st = check_matrix("grad_weight", grad_weight, dtype, items, width, grad_weight_stride);
+  if (st == TBE_OK && grad_bias) st = check_matrix("grad_bias", grad_bias, TBE_F32, 1, items, items);
+  if (st == TBE_OK)
+    st = check_workspace("cross entropy backward", workspace, workspace_bytes, cross_entropy_backward_workspace(rows, items, width));
+  if (st != TBE_OK || (!grad_x && !grad_weight && !grad_bias)) return st;
+  return launch_cross_entropy_backward(rows, items, width, x, x_stride, weight, weight_stride, dtype, bias, targets, target_type, scale,
+                                       lse, grad_loss, grad_x, grad_x_stride, grad_weight, grad_weight_stride, grad_bias, workspace,
+                                       static_cast<hipStream_t>(stream));
+}
 
 extern "C" tbe_status tbe_lookup_forward(int64_t num_ids, int64_t items, int64_t width, const void* table, int64_t table_stride,
                                          int32_t table_dtype, const void* ids, int32_t id_type, float scale, void* y,

@@ -1,5 +1,5 @@
 """The two ends of a model that reads and predicts the rows of one table (``include/tbe_items.h``): scaled
-lookup of single rows with the table's dense gradient.
+lookup of single rows with the table's dense gradient, softmax cross entropy over all rows with its gradients.
 
 Argument marshalling as in tower.py: torch tensors in, the C entry point of the same name called on the
 current stream, TbeError where it refuses.  What the C interface cannot see, a tensor's shape, strides,
@@ -12,9 +12,11 @@ from typing import Optional
 import torch
 
 from . import _I_DTYPE, _check, lib
-from .tower import _at, _bytes, _current, _device, _dtype, _off_gpu, _refuse, _rows
+from .tower import _at, _bytes, _current, _device, _dtype, _off_gpu, _refuse, _rows, _same, _whole
 
 TBE_ITEMS_MAX_WIDTH = 1 << 20
+TBE_CROSS_ENTROPY_MAX_ROWS = 1 << 22
+TBE_CROSS_ENTROPY_MAX_WIDTH = 1 << 16
 
 
 def _ids(name: str, t: torch.Tensor, dev: int, n: Optional[int] = None) -> int:
@@ -63,3 +65,68 @@ def tbe_lookup_backward(ids: torch.Tensor, grad_y: torch.Tensor, scale: float, g
                                    grad_table.data_ptr(), ts, _dtype("grad_table", grad_table), int(bool(accumulate)),
                                    _at(workspace), _bytes(workspace, dev), _current(stream, dev))
     _check(st, "tbe_lookup_backward")
+
+
+# ---------------------------------------------------------------------------
+# softmax cross entropy over all items
+# ---------------------------------------------------------------------------
+def tbe_cross_entropy_forward_workspace_bytes(rows: int, items: int, width: int) -> int:
+    return int(lib().tbe_cross_entropy_forward_workspace_bytes(int(rows), int(items), int(width)))
+
+
+def _loss_inputs(x, weight, bias, targets, dev):
+    xs = _rows("x", x, dev)
+    rows, width = x.shape
+    ws = _rows("weight", weight, dev)
+    items = weight.shape[0]
+    if weight.shape[1] != width:
+        _refuse(f"weight has shape {tuple(weight.shape)}, x rows of {width}")
+    _same("weight", weight, "x", x.dtype)
+    if bias is not None:
+        _whole("bias", bias, dev, (items,), torch.float32)
+    return rows, items, width, xs, ws, _ids("targets", targets, dev, rows)
+
+
+def tbe_cross_entropy_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor], targets: torch.Tensor,
+                              scale: float, loss: torch.Tensor, lse: torch.Tensor, workspace: Optional[torch.Tensor],
+                              stream=None):
+    """With logits = scale * x @ weight.T + bias: lse[i] = logsumexp(logits[i]), loss[i] = lse[i] -
+    logits[i, targets[i]]; both 0 for a row whose target lies outside the items."""
+    dev = _device()
+    rows, items, width, xs, ws, tt = _loss_inputs(x, weight, bias, targets, dev)
+    _whole("loss", loss, dev, (rows,), torch.float32)
+    _whole("lse", lse, dev, (rows,), torch.float32)
+    st = lib().tbe_cross_entropy_forward(rows, items, width, x.data_ptr(), xs, weight.data_ptr(), ws, _dtype("x", x), _at(bias),
+                                         targets.data_ptr(), tt, scale, loss.data_ptr(), lse.data_ptr(), _at(workspace),
+                                         _bytes(workspace, dev), _current(stream, dev))
+    _check(st, "tbe_cross_entropy_forward")
+
+
+def tbe_cross_entropy_backward_workspace_bytes(rows: int, items: int, width: int) -> int:
+    return int(lib().tbe_cross_entropy_backward_workspace_bytes(int(rows), int(items), int(width)))
+
+
+def tbe_cross_entropy_backward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor], targets: torch.Tensor,
+                               scale: float, lse: torch.Tensor, grad_loss: torch.Tensor, grad_x: Optional[torch.Tensor],
+                               grad_weight: Optional[torch.Tensor], grad_bias: Optional[torch.Tensor],
+                               workspace: Optional[torch.Tensor], stream=None):
+    """The gradients of tbe_cross_entropy_forward's losses, each weighted by grad_loss [rows]; any of the three may be
+    left out (None)."""
+    dev = _device()
+    rows, items, width, xs, ws, tt = _loss_inputs(x, weight, bias, targets, dev)
+    _whole("lse", lse, dev, (rows,), torch.float32)
+    _whole("grad_loss", grad_loss, dev, (rows,), torch.float32)
+    gxs = gws = 0
+    if grad_x is not None:
+        gxs = _rows("grad_x", grad_x, dev, x.shape)
+        _same("grad_x", grad_x, "x", x.dtype)
+    if grad_weight is not None:
+        gws = _rows("grad_weight", grad_weight, dev, weight.shape)
+        _same("grad_weight", grad_weight, "x", x.dtype)
+    if grad_bias is not None:
+        _whole("grad_bias", grad_bias, dev, (items,), torch.float32)
+    st = lib().tbe_cross_entropy_backward(rows, items, width, x.data_ptr(), xs, weight.data_ptr(), ws, _dtype("x", x), _at(bias),
+                                          targets.data_ptr(), tt, scale, lse.data_ptr(), grad_loss.data_ptr(), _at(grad_x), gxs,
+                                          _at(grad_weight), gws, _at(grad_bias), _at(workspace), _bytes(workspace, dev),
+                                          _current(stream, dev))
+    _check(st, "tbe_cross_entropy_backward")

@@ -62,6 +62,60 @@ tbe_status tbe_lookup_backward(int64_t num_ids, int64_t items, int64_t width, co
                                int64_t grad_table_stride, int32_t table_dtype, int32_t accumulate,
                                void* workspace, size_t workspace_bytes, tbe_stream_t stream);
 
+/*
+ * Softmax cross entropy of each row over all items.  x is [rows][width] with
+ * rows x_stride apart, weight [items][width] with rows weight_stride apart,
+ * both of one type, dtype: fp16 or bf16; bias [items] fp32 may be NULL (0).
+ *   logit_iv = scale * (x_i . weight_v) + bias_v
+ *   lse_i    = log (sum over v of exp logit_iv)
+ *   loss_i   = lse_i - logit_{i, target_i}
+ * loss and lse [rows] are fp32.  A row whose target lies outside [0, items) is
+ * left out: its loss and lse are 0 and its x is not looked at.  An item whose
+ * bias is -infinity is masked: its probability is 0, and the loss of a row
+ * with such a target is +infinity; a row with every item masked has lse
+ * -infinity.  A row with an infinity or a NaN gives NaN (or an infinity) in
+ * that row only.  Products, maxima and sums are kept in fp32; the logits go
+ * through registers, a tile of items at a time, and are never stored.  rows may
+ * be 0 and at most TBE_CROSS_ENTROPY_MAX_ROWS; 1 <= items < 2^31 - 1;
+ * 1 <= width <= TBE_CROSS_ENTROPY_MAX_WIDTH.  workspace: at least
+ * tbe_cross_entropy_forward_workspace_bytes bytes, 256-byte aligned; the bytes
+ * grow with the rows, so one for the largest batch serves every smaller one.
+ */
+#define TBE_CROSS_ENTROPY_MAX_ROWS (1 << 22)
+#define TBE_CROSS_ENTROPY_MAX_WIDTH (1 << 16)
+size_t tbe_cross_entropy_forward_workspace_bytes(int64_t rows, int64_t items, int64_t width);
+tbe_status tbe_cross_entropy_forward(int64_t rows, int64_t items, int64_t width, const void* x,
+                                     int64_t x_stride, const void* weight, int64_t weight_stride,
+                                     int32_t dtype, const float* bias, const void* targets,
+                                     int32_t target_type, float scale, float* loss, float* lse,
+                                     void* workspace, size_t workspace_bytes, tbe_stream_t stream);
+
+/*
+ * Backward of tbe_cross_entropy_forward, with its inputs and its lse.  With
+ *   z_iv = grad_loss_i * (exp(logit_iv - lse_i) - [v = target_i])
+ * for the rows that have a target and 0 for the others,
+ *   grad_x_i      = scale * sum over v of z_iv weight_v
+ *   grad_weight_v = scale * sum over i of z_iv x_i
+ *   grad_bias_v   = sum over i of z_iv.
+ * Any of the three may be NULL.  grad_x and grad_weight are of type dtype with
+ * strides of their own, grad_bias [items] is fp32; all are overwritten (zeros
+ * for rows without a target).  The logits are computed again, a piece of the
+ * items at a time.  exp(...) - [...] is rounded to dtype for its two products,
+ * as x times grad_loss over the largest |grad_loss| is (exactly x where all
+ * are equal); sums are kept in fp32 and rounded once.  In fp16 probabilities
+ * keep their digits down to 2^-29, and the weights' gradient those of rows
+ * whose |grad_loss| is not below 2^-14 of the largest.
+ */
+size_t tbe_cross_entropy_backward_workspace_bytes(int64_t rows, int64_t items, int64_t width);
+tbe_status tbe_cross_entropy_backward(int64_t rows, int64_t items, int64_t width, const void* x,
+                                      int64_t x_stride, const void* weight, int64_t weight_stride,
+                                      int32_t dtype, const float* bias, const void* targets,
+                                      int32_t target_type, float scale, const float* lse,
+                                      const float* grad_loss, void* grad_x, int64_t grad_x_stride,
+                                      void* grad_weight, int64_t grad_weight_stride,
+                                      float* grad_bias, void* workspace, size_t workspace_bytes,
+                                      tbe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
