@@ -44,7 +44,7 @@ struct CeArgs {
   // products of z
   const void* xg;          // x * grad_loss / largest, like x
   float* sum;              // [splits][rows or items][width] fp32 sums
-  int32_t splits;
+  int32_t splits;          // of k; of the items for narrow rows
   int32_t add;             // to what is there
   void* out;               // gradient of the weights, the piece's first item, with one split
   int64_t out_stride;
@@ -53,12 +53,22 @@ struct CeArgs {
 // z is stored times this, so that fp16 holds probabilities down to 2^-29 as normal numbers.
 template <int DT> constexpr float kUnit = DT == 1 ? 32768.0f : 1.0f;
 
+constexpr float kInfinity = __builtin_huge_valf();
+
+// Two parts of a row: their maximum, and the sum of the exponentials less it.
+__device__ __forceinline__ float2 ce_join(float2 a, float2 b) {
+  const float top = fmaxf(a.x, b.x), from = top == -kInfinity ? 0.0f : top;
+  return make_float2(top, a.y * expf(a.x - from) + b.y * expf(b.x - from));
+}
+
 // A tile of C and how it is walked, as for the grouped layers.
 enum { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
 
 // Defined in translation units of their own (cross_entropy_forward_f16.hip and its siblings).
 template <int DT> tbe_status ce_launch_forward(const CeArgs& a, int tile, bool direct, hipStream_t s);
 template <int DT> tbe_status ce_launch_z(const CeArgs& a, int tile, bool direct, hipStream_t s);
+template <int DT> tbe_status ce_launch_narrow_forward(const CeArgs& a, bool few, hipStream_t s);
+template <int DT> tbe_status ce_launch_narrow_z(const CeArgs& a, bool few, hipStream_t s);
 template <int DT> tbe_status ce_launch_grad_x(const CeArgs& a, int tile, bool direct, hipStream_t s);
 template <int DT> tbe_status ce_launch_grad_w(const CeArgs& a, int tile, hipStream_t s);
 

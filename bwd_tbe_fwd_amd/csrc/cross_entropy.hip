@@ -8,8 +8,6 @@
 namespace tbe {
 namespace {
 
-constexpr float kInf = __builtin_huge_valf();
-
 // ---------------------------------------------------------------------------
 // the rows that have a target
 // ---------------------------------------------------------------------------
@@ -92,7 +90,7 @@ __global__ __launch_bounds__(kBlock) void ce_list_kernel(CeBatch b) {
 // wave a row.
 template <int DT>
 __global__ __launch_bounds__(kBlock) void ce_copy_kernel(const CeBatch b, const uint16_t* __restrict__ x, int64_t stride, int width,
-                                                         int pitch, uint16_t* __restrict__ xc, uint16_t* __restrict__ xg) {
+                                                         int pitch, int negate, uint16_t* __restrict__ xc, uint16_t* __restrict__ xg) {
   const int count = *b.count, l = lane_id();
   for (int64_t c = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6); c < count;
        c += static_cast<int64_t>(gridDim.x) * kWavesPerBlock) {
@@ -101,12 +99,15 @@ __global__ __launch_bounds__(kBlock) void ce_copy_kernel(const CeBatch b, const 
     for (int d = l * 8; d < pitch; d += kWave * 8) {
       Vec<uint16_t, 8> v;
       load_vec_part<uint16_t, 8>(p + d, width - d, v);
-      if (xc) store_vec_any<uint16_t, 8>(xc + c * pitch + d, v);
       if (xg) {
+        Vec<uint16_t, 8> u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v.e[e] = tower_from_f<DT>(Fmt<DT>::to_f(v.e[e]) * g);
-        store_vec_any<uint16_t, 8>(xg + c * pitch + d, v);
+        for (int e = 0; e < 8; ++e) u.e[e] = tower_from_f<DT>(Fmt<DT>::to_f(v.e[e]) * g);
+        store_vec_any<uint16_t, 8>(xg + c * pitch + d, u);
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v.e[e] ^= negate ? 0x8000 : 0;
+      store_vec_any<uint16_t, 8>(xc + c * pitch + d, v);
     }
   }
 }
@@ -114,11 +115,6 @@ __global__ __launch_bounds__(kBlock) void ce_copy_kernel(const CeBatch b, const 
 // ---------------------------------------------------------------------------
 // joins
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float2 join(float2 a, float2 b) {
-  const float top = fmaxf(a.x, b.x), from = top == -kInf ? 0.0f : top;
-  return make_float2(top, a.y * expf(a.x - from) + b.y * expf(b.x - from));
-}
-
 // A piece's maxima and sums of each row, its tiles in a fixed order, joined with the pieces before: 16 rows a workgroup, 64
 // groups of 16 lanes.  The last piece's ends in the loss.
 constexpr int kJoinRows = 16, kJoinGroups = 64;
@@ -128,27 +124,28 @@ __global__ __launch_bounds__(kJoinRows * kJoinGroups) void ce_join_kernel(const 
   __shared__ float2 s_all[kJoinGroups][kJoinRows + 1];
   const int q = threadIdx.x / kJoinRows, k = threadIdx.x % kJoinRows, count = *b.count;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * kJoinRows + k;
-  float2 sum = make_float2(-kInf, 0.0f);
+  float2 sum = make_float2(-kInfinity, 0.0f);
   if (c < count) {
 #pragma unroll 4
-    for (int t = q; t < tiles; t += kJoinGroups) sum = join(sum, part[t * rows + c]);
+    for (int t = q; t < tiles; t += kJoinGroups) sum = ce_join(sum, part[t * rows + c]);
   }
   s_all[q][k] = sum;
   __syncthreads();
   for (int n = kJoinGroups / 2; n > 0; n /= 2) {
-    if (q < n) s_all[q][k] = join(s_all[q][k], s_all[q + n][k]);
+    if (q < n) s_all[q][k] = ce_join(s_all[q][k], s_all[q + n][k]);
     __syncthreads();
   }
   if (q || c >= count) return;
   sum = s_all[0][k];
-  if (!first) sum = join(all[c], sum);
+  if (!first) sum = ce_join(all[c], sum);
   if (!last) {
     all[c] = sum;
     return;
   }
-  const float lse = sum.x + logf(sum.y), at = picked[c];  // every item masked: -inf + log 0
+  // no sum is left where every item is masked, or by the lowest value
+  const float lse = sum.y == 0.0f ? sum.x : sum.x + logf(sum.y), at = picked[c];
   b.lse_out[b.row[c]] = lse;
-  b.loss[b.row[c]] = at == -kInf && !(lse != lse) ? kInf : lse - at;
+  b.loss[b.row[c]] = at == -kInfinity && !(lse != lse) ? kInfinity : lse - at;
 }
 
 // The rows' gradients: the parts' sums times scale * grad_loss; zero for a row without a target.
@@ -227,6 +224,9 @@ __global__ __launch_bounds__(1024) void ce_grad_bias_kernel(const float* __restr
 constexpr int64_t kPartBytes = int64_t{64} << 20;    // forward: of the rows' maxima and sums over a piece's tiles
 constexpr int64_t kZElems = int64_t{1} << 27;        // backward: of z
 constexpr int64_t kLeastPiece = 1024, kMostPiece = 131072;  // items of a piece, backward
+// rows of z lie a cache line further apart than their items need: at a power of two apart, the rows of a tile meet in the
+// same sets and channels
+constexpr int64_t kZPad = 64;
 constexpr int64_t kSumBytes = int64_t{128} << 20;    // of the sums over shares of k, beyond one share of x's gradient
 constexpr int kMostSplits = 16;
 
@@ -281,7 +281,7 @@ CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   const int64_t all = up(items, 256), most = hmin(all, kMostPiece);
   L.piece = hmin(most, hmax(kLeastPiece, kZElems / hmax(rows, 1) / 256 * 256));
   const int64_t z = hmin(rows * most, hmax(kZElems, rows * kLeastPiece));
-  L.z = c.take(z * 2);
+  L.z = c.take((z + rows * kZPad) * 2);
   L.sum_x = c.take(hmax(rows * width * 4, hmin(kSumBytes, kMostSplits * rows * width * 4)));
   L.sum_w = c.take(kSumBytes);
   L.bias_part = c.take(z / 64 * 4 + most * 4);
@@ -314,6 +314,15 @@ TilePick pick_tile(const TileCost (&costs)[3], int64_t m, int64_t n, int64_t k, 
 // Costs of the kernels here: grouped_linear.h's, with square tiles through registers as well.
 constexpr TileCost kAlongRegisters[3] = {{256, 256, 512, 256, 6.0, 1.3, 2.05}, {128, 128, 256, 512, 5.0, 0.8, 1.5}, {64, 64, 256, 1024, 3.0, 0.55, 1.35}};
 
+// Rows of up to so many columns stay in registers (cross_entropy_narrow.h).
+constexpr int64_t kNarrowWidth = 128;
+// Into how many ranges their items go: about 2048 workgroups, of 16 tiles of 64 items at least, of fewer where that leaves
+// CUs idle.
+int narrow_splits(int64_t rows, int64_t items, bool few) {
+  const int64_t row_tiles = few ? 1 : (rows + 255) / 256, tiles = (items + 63) / 64;
+  return static_cast<int>(hmax(1, hmin(tiles, hmin(2048 / row_tiles, hmax(tiles / 16, 512 / row_tiles)))));
+}
+
 bool whole_16(const void* p, int64_t stride, int64_t width) {
   return !(reinterpret_cast<uintptr_t>(p) & 15) && stride % 8 == 0 && width % 8 == 0 && stride < (int64_t{1} << 21);
 }
@@ -329,8 +338,8 @@ CeBatch batch_of(char* ws, const CeLayout& L, int64_t rows, int64_t items, const
   b.target = reinterpret_cast<int32_t*>(ws + L.target);
   return b;
 }
-tbe_status launch_rows(const CeBatch& b, const void* x, int64_t x_stride, int64_t width, int64_t pitch, int dtype, void* xc, void* xg,
-                       hipStream_t s) {
+tbe_status launch_rows(const CeBatch& b, const void* x, int64_t x_stride, int64_t width, int64_t pitch, int dtype, bool negate, void* xc,
+                       void* xg, hipStream_t s) {
   const unsigned blocks = static_cast<unsigned>(hmax(1, (b.rows + kBlock - 1) / kBlock));  // no rows: their count, 0
   ProfScope ps("ce_rows", s);
   hipLaunchKernelGGL(ce_count_kernel, dim3(blocks), dim3(kBlock), 0, s, b);
@@ -338,7 +347,7 @@ tbe_status launch_rows(const CeBatch& b, const void* x, int64_t x_stride, int64_
   const unsigned groups = static_cast<unsigned>(hmax(1, hmin((b.rows + kWavesPerBlock - 1) / kWavesPerBlock, 8192)));
   auto kernel = dtype == TBE_F16 ? ce_copy_kernel<1> : ce_copy_kernel<2>;
   hipLaunchKernelGGL(kernel, dim3(groups), dim3(kBlock), 0, s, b, static_cast<const uint16_t*>(x), x_stride, static_cast<int>(width),
-                     static_cast<int>(pitch), static_cast<uint16_t*>(xc), static_cast<uint16_t*>(xg));
+                     static_cast<int>(pitch), negate ? 1 : 0, static_cast<uint16_t*>(xc), static_cast<uint16_t*>(xg));
   return check_launch("ce_rows");
 }
 CeRows rows_of(const CeBatch& b) { return CeRows{b.count, b.row, b.target, b.lse, b.grad, b.largest}; }
@@ -356,28 +365,39 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
   CeBatch b = batch_of(ws, L, rows, items, targets, target_type);
   b.loss = loss;
   b.lse_out = lse;
-  tbe_status st = launch_rows(b, x, x_stride, width, L.pitch, dtype, ws + L.xc, nullptr, s);
-  const bool direct = whole_16(weight, weight_stride, width);
+  const bool direct = whole_16(weight, weight_stride, width), narrow = direct && width <= kNarrowWidth;
+  // the narrow kernel looks for the largest product: a negative factor goes into x
+  const bool negate = narrow && !bias && scale < 0.0f;
+  if (negate) scale = -scale;
+  tbe_status st = launch_rows(b, x, x_stride, width, L.pitch, dtype, negate, ws + L.xc, nullptr, s);
   CeArgs a = {};
   a.rows = rows; a.width = static_cast<int>(width);
   a.x = ws + L.xc; a.x_stride = L.pitch;
   a.w_stride = weight_stride; a.scale = scale; a.r = rows_of(b);
   a.part = reinterpret_cast<float2*>(ws + L.part);
   a.picked = reinterpret_cast<float*>(ws + L.picked);
-  for (int64_t first = 0; st == TBE_OK && first < items; first += L.piece) {
+  const int64_t piece = narrow ? items : L.piece;
+  for (int64_t first = 0; st == TBE_OK && first < items; first += piece) {
     a.first = static_cast<int>(first);
-    a.items = static_cast<int>(hmin(L.piece, items - first));
+    a.items = static_cast<int>(hmin(piece, items - first));
     a.w = static_cast<const uint16_t*>(weight) + first * weight_stride;
     a.bias = bias ? bias + first : nullptr;
-    const TileCost(&costs)[3] = direct ? kDirectTiles : kAlongRegisters;
-    const int tile = pick_tile(costs, rows, a.items, width, 1, 0).tile;
-    st = dtype == TBE_F16 ? ce_launch_forward<1>(a, tile, direct, s) : ce_launch_forward<2>(a, tile, direct, s);
+    int parts;  // of a row
+    if (narrow) {
+      const bool few = rows <= 64;
+      parts = a.splits = narrow_splits(rows, a.items, few);
+      st = dtype == TBE_F16 ? ce_launch_narrow_forward<1>(a, few, s) : ce_launch_narrow_forward<2>(a, few, s);
+    } else {
+      const TileCost(&costs)[3] = direct ? kDirectTiles : kAlongRegisters;
+      const int tile = pick_tile(costs, rows, a.items, width, 1, 0).tile;
+      parts = (a.items + costs[tile].bn - 1) / costs[tile].bn;
+      st = dtype == TBE_F16 ? ce_launch_forward<1>(a, tile, direct, s) : ce_launch_forward<2>(a, tile, direct, s);
+    }
     if (st != TBE_OK) break;
     ProfScope ps("ce_join", s);
-    const int bn = costs[tile].bn;
     hipLaunchKernelGGL(ce_join_kernel, dim3(static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows)), dim3(kJoinRows * kJoinGroups), 0, s,
-                       a.part, rows, (a.items + bn - 1) / bn, reinterpret_cast<float2*>(ws + L.all), first == 0 ? 1 : 0,
-                       first + L.piece >= items ? 1 : 0, a.picked, b);
+                       a.part, rows, parts, reinterpret_cast<float2*>(ws + L.all), first == 0 ? 1 : 0, first + piece >= items ? 1 : 0,
+                       a.picked, b);
     st = check_launch("ce_join");
   }
   return st;
@@ -395,14 +415,14 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   b.slot = reinterpret_cast<int32_t*>(ws + L.slot);
   b.lse = reinterpret_cast<float*>(ws + L.lse);
   b.grad = reinterpret_cast<float*>(ws + L.grad);
-  tbe_status st = launch_rows(b, x, x_stride, width, L.pitch, dtype, ws + L.xc, grad_weight ? ws + L.xg : nullptr, s);
-  const bool direct = whole_16(weight, weight_stride, width);
+  tbe_status st = launch_rows(b, x, x_stride, width, L.pitch, dtype, false, ws + L.xc, grad_weight ? ws + L.xg : nullptr, s);
+  const bool direct = whole_16(weight, weight_stride, width), narrow = direct && width <= kNarrowWidth;
   const bool f16 = dtype == TBE_F16;
   CeArgs a = {};
   a.rows = rows; a.width = static_cast<int>(width);
   a.x = ws + L.xc; a.x_stride = L.pitch; a.xg = ws + L.xg;
   a.w_stride = weight_stride; a.scale = scale; a.r = rows_of(b);
-  a.z = reinterpret_cast<uint16_t*>(ws + L.z); a.z_stride = L.piece;
+  a.z = reinterpret_cast<uint16_t*>(ws + L.z); a.z_stride = L.piece + kZPad;
   a.bias_part = grad_bias ? reinterpret_cast<float*>(ws + L.bias_part) : nullptr;
   a.bias_stride = L.piece;
   const TileCost(&costs)[3] = direct ? kDirectTiles : kAlongRegisters;
@@ -414,12 +434,20 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
     a.items = static_cast<int>(hmin(L.piece, items - first));
     a.w = static_cast<const uint16_t*>(weight) + first * weight_stride;
     a.bias = bias ? bias + first : nullptr;
-    const int tile = pick_tile(costs, rows, a.items, width, 1, 0).tile;
-    if (rows > 0) st = f16 ? ce_launch_z<1>(a, tile, direct, s) : ce_launch_z<2>(a, tile, direct, s);
+    int bm = 64;  // rows that a part of the biases' gradient sums over
+    if (rows > 0 && narrow) {
+      const bool few = rows <= 64;
+      a.splits = narrow_splits(rows, a.items, few);
+      st = f16 ? ce_launch_narrow_z<1>(a, few, s) : ce_launch_narrow_z<2>(a, few, s);
+    } else if (rows > 0) {
+      const int tile = pick_tile(costs, rows, a.items, width, 1, 0).tile;
+      bm = costs[tile].bm;
+      st = f16 ? ce_launch_z<1>(a, tile, direct, s) : ce_launch_z<2>(a, tile, direct, s);
+    }
     if (st == TBE_OK && grad_bias) {
       ProfScope ps("ce_grad_bias", s);
       hipLaunchKernelGGL(ce_grad_bias_kernel, dim3(static_cast<unsigned>((a.items + kWave - 1) / kWave)), dim3(1024), 0, s, a.bias_part,
-                         a.bias_stride, b.count, costs[tile].bm, a.items, grad_bias + first);
+                         a.bias_stride, b.count, bm, a.items, grad_bias + first);
       st = check_launch("ce_grad_bias");
     }
     if (st == TBE_OK && grad_x) {

@@ -7,7 +7,6 @@
 namespace tbe {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kInfinity = __builtin_huge_valf();
 
 // Workgroup blockIdx.x's place among m_tiles x n_tiles: a contiguous share for each chiplet, and in it bands of 8 tiles of m
 // walked along n, so that the 32 workgroups that a chiplet runs at once read 8 + 4 tiles of operands and not 1 + 32.  False:
@@ -90,11 +89,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
     __syncthreads();
     for (int m = threadIdx.x; m < BM; m += T) {
       float2 all = stat[m];
-      for (int k = 1; k < WN; ++k) {
-        const float2 s = stat[k * BM + m];
-        const float top = fmaxf(all.x, s.x), from = top == -kInfinity ? 0.0f : top;
-        all = make_float2(top, all.y * __builtin_amdgcn_exp2f((all.x - from) * kLog2e) + s.y * __builtin_amdgcn_exp2f((s.x - from) * kLog2e));
-      }
+      for (int k = 1; k < WN; ++k) all = ce_join(all, stat[k * BM + m]);
       if (m < m_left) a.part[t.n * a.rows + m0 + m] = all;
     }
   } else {

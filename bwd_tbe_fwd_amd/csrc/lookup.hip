@@ -10,7 +10,7 @@
 // The backward sorts the positions by id, stably, and walks the sorted positions once.  Overwriting, it walks the merged
 // sequence of positions and of the rows' ends (row v's end follows its last position), so that one pass writes the sums and
 // the zeros between them; adding, the positions alone.  That sequence is cut into shares of equal length, whatever the
-// ids' popularity; a share finds its start by a search of d = i + key_i.  A row that a cut would split within its last 64
+// ids' popularity; a share finds its start by a search of d = i + key_i.  A row that a cut would split within its last 31
 // positions stays with the share before, so most rows are summed and rounded where they are read; of the others each share
 // leaves its sum in the workspace, and the share in which the row ends has them joined, in order.
 #include "items.h"
@@ -23,7 +23,7 @@ namespace {
 constexpr int kVec = 8;        // columns of a lane
 constexpr int kFlight = 4;     // forward: rows of a group of lanes whose loads are under way together
 constexpr int kWalk = 8;       // backward: the same
-constexpr int kKeep = 64;      // positions of a row at most that a share takes over from the next one
+constexpr int kKeep = 32;      // positions of a row at most, less one, that a share takes over from the next one
 constexpr int kRankMost = 4096;  // ids that are sorted by counting, in one launch
 
 template <int DT>
@@ -182,6 +182,8 @@ struct LookupGradArgs {
   int32_t shares;
   float* part;               // [shares][2][width]: the sum of a row that began before the share and ends in it, of one that
                              // goes on behind it
+  int32_t* begun;            // [shares] of such a first row, the share in which it began; -1: none ends here
+  int32_t* row;              // [shares] and which row it is
   Columns c;
 };
 
@@ -234,7 +236,7 @@ __device__ __forceinline__ Cut cut_at(const LookupGradArgs& a, int64_t n, int64_
 #pragma unroll
     for (int k = 0; k < kKeep; k += G) {
       const int64_t i = c.i + k + l;
-      more += __popcll(group_ballot<G>(i < n && a.keys[i] == c.row));
+      more += __popcll(group_ballot<G>(k + l < kKeep && i < n && a.keys[i] == c.row));
     }
     if (more == kKeep) {
       c.split = true;
@@ -258,6 +260,19 @@ __global__ __launch_bounds__(kBlock) void lookup_sum_kernel(LookupGradArgs a) {
   // all lanes take part in the searches
   const Cut from = cut_at<G>(a, n, d), to = cut_at<G>(a, n, share + 1 < a.shares ? d + a.share : n + a.items);
   if (share >= a.shares) return;
+  if (blockIdx.y == 0) {
+    // a row that began earlier and ends here: the share that has its first position, whose place in the sequence is i + row, or
+    // i (a share whose end was moved behind that place would not have split the row)
+    int32_t begun = -1;
+    if (from.split && !(to.split && to.row == from.row)) {
+      const int64_t i = first_at_least<G>(0, n, from.row, [&](int64_t k) { return static_cast<int64_t>(a.keys[k]); });
+      begun = static_cast<int32_t>((a.add ? i : i + from.row) / a.share);
+    }
+    if (l == 0) {
+      a.begun[share] = begun;
+      a.row[share] = static_cast<int32_t>(from.row);
+    }
+  }
   const int64_t c = static_cast<int64_t>(blockIdx.y) * a.c.cols + l * kVec;
   const int left = l * kVec < a.c.cols ? static_cast<int>(min(a.c.width - c, static_cast<int64_t>(kVec))) : 0;
   if (left <= 0) return;
@@ -342,47 +357,47 @@ __global__ __launch_bounds__(kBlock) void lookup_sum_kernel(LookupGradArgs a) {
   if (!a.add) zeros(row, to.row);
 }
 
-// Joins the sums of a row that several shares have parts of: a workgroup for each share (blockIdx.x, from 1 on) that
-// finds one ending in it, 256 columns each.  16 waves add the shares' sums, each wave a contiguous part of them, then the
-// waves' sums are added in order.
+// Joins the sums of the rows that several shares have parts of: a workgroup looks at 64 shares for those in which such a row
+// ends, 256 columns of it.  16 waves add the shares' sums, each wave a contiguous part of them, then the waves' sums are
+// added in order.  (A workgroup for every share took 105 us where few had anything to join.)
 template <int WT>
 __global__ __launch_bounds__(1024) void lookup_join_kernel(LookupGradArgs a) {
   using SW = typename Fmt<WT>::S;
   constexpr int kWaves = 16, kCols = 4 * kWave;
   __shared__ __align__(16) float s_sum[kWaves][kCols];
-  const int64_t share = blockIdx.x + 1;
-  const int64_t n = *a.n_sorted, d = share * a.share;
-  const Cut from = cut_at<kWave>(a, n, d);
-  if (!from.split) return;
-  const Cut to = cut_at<kWave>(a, n, share + 1 < a.shares ? d + a.share : n + a.items);
-  if (to.split && to.row == from.row) return;  // the row goes on
-  // the share that has the row's first position: its place in the sequence is i + row, or i; a share whose end was moved
-  // behind that place does not split the row, so the row is in that share
-  const int64_t i0 = first_at_least<kWave>(0, n, from.row, [&](int64_t i) { return static_cast<int64_t>(a.keys[i]); });
-  const int64_t first = (a.add ? i0 : i0 + from.row) / a.share;
   const int w = threadIdx.x / kWave, l = lane_id();
   const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + 4 * l;
   const int left = static_cast<int>(min(max(a.c.width - c, int64_t{0}), int64_t{4}));
-  // parts: the shares' from `first` to the one before, then this one's
-  const int64_t parts = share - first + 1, each = (parts + kWaves - 1) / kWaves;
-  f32x4 sum = {0, 0, 0, 0};
-  if (left > 0) {
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kWave;
+  const int32_t mine = base + l < a.shares ? a.begun[base + l] : -1;
+  for (uint64_t found = __ballot(mine >= 0); found; found &= found - 1) {
+    const int at = __ffsll(static_cast<unsigned long long>(found)) - 1;
+    const int64_t share = base + at, first = read_lane(mine, at);
+    // parts: the shares' from `first` to the one before, then this one's
+    const int64_t parts = share - first + 1, each = (parts + kWaves - 1) / kWaves;
+    f32x4 sum = {0, 0, 0, 0};
+    if (left > 0) {
+      const int64_t end = (w + 1) * each < parts ? (w + 1) * each : parts;
 #pragma unroll 8
-    for (int64_t k = w * each; k < min(parts, (w + 1) * each); ++k) {
-      Vec<float, 4> v;
-      load_vec_part<float, 4>(a.part + ((first + k) * 2 + (k + 1 < parts ? 1 : 0)) * a.c.width + c, left, v);
+      for (int64_t k = w * each; k < end; ++k) {
+        Vec<float, 4> v;
+        load_vec_part<float, 4>(a.part + ((first + k) * 2 + (k + 1 < parts ? 1 : 0)) * a.c.width + c, left, v);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] += v.e[e];
+        for (int e = 0; e < 4; ++e) sum[e] += v.e[e];
+      }
     }
-  }
-  *reinterpret_cast<f32x4*>(&s_sum[w][4 * l]) = sum;
-  __syncthreads();
-  if (w > 0 || left <= 0) return;
-  for (int k = 1; k < kWaves; ++k) sum += *reinterpret_cast<const f32x4*>(&s_sum[k][4 * l]);
-  SW* p = static_cast<SW*>(a.grad) + from.row * a.grad_stride + c;
+    *reinterpret_cast<f32x4*>(&s_sum[w][4 * l]) = sum;
+    __syncthreads();
+    if (w == 0 && left > 0) {
+      for (int k = 1; k < kWaves; ++k) sum += *reinterpret_cast<const f32x4*>(&s_sum[k][4 * l]);
+      const int64_t row = a.row[share];
+      SW* p = static_cast<SW*>(a.grad) + row * a.grad_stride + c;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (e < left) p[e] = tower_from_f<WT>(a.add ? Fmt<WT>::to_f(p[e]) + sum[e] * a.scale : sum[e] * a.scale);
+      for (int e = 0; e < 4; ++e) {
+        if (e < left) p[e] = tower_from_f<WT>(a.add ? Fmt<WT>::to_f(p[e]) + sum[e] * a.scale : sum[e] * a.scale);
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -417,28 +432,33 @@ tbe_status by_lanes(int lanes, F f) {
   return f(std::integral_constant<int, 64>{});
 }
 
-// Shares: of 128, shorter ones where that leaves fewer than 4096, longer ones from 65536 shares on.  And how many there are
-// at most for any sequence up to this length: a workspace serves every smaller batch.
-constexpr int kLeastShare = 16, kShare = 128, kFewShares = 4096, kMostShares = 65536;
-int share_of(int64_t all) {
-  return static_cast<int>(hmax((all + kMostShares - 1) / kMostShares, hmin(kShare, hmax(kLeastShare, all / kFewShares))));
+// Length of a share, so that there are about kFewWaves waves (a group of lanes takes a share of a part of the columns), and how
+// many shares there are at most for any sequence up to this length: a workspace serves every smaller batch.
+constexpr int64_t kLeastShare = 16, kLongShare = 128, kFewWaves = 8192, kMostShares = 1 << 18;
+int64_t share_of(int64_t all, const Split& s) {
+  const int64_t even = all * s.lanes / kWave * s.parts / kFewWaves;
+  return hmax((all + kMostShares - 1) / kMostShares, hmin(kLongShare, hmax(kLeastShare, even)));
 }
-int64_t shares_bound(int64_t all) {
-  const int64_t least = (all + kLeastShare - 1) / kLeastShare, few = kFewShares + kFewShares / kLeastShare;
-  return hmin(least, hmax(few, hmin(kMostShares, (all + kShare - 1) / kShare)));
+int64_t shares_bound(int64_t all, const Split& s) {
+  // even = k: all >= k * unit, so ceil(all / k) <= all / k + 1 < unit * (k + 1) / k + 2
+  const int64_t unit = (kFewWaves * kWave + s.lanes * s.parts - 1) / (s.lanes * s.parts);
+  const int64_t least = (all + kLeastShare - 1) / kLeastShare, few = unit + unit / kLeastShare + 2;
+  return hmin(least, hmax(few, hmin(kMostShares, (all + kLongShare - 1) / kLongShare)));
 }
 
 // The workspace: sorted pairs twice, the sort's counts, the shares' sums.
 struct LookupPlan {
   int64_t seg, shares;
   int nblocks, share;
-  size_t keys[2], pay[2], hist, n_sorted, part, total;
+  size_t keys[2], pay[2], hist, n_sorted, begun, row, part, total;
 };
 LookupPlan lookup_plan(int64_t n, int64_t items, int64_t width, bool add) {
   LookupPlan p = {};
   sort_segments(n, &p.seg, &p.nblocks);
   const int64_t all = add ? n : n + items, tiles = (n + kRadixTile - 1) / kRadixTile;
-  p.share = share_of(all);
+  const Split sp = split_of(width);
+  const int64_t bound = shares_bound(n + items, sp);
+  p.share = static_cast<int>(share_of(all, sp));
   p.shares = (all + p.share - 1) / p.share;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -452,7 +472,9 @@ LookupPlan lookup_plan(int64_t n, int64_t items, int64_t width, bool add) {
   }
   p.hist = take(static_cast<size_t>(kRadixDigits) * (hmin(tiles, kMaxSortBlocks) + 1) * 4);
   p.n_sorted = take(4);
-  p.part = take(static_cast<size_t>(shares_bound(n + items)) * 2 * width * 4);
+  p.begun = take(bound * 4);
+  p.row = take(bound * 4);
+  p.part = take(static_cast<size_t>(bound) * 2 * width * 4);
   p.total = at;
   return p;
 }
@@ -522,6 +544,7 @@ tbe_status launch_lookup_backward(int64_t n, int64_t items, int64_t width, const
   a.scale = scale; a.grad = grad; a.grad_stride = grad_stride; a.add = add;
   a.stream = !add && rows_on_16(grad, grad_stride, table_dtype);
   a.share = p.share; a.shares = static_cast<int32_t>(p.shares); a.part = reinterpret_cast<float*>(ws + p.part); a.c = sp.c;
+  a.begun = reinterpret_cast<int32_t*>(ws + p.begun); a.row = reinterpret_cast<int32_t*>(ws + p.row);
   st = by_type(y_dtype, [&](auto yt) {
     return by_type(table_dtype, [&](auto wt) {
       return by_lanes(sp.lanes, [&](auto g) {
@@ -533,12 +556,12 @@ tbe_status launch_lookup_backward(int64_t n, int64_t items, int64_t width, const
       });
     });
   });
-  // a row has more than kKeep positions on the far side of a cut that splits it
+  // a row has kKeep positions at least on the far side of a cut that splits it
   if (st != TBE_OK || p.shares < 2 || n <= kKeep) return st;
   return by_type(table_dtype, [&](auto wt) {
     ProfScope ps("lookup_join", s);
     hipLaunchKernelGGL((lookup_join_kernel<decltype(wt)::value>),
-                       dim3(static_cast<unsigned>(p.shares - 1), static_cast<unsigned>((width + 4 * kWave - 1) / (4 * kWave))), dim3(1024), 0, s, a);
+                       dim3(static_cast<unsigned>((p.shares + kWave - 1) / kWave), static_cast<unsigned>((width + 4 * kWave - 1) / (4 * kWave))), dim3(1024), 0, s, a);
     return check_launch("lookup_join");
   });
 }
