@@ -31,14 +31,13 @@ struct CeArgs {
   int64_t x_stride;
   const void* w;           // the piece's first item
   int64_t w_stride;
-  const float* bias;       // the piece's; NULL: none
+  const float* bias;       // the piece's; NULL: none; for narrow rows over the scale
   float scale;
   CeRows r;
   int32_t first, items;    // of the piece
   float2* part;            // forward: [tiles of items][rows] maximum and sum
-  float* picked;           // forward: [rows] the target's logit
-  uint16_t* z;             // backward: [rows][z_stride]
-  int64_t z_stride;
+  uint16_t* z;             // backward: panels of 64 items, each [rows][64], `panel` elements apart
+  int64_t panel;
   float* bias_part;        // backward: [tiles of rows][items of a piece at most]; NULL: none
   int64_t bias_stride;
   // products of z
@@ -46,6 +45,7 @@ struct CeArgs {
   float* sum;              // [splits][rows or items][width] fp32 sums
   int32_t splits;          // of k; of the items for narrow rows
   int32_t add;             // to what is there
+  float factor;            // of a product of z
   void* out;               // gradient of the weights, the piece's first item, with one split
   int64_t out_stride;
 };

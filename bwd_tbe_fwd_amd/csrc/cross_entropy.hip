@@ -15,19 +15,34 @@ struct CeBatch {
   int64_t rows, items;
   const void* targets;
   int32_t target64;
-  const float* grad_loss;  // backward, else NULL
-  const float* lse_in;     // backward
-  float* loss;             // forward: 0 for the rows without a target
-  float* lse_out;
-  int32_t* counts;         // per kBlock rows: of those with a target
+  int32_t width, pitch;
+  const uint16_t* x;
+  int64_t x_stride;
+  uint16_t* xc;            // x of the rows with a target side by side, rows of `pitch` (whole 16 bytes, zeros behind the width)
+  int32_t flip;            // 0: as it is, 1: negated, 2: zeros
+  int32_t* counts;         // many rows: of each 256, how many have a target
   float* tops;             // and their largest |grad_loss|
   int32_t* count;
   float* largest;
   int32_t* row;
   int32_t* target;
-  int32_t* slot;           // backward: of every row, -1: none
+  const float* bias;       // NULL: none
+  float* bias_over;        // the biases over the scale; NULL: not asked for
+  float over;              // 1 / scale
+  // forward
+  const uint16_t* w;
+  int64_t w_stride;
+  float scale;
+  float* picked;           // the target's logit
+  float* loss;             // 0 for the rows without a target
+  float* lse_out;
+  // backward
+  const float* grad_loss;
+  const float* lse_in;
+  int32_t* slot;           // of every row, -1: none
   float* lse;
   float* grad;
+  uint16_t* xg;            // x times grad_loss over the largest; NULL: not asked for
 };
 __device__ __forceinline__ int target_of(const CeBatch& b, int64_t i) {
   if (i >= b.rows) return -1;
@@ -55,60 +70,105 @@ __global__ __launch_bounds__(kBlock) void ce_count_kernel(CeBatch b) {
   }
 }
 
-__global__ __launch_bounds__(kBlock) void ce_list_kernel(CeBatch b) {
+// Places the rows that have a target and copies what the products need of them.  A workgroup takes `each` rows (a multiple of
+// kRowsAtOnce that 256 is a multiple of).  With `counted` it finds the rows before its own in ce_count_kernel's counts, else in
+// the targets themselves: one launch for up to kCountHere rows.
+constexpr int kRowsAtOnce = 16;
+constexpr int64_t kCountHere = 4096;
+template <int DT>
+__global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, int counted) {
   __shared__ uint32_t s_n[kWavesPerBlock];
   __shared__ float s_top[kWavesPerBlock];
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
-  const int t = target_of(b, i);
-  uint32_t before = 0, here;
-  for (unsigned k = threadIdx.x; k < blockIdx.x; k += kBlock) before += b.counts[k];
-  before = block_sum(before, s_n);
-  const uint32_t at = before + block_exclusive_sum(t >= 0 ? 1u : 0u, s_n, &here);
-  if (t >= 0) {
-    b.row[at] = static_cast<int32_t>(i);
-    b.target[at] = t;
-    if (b.grad_loss) {
-      b.lse[at] = b.lse_in[i];
-      b.grad[at] = b.grad_loss[i];
-    }
-  } else if (i < b.rows && b.loss) {
-    b.loss[i] = 0.0f;
-    b.lse_out[i] = 0.0f;
-  }
-  if (b.slot && i < b.rows) b.slot[i] = t >= 0 ? static_cast<int32_t>(at) : -1;
-  if (blockIdx.x + 1 < gridDim.x) return;
+  __shared__ int s_target[kRowsAtOnce];
+  __shared__ int s_slot[kRowsAtOnce];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * each, end = min(first + each, b.rows);
+  const int w = threadIdx.x >> 6, l = lane_id();
+  uint32_t before = 0;
   float top = 0.0f;
-  for (unsigned k = threadIdx.x; k < gridDim.x; k += kBlock) top = fmaxf(top, b.tops[k]);
-  top = block_max(top, s_top);
-  if (threadIdx.x == 0) {
-    *b.count = static_cast<int32_t>(before + here);
-    *b.largest = top;
-  }
-}
-
-// Their x side by side, rows of `pitch` (whole 16 bytes, zeros behind the width), and x times grad_loss over the largest.  A
-// wave a row.
-template <int DT>
-__global__ __launch_bounds__(kBlock) void ce_copy_kernel(const CeBatch b, const uint16_t* __restrict__ x, int64_t stride, int width,
-                                                         int pitch, int negate, uint16_t* __restrict__ xc, uint16_t* __restrict__ xg) {
-  const int count = *b.count, l = lane_id();
-  for (int64_t c = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6); c < count;
-       c += static_cast<int64_t>(gridDim.x) * kWavesPerBlock) {
-    const uint16_t* p = x + b.row[c] * stride;
-    const float g = xg ? (*b.largest > 0.0f ? b.grad[c] / *b.largest : 0.0f * b.grad[c]) : 1.0f;
-    for (int d = l * 8; d < pitch; d += kWave * 8) {
-      Vec<uint16_t, 8> v;
-      load_vec_part<uint16_t, 8>(p + d, width - d, v);
-      if (xg) {
-        Vec<uint16_t, 8> u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u.e[e] = tower_from_f<DT>(Fmt<DT>::to_f(v.e[e]) * g);
-        store_vec_any<uint16_t, 8>(xg + c * pitch + d, u);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v.e[e] ^= negate ? 0x8000 : 0;
-      store_vec_any<uint16_t, 8>(xc + c * pitch + d, v);
+  int64_t from = 0;
+  if (counted) {
+    const int64_t blocks = (b.rows + kBlock - 1) / kBlock, mine = first / kBlock;
+    for (int64_t k = threadIdx.x; k < blocks; k += kBlock) {
+      if (k < mine) before += b.counts[k];
+      top = fmaxf(top, b.tops[k]);
     }
+    from = mine * kBlock;
+  }
+  for (int64_t i = from + threadIdx.x; i < (counted || !b.grad_loss ? first : b.rows); i += kBlock) {
+    const bool has = target_of(b, i) >= 0;
+    if (has && i < first) ++before;
+    if (has && !counted && b.grad_loss) top = fmaxf(top, fabsf(b.grad_loss[i]));
+  }
+  before = block_sum(before, s_n);
+  top = block_max(top, s_top);
+  if (b.bias_over) {
+    // finite biases stay finite: the lowest value is no mask where every item has it
+    for (int64_t v = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; v < b.items; v += static_cast<int64_t>(gridDim.x) * kBlock) {
+      const float x = b.bias[v], y = x * b.over;
+      b.bias_over[v] = y == -kInfinity && x != y ? -3.4028234664e38f : y;
+    }
+  }
+  for (int64_t i0 = first; i0 < end; i0 += kRowsAtOnce) {
+    __syncthreads();
+    if (w == 0) {
+      const int64_t i = i0 + l;
+      const int t = l < kRowsAtOnce ? target_of(b, i) : -1;
+      const uint64_t has = __ballot(t >= 0);
+      const int slot = t >= 0 ? static_cast<int>(before) + __popcll(has & lanemask_lt()) : -1;
+      if (l < kRowsAtOnce) {
+        s_target[l] = t;
+        s_slot[l] = slot;
+      }
+      if (t >= 0) {
+        b.row[slot] = static_cast<int32_t>(i);
+        b.target[slot] = t;
+        if (b.grad_loss) {
+          b.lse[slot] = b.lse_in[i];
+          b.grad[slot] = b.grad_loss[i];
+        }
+      } else if (l < kRowsAtOnce && i < b.rows && b.loss) {
+        b.loss[i] = 0.0f;
+        b.lse_out[i] = 0.0f;
+      }
+      if (b.slot && l < kRowsAtOnce && i < b.rows) b.slot[i] = slot;
+      if (l == 0) s_n[0] = static_cast<uint32_t>(__popcll(has));
+    }
+    __syncthreads();
+    before += s_n[0];
+    for (int r = w; r < kRowsAtOnce; r += kWavesPerBlock) {
+      const int t = s_target[r], slot = s_slot[r];
+      if (t < 0) continue;
+      const uint16_t* p = b.x + (i0 + r) * b.x_stride;
+      const float g = b.xg ? (top > 0.0f ? b.grad_loss[i0 + r] / top : 0.0f * b.grad_loss[i0 + r]) : 1.0f;
+      float dot = 0.0f;
+      for (int d = l * 8; d < b.pitch; d += kWave * 8) {
+        Vec<uint16_t, 8> v;
+        load_vec_part<uint16_t, 8>(p + d, b.width - d, v);
+        if (b.picked) {
+          Vec<uint16_t, 8> u;
+          load_vec_part<uint16_t, 8>(b.w + t * b.w_stride + d, b.width - d, u);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = fmaf(Fmt<DT>::to_f(v.e[e]), Fmt<DT>::to_f(u.e[e]), dot);
+        }
+        if (b.xg) {
+          Vec<uint16_t, 8> u;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u.e[e] = tower_from_f<DT>(Fmt<DT>::to_f(v.e[e]) * g);
+          store_vec_any<uint16_t, 8>(b.xg + static_cast<int64_t>(slot) * b.pitch + d, u);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.e[e] = b.flip == 2 ? 0 : v.e[e] ^ (b.flip ? 0x8000 : 0);
+        store_vec_any<uint16_t, 8>(b.xc + static_cast<int64_t>(slot) * b.pitch + d, v);
+      }
+      if (b.picked) {
+        dot = lanes_sum<64>(dot);
+        if (l == 0) b.picked[slot] = fmaf(dot, b.scale, b.bias ? b.bias[t] : 0.0f);
+      }
+    }
+  }
+  if (blockIdx.x + 1 == gridDim.x && threadIdx.x == 0) {
+    *b.count = static_cast<int32_t>(before);
+    *b.largest = top;
   }
 }
 
@@ -119,15 +179,20 @@ __global__ __launch_bounds__(kBlock) void ce_copy_kernel(const CeBatch b, const 
 // groups of 16 lanes.  The last piece's ends in the loss.
 constexpr int kJoinRows = 16, kJoinGroups = 64;
 __global__ __launch_bounds__(kJoinRows * kJoinGroups) void ce_join_kernel(const float2* __restrict__ part, int64_t rows, int tiles,
-                                                                         float2* __restrict__ all, int first, int last,
-                                                                         const float* __restrict__ picked, CeBatch b) {
+                                                                         float2* __restrict__ all, int first, int last, CeBatch b) {
   __shared__ float2 s_all[kJoinGroups][kJoinRows + 1];
   const int q = threadIdx.x / kJoinRows, k = threadIdx.x % kJoinRows, count = *b.count;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * kJoinRows + k;
   float2 sum = make_float2(-kInfinity, 0.0f);
   if (c < count) {
-#pragma unroll 4
-    for (int t = q; t < tiles; t += kJoinGroups) sum = ce_join(sum, part[t * rows + c]);
+    constexpr int kAhead = 8;
+    for (int t = q; t < tiles; t += kAhead * kJoinGroups) {
+      float2 v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) v[u] = t + u * kJoinGroups < tiles ? part[(t + u * kJoinGroups) * rows + c] : make_float2(-kInfinity, 0.0f);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) sum = ce_join(sum, v[u]);
+    }
   }
   s_all[q][k] = sum;
   __syncthreads();
@@ -143,7 +208,7 @@ __global__ __launch_bounds__(kJoinRows * kJoinGroups) void ce_join_kernel(const 
     return;
   }
   // no sum is left where every item is masked, or by the lowest value
-  const float lse = sum.y == 0.0f ? sum.x : sum.x + logf(sum.y), at = picked[c];
+  const float lse = sum.y == 0.0f ? sum.x : sum.x + logf(sum.y), at = b.picked[c];
   b.lse_out[b.row[c]] = lse;
   b.loss[b.row[c]] = at == -kInfinity && !(lse != lse) ? kInfinity : lse - at;
 }
@@ -224,11 +289,11 @@ __global__ __launch_bounds__(1024) void ce_grad_bias_kernel(const float* __restr
 constexpr int64_t kPartBytes = int64_t{64} << 20;    // forward: of the rows' maxima and sums over a piece's tiles
 constexpr int64_t kZElems = int64_t{1} << 27;        // backward: of z
 constexpr int64_t kLeastPiece = 1024, kMostPiece = 131072;  // items of a piece, backward
-// rows of z lie a cache line further apart than their items need: at a power of two apart, the rows of a tile meet in the
-// same sets and channels
-constexpr int64_t kZPad = 64;
 constexpr int64_t kSumBytes = int64_t{128} << 20;    // of the sums over shares of k, beyond one share of x's gradient
 constexpr int kMostSplits = 16;
+
+// Rows of up to so many columns stay in registers (cross_entropy_narrow.h).
+constexpr int64_t kNarrowWidth = 128;
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
@@ -243,11 +308,12 @@ struct Carve {
 struct CeLayout {
   int64_t pitch, piece;
   size_t counts, tops, count, largest, row, target, slot, lse, grad, xc;
+  size_t bias_over;                         // narrow rows
   size_t part, picked, all;                 // forward
   size_t xg, z, sum_x, sum_w, bias_part;    // backward
   size_t total;
 };
-void carve_rows(CeLayout& L, Carve& c, int64_t rows, int64_t width) {
+void carve_rows(CeLayout& L, Carve& c, int64_t rows, int64_t items, int64_t width) {
   const int64_t blocks = (rows + kBlock - 1) / kBlock;
   L.pitch = up(width, 8);
   L.counts = c.take(blocks * 4);
@@ -257,11 +323,12 @@ void carve_rows(CeLayout& L, Carve& c, int64_t rows, int64_t width) {
   L.row = c.take(rows * 4);
   L.target = c.take(rows * 4);
   L.xc = c.take(rows * L.pitch * 2);
+  L.bias_over = c.take(width <= kNarrowWidth ? items * 4 : 0);
 }
 CeLayout forward_layout(int64_t rows, int64_t items, int64_t width) {
   CeLayout L = {};
   Carve c;
-  carve_rows(L, c, rows, width);
+  carve_rows(L, c, rows, items, width);
   // pieces of whole 256s; the smallest tile has 64 items
   L.piece = hmin(up(items, 256), hmax(1, kPartBytes / (8 * hmax(rows, 1)) / 4) * 256);
   L.part = c.take(hmin(rows * (up(items, 256) / 64) * 8, hmax(kPartBytes, rows * 4 * 8)));
@@ -273,7 +340,7 @@ CeLayout forward_layout(int64_t rows, int64_t items, int64_t width) {
 CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   CeLayout L = {};
   Carve c;
-  carve_rows(L, c, rows, width);
+  carve_rows(L, c, rows, items, width);
   L.slot = c.take(rows * 4);
   L.lse = c.take(rows * 4);
   L.grad = c.take(rows * 4);
@@ -281,7 +348,7 @@ CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   const int64_t all = up(items, 256), most = hmin(all, kMostPiece);
   L.piece = hmin(most, hmax(kLeastPiece, kZElems / hmax(rows, 1) / 256 * 256));
   const int64_t z = hmin(rows * most, hmax(kZElems, rows * kLeastPiece));
-  L.z = c.take((z + rows * kZPad) * 2);
+  L.z = c.take((z + 64 * most) * 2);  // panels of whole 64 rows
   L.sum_x = c.take(hmax(rows * width * 4, hmin(kSumBytes, kMostSplits * rows * width * 4)));
   L.sum_w = c.take(kSumBytes);
   L.bias_part = c.take(z / 64 * 4 + most * 4);
@@ -314,8 +381,6 @@ TilePick pick_tile(const TileCost (&costs)[3], int64_t m, int64_t n, int64_t k, 
 // Costs of the kernels here: grouped_linear.h's, with square tiles through registers as well.
 constexpr TileCost kAlongRegisters[3] = {{256, 256, 512, 256, 6.0, 1.3, 2.05}, {128, 128, 256, 512, 5.0, 0.8, 1.5}, {64, 64, 256, 1024, 3.0, 0.55, 1.35}};
 
-// Rows of up to so many columns stay in registers (cross_entropy_narrow.h).
-constexpr int64_t kNarrowWidth = 128;
 // Into how many ranges their items go: about 2048 workgroups, of 16 tiles of 64 items at least, of fewer where that leaves
 // CUs idle.
 int narrow_splits(int64_t rows, int64_t items, bool few) {
@@ -327,27 +392,41 @@ bool whole_16(const void* p, int64_t stride, int64_t width) {
   return !(reinterpret_cast<uintptr_t>(p) & 15) && stride % 8 == 0 && width % 8 == 0 && stride < (int64_t{1} << 21);
 }
 
-CeBatch batch_of(char* ws, const CeLayout& L, int64_t rows, int64_t items, const void* targets, int target_type) {
+// One CeBatch for both directions.  A negative scale of narrow rows goes into x (their kernel looks for the largest product),
+// and so does 0, by which no bias can be divided.
+CeBatch batch_of(char* ws, const CeLayout& L, int64_t rows, int64_t items, int64_t width, const void* x, int64_t x_stride,
+                 const void* targets, int target_type, const float* bias, bool narrow, float& scale) {
   CeBatch b = {};
   b.rows = rows; b.items = items; b.targets = targets; b.target64 = target_type == TBE_I64;
+  b.width = static_cast<int>(width); b.pitch = static_cast<int>(L.pitch);
+  b.x = static_cast<const uint16_t*>(x); b.x_stride = x_stride; b.xc = reinterpret_cast<uint16_t*>(ws + L.xc);
   b.counts = reinterpret_cast<int32_t*>(ws + L.counts);
   b.tops = reinterpret_cast<float*>(ws + L.tops);
   b.count = reinterpret_cast<int32_t*>(ws + L.count);
   b.largest = reinterpret_cast<float*>(ws + L.largest);
   b.row = reinterpret_cast<int32_t*>(ws + L.row);
   b.target = reinterpret_cast<int32_t*>(ws + L.target);
+  b.bias = bias;
+  b.scale = scale;
+  if (narrow) {
+    b.flip = scale < 0.0f ? 1 : scale == 0.0f ? 2 : 0;
+    scale = scale < 0.0f ? -scale : scale == 0.0f ? 1.0f : scale;
+    if (bias) b.bias_over = reinterpret_cast<float*>(ws + L.bias_over);
+    b.over = 1.0f / scale;
+  }
   return b;
 }
-tbe_status launch_rows(const CeBatch& b, const void* x, int64_t x_stride, int64_t width, int64_t pitch, int dtype, bool negate, void* xc,
-                       void* xg, hipStream_t s) {
-  const unsigned blocks = static_cast<unsigned>(hmax(1, (b.rows + kBlock - 1) / kBlock));  // no rows: their count, 0
+tbe_status launch_rows(const CeBatch& b, int dtype, hipStream_t s) {
+  const bool counted = b.rows > kCountHere;
   ProfScope ps("ce_rows", s);
-  hipLaunchKernelGGL(ce_count_kernel, dim3(blocks), dim3(kBlock), 0, s, b);
-  hipLaunchKernelGGL(ce_list_kernel, dim3(blocks), dim3(kBlock), 0, s, b);
-  const unsigned groups = static_cast<unsigned>(hmax(1, hmin((b.rows + kWavesPerBlock - 1) / kWavesPerBlock, 8192)));
-  auto kernel = dtype == TBE_F16 ? ce_copy_kernel<1> : ce_copy_kernel<2>;
-  hipLaunchKernelGGL(kernel, dim3(groups), dim3(kBlock), 0, s, b, static_cast<const uint16_t*>(x), x_stride, static_cast<int>(width),
-                     static_cast<int>(pitch), negate ? 1 : 0, static_cast<uint16_t*>(xc), static_cast<uint16_t*>(xg));
+  if (counted) {
+    hipLaunchKernelGGL(ce_count_kernel, dim3(static_cast<unsigned>((b.rows + kBlock - 1) / kBlock)), dim3(kBlock), 0, s, b);
+    if (tbe_status st = check_launch("ce_count")) return st;
+  }
+  const int each = b.rows > (1 << 17) ? kBlock : kRowsAtOnce;
+  const unsigned groups = static_cast<unsigned>(hmax(1, (b.rows + each - 1) / each));  // no rows: their count, 0
+  auto kernel = dtype == TBE_F16 ? ce_rows_kernel<1> : ce_rows_kernel<2>;
+  hipLaunchKernelGGL(kernel, dim3(groups), dim3(kBlock), 0, s, b, each, counted ? 1 : 0);
   return check_launch("ce_rows");
 }
 CeRows rows_of(const CeBatch& b) { return CeRows{b.count, b.row, b.target, b.lse, b.grad, b.largest}; }
@@ -362,20 +441,19 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
                                         float scale, float* loss, float* lse, void* workspace, hipStream_t s) {
   const CeLayout L = forward_layout(rows, items, width);
   char* ws = static_cast<char*>(workspace);
-  CeBatch b = batch_of(ws, L, rows, items, targets, target_type);
+  const bool direct = whole_16(weight, weight_stride, width), narrow = direct && width <= kNarrowWidth;
+  CeBatch b = batch_of(ws, L, rows, items, width, x, x_stride, targets, target_type, bias, narrow, scale);
+  b.w = static_cast<const uint16_t*>(weight); b.w_stride = weight_stride;
+  b.picked = reinterpret_cast<float*>(ws + L.picked);
   b.loss = loss;
   b.lse_out = lse;
-  const bool direct = whole_16(weight, weight_stride, width), narrow = direct && width <= kNarrowWidth;
-  // the narrow kernel looks for the largest product: a negative factor goes into x
-  const bool negate = narrow && !bias && scale < 0.0f;
-  if (negate) scale = -scale;
-  tbe_status st = launch_rows(b, x, x_stride, width, L.pitch, dtype, negate, ws + L.xc, nullptr, s);
+  tbe_status st = launch_rows(b, dtype, s);
+  if (b.bias_over) bias = b.bias_over;
   CeArgs a = {};
   a.rows = rows; a.width = static_cast<int>(width);
   a.x = ws + L.xc; a.x_stride = L.pitch;
   a.w_stride = weight_stride; a.scale = scale; a.r = rows_of(b);
   a.part = reinterpret_cast<float2*>(ws + L.part);
-  a.picked = reinterpret_cast<float*>(ws + L.picked);
   const int64_t piece = narrow ? items : L.piece;
   for (int64_t first = 0; st == TBE_OK && first < items; first += piece) {
     a.first = static_cast<int>(first);
@@ -396,8 +474,7 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
     if (st != TBE_OK) break;
     ProfScope ps("ce_join", s);
     hipLaunchKernelGGL(ce_join_kernel, dim3(static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows)), dim3(kJoinRows * kJoinGroups), 0, s,
-                       a.part, rows, parts, reinterpret_cast<float2*>(ws + L.all), first == 0 ? 1 : 0, first + piece >= items ? 1 : 0,
-                       a.picked, b);
+                       a.part, rows, parts, reinterpret_cast<float2*>(ws + L.all), first == 0 ? 1 : 0, first + piece >= items ? 1 : 0, b);
     st = check_launch("ce_join");
   }
   return st;
@@ -409,20 +486,24 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
                                          void* grad_weight, int64_t grad_weight_stride, float* grad_bias, void* workspace, hipStream_t s) {
   const CeLayout L = backward_layout(rows, items, width);
   char* ws = static_cast<char*>(workspace);
-  CeBatch b = batch_of(ws, L, rows, items, targets, target_type);
+  const bool direct = whole_16(weight, weight_stride, width), narrow = direct && width <= kNarrowWidth;
+  const float factor = scale / (dtype == TBE_F16 ? kUnit<1> : kUnit<2>);  // of a product of z
+  CeBatch b = batch_of(ws, L, rows, items, width, x, x_stride, targets, target_type, bias, narrow, scale);
   b.grad_loss = grad_loss;
   b.lse_in = lse;
   b.slot = reinterpret_cast<int32_t*>(ws + L.slot);
   b.lse = reinterpret_cast<float*>(ws + L.lse);
   b.grad = reinterpret_cast<float*>(ws + L.grad);
-  tbe_status st = launch_rows(b, x, x_stride, width, L.pitch, dtype, false, ws + L.xc, grad_weight ? ws + L.xg : nullptr, s);
-  const bool direct = whole_16(weight, weight_stride, width), narrow = direct && width <= kNarrowWidth;
+  b.xg = grad_weight ? reinterpret_cast<uint16_t*>(ws + L.xg) : nullptr;
+  tbe_status st = launch_rows(b, dtype, s);
+  if (b.bias_over) bias = b.bias_over;
   const bool f16 = dtype == TBE_F16;
   CeArgs a = {};
   a.rows = rows; a.width = static_cast<int>(width);
   a.x = ws + L.xc; a.x_stride = L.pitch; a.xg = ws + L.xg;
   a.w_stride = weight_stride; a.scale = scale; a.r = rows_of(b);
-  a.z = reinterpret_cast<uint16_t*>(ws + L.z); a.z_stride = L.piece + kZPad;
+  a.z = reinterpret_cast<uint16_t*>(ws + L.z); a.panel = up(rows, 64) * 64;
+  a.factor = factor;
   a.bias_part = grad_bias ? reinterpret_cast<float*>(ws + L.bias_part) : nullptr;
   a.bias_stride = L.piece;
   const TileCost(&costs)[3] = direct ? kDirectTiles : kAlongRegisters;
@@ -470,7 +551,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
         ProfScope ps("ce_grad_w_sum", s);
         auto kernel = f16 ? ce_grad_w_kernel<1> : ce_grad_w_kernel<2>;
         hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((a.items + 3) / 4, 8192))), dim3(kBlock), 0, s, a.sum, p.splits, a.items,
-                           a.width, scale / (f16 ? kUnit<1> : kUnit<2>), b.largest, static_cast<uint16_t*>(a.out), grad_weight_stride);
+                           a.width, factor, b.largest, static_cast<uint16_t*>(a.out), grad_weight_stride);
         st = check_launch("ce_grad_w_sum");
       }
     }
@@ -480,7 +561,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   auto kernel = f16 ? ce_grad_x_kernel<1> : ce_grad_x_kernel<2>;
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((rows + 3) / 4, 8192))), dim3(kBlock), 0, s, b,
                      reinterpret_cast<const float*>(ws + L.sum_x), x_pick.splits, static_cast<int>(width),
-                     scale / (f16 ? kUnit<1> : kUnit<2>), static_cast<uint16_t*>(grad_x), grad_x_stride);
+                     factor, static_cast<uint16_t*>(grad_x), grad_x_stride);
   return check_launch("ce_grad_x_sum");
 }
 

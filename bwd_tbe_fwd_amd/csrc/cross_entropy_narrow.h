@@ -9,7 +9,8 @@
 //  * A ring of three tiles of 64 items in LDS, loaded two ahead, one barrier a tile.  What a wave stores leaves before the
 //    loads of its step start: the loads' counter then needs no look at the stores.
 //  * Forward a lane keeps a maximum and a sum for its 4 rows over all its items; lanes, waves and workgroups are joined at
-//    the end.  The logits' factor goes into the exponential's argument: one multiply-add a logit without a bias, two with.
+//    the end.  The logits' factor goes into the exponential's argument and the biases, divided by it beforehand, are where
+//    the products' sums begin: a logit then costs a multiply-add, an exponential, a half of a maximum and an addition.
 #pragma once
 
 #include "cross_entropy_tile.h"
@@ -59,15 +60,15 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
       fa[i][k] = u16x8_t{};
       if (in && c < a.x_stride) fa[i][k] = *reinterpret_cast<const u16x8_t*>(static_cast<const uint16_t*>(a.x) + m * a.x_stride + c);
     }
-    target[i] = in ? a.r.target[m] - a.first - wn - g * LEN : -1;
     if constexpr (BACK) {
+      target[i] = in ? a.r.target[m] - a.first - wn - g * LEN : -1;
       const float e = in ? a.r.lse[m] : 0.0f;
-      lse[i] = e < -1e38f ? -kInfinity : -e * kLog2e;  // every item masked: no probability
-      grad[i] = in ? a.r.grad[m] : 0.0f;
+      lse[i] = e < -1e38f ? -kInfinity : fmaf(e, -kLog2e, DT == 1 ? 15.0f : 0.0f);  // every item masked: no probability
+      grad[i] = in ? a.r.grad[m] / kUnit<DT> : 0.0f;
     }
   }
-  // what the exponential of base 2 takes: v * unit less the row's reference
-  const float unit = BIAS ? kLog2e : a.scale * kLog2e;
+  // what the exponential of base 2 takes: the sum of products times `unit`, less the row's reference
+  const float unit = a.scale * kLog2e;
 
   OB B;
   auto stage = [&](int t) {
@@ -88,14 +89,12 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
     }
   };
 
-  float top[MF], sum[MF], picked[MF];  // forward
+  float top[MF], sum[MF];  // forward
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
     top[i] = -kInfinity;
     sum[i] = 0.0f;
-    picked[i] = 0.0f;
   }
-  bool found[MF] = {};
   u32x2 z[BACK ? MF : 1][BACK ? NF : 1];  // backward: the last tile's, and its columns' sums
   float column = 0.0f;
   auto store_z = [&](int t) {
@@ -104,7 +103,7 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
       for (int i = 0; i < MF; ++i) {
         const int m = m0 + wm + 16 * i + (l & 15);
         if (m < count) {
-          uint16_t* p = a.z + m * a.z_stride + t * kNarrowItems + wn + g * LEN;
+          uint16_t* p = a.z + t * a.panel + static_cast<int64_t>(m) * 64 + wn + g * LEN;
 #pragma unroll
           for (int j = 0; j + 1 < NF; j += 2) *reinterpret_cast<u32x4*>(p + 4 * j) = u32x4{z[i][j].x, z[i][j].y, z[i][j + 1].x, z[i][j + 1].y};
           if constexpr (NF == 1) *reinterpret_cast<u32x2*>(p) = z[i][0];
@@ -130,29 +129,17 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
     f32x4 acc[MF][NF];
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-#pragma unroll
-      for (int i = 0; i < MF; ++i) acc[i][j] = f32x4{0, 0, 0, 0};
+      f32x4 from = {0, 0, 0, 0};
+      if constexpr (BIAS) from = *reinterpret_cast<const f32x4*>(s_bias + (slot * 4 + w) * kNarrowItems + wn + g * LEN + 4 * j);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const u16x8_t fb = OB::read(lds + slot * kTile + k / 2 * OB::kElems + b_half[k % 2], 4 * j);
 #pragma unroll
-        for (int i = 0; i < MF; ++i) acc[i][j] = mfma16<DT>(fb, fa[i][k], acc[i][j]);
+        for (int i = 0; i < MF; ++i) acc[i][j] = mfma16<DT>(fb, fa[i][k], k == 0 ? from : acc[i][j]);
       }
     }
-    // v: the logit, or the product alone where there is no bias
     const int n0 = t * kNarrowItems;
     const int left = a.items - n0 - wn - g * LEN;  // of this lane's items
-    if constexpr (BIAS) {
-      const float* s = s_bias + (slot * 4 + w) * kNarrowItems + wn + g * LEN;
-#pragma unroll
-      for (int j = 0; j < NF; ++j) {
-        const f32x4 b = *reinterpret_cast<const f32x4*>(s + 4 * j);
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(acc[i][j][e], a.scale, b[e]);
-      }
-    }
     const bool edge = a.items - n0 < kNarrowItems;
     if constexpr (!BACK) {
       if (edge) {
@@ -164,13 +151,6 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
-        const unsigned at = static_cast<unsigned>(target[i] - n0);
-        if (at < LEN) {
-          found[i] = true;
-#pragma unroll
-          for (int c = 0; c < LEN; ++c)
-            if (c == static_cast<int>(at)) picked[i] = acc[i][c / 4][c % 4];
-        }
         float most = acc[i][0][0];
 #pragma unroll
         for (int c = 1; c < LEN; ++c) most = fmaxf(most, acc[i][c / 4][c % 4]);
@@ -193,10 +173,9 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
 #pragma unroll
         for (int c = 0; c < LEN; ++c) p[c] = __builtin_amdgcn_exp2f(fmaf(acc[i][c / 4][c % 4], unit, lse[i]));
         const unsigned at = static_cast<unsigned>(target[i] - n0);
-        if (at < LEN) {
+        if (__any(at < LEN)) {
 #pragma unroll
-          for (int c = 0; c < LEN; ++c)
-            if (c == static_cast<int>(at)) p[c] -= 1.0f;
+          for (int c = 0; c < LEN; ++c) p[c] -= c == static_cast<int>(at) ? kUnit<DT> : 0.0f;
         }
         if (edge) {
 #pragma unroll
@@ -211,7 +190,7 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
         for (int j = 0; j < NF; ++j) {
           Vec<uint16_t, 4> v;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v.e[e] = tower_from_f<DT>(p[4 * j + e] * kUnit<DT>);
+          for (int e = 0; e < 4; ++e) v.e[e] = tower_from_f<DT>(p[4 * j + e]);
           z[i][j] = __builtin_bit_cast(u32x2, v);
         }
       }
@@ -232,16 +211,13 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
-      const int m = m0 + wm + 16 * i + (l & 15);
-      const float factor = BIAS ? 1.0f : a.scale;  // to logits
-      if (found[i]) a.picked[m] = picked[i] * factor;
       const float from = fmaxf(top[i], -1e38f);
       float all = fmaxf(top[i], __shfl_xor(top[i], 16));
       all = fmaxf(all, __shfl_xor(all, 32));
       float s = sum[i] * __builtin_amdgcn_exp2f((from - fmaxf(all, -1e38f)) * unit);
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
-      if (l < 16) stat[w % WN * kNarrowRows<WM> + wm + 16 * i + l] = make_float2(all == -kInfinity ? all : all * factor, s);
+      if (l < 16) stat[w % WN * kNarrowRows<WM> + wm + 16 * i + l] = make_float2(all == -kInfinity ? all : all * a.scale, s);
     }
     __syncthreads();
     if (threadIdx.x < kNarrowRows<WM> && m0 + static_cast<int>(threadIdx.x) < count) {

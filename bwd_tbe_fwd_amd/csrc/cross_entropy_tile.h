@@ -70,12 +70,6 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
         v[c] = n + c < n_left ? logit(i, c) : -kInfinity;
         top = fmaxf(top, v[c]);
       }
-      const int at = m < m_left ? a.r.target[m0 + m] - a.first - n0 - n : -1;
-      if (at >= 0 && at < LEN) {
-#pragma unroll
-        for (int c = 0; c < LEN; ++c)
-          if (c == at) a.picked[m0 + m] = v[c];
-      }
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float from = top == -kInfinity ? 0.0f : top;  // no item that is not masked: the sum is 0
@@ -93,7 +87,9 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
       if (m < m_left) a.part[t.n * a.rows + m0 + m] = all;
     }
   } else {
-    // z in place of the logits
+    // z in place of the logits, times its unit
+    constexpr float kOne = kUnit<DT>;
+    const float shift = DT == 1 ? 15.0f : 0.0f;
     float columns[LEN];
 #pragma unroll
     for (int c = 0; c < LEN; ++c) columns[c] = 0.0f;
@@ -101,17 +97,24 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
     for (int i = 0; i < MF; ++i) {
       const int m = wm + 16 * i + (l & 15);
       const bool in = m < m_left;
-      float lse = in ? a.r.lse[m0 + m] : kInfinity;
-      if (lse == -kInfinity) lse = kInfinity;  // every item is masked: no probability
-      const int at = in ? a.r.target[m0 + m] - a.first - n0 - n : -1;
-      const float g = in && a.bias_part ? a.r.grad[m0 + m] : 0.0f;
+      const float lse = in ? a.r.lse[m0 + m] : 0.0f;
+      const float base = lse < -1e38f ? -kInfinity : fmaf(lse, -kLog2e, shift);  // every item masked: no probability
+      const unsigned at = in ? static_cast<unsigned>(a.r.target[m0 + m] - a.first - n0 - n) : ~0u;
 #pragma unroll
-      for (int c = 0; c < LEN; ++c) {
-        float p = __builtin_amdgcn_exp2f((logit(i, c) - lse) * kLog2e);
-        if (c == at) p -= 1.0f;
-        if (n_left < BN && n + c >= n_left) p = 0.0f;  // z's columns up to a whole 16 bytes are read
-        acc[i][c / 4][c % 4] = p;
-        if (in) columns[c] = fmaf(p, g, columns[c]);
+      for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] = __builtin_amdgcn_exp2f(fmaf(logit(i, c), kLog2e, base));
+      if (__any(at < LEN)) {
+#pragma unroll
+        for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] -= c == static_cast<int>(at) ? kOne : 0.0f;
+      }
+      if (n_left < BN) {  // z's columns up to a whole 16 bytes are read
+#pragma unroll
+        for (int c = 0; c < LEN; ++c)
+          if (n + c >= n_left) acc[i][c / 4][c % 4] = 0.0f;
+      }
+      if (a.bias_part) {
+        const float g = in ? a.r.grad[m0 + m] / kOne : 0.0f;
+#pragma unroll
+        for (int c = 0; c < LEN; ++c) columns[c] = in ? fmaf(acc[i][c / 4][c % 4], g, columns[c]) : columns[c];
       }
     }
     if (a.bias_part) {
@@ -130,9 +133,10 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
       __syncthreads();
     }
     constexpr int kWaveBytes = kBytes / (WM * WN) / 16 * 16;
-    store_tile<uint16_t, false, MF, NF, LEN, kWaveBytes>(a.z + (m0 + wm) * a.z_stride + n0 + wn, a.z_stride, m_left - wm, (n_left + 7) / 8 * 8 - wn,
-                                                         lds + w * kWaveBytes,
-                                                         [&](int i, int j, int e) { return tower_from_f<DT>(acc[i][j][e] * kUnit<DT>); });
+    static_assert(NF * 16 <= 64, "a wave's items lie in one panel");
+    uint16_t* out = a.z + (n0 + wn) / 64 * a.panel + static_cast<int64_t>(m0 + wm) * 64 + (n0 + wn) % 64;
+    store_tile<uint16_t, false, MF, NF, LEN, kWaveBytes>(out, 64, m_left - wm, (n_left + 7) / 8 * 8 - wn, lds + w * kWaveBytes,
+                                                         [&](int i, int j, int e) { return tower_from_f<DT>(acc[i][j][e]); });
   }
 }
 
@@ -141,7 +145,7 @@ template <int DT, bool X, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void ce_grad_kernel(CeArgs a) {
   constexpr int T = WM * WN * kWave;
   constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
-  using OA = Operand<X, BM, 4, T, DIRECT>;
+  using OA = PanelOperand<X, BM, 4, T, DIRECT>;
   using OB = Operand<false, BN, 4 * NF, T, DIRECT>;
   constexpr int kBytes = 2 * 2 * (OA::kElems + OB::kElems);
   __shared__ __align__(16) char lds[kBytes];
@@ -159,10 +163,10 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
   OA A;
   OB B;
   if constexpr (X) {
-    A.init(a.z + m0 * a.z_stride + k0, a.z_stride, m_left, k, k);
+    A.init(a.z, a.panel, m0, k0, m_left, k);
     B.init(static_cast<const uint16_t*>(a.w) + k0 * a.w_stride + n0, a.w_stride, n_left, k, a.width);
   } else {
-    A.init(a.z + k0 * a.z_stride + m0, a.z_stride, m_left, k, a.items);
+    A.init(a.z, a.panel, m0, k0, m_left, k);
     B.init(static_cast<const uint16_t*>(a.xg) + k0 * a.x_stride + n0, a.x_stride, n_left, k, a.width);
   }
   const int64_t pitch = a.width;
@@ -187,7 +191,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
   constexpr int kWaveBytes = kBytes / (WM * WN) / 16 * 16;
   char* s = lds + w * kWaveBytes;
   if (!X && a.splits == 1) {
-    const float factor = a.scale * *a.r.largest / kUnit<DT>;
+    const float factor = a.factor * *a.r.largest;
     store_tile<uint16_t, true, MF, NF, 4, kWaveBytes>(static_cast<uint16_t*>(a.out) + (m0 + wm) * a.out_stride + n0 + wn, a.out_stride,
                                                       m_left - wm, n_left - wn, s,
                                                       [&](int i, int j, int e) { return tower_from_f<DT>(acc[i][j][e] * factor); });

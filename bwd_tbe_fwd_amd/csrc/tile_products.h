@@ -221,6 +221,50 @@ struct Operand {
   }
 };
 
+// An operand in panels of 64: element (m, k) of an along one, or (k, m) of an across one, lies at row * 64 + column % 64 of
+// panel column / 64, panels `panel` elements apart, so that what a tile reads in a step is contiguous.  What lies between the
+// matrix's end and a whole 16 bytes has to be there, zero where it is along.
+template <bool ALONG, int SIDE, int GAP, int THREADS, bool DIRECT>
+struct PanelOperand : Operand<ALONG, SIDE, GAP, THREADS, DIRECT> {
+  using Base = Operand<ALONG, SIDE, GAP, THREADS, DIRECT>;
+  using Base::K;
+  using Base::kEach;
+  // m0, k0: whole panels and any rows
+  __device__ __forceinline__ void init(const uint16_t* z, int64_t panel, int64_t m0, int64_t k0, int m_left, int k_left) {
+    this->base = z + (ALONG ? k0 / 64 * panel + m0 * 64 : m0 / 64 * panel + k0 * 64);
+    this->ld = ALONG ? panel / 64 : 64;  // of k
+    this->ms = m_left;
+    this->ks = k_left;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      int row, chunk;
+      Base::place(i, threadIdx.x, row, chunk);
+      const bool in = ALONG ? row < m_left : chunk * 8 < m_left;
+      this->at[i] = in ? static_cast<uint32_t>(chunk / 8) * static_cast<uint32_t>(panel) * 2 + row * 128 + chunk % 8 * 16 : kOutside;
+    }
+  }
+  __device__ __forceinline__ int whole_steps() const { return this->ks > 0 ? this->ks / K : 0; }
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(int i, int k0, uint16_t* s) {
+    const uint16_t* p = this->base + k0 * this->ld;
+    const int left = this->ks - k0;
+    int row, chunk;
+    Base::place(i, threadIdx.x, row, chunk);
+    uint32_t o = this->at[i];
+    if (!WHOLE && left < K && (ALONG ? chunk * 8 : row) >= left) o = kOutside;
+    if constexpr (DIRECT) {
+      const uint64_t u = reinterpret_cast<uint64_t>(p);
+      const u32x4 r = {static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32) & 0xffffu, 0x7fffffffu, 0x00027000u};
+      const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      const int to = ALONG ? (i * THREADS + w * kWave) * 8 : (i * (THREADS / kWave) + w) * (512 + 16);
+      load_to_lds(r, o, static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)(s + to))));
+    } else {
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, 0x7fffffff, 0x00027000);
+      this->reg[i] = __builtin_bit_cast(u16x8_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
+    }
+  }
+};
+
 // Waits until at most N of this wave's loads are on their way and its LDS reads are done.  (Fields of
 // the counter word: loads in bits 0-3 and 14-15, LDS in 8-11, exports in 4-6, left alone.)
 template <int N>
