@@ -42,7 +42,8 @@ struct CeArgs {
   int64_t bias_stride;
   // products of z
   const void* xg;          // x * grad_loss / largest, like x
-  float* sum;              // [splits][rows or items][width] fp32 sums
+  float* sum;              // [splits][rows or items][sum_pitch] fp32 sums
+  int64_t sum_pitch;
   int32_t splits;          // of k; of the items for narrow rows
   int32_t add;             // to what is there
   float factor;            // of a product of z
@@ -62,7 +63,7 @@ __device__ __forceinline__ float2 ce_join(float2 a, float2 b) {
 }
 
 // A tile of C and how it is walked, as for the grouped layers.
-enum { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile256x128 = 3 };  // the last for the gradient of x
 
 // Defined in translation units of their own (cross_entropy_forward_f16.hip and its siblings).
 template <int DT> tbe_status ce_launch_forward(const CeArgs& a, int tile, bool direct, hipStream_t s);

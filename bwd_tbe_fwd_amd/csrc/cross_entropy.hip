@@ -27,7 +27,7 @@ struct CeBatch {
   int32_t* row;
   int32_t* target;
   const float* bias;       // NULL: none
-  float* bias_over;        // the biases over the scale; NULL: not asked for
+  float* bias_over;        // narrow rows: the biases over the scale (0 without), -infinity up to a whole 64 items; else NULL
   float over;              // 1 / scale
   // forward
   const uint16_t* w;
@@ -73,16 +73,26 @@ __global__ __launch_bounds__(kBlock) void ce_count_kernel(CeBatch b) {
 // Places the rows that have a target and copies what the products need of them.  A workgroup takes `each` rows (a multiple of
 // kRowsAtOnce that 256 is a multiple of).  With `counted` it finds the rows before its own in ce_count_kernel's counts, else in
 // the targets themselves: one launch for up to kCountHere rows.
-constexpr int kRowsAtOnce = 16;
+constexpr int kRowsAtOnce = 4;  // a wave each
 constexpr int64_t kCountHere = 4096;
 template <int DT>
-__global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, int counted) {
+__global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, int groups, int counted) {
   __shared__ uint32_t s_n[kWavesPerBlock];
   __shared__ float s_top[kWavesPerBlock];
   __shared__ int s_target[kRowsAtOnce];
   __shared__ int s_slot[kRowsAtOnce];
   const int64_t first = static_cast<int64_t>(blockIdx.x) * each, end = min(first + each, b.rows);
   const int w = threadIdx.x >> 6, l = lane_id();
+  if (static_cast<int>(blockIdx.x) >= groups) {
+    // the biases' workgroups.  Finite ones stay finite: the lowest value is no mask where every item has it
+    const int64_t end = (b.items + 63) / 64 * 64;
+    for (int64_t v = static_cast<int64_t>(blockIdx.x - groups) * kBlock + threadIdx.x; v < end;
+         v += static_cast<int64_t>(gridDim.x - groups) * kBlock) {
+      const float x = v >= b.items ? -kInfinity : b.bias ? b.bias[v] : 0.0f, y = x * b.over;
+      b.bias_over[v] = y == -kInfinity && x != y ? -3.4028234664e38f : y;
+    }
+    return;
+  }
   uint32_t before = 0;
   float top = 0.0f;
   int64_t from = 0;
@@ -101,13 +111,6 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
   }
   before = block_sum(before, s_n);
   top = block_max(top, s_top);
-  if (b.bias_over) {
-    // finite biases stay finite: the lowest value is no mask where every item has it
-    for (int64_t v = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; v < b.items; v += static_cast<int64_t>(gridDim.x) * kBlock) {
-      const float x = b.bias[v], y = x * b.over;
-      b.bias_over[v] = y == -kInfinity && x != y ? -3.4028234664e38f : y;
-    }
-  }
   for (int64_t i0 = first; i0 < end; i0 += kRowsAtOnce) {
     __syncthreads();
     if (w == 0) {
@@ -135,9 +138,9 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
     }
     __syncthreads();
     before += s_n[0];
-    for (int r = w; r < kRowsAtOnce; r += kWavesPerBlock) {
-      const int t = s_target[r], slot = s_slot[r];
-      if (t < 0) continue;
+    static_assert(kRowsAtOnce == kWavesPerBlock, "a row a wave");
+    const int r = w, t = s_target[r], slot = s_slot[r];
+    if (t >= 0) {
       const uint16_t* p = b.x + (i0 + r) * b.x_stride;
       const float g = b.xg ? (top > 0.0f ? b.grad_loss[i0 + r] / top : 0.0f * b.grad_loss[i0 + r]) : 1.0f;
       float dot = 0.0f;
@@ -166,7 +169,7 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
       }
     }
   }
-  if (blockIdx.x + 1 == gridDim.x && threadIdx.x == 0) {
+  if (static_cast<int>(blockIdx.x) + 1 == groups && threadIdx.x == 0) {
     *b.count = static_cast<int32_t>(before);
     *b.largest = top;
   }
@@ -175,28 +178,34 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
 // ---------------------------------------------------------------------------
 // joins
 // ---------------------------------------------------------------------------
-// A piece's maxima and sums of each row, its tiles in a fixed order, joined with the pieces before: 16 rows a workgroup, 64
-// groups of 16 lanes.  The last piece's ends in the loss.
-constexpr int kJoinRows = 16, kJoinGroups = 64;
-__global__ __launch_bounds__(kJoinRows * kJoinGroups) void ce_join_kernel(const float2* __restrict__ part, int64_t rows, int tiles,
-                                                                         float2* __restrict__ all, int first, int last, CeBatch b) {
-  __shared__ float2 s_all[kJoinGroups][kJoinRows + 1];
-  const int q = threadIdx.x / kJoinRows, k = threadIdx.x % kJoinRows, count = *b.count;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kJoinRows + k;
+// A piece's maxima and sums of each row, its tiles in a fixed order, joined with the pieces before.  ROWS rows a workgroup of
+// 1024 threads: 16, or 1 where there are few rows and many tiles.  The last piece's ends in the loss.
+template <int ROWS>
+__global__ __launch_bounds__(1024) void ce_join_kernel(const float2* __restrict__ part, int64_t rows, int tiles, float2* __restrict__ all, int first,
+                                                       int last, CeBatch b) {
+  constexpr int kGroups = 1024 / ROWS, kAhead = 8;
+  __shared__ float2 s_all[kGroups][ROWS + (ROWS > 1 ? 1 : 0)];
+  const int q = threadIdx.x / ROWS, k = threadIdx.x % ROWS, count = *b.count;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * ROWS + k;
   float2 sum = make_float2(-kInfinity, 0.0f);
   if (c < count) {
-    constexpr int kAhead = 8;
-    for (int t = q; t < tiles; t += kAhead * kJoinGroups) {
+    for (int t = q; t < tiles; t += kAhead * kGroups) {
       float2 v[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) v[u] = t + u * kJoinGroups < tiles ? part[(t + u * kJoinGroups) * rows + c] : make_float2(-kInfinity, 0.0f);
+      for (int u = 0; u < kAhead; ++u) v[u] = t + u * kGroups < tiles ? part[(t + u * kGroups) * rows + c] : make_float2(-kInfinity, 0.0f);
+      float top = sum.x;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) sum = ce_join(sum, v[u]);
+      for (int u = 0; u < kAhead; ++u) top = fmaxf(top, v[u].x);
+      const float from = top == -kInfinity ? 0.0f : top;
+      float s = sum.y * expf(sum.x - from);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) s += v[u].y * expf(v[u].x - from);
+      sum = make_float2(top, s);
     }
   }
   s_all[q][k] = sum;
   __syncthreads();
-  for (int n = kJoinGroups / 2; n > 0; n /= 2) {
+  for (int n = kGroups / 2; n > 0; n /= 2) {
     if (q < n) s_all[q][k] = ce_join(s_all[q][k], s_all[q + n][k]);
     __syncthreads();
   }
@@ -214,8 +223,14 @@ __global__ __launch_bounds__(kJoinRows * kJoinGroups) void ce_join_kernel(const 
 }
 
 // The rows' gradients: the parts' sums times scale * grad_loss; zero for a row without a target.
+__device__ __forceinline__ f32x4 sum_parts(const float* p, int64_t stride, int n) {
+  f32x4 all = {0, 0, 0, 0};
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) all += load_f4(p + k * stride);
+  return all;
+}
 template <int DT>
-__global__ __launch_bounds__(kBlock) void ce_grad_x_kernel(const CeBatch b, const float* __restrict__ sum, int splits, int width, float factor,
+__global__ __launch_bounds__(kBlock) void ce_grad_x_kernel(const CeBatch b, const float* __restrict__ sum, int64_t pitch, int splits, int width, float factor,
                                                            uint16_t* __restrict__ gx, int64_t stride) {
   const int l = lane_id();
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6); i < b.rows;
@@ -223,18 +238,11 @@ __global__ __launch_bounds__(kBlock) void ce_grad_x_kernel(const CeBatch b, cons
     const int64_t c = b.slot[i];
     const float g = c >= 0 ? b.grad[c] * factor : 0.0f;
     for (int d = l * 4; d < width; d += kWave * 4) {
-      Vec<float, 4> all = {};
-      if (c >= 0) {
-        for (int k = 0; k < splits; ++k) {
-          Vec<float, 4> v;
-          load_vec_part<float, 4>(sum + (k * b.rows + c) * width + d, width - d, v);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) all.e[e] += v.e[e];
-        }
-      }
+      f32x4 all = {0, 0, 0, 0};
+      if (c >= 0) all = sum_parts(sum + c * pitch + d, b.rows * pitch, splits);
       Vec<uint16_t, 4> out;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) out.e[e] = c >= 0 ? tower_from_f<DT>(all.e[e] * g) : static_cast<uint16_t>(0);
+      for (int e = 0; e < 4; ++e) out.e[e] = c >= 0 ? tower_from_f<DT>(all[e] * g) : static_cast<uint16_t>(0);
       store_vec_part<uint16_t, 4>(gx + i * stride + d, width - d, out);
     }
   }
@@ -242,23 +250,17 @@ __global__ __launch_bounds__(kBlock) void ce_grad_x_kernel(const CeBatch b, cons
 
 // The weights' gradients of a piece whose rows were shared.
 template <int DT>
-__global__ __launch_bounds__(kBlock) void ce_grad_w_kernel(const float* __restrict__ sum, int splits, int items, int width, float scale,
+__global__ __launch_bounds__(kBlock) void ce_grad_w_kernel(const float* __restrict__ sum, int64_t pitch, int splits, int items, int width, float scale,
                                                            const float* __restrict__ largest, uint16_t* __restrict__ gw, int64_t stride) {
   const float factor = scale * *largest;
   const int l = lane_id();
   for (int64_t v = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6); v < items;
        v += static_cast<int64_t>(gridDim.x) * kWavesPerBlock) {
     for (int d = l * 4; d < width; d += kWave * 4) {
-      Vec<float, 4> all = {};
-      for (int k = 0; k < splits; ++k) {
-        Vec<float, 4> p;
-        load_vec_part<float, 4>(sum + (static_cast<int64_t>(k) * items + v) * width + d, width - d, p);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) all.e[e] += p.e[e];
-      }
+      const f32x4 all = sum_parts(sum + v * pitch + d, items * pitch, splits);
       Vec<uint16_t, 4> out;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) out.e[e] = tower_from_f<DT>(all.e[e] * factor);
+      for (int e = 0; e < 4; ++e) out.e[e] = tower_from_f<DT>(all[e] * factor);
       store_vec_part<uint16_t, 4>(gw + v * stride + d, width - d, out);
     }
   }
@@ -290,7 +292,7 @@ constexpr int64_t kPartBytes = int64_t{64} << 20;    // forward: of the rows' ma
 constexpr int64_t kZElems = int64_t{1} << 27;        // backward: of z
 constexpr int64_t kLeastPiece = 1024, kMostPiece = 131072;  // items of a piece, backward
 constexpr int64_t kSumBytes = int64_t{128} << 20;    // of the sums over shares of k, beyond one share of x's gradient
-constexpr int kMostSplits = 16;
+constexpr int kMostSplits = 64;
 
 // Rows of up to so many columns stay in registers (cross_entropy_narrow.h).
 constexpr int64_t kNarrowWidth = 128;
@@ -323,7 +325,7 @@ void carve_rows(CeLayout& L, Carve& c, int64_t rows, int64_t items, int64_t widt
   L.row = c.take(rows * 4);
   L.target = c.take(rows * 4);
   L.xc = c.take(rows * L.pitch * 2);
-  L.bias_over = c.take(width <= kNarrowWidth ? items * 4 : 0);
+  L.bias_over = c.take(width <= kNarrowWidth ? up(items, 64) * 4 : 0);
 }
 CeLayout forward_layout(int64_t rows, int64_t items, int64_t width) {
   CeLayout L = {};
@@ -337,6 +339,10 @@ CeLayout forward_layout(int64_t rows, int64_t items, int64_t width) {
   L.total = c.at;
   return L;
 }
+int64_t sum_x_bytes(int64_t rows, int64_t width) {
+  const int64_t one = rows * up(width, 4) * 4;
+  return hmax(one, hmin(kSumBytes, kMostSplits * one));
+}
 CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   CeLayout L = {};
   Carve c;
@@ -349,9 +355,9 @@ CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   L.piece = hmin(most, hmax(kLeastPiece, kZElems / hmax(rows, 1) / 256 * 256));
   const int64_t z = hmin(rows * most, hmax(kZElems, rows * kLeastPiece));
   L.z = c.take((z + 64 * most) * 2);  // panels of whole 64 rows
-  L.sum_x = c.take(hmax(rows * width * 4, hmin(kSumBytes, kMostSplits * rows * width * 4)));
+  L.sum_x = c.take(sum_x_bytes(rows, width));
   L.sum_w = c.take(kSumBytes);
-  L.bias_part = c.take(z / 64 * 4 + most * 4);
+  L.bias_part = c.take(z / 64 * 4 + 4 * most * 4);  // of 64 rows, of 16 where there are up to 64
   L.total = c.at;
   return L;
 }
@@ -360,10 +366,11 @@ CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
 struct TilePick {
   int tile, splits;
 };
-TilePick pick_tile(const TileCost (&costs)[3], int64_t m, int64_t n, int64_t k, int most_splits, int64_t most_bytes) {
+template <int N>
+TilePick pick_tile(const TileCost (&costs)[N], int64_t m, int64_t n, int64_t k, int most_splits, int64_t most_bytes) {
   TilePick best = {0, 1};
   double least = -1.0;
-  for (int t = 0; t < 3; ++t) {
+  for (int t = 0; t < N; ++t) {
     const TileCost& c = costs[t];
     const double tiles = static_cast<double>(((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn));
     for (int split = 1; split <= most_splits; split *= 2) {
@@ -379,6 +386,8 @@ TilePick pick_tile(const TileCost (&costs)[3], int64_t m, int64_t n, int64_t k, 
   return best;
 }
 // Costs of the kernels here: grouped_linear.h's, with square tiles through registers as well.
+constexpr TileCost kGradX[4] = {kDirectTiles[0], kDirectTiles[1], kDirectTiles[2], {256, 128, 512, 256, 5.0, 0.8, 0.8}};
+constexpr TileCost kGradXRegisters[4] = {kRegisterTiles[0], {128, 128, 256, 512, 5.0, 0.8, 1.5}, kRegisterTiles[2], kRegisterTiles[1]};
 constexpr TileCost kAlongRegisters[3] = {{256, 256, 512, 256, 6.0, 1.3, 2.05}, {128, 128, 256, 512, 5.0, 0.8, 1.5}, {64, 64, 256, 1024, 3.0, 0.55, 1.35}};
 
 // Into how many ranges their items go: about 2048 workgroups, of 16 tiles of 64 items at least, of fewer where that leaves
@@ -411,7 +420,7 @@ CeBatch batch_of(char* ws, const CeLayout& L, int64_t rows, int64_t items, int64
   if (narrow) {
     b.flip = scale < 0.0f ? 1 : scale == 0.0f ? 2 : 0;
     scale = scale < 0.0f ? -scale : scale == 0.0f ? 1.0f : scale;
-    if (bias) b.bias_over = reinterpret_cast<float*>(ws + L.bias_over);
+    b.bias_over = reinterpret_cast<float*>(ws + L.bias_over);
     b.over = 1.0f / scale;
   }
   return b;
@@ -423,10 +432,11 @@ tbe_status launch_rows(const CeBatch& b, int dtype, hipStream_t s) {
     hipLaunchKernelGGL(ce_count_kernel, dim3(static_cast<unsigned>((b.rows + kBlock - 1) / kBlock)), dim3(kBlock), 0, s, b);
     if (tbe_status st = check_launch("ce_count")) return st;
   }
-  const int each = b.rows > (1 << 17) ? kBlock : kRowsAtOnce;
-  const unsigned groups = static_cast<unsigned>(hmax(1, (b.rows + each - 1) / each));  // no rows: their count, 0
+  const int each = b.rows > (1 << 17) ? kBlock : b.rows > (1 << 15) ? 32 : kRowsAtOnce;
+  const int groups = static_cast<int>(hmax(1, (b.rows + each - 1) / each));  // no rows: their count, 0
+  const int more = b.bias_over ? static_cast<int>(hmin(2048, (b.items + 4 * kBlock - 1) / (4 * kBlock))) : 0;
   auto kernel = dtype == TBE_F16 ? ce_rows_kernel<1> : ce_rows_kernel<2>;
-  hipLaunchKernelGGL(kernel, dim3(groups), dim3(kBlock), 0, s, b, each, counted ? 1 : 0);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups + more)), dim3(kBlock), 0, s, b, each, groups, counted ? 1 : 0);
   return check_launch("ce_rows");
 }
 CeRows rows_of(const CeBatch& b) { return CeRows{b.count, b.row, b.target, b.lse, b.grad, b.largest}; }
@@ -473,8 +483,10 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
     }
     if (st != TBE_OK) break;
     ProfScope ps("ce_join", s);
-    hipLaunchKernelGGL(ce_join_kernel, dim3(static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows)), dim3(kJoinRows * kJoinGroups), 0, s,
-                       a.part, rows, parts, reinterpret_cast<float2*>(ws + L.all), first == 0 ? 1 : 0, first + piece >= items ? 1 : 0, b);
+    const bool each = rows <= 256 && parts >= 128;  // a workgroup for each row
+    auto join = each ? ce_join_kernel<1> : ce_join_kernel<16>;
+    hipLaunchKernelGGL(join, dim3(static_cast<unsigned>(each ? rows : (rows + 15) / 16)), dim3(1024), 0, s, a.part, rows, parts,
+                       reinterpret_cast<float2*>(ws + L.all), first == 0 ? 1 : 0, first + piece >= items ? 1 : 0, b);
     st = check_launch("ce_join");
   }
   return st;
@@ -504,10 +516,10 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   a.w_stride = weight_stride; a.scale = scale; a.r = rows_of(b);
   a.z = reinterpret_cast<uint16_t*>(ws + L.z); a.panel = up(rows, 64) * 64;
   a.factor = factor;
+  a.sum_pitch = up(width, 4);
   a.bias_part = grad_bias ? reinterpret_cast<float*>(ws + L.bias_part) : nullptr;
   a.bias_stride = L.piece;
   const TileCost(&costs)[3] = direct ? kDirectTiles : kAlongRegisters;
-  const int64_t sum_x_bytes = hmax(rows * width * 4, hmin(kSumBytes, kMostSplits * rows * width * 4));
   TilePick x_pick = {0, 1};
   if (rows == 0) grad_x = nullptr;  // the gradients of the weights and biases are zeros
   for (int64_t first = 0; st == TBE_OK && first < items; first += L.piece) {
@@ -515,9 +527,9 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
     a.items = static_cast<int>(hmin(L.piece, items - first));
     a.w = static_cast<const uint16_t*>(weight) + first * weight_stride;
     a.bias = bias ? bias + first : nullptr;
-    int bm = 64;  // rows that a part of the biases' gradient sums over
+    const bool few = rows <= 64;
+    int bm = few ? 16 : 64;  // rows that a part of the biases' gradient sums over
     if (rows > 0 && narrow) {
-      const bool few = rows <= 64;
       a.splits = narrow_splits(rows, a.items, few);
       st = f16 ? ce_launch_narrow_z<1>(a, few, s) : ce_launch_narrow_z<2>(a, few, s);
     } else if (rows > 0) {
@@ -533,14 +545,15 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
     }
     if (st == TBE_OK && grad_x) {
       // the same shares for every piece: their sums go on
-      if (first == 0) x_pick = pick_tile(costs, rows, width, a.items, kMostSplits, sum_x_bytes);
+      if (first == 0 && direct) x_pick = pick_tile(kGradX, rows, a.sum_pitch, a.items, kMostSplits, sum_x_bytes(rows, width));
+      else if (first == 0) x_pick = pick_tile(kGradXRegisters, rows, a.sum_pitch, a.items, kMostSplits, sum_x_bytes(rows, width));
       a.sum = reinterpret_cast<float*>(ws + L.sum_x);
       a.splits = x_pick.splits;
       a.add = first > 0;
       st = f16 ? ce_launch_grad_x<1>(a, x_pick.tile, direct, s) : ce_launch_grad_x<2>(a, x_pick.tile, direct, s);
     }
     if (st == TBE_OK && grad_weight) {
-      const TilePick p = pick_tile(kWeightTiles, a.items, width, rows, kMostSplits, kSumBytes);
+      const TilePick p = pick_tile(kWeightTiles, a.items, a.sum_pitch, rows, kMostSplits, kSumBytes);
       a.sum = reinterpret_cast<float*>(ws + L.sum_w);
       a.splits = p.splits;
       a.add = 0;
@@ -550,7 +563,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
       if (st == TBE_OK && p.splits > 1) {
         ProfScope ps("ce_grad_w_sum", s);
         auto kernel = f16 ? ce_grad_w_kernel<1> : ce_grad_w_kernel<2>;
-        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((a.items + 3) / 4, 8192))), dim3(kBlock), 0, s, a.sum, p.splits, a.items,
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((a.items + 3) / 4, 8192))), dim3(kBlock), 0, s, a.sum, a.sum_pitch, p.splits, a.items,
                            a.width, factor, b.largest, static_cast<uint16_t*>(a.out), grad_weight_stride);
         st = check_launch("ce_grad_w_sum");
       }
@@ -560,7 +573,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   ProfScope ps("ce_grad_x_sum", s);
   auto kernel = f16 ? ce_grad_x_kernel<1> : ce_grad_x_kernel<2>;
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((rows + 3) / 4, 8192))), dim3(kBlock), 0, s, b,
-                     reinterpret_cast<const float*>(ws + L.sum_x), x_pick.splits, static_cast<int>(width),
+                     reinterpret_cast<const float*>(ws + L.sum_x), a.sum_pitch, x_pick.splits, static_cast<int>(width),
                      factor, static_cast<uint16_t*>(grad_x), grad_x_stride);
   return check_launch("ce_grad_x_sum");
 }

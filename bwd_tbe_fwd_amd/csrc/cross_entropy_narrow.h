@@ -1,16 +1,19 @@
 // Logits of rows of up to 256 columns (cross_entropy.h says what becomes of them).
 //
-// So few columns leave 2 width operations of the matrix instructions for each logit, as long as the exponential and what
-// stands around it take on the vector unit: at 128 columns 16 cycles a product of 16 x 16 x 32 against 4 cycles an
-// instruction and 16 an exponential, 256 logits a wave.  So the rows stay in registers, the items pass through LDS, and the
-// two waves of a SIMD, of different workgroups, overlap: while one takes products the other takes exponentials.
-//  * A workgroup takes kRows<WM> rows and a range of the items.  WM = 4: 64 rows a wave, all waves the same items; WM = 1,
-//    for few rows: 64 rows in all, a quarter of the items a wave.
-//  * A ring of three tiles of 64 items in LDS, loaded two ahead, one barrier a tile.  What a wave stores leaves before the
-//    loads of its step start: the loads' counter then needs no look at the stores.
-//  * Forward a lane keeps a maximum and a sum for its 4 rows over all its items; lanes, waves and workgroups are joined at
-//    the end.  The logits' factor goes into the exponential's argument and the biases, divided by it beforehand, are where
-//    the products' sums begin: a logit then costs a multiply-add, an exponential, a half of a maximum and an addition.
+// So few columns leave the matrix instructions no more to do for a logit than the exponential and what stands around it
+// leave the vector unit: at 128 columns 16 cycles a product of 16 x 16 x 32, four for each 64 x 32 logits of a lane group's 32,
+// against 16 an exponential and 4 an instruction.  So the rows stay in registers, the items pass through LDS, and a wave's
+// products of 32 items are taken between the exponentials of the 32 items before.
+//  * A workgroup takes 64 MF rows, 16 MF a wave, and a range of the items.  MF = 4; MF = 1 for few rows, where the items'
+//    way from memory bounds it.
+//  * A ring of three tiles of 64 items in LDS, loaded two ahead, one barrier a tile.  z is stored by equally many stores in
+//    every wave (what lies outside goes past the buffer's range), so that the wait for a tile's loads leaves the stores and
+//    loads of the last step on their way.
+//  * Each item has a bias, divided by the logits' factor beforehand, where the products' sums begin: 0 without biases,
+//    -infinity behind the last item, so that no tile looks at the edge.
+//  * Forward a lane keeps a sum for each of its rows over all its items, less a reference that moves only when a logit is
+//    2^kSlack above it, as powers of two go: most tiles change nothing but the sums.  A logit costs a multiply-add, an
+//    exponential, an addition and less than one instruction more.
 #pragma once
 
 #include "cross_entropy_tile.h"
@@ -19,56 +22,48 @@ namespace tbe {
 
 constexpr int kNarrowItems = 64;  // of a tile
 constexpr int kRing = 3;
-template <int WM> constexpr int kNarrowRows = 64 * WM;
+constexpr float kSlack = 16.0f;
+constexpr float kFloor = -1e38f;  // a reference is no lower, so that it stays finite
 
 // One dword a lane from offset `o` of the buffer to LDS, lane l's at lds + 4 l (load_to_lds of tile_products.h is its like).
 __device__ __forceinline__ void load_dword_to_lds(u32x4 r, uint32_t o, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(o), "s"(r) : "memory", "m0");
 }
 
-template <int DT, bool BACK, bool BIAS, int KS, int WM>
+// Sums over the 16 lanes of a row of v[c], c < 8: lane l gets that of c = l % 8.  Lanes exchange halves: 7 additions, not 32.
+__device__ __forceinline__ float columns_sum(const float (&v)[8]) {
+  const int l = lane_id();
+  float a[4], b[2];
+  const bool h2 = l & 4, h1 = l & 2, h0 = l & 1;
+  // lanes l and 7 - l of 8: the lower keeps c < 4 and hands over the others
+#pragma unroll
+  for (int c = 0; c < 4; ++c) a[c] = (h2 ? v[c + 4] : v[c]) + dpp_f<kDppHalfMirror>(h2 ? v[c] : v[c + 4]);
+  // then l xor 2, then l xor 1
+#pragma unroll
+  for (int c = 0; c < 2; ++c) b[c] = (h1 ? a[c + 2] : a[c]) + dpp_f<kDppXor2>(h1 ? a[c] : a[c + 2]);
+  const float s = (h0 ? b[1] : b[0]) + dpp_f<kDppXor1>(h0 ? b[0] : b[1]);
+  return s + dpp_f<0x128>(s);  // row_ror:8, the other 8 lanes of the row
+}
+
+template <int DT, bool BACK, int KS, int MF>
 __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
-  constexpr int T = 256, MF = 4, WN = 4 / WM, NF = 4 / WN, LEN = 4 * NF, KT = KS / 2;
-  using OB = Operand<true, kNarrowItems, 4 * NF, T, true>;
+  constexpr int T = 256, NF = 2, LEN = 4 * NF, KT = KS / 2, kRows = 64 * MF;
+  using OB = Operand<true, kNarrowItems, LEN, T, true>;
   constexpr int kTile = KT * OB::kElems;
-  constexpr int kLoads = KT * OB::kEach + (BIAS ? 1 : 0);  // a wave's, of a tile
+  constexpr int kLoads = KT * OB::kEach + 1;  // a wave's, of a tile
+  constexpr int kStores = MF;                 // of 32 items of z, and one for their columns' sums
   __shared__ __align__(16) uint16_t lds[kRing * kTile];
-  __shared__ __align__(16) float s_bias[BIAS ? kRing * 4 * kNarrowItems : 1];  // a copy for each wave
+  __shared__ __align__(16) float s_bias[kRing * 4 * kNarrowItems];  // a copy for each wave
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id(), g = l >> 4;
-  const int wm = w / WN * 64, wn = w % WN * (16 * NF);
-  const int count = *a.r.count, row_tiles = (count + kNarrowRows<WM> - 1) / kNarrowRows<WM>;
+  const int count = *a.r.count, row_tiles = (count + kRows - 1) / kRows;
   // this workgroup's rows and tiles of items: a chiplet's workgroups share ranges of items
   const int64_t total = static_cast<int64_t>(row_tiles) * a.splits, x = blockIdx.x % 8;
   const int64_t id = total * x / 8 + blockIdx.x / 8;
   if (id >= total * (x + 1) / 8) return;
-  const int split = static_cast<int>(id / row_tiles), m0 = static_cast<int>(id % row_tiles) * kNarrowRows<WM>;
+  const int split = static_cast<int>(id / row_tiles), m0 = static_cast<int>(id % row_tiles) * kRows + w * (16 * MF);  // the wave's first row
   const int tiles = (a.items + kNarrowItems - 1) / kNarrowItems;
   const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / a.splits), t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / a.splits);
   const int steps = (a.width + kStepK - 1) / kStepK;
-
-  // the rows: lane l holds row l % 16 of each 16, 8 columns from 8 (l / 16) on of each 32
-  u16x8_t fa[MF][KS];
-  int target[MF];
-  float lse[MF], grad[MF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const int m = m0 + wm + 16 * i + (l & 15);
-    const bool in = m < count;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const int c = 32 * k + 8 * g;
-      fa[i][k] = u16x8_t{};
-      if (in && c < a.x_stride) fa[i][k] = *reinterpret_cast<const u16x8_t*>(static_cast<const uint16_t*>(a.x) + m * a.x_stride + c);
-    }
-    if constexpr (BACK) {
-      target[i] = in ? a.r.target[m] - a.first - wn - g * LEN : -1;
-      const float e = in ? a.r.lse[m] : 0.0f;
-      lse[i] = e < -1e38f ? -kInfinity : fmaf(e, -kLog2e, DT == 1 ? 15.0f : 0.0f);  // every item masked: no probability
-      grad[i] = in ? a.r.grad[m] / kUnit<DT> : 0.0f;
-    }
-  }
-  // what the exponential of base 2 takes: the sum of products times `unit`, less the row's reference
-  const float unit = a.scale * kLog2e;
 
   OB B;
   auto stage = [&](int t) {
@@ -81,164 +76,201 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
 #pragma unroll
       for (int i = 0; i < OB::kEach; ++i) B.template load<false>(i, k < steps ? k * kStepK : a.width, lds + slot * kTile + k * OB::kElems);
     }
-    if constexpr (BIAS) {
-      const uint64_t u = reinterpret_cast<uint64_t>(a.bias + (t < t1 ? n0 : 0));
-      const u32x4 r = {static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32) & 0xffffu, 0x7fffffffu, 0x00027000u};
-      load_dword_to_lds(r, l < n_left ? 4 * l : kOutside,
-                        static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)(s_bias + (slot * 4 + w) * kNarrowItems))));
-    }
+    const uint64_t u = reinterpret_cast<uint64_t>(a.bias + (t < t1 ? n0 : 0));
+    const u32x4 r = {static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32) & 0xffffu, 0x7fffffffu, 0x00027000u};
+    load_dword_to_lds(r, 4 * l, static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)(s_bias + (slot * 4 + w) * kNarrowItems))));
   };
-
-  float top[MF], sum[MF];  // forward
-#pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    top[i] = -kInfinity;
-    sum[i] = 0.0f;
-  }
-  u32x2 z[BACK ? MF : 1][BACK ? NF : 1];  // backward: the last tile's, and its columns' sums
-  float column = 0.0f;
-  auto store_z = [&](int t) {
-    if constexpr (BACK) {
-#pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        const int m = m0 + wm + 16 * i + (l & 15);
-        if (m < count) {
-          uint16_t* p = a.z + t * a.panel + static_cast<int64_t>(m) * 64 + wn + g * LEN;
-#pragma unroll
-          for (int j = 0; j + 1 < NF; j += 2) *reinterpret_cast<u32x4*>(p + 4 * j) = u32x4{z[i][j].x, z[i][j].y, z[i][j + 1].x, z[i][j + 1].y};
-          if constexpr (NF == 1) *reinterpret_cast<u32x2*>(p) = z[i][0];
-        }
-      }
-      // lane l has the sum of item g LEN + l % 16; with 4 items a lane group the first 4 lanes do
-      const int n = t * kNarrowItems + wn + g * LEN + (l & 15);
-      if (a.bias_part && (l & 15) < LEN && n < a.items && m0 + wm < count) a.bias_part[(m0 + wm) / 64 * a.bias_stride + n] = column;
-    }
-  };
-
-  const int b_place = OB::read_place(wn + ((l & 15) >> 2) * LEN + (l & 3));
-  const int b_half[2] = {b_place, OB::second_half(b_place)};
   stage(t0);
   stage(t0 + 1);
-  for (int t = t0; t < t1; ++t) {
-    wait_loads<kLoads>();  // this tile's: those of the next one may be on their way
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (BACK && t > t0) store_z(t - 1);
-    stage(t + 2);          // where the tile before this one was: every wave has read it
-    const int slot = (t - t0) % kRing;
-    f32x4 acc[MF][NF];
+
+  // the rows: lane l holds row l % 16 of each 16, 8 columns from 8 (l / 16) on of each 32
+  u16x8_t fa[MF][KS];
+  int target[MF];
+  float ref[MF], grad[MF];      // backward: -lse in powers of two
+  float top[MF], sum[MF];       // forward
+#pragma unroll
+  for (int i = 0; i < MF; ++i) {
+    const int m = m0 + 16 * i + (l & 15);
+    const bool in = m < count;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const int c = 32 * k + 8 * g;
+      fa[i][k] = u16x8_t{};
+      if (in && c < a.x_stride) fa[i][k] = *reinterpret_cast<const u16x8_t*>(static_cast<const uint16_t*>(a.x) + m * a.x_stride + c);
+    }
+    top[i] = -kInfinity;
+    sum[i] = 0.0f;
+    ref[i] = kFloor;
+    if constexpr (BACK) {
+      target[i] = in ? a.r.target[m] - a.first : -1;
+      const float e = in ? a.r.lse[m] : 0.0f;
+      ref[i] = e < kFloor ? -kInfinity : fmaf(e, -kLog2e, DT == 1 ? 15.0f : 0.0f);  // every item masked: no probability
+      grad[i] = in && a.bias_part ? a.r.grad[m] / kUnit<DT> : 0.0f;
+    }
+  }
+  // what the exponential of base 2 takes: the sum of products times `unit`, less the row's reference
+  const float unit = a.scale * kLog2e;
+
+  const int b_place = OB::read_place(((l & 15) >> 2) * LEN + (l & 3));
+  // 32 items from `half` * 32 on of the tile in `slot`
+  auto products = [&](f32x4 (&acc)[MF][NF], int slot, int half) {
+    const uint16_t* s = lds + slot * kTile + half * 32 * kStepK;
+    const int place[2] = {b_place, OB::second_half(b_place)};
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-      f32x4 from = {0, 0, 0, 0};
-      if constexpr (BIAS) from = *reinterpret_cast<const f32x4*>(s_bias + (slot * 4 + w) * kNarrowItems + wn + g * LEN + 4 * j);
+      const f32x4 from = *reinterpret_cast<const f32x4*>(s_bias + (slot * 4 + w) * kNarrowItems + half * 32 + g * LEN + 4 * j);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const u16x8_t fb = OB::read(lds + slot * kTile + k / 2 * OB::kElems + b_half[k % 2], 4 * j);
+        const u16x8_t fb = OB::read(s + k / 2 * OB::kElems + place[k % 2], 4 * j);
 #pragma unroll
         for (int i = 0; i < MF; ++i) acc[i][j] = mfma16<DT>(fb, fa[i][k], k == 0 ? from : acc[i][j]);
       }
     }
-    const int n0 = t * kNarrowItems;
-    const int left = a.items - n0 - wn - g * LEN;  // of this lane's items
-    const bool edge = a.items - n0 < kNarrowItems;
+  };
+  // Products between the exponentials' instructions, an equal share each.
+  auto interleave = [&] {
+    constexpr int kProducts = MF * NF * KS, kVector = MF * (BACK ? LEN : 2 * LEN + 2);
+#pragma unroll
+    for (int q = 0; q < kProducts; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, (kVector + kProducts - 1) / kProducts, 0);
+      __builtin_amdgcn_sched_group_barrier(0x400, (MF * LEN + kProducts - 1) / kProducts, 0);
+    }
+  };
+  // Forward, ahead of their exponentials: whether a logit asks for another reference.
+  auto look = [&](const f32x4 (&acc)[MF][NF]) {
     if constexpr (!BACK) {
-      if (edge) {
-#pragma unroll
-        for (int c = 0; c < LEN; ++c)
-          if (c >= left)
-#pragma unroll
-            for (int i = 0; i < MF; ++i) acc[i][c / 4][c % 4] = -kInfinity;
-      }
+      float over = kFloor;
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
-        float most = acc[i][0][0];
+        float most = acc[i][0][0];  // NaN stays NaN: no instruction to make sure that it is a quiet one
 #pragma unroll
-        for (int c = 1; c < LEN; ++c) most = fmaxf(most, acc[i][c / 4][c % 4]);
-        const float old = fmaxf(top[i], -1e38f);  // a reference that stays finite
-        top[i] = fmaxf(top[i], most);
-        const float from = fmaxf(top[i], -1e38f), base = -from * unit;
-        if (__any(from > old)) sum[i] *= __builtin_amdgcn_exp2f((old - from) * unit);
-        float part[4] = {};
-#pragma unroll
-        for (int c = 0; c < LEN; ++c) part[c % 4] += __builtin_amdgcn_exp2f(fmaf(acc[i][c / 4][c % 4], unit, base));
-        sum[i] += (part[0] + part[1]) + (part[2] + part[3]);
+        for (int c = 1; c < LEN; ++c) most = __builtin_elementwise_maximum(most, acc[i][c / 4][c % 4]);
+        top[i] = __builtin_elementwise_maximum(top[i], most);
+        over = __builtin_elementwise_maximum(over, (most - ref[i]) * unit);
       }
-    } else {
-      float columns[LEN];
+      if (__any(over > kSlack)) {
 #pragma unroll
-      for (int c = 0; c < LEN; ++c) columns[c] = 0.0f;
+        for (int i = 0; i < MF; ++i) {
+          float now = fmaxf(top[i], kFloor);
+          asm volatile("" : "+v"(now));  // keeps what follows from being worked out where it is not needed
+          sum[i] *= __builtin_amdgcn_exp2f((ref[i] - now) * unit);
+          ref[i] = now;
+        }
+      }
+    }
+  };
+  // The logits of 32 items from n0 on, and what becomes of them.
+  auto consume = [&](f32x4 (&acc)[MF][NF], int n0) {
+    if constexpr (!BACK) {
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
+        const float base = -ref[i] * unit;
         float p[LEN];
 #pragma unroll
-        for (int c = 0; c < LEN; ++c) p[c] = __builtin_amdgcn_exp2f(fmaf(acc[i][c / 4][c % 4], unit, lse[i]));
-        const unsigned at = static_cast<unsigned>(target[i] - n0);
-        if (__any(at < LEN)) {
+        for (int c = 0; c < LEN; ++c) p[c] = __builtin_amdgcn_exp2f(fmaf(acc[i][c / 4][c % 4], unit, base));
+        sum[i] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      }
+    } else {
+      bool here = false;
 #pragma unroll
-          for (int c = 0; c < LEN; ++c) p[c] -= c == static_cast<int>(at) ? kUnit<DT> : 0.0f;
+      for (int i = 0; i < MF; ++i) {
+        here |= static_cast<unsigned>(target[i] - n0) < 32u;
+#pragma unroll
+        for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] = __builtin_amdgcn_exp2f(fmaf(acc[i][c / 4][c % 4], unit, ref[i]));
+      }
+      if (__any(here)) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          int at = target[i] - n0 - g * LEN;
+          asm volatile("" : "+v"(at));  // keeps what follows from being worked out where it is not needed
+#pragma unroll
+          for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] -= c == at ? kUnit<DT> : 0.0f;
         }
-        if (edge) {
+      }
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(a.z + n0 / 64 * a.panel + n0 % 64, 0, 0x7fffffff, 0x00027000);
 #pragma unroll
-          for (int c = 0; c < LEN; ++c)
-            if (c >= left) p[c] = 0.0f;
-        }
-        if (a.bias_part && m0 + wm + 16 * i + (l & 15) < count) {
+      for (int i = 0; i < MF; ++i) {
+        const int m = m0 + 16 * i + (l & 15);
+        Vec<uint16_t, LEN> v;
 #pragma unroll
-          for (int c = 0; c < LEN; ++c) columns[c] = fmaf(p[c], grad[i], columns[c]);
-        }
-#pragma unroll
-        for (int j = 0; j < NF; ++j) {
-          Vec<uint16_t, 4> v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v.e[e] = tower_from_f<DT>(p[4 * j + e]);
-          z[i][j] = __builtin_bit_cast(u32x2, v);
-        }
+        for (int c = 0; c < LEN; ++c) v.e[c] = tower_from_f<DT>(acc[i][c / 4][c % 4]);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, m < count ? static_cast<uint32_t>(m) * 128 + g * LEN * 2 : kOutside, 0, 0);
       }
       if (a.bias_part) {
+        float columns[LEN];
 #pragma unroll
         for (int c = 0; c < LEN; ++c) {
-          const float s = lanes_sum<16>(columns[c]);
-          if (c == (l & 15)) column = s;
+          columns[c] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < MF; ++i)
+            if (m0 + 16 * i + (l & 15) < count) columns[c] = fmaf(acc[i][c / 4][c % 4], grad[i], columns[c]);
         }
+        const float column = columns_sum(columns);
+        const int n = n0 + g * LEN + (l & 7);
+        const __amdgpu_buffer_rsrc_t q = __builtin_amdgcn_make_buffer_rsrc(a.bias_part + m0 / (16 * MF) * a.bias_stride, 0, 0x7fffffff, 0x00027000);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(column), q, (l & 8) == 0 && n < a.items && m0 < count ? 4 * n : kOutside, 0, 0);
       }
     }
+  };
+
+  f32x4 first[MF][NF], second[MF][NF];  // of a tile's two halves
+  for (int t = t0; t < t1; ++t) {
+    // this tile's loads: the next one's may be on their way, and the stores of the last step
+    if (BACK && t > t0 + 1) {
+      if (a.bias_part) wait_loads<kLoads + 2 * (kStores + 1)>();
+      else wait_loads<kLoads + 2 * kStores>();
+    } else if (BACK && t > t0) {
+      if (a.bias_part) wait_loads<kLoads + kStores + 1>();
+      else wait_loads<kLoads + kStores>();
+    } else {
+      wait_loads<kLoads>();
+    }
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    stage(t + 2);  // where the tile before this one was: every wave has read it
+    const int slot = (t - t0) % kRing;
+    if (t > t0) {
+      look(second);
+      products(first, slot, 0);
+      consume(second, (t - 1) * kNarrowItems + 32);
+      interleave();
+    } else {
+      products(first, slot, 0);
+    }
+    look(first);
+    products(second, slot, 1);
+    consume(first, t * kNarrowItems);
+    interleave();
+  }
+  if (t1 > t0) {
+    look(second);
+    consume(second, (t1 - 1) * kNarrowItems + 32);
   }
   wait_loads<0>();  // nothing is on its way into LDS when the workgroup ends
-  if constexpr (BACK) {
-    if (t1 > t0) store_z(t1 - 1);
-  } else {
-    float2* stat = reinterpret_cast<float2*>(lds);  // [WN][rows]
-    __syncthreads();
+  if constexpr (!BACK) {
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
-      const float from = fmaxf(top[i], -1e38f);
-      float all = fmaxf(top[i], __shfl_xor(top[i], 16));
+      // the lanes that share a row; where no logit was above kFloor the sum is 0 and the maximum tells what there was
+      const int m = m0 + 16 * i + (l & 15);
+      float all = fmaxf(ref[i], __shfl_xor(ref[i], 16)), most = fmaxf(top[i], __shfl_xor(top[i], 16));
       all = fmaxf(all, __shfl_xor(all, 32));
-      float s = sum[i] * __builtin_amdgcn_exp2f((from - fmaxf(all, -1e38f)) * unit);
+      most = fmaxf(most, __shfl_xor(most, 32));
+      float s = sum[i] * __builtin_amdgcn_exp2f((ref[i] - all) * unit);
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
-      if (l < 16) stat[w % WN * kNarrowRows<WM> + wm + 16 * i + l] = make_float2(all == -kInfinity ? all : all * a.scale, s);
-    }
-    __syncthreads();
-    if (threadIdx.x < kNarrowRows<WM> && m0 + static_cast<int>(threadIdx.x) < count) {
-      float2 all = stat[threadIdx.x];
-      for (int k = 1; k < WN; ++k) all = ce_join(all, stat[k * kNarrowRows<WM> + threadIdx.x]);
-      a.part[split * a.rows + m0 + threadIdx.x] = all;
+      if (l < 16 && m < count) a.part[split * a.rows + m] = make_float2(most <= kFloor ? (most == -kInfinity ? most : most * a.scale) : all * a.scale, s);
     }
   }
 }
 
-template <int DT, bool BACK, int KS, int WM>
-tbe_status ce_narrow_go(CeArgs a, hipStream_t s) {
-  const int64_t groups = ((a.rows + kNarrowRows<WM> - 1) / kNarrowRows<WM>) * a.splits;
-  const char* what = BACK ? "ce_z" : "ce_logits";
-  return a.bias ? ce_launch(ce_narrow_kernel<DT, BACK, true, KS, WM>, what, 256, groups, 1, a, s)
-                : ce_launch(ce_narrow_kernel<DT, BACK, false, KS, WM>, what, 256, groups, 1, a, s);
+template <int DT, bool BACK, int KS, int MF>
+tbe_status ce_narrow_go(const CeArgs& a, hipStream_t s) {
+  return ce_launch(ce_narrow_kernel<DT, BACK, KS, MF>, BACK ? "ce_z" : "ce_logits", 256, (a.rows + 64 * MF - 1) / (64 * MF) * a.splits, 1, a, s);
 }
 template <int DT, bool BACK>
 tbe_status ce_narrow(const CeArgs& a, bool few, hipStream_t s) {
-  if (few)
-    return a.width <= 64 ? ce_narrow_go<DT, BACK, 2, 1>(a, s) : a.width <= 128 ? ce_narrow_go<DT, BACK, 4, 1>(a, s) : ce_narrow_go<DT, BACK, 8, 1>(a, s);
+  if (few) return a.width <= 64 ? ce_narrow_go<DT, BACK, 2, 1>(a, s) : a.width <= 128 ? ce_narrow_go<DT, BACK, 4, 1>(a, s) : ce_narrow_go<DT, BACK, 8, 1>(a, s);
   return a.width <= 64 ? ce_narrow_go<DT, BACK, 2, 4>(a, s) : a.width <= 128 ? ce_narrow_go<DT, BACK, 4, 4>(a, s) : ce_narrow_go<DT, BACK, 8, 4>(a, s);
 }
 

@@ -103,8 +103,10 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
 #pragma unroll
       for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] = __builtin_amdgcn_exp2f(fmaf(logit(i, c), kLog2e, base));
       if (__any(at < LEN)) {
+        int here = static_cast<int>(at);
+        asm volatile("" : "+v"(here));  // keeps what follows from being worked out where it is not needed
 #pragma unroll
-        for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] -= c == static_cast<int>(at) ? kOne : 0.0f;
+        for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] -= c == here ? kOne : 0.0f;
       }
       if (n_left < BN) {  // z's columns up to a whole 16 bytes are read
 #pragma unroll
@@ -169,7 +171,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
     A.init(a.z, a.panel, m0, k0, m_left, k);
     B.init(static_cast<const uint16_t*>(a.xg) + k0 * a.x_stride + n0, a.x_stride, n_left, k, a.width);
   }
-  const int64_t pitch = a.width;
+  const int64_t pitch = a.sum_pitch;
   float* const sum = a.sum + (static_cast<int64_t>(blockIdx.y) * (X ? a.rows : a.items) + m0 + wm) * pitch + n0 + wn;
   f32x4 acc[MF][NF];
 #pragma unroll
@@ -226,6 +228,9 @@ tbe_status ce_grad(const CeArgs& a, int tile, hipStream_t s) {
   const char* what = X ? "ce_grad_x" : "ce_grad_w";
   const int64_t m = X ? a.rows : a.items;
   if (tile == kTile256) return ce_launch(ce_grad_kernel<DT, X, 256, 256, 2, 4, DIRECT>, what, 512, ce_tiles(m, 256, a.width, 256), a.splits, a, s);
+  if constexpr (X) {
+    if (tile == kTile256x128) return ce_launch(ce_grad_kernel<DT, X, 256, 128, 4, 2, DIRECT>, what, 512, ce_tiles(m, 256, a.width, 128), a.splits, a, s);
+  }
   if (tile == kTile128) return ce_launch(ce_grad_kernel<DT, X, 128, 128, 2, 2, DIRECT>, what, 256, ce_tiles(m, 128, a.width, 128), a.splits, a, s);
   return ce_launch(ce_grad_kernel<DT, X, 64, 64, 2, 2, DIRECT>, what, 256, ce_tiles(m, 64, a.width, 64), a.splits, a, s);
 }
