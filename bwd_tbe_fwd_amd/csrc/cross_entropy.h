@@ -22,6 +22,8 @@ struct CeRows {
   const float* lse;        // backward
   const float* grad;       // backward: grad_loss
   const float* largest;    // backward: of |grad_loss|
+  const float* ref;        // backward, narrow rows: -lse in powers of two, -infinity up to a whole 64 rows
+  const float* part;       // backward, narrow rows: grad_loss over the largest
 };
 
 struct CeArgs {
@@ -55,6 +57,8 @@ struct CeArgs {
 template <int DT> constexpr float kUnit = DT == 1 ? 32768.0f : 1.0f;
 
 constexpr float kInfinity = __builtin_huge_valf();
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kFloor = -1e38f;  // lower logits count as masked where they would overflow as powers of two
 
 // Two parts of a row: their maximum, and the sum of the exponentials less it.
 __device__ __forceinline__ float2 ce_join(float2 a, float2 b) {
@@ -69,7 +73,7 @@ enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile256x128 = 3 };  // the last
 template <int DT> tbe_status ce_launch_forward(const CeArgs& a, int tile, bool direct, hipStream_t s);
 template <int DT> tbe_status ce_launch_z(const CeArgs& a, int tile, bool direct, hipStream_t s);
 template <int DT> tbe_status ce_launch_narrow_forward(const CeArgs& a, bool few, hipStream_t s);
-template <int DT> tbe_status ce_launch_narrow_z(const CeArgs& a, bool few, hipStream_t s);
+template <int DT> tbe_status ce_launch_fused(const CeArgs& a, bool x, hipStream_t s);
 template <int DT> tbe_status ce_launch_grad_x(const CeArgs& a, int tile, bool direct, hipStream_t s);
 template <int DT> tbe_status ce_launch_grad_w(const CeArgs& a, int tile, hipStream_t s);
 

@@ -43,6 +43,8 @@ struct CeBatch {
   float* lse;
   float* grad;
   uint16_t* xg;            // x times grad_loss over the largest; NULL: not asked for
+  float* ref;              // narrow rows: -lse in powers of two (fp16: 15 more, kUnit), and grad_loss over the largest, with
+  float* part;             // -infinity and 0 up to a whole 64 rows; NULL: not asked for
 };
 __device__ __forceinline__ int target_of(const CeBatch& b, int64_t i) {
   if (i >= b.rows) return -1;
@@ -126,8 +128,13 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
         b.row[slot] = static_cast<int32_t>(i);
         b.target[slot] = t;
         if (b.grad_loss) {
-          b.lse[slot] = b.lse_in[i];
-          b.grad[slot] = b.grad_loss[i];
+          const float lse = b.lse_in[i], grad = b.grad_loss[i];
+          b.lse[slot] = lse;
+          b.grad[slot] = grad;
+          if (b.ref) {
+            b.ref[slot] = lse < kFloor ? -kInfinity : fmaf(lse, -kLog2e, DT == 1 ? 15.0f : 0.0f);  // every item masked: no probability
+            b.part[slot] = top > 0.0f ? grad / top : 0.0f * grad;
+          }
         }
       } else if (l < kRowsAtOnce && i < b.rows && b.loss) {
         b.loss[i] = 0.0f;
@@ -169,9 +176,17 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
       }
     }
   }
-  if (static_cast<int>(blockIdx.x) + 1 == groups && threadIdx.x == 0) {
-    *b.count = static_cast<int32_t>(before);
-    *b.largest = top;
+  if (static_cast<int>(blockIdx.x) + 1 == groups) {
+    const int more = static_cast<int>(before) + threadIdx.x;
+    if (b.ref && more < (static_cast<int>(before) + 63) / 64 * 64) {
+      b.ref[more] = -kInfinity;
+      b.part[more] = 0.0f;
+      b.target[more] = -1;
+    }
+    if (threadIdx.x == 0) {
+      *b.count = static_cast<int32_t>(before);
+      *b.largest = top;
+    }
   }
 }
 
@@ -266,12 +281,13 @@ __global__ __launch_bounds__(kBlock) void ce_grad_w_kernel(const float* __restri
   }
 }
 
-// A piece's bias gradients: the sums over the tiles of rows (bm rows each), in order.  64 items a workgroup, 16 groups.
-__global__ __launch_bounds__(1024) void ce_grad_bias_kernel(const float* __restrict__ part, int64_t stride, const int32_t* __restrict__ count,
-                                                            int bm, int items, float* __restrict__ gb) {
+// A piece's bias gradients: the sums over its parts, in order.  The parts are tiles of bm rows, or `parts` of them where bm is 0,
+// which then count in the largest |grad_loss| times `factor`.  64 items a workgroup, 16 groups.
+__global__ __launch_bounds__(1024) void ce_grad_bias_kernel(const float* __restrict__ part, int64_t stride, CeBatch b, int bm, int parts,
+                                                            float factor, int items, float* __restrict__ gb) {
   __shared__ float s_sum[16][kWave];
   const int q = threadIdx.x / kWave, l = lane_id();
-  const int v = blockIdx.x * kWave + l, tiles = (*count + bm - 1) / bm;
+  const int v = blockIdx.x * kWave + l, tiles = bm ? (*b.count + bm - 1) / bm : parts;
   float sum = 0.0f;
   if (v < items) {
 #pragma unroll 4
@@ -281,7 +297,7 @@ __global__ __launch_bounds__(1024) void ce_grad_bias_kernel(const float* __restr
   __syncthreads();
   if (q || v >= items) return;
   for (int k = 1; k < 16; ++k) sum += s_sum[k][l];
-  gb[v] = sum;
+  gb[v] = bm ? sum : sum * (factor * *b.largest);
 }
 
 // ---------------------------------------------------------------------------
@@ -313,6 +329,7 @@ struct CeLayout {
   size_t bias_over;                         // narrow rows
   size_t part, picked, all;                 // forward
   size_t xg, z, sum_x, sum_w, bias_part;    // backward
+  size_t ref, part_of;                      // backward, narrow rows
   size_t total;
 };
 void carve_rows(CeLayout& L, Carve& c, int64_t rows, int64_t items, int64_t width) {
@@ -323,7 +340,7 @@ void carve_rows(CeLayout& L, Carve& c, int64_t rows, int64_t items, int64_t widt
   L.count = c.take(4);
   L.largest = c.take(4);
   L.row = c.take(rows * 4);
-  L.target = c.take(rows * 4);
+  L.target = c.take(up(rows, 64) * 4);
   L.xc = c.take(rows * L.pitch * 2);
   L.bias_over = c.take(width <= kNarrowWidth ? up(items, 64) * 4 : 0);
 }
@@ -357,7 +374,10 @@ CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   L.z = c.take((z + 64 * most) * 2);  // panels of whole 64 rows
   L.sum_x = c.take(sum_x_bytes(rows, width));
   L.sum_w = c.take(kSumBytes);
-  L.bias_part = c.take(z / 64 * 4 + 4 * most * 4);  // of 64 rows, of 16 where there are up to 64
+  // z: of 64 rows a part; narrow rows without z: of fused_splits shares of the rows
+  L.bias_part = c.take(hmax(z / 64 * 4 + most * 4, width <= kNarrowWidth ? (items + 131072) * 4 : 0));
+  L.ref = c.take(up(rows, 64) * 4);
+  L.part_of = c.take(up(rows, 64) * 4);
   L.total = c.at;
   return L;
 }
@@ -395,6 +415,12 @@ constexpr TileCost kAlongRegisters[3] = {{256, 256, 512, 256, 6.0, 1.3, 2.05}, {
 int narrow_splits(int64_t rows, int64_t items, bool few) {
   const int64_t row_tiles = few ? 1 : (rows + 255) / 256, tiles = (items + 63) / 64;
   return static_cast<int>(hmax(1, hmin(tiles, hmin(2048 / row_tiles, hmax(tiles / 16, 512 / row_tiles)))));
+}
+
+// Into how many shares the passing side of the fused kernels goes: what stays fills two workgroups a CU, the shares make up for
+// what it does not.  Four tiles a share at least.
+int fused_splits(int64_t stay, int64_t pass, int64_t of, int64_t most) {
+  return static_cast<int>(hmax(1, hmin(hmin(512 / ((stay + of - 1) / of), (pass + 63) / 64 / 4), most)));
 }
 
 bool whole_16(const void* p, int64_t stride, int64_t width) {
@@ -439,7 +465,14 @@ tbe_status launch_rows(const CeBatch& b, int dtype, hipStream_t s) {
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups + more)), dim3(kBlock), 0, s, b, each, groups, counted ? 1 : 0);
   return check_launch("ce_rows");
 }
-CeRows rows_of(const CeBatch& b) { return CeRows{b.count, b.row, b.target, b.lse, b.grad, b.largest}; }
+tbe_status launch_grad_w_sum(const CeArgs& a, bool f16, const float* largest, hipStream_t s) {
+  ProfScope ps("ce_grad_w_sum", s);
+  auto kernel = f16 ? ce_grad_w_kernel<1> : ce_grad_w_kernel<2>;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((a.items + 3) / 4, 8192))), dim3(kBlock), 0, s, a.sum, a.sum_pitch, a.splits,
+                     a.items, a.width, a.factor, largest, static_cast<uint16_t*>(a.out), a.out_stride);
+  return check_launch("ce_grad_w_sum");
+}
+CeRows rows_of(const CeBatch& b) { return CeRows{b.count, b.row, b.target, b.lse, b.grad, b.largest, b.ref, b.part}; }
 
 }  // namespace
 
@@ -506,7 +539,11 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   b.slot = reinterpret_cast<int32_t*>(ws + L.slot);
   b.lse = reinterpret_cast<float*>(ws + L.lse);
   b.grad = reinterpret_cast<float*>(ws + L.grad);
-  b.xg = grad_weight ? reinterpret_cast<uint16_t*>(ws + L.xg) : nullptr;
+  b.xg = grad_weight && !narrow ? reinterpret_cast<uint16_t*>(ws + L.xg) : nullptr;
+  if (narrow) {
+    b.ref = reinterpret_cast<float*>(ws + L.ref);
+    b.part = reinterpret_cast<float*>(ws + L.part_of);
+  }
   tbe_status st = launch_rows(b, dtype, s);
   if (b.bias_over) bias = b.bias_over;
   const bool f16 = dtype == TBE_F16;
@@ -522,25 +559,45 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   const TileCost(&costs)[3] = direct ? kDirectTiles : kAlongRegisters;
   TilePick x_pick = {0, 1};
   if (rows == 0) grad_x = nullptr;  // the gradients of the weights and biases are zeros
-  for (int64_t first = 0; st == TBE_OK && first < items; first += L.piece) {
+  if (narrow && st == TBE_OK) {
+    a.items = static_cast<int>(items);
+    a.w = weight;
+    a.bias = bias;
+    const int64_t stay = width <= 64 ? 256 : 192;  // rows or items of a workgroup
+    if (grad_x) {
+      a.sum = reinterpret_cast<float*>(ws + L.sum_x);
+      x_pick.splits = a.splits = fused_splits(rows, items, stay, sum_x_bytes(rows, width) / (rows * a.sum_pitch * 4));
+      a.bias_part = nullptr;
+      st = f16 ? ce_launch_fused<1>(a, true, s) : ce_launch_fused<2>(a, true, s);
+    }
+    if (st == TBE_OK && (grad_weight || grad_bias)) {
+      a.sum = reinterpret_cast<float*>(ws + L.sum_w);
+      a.splits = fused_splits(items, rows, stay, kSumBytes / (items * a.sum_pitch * 4));
+      a.out = grad_weight; a.out_stride = grad_weight_stride;
+      a.factor = a.scale / (f16 ? kUnit<1> : kUnit<2>);  // x as it was copied
+      a.bias_part = grad_bias ? reinterpret_cast<float*>(ws + L.bias_part) : nullptr;
+      a.bias_stride = items;
+      st = f16 ? ce_launch_fused<1>(a, false, s) : ce_launch_fused<2>(a, false, s);
+      if (st == TBE_OK && grad_weight && a.splits > 1) st = launch_grad_w_sum(a, f16, b.largest, s);
+    }
+    if (st == TBE_OK && grad_bias) {
+      ProfScope ps("ce_grad_bias", s);
+      hipLaunchKernelGGL(ce_grad_bias_kernel, dim3(static_cast<unsigned>((items + kWave - 1) / kWave)), dim3(1024), 0, s, a.bias_part, items, b, 0,
+                         a.splits, 1.0f / (f16 ? kUnit<1> : kUnit<2>), a.items, grad_bias);
+      st = check_launch("ce_grad_bias");
+    }
+  }
+  for (int64_t first = 0; !narrow && st == TBE_OK && first < items; first += L.piece) {
     a.first = static_cast<int>(first);
     a.items = static_cast<int>(hmin(L.piece, items - first));
     a.w = static_cast<const uint16_t*>(weight) + first * weight_stride;
     a.bias = bias ? bias + first : nullptr;
-    const bool few = rows <= 64;
-    int bm = few ? 16 : 64;  // rows that a part of the biases' gradient sums over
-    if (rows > 0 && narrow) {
-      a.splits = narrow_splits(rows, a.items, few);
-      st = f16 ? ce_launch_narrow_z<1>(a, few, s) : ce_launch_narrow_z<2>(a, few, s);
-    } else if (rows > 0) {
-      const int tile = pick_tile(costs, rows, a.items, width, 1, 0).tile;
-      bm = costs[tile].bm;
-      st = f16 ? ce_launch_z<1>(a, tile, direct, s) : ce_launch_z<2>(a, tile, direct, s);
-    }
+    const int tile = pick_tile(costs, rows, a.items, width, 1, 0).tile;
+    if (rows > 0) st = f16 ? ce_launch_z<1>(a, tile, direct, s) : ce_launch_z<2>(a, tile, direct, s);
     if (st == TBE_OK && grad_bias) {
       ProfScope ps("ce_grad_bias", s);
       hipLaunchKernelGGL(ce_grad_bias_kernel, dim3(static_cast<unsigned>((a.items + kWave - 1) / kWave)), dim3(1024), 0, s, a.bias_part,
-                         a.bias_stride, b.count, bm, a.items, grad_bias + first);
+                         a.bias_stride, b, costs[tile].bm, 0, 0.0f, a.items, grad_bias + first);
       st = check_launch("ce_grad_bias");
     }
     if (st == TBE_OK && grad_x) {
@@ -560,13 +617,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
       a.out = static_cast<uint16_t*>(grad_weight) + first * grad_weight_stride;
       a.out_stride = grad_weight_stride;
       st = f16 ? ce_launch_grad_w<1>(a, p.tile, s) : ce_launch_grad_w<2>(a, p.tile, s);
-      if (st == TBE_OK && p.splits > 1) {
-        ProfScope ps("ce_grad_w_sum", s);
-        auto kernel = f16 ? ce_grad_w_kernel<1> : ce_grad_w_kernel<2>;
-        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((a.items + 3) / 4, 8192))), dim3(kBlock), 0, s, a.sum, a.sum_pitch, p.splits, a.items,
-                           a.width, factor, b.largest, static_cast<uint16_t*>(a.out), grad_weight_stride);
-        st = check_launch("ce_grad_w_sum");
-      }
+      if (st == TBE_OK && p.splits > 1) st = launch_grad_w_sum(a, f16, b.largest, s);
     }
   }
   if (st != TBE_OK || !grad_x) return st;

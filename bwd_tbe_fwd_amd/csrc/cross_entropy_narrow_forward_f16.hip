@@ -4,6 +4,6 @@
 namespace tbe {
 template <>
 tbe_status ce_launch_narrow_forward<1>(const CeArgs& a, bool few, hipStream_t s) {
-  return ce_narrow<1, false>(a, few, s);
+  return ce_narrow<1>(a, few, s);
 }
 }  // namespace tbe

@@ -6,8 +6,6 @@
 
 namespace tbe {
 
-constexpr float kLog2e = 1.44269504088896340736f;
-
 // Workgroup blockIdx.x's place among m_tiles x n_tiles: a contiguous share for each chiplet, and in it bands of 8 tiles of m
 // walked along n, so that the 32 workgroups that a chiplet runs at once read 8 + 4 tiles of operands and not 1 + 32.  False:
 // none.
@@ -98,7 +96,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
       const int m = wm + 16 * i + (l & 15);
       const bool in = m < m_left;
       const float lse = in ? a.r.lse[m0 + m] : 0.0f;
-      const float base = lse < -1e38f ? -kInfinity : fmaf(lse, -kLog2e, shift);  // every item masked: no probability
+      const float base = lse < kFloor ? -kInfinity : fmaf(lse, -kLog2e, shift);  // every item masked: no probability
       const unsigned at = in ? static_cast<unsigned>(a.r.target[m0 + m] - a.first - n0 - n) : ~0u;
 #pragma unroll
       for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] = __builtin_amdgcn_exp2f(fmaf(logit(i, c), kLog2e, base));

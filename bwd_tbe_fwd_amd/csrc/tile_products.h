@@ -56,9 +56,11 @@ typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 // lanes 0-3, 12-15 and 20-27, then 4-11, 16-19 and 28-31: of the blocks q = 0 .. 3 of 4 rows that a
 // read takes, 0 and 3 at one column with 1 and 2 at the next.  With these patterns they differ in
 // their place within 256 bytes, all banks (conflict counter: 0).  A read's blocks lie GAP rows apart.
+// GAP = 0: for rows that are also read turned, 4 rows r = q + 4 k of one q < 4 together (cross_entropy_fused.h).
 template <int GAP>
 __device__ __forceinline__ int along_pattern(int r) {
-  return ((r >> 1) & 1) | ((r / GAP) & 3) << 1;
+  if constexpr (GAP == 0) return ((r >> 2) & 3) << 1;
+  else return ((r >> 1) & 1) | ((r / GAP) & 3) << 1;
 }
 // Place of an across row k in LDS, in elements.  A load instruction fills 1024 bytes: rows k = 8 g + 4 h
 // + r of one r together (h = 0, 1, and as many g as fit), 32 bytes before those of the next r: the 4
@@ -75,6 +77,11 @@ __device__ __forceinline__ int across_place(int k) {
 // load under way before each LDS read; it writes no register but m0, and wait_loads is its wait.
 __device__ __forceinline__ void load_to_lds(u32x4 r, uint32_t o, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(o), "s"(r) : "memory", "m0");
+}
+
+// One dword a lane, lane l's at lds + 4 l.
+__device__ __forceinline__ void load_dword_to_lds(u32x4 r, uint32_t o, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(o), "s"(r) : "memory", "m0");
 }
 
 // One operand's tile of SIDE m by kStepK k, THREADS threads.
