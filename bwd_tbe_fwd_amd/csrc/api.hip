@@ -184,6 +184,11 @@ static void sort_geometry(int64_t n, const Config& cfg, int T, bool all_keys, in
 }
 
 void sort_segments(int64_t n, int64_t* seg, int* nblocks) {
+  if (n <= kFewKeys) {
+    *seg = kBlock * kRadixFewItems;
+    *nblocks = static_cast<int>(hmax(1, (n + *seg - 1) / *seg));
+    return;
+  }
   int cls_blocks;
   sort_geometry(n, resolve_config(nullptr), 1, true, seg, nblocks, &cls_blocks);
 }

@@ -13,44 +13,13 @@
 // ids' popularity; a share finds its start by a search of d = i + key_i.  A row that a cut would split within its last 31
 // positions stays with the share before, so most rows are summed and rounded where they are read; of the others each share
 // leaves its sum in the workspace, and the share in which the row ends has them joined, in order.
-#include "items.h"
-
-#include "tower_device.h"
+#include "lookup.h"
 
 namespace tbe {
 namespace {
 
-constexpr int kVec = 8;        // columns of a lane
-constexpr int kFlight = 4;     // forward: rows of a group of lanes whose loads are under way together
-constexpr int kWalk = 8;       // backward: the same
-constexpr int kKeep = 32;      // positions of a row at most, less one, that a share takes over from the next one
+constexpr int kFlight = 4;       // forward: rows of a group of lanes whose loads are under way together
 constexpr int kRankMost = 4096;  // ids that are sorted by counting, in one launch
-
-template <int DT>
-struct RowVec {
-  Vec<typename Fmt<DT>::S, kVec> v;
-  // the columns [0, left) at p
-  __device__ __forceinline__ void load(const typename Fmt<DT>::S* p, int left) { load_vec_part<typename Fmt<DT>::S, kVec>(p, left, v); }
-  __device__ __forceinline__ float at(int e) const { return Fmt<DT>::to_f(v.e[e]); }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) v.e[e] = 0;
-  }
-};
-template <int DT>
-__device__ __forceinline__ void store_row(typename Fmt<DT>::S* p, int left, const float (&x)[kVec], bool stream) {
-  Vec<typename Fmt<DT>::S, kVec> v;
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) v.e[e] = tower_from_f<DT>(x[e]);
-  if (stream && left >= kVec) store_vec_stream<typename Fmt<DT>::S, kVec>(p, v);
-  else store_vec_part<typename Fmt<DT>::S, kVec>(p, left, v);
-}
-
-// A launch's columns: blockIdx.y takes `cols` of them (a multiple of kVec), a group of G lanes a row of these.
-struct Columns {
-  int64_t width;
-  int cols;
-};
 
 // ---------------------------------------------------------------------------
 // forward
@@ -72,7 +41,7 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int id64, int64_t i) {
 }
 
 // A group of G lanes takes kFlight rows, a workgroup consecutive ones.
-template <int WT, int YT, int G>
+template <int WT, int YT, int G, bool WHOLE>
 __global__ __launch_bounds__(kBlock) void lookup_forward_kernel(LookupArgs a) {
   using S = typename Fmt<WT>::S;
   constexpr int kGroups = kBlock / G;
@@ -87,7 +56,7 @@ __global__ __launch_bounds__(kBlock) void lookup_forward_kernel(LookupArgs a) {
       const int64_t i = i0 + u * kGroups;
       id[u] = i < a.n ? id_at(a.ids, a.id64, i) : -1;
     }
-    RowVec<WT> r[kFlight];
+    RowVec<WT, WHOLE> r[kFlight];
 #pragma unroll
     for (int u = 0; u < kFlight; ++u) {
       if (static_cast<uint64_t>(id[u]) < static_cast<uint64_t>(a.items))
@@ -103,7 +72,7 @@ __global__ __launch_bounds__(kBlock) void lookup_forward_kernel(LookupArgs a) {
       float x[kVec];
 #pragma unroll
       for (int e = 0; e < kVec; ++e) x[e] = there ? r[u].at(e) * a.scale : 0.0f;  // 0, whatever the scale
-      store_row<YT>(static_cast<typename Fmt<YT>::S*>(a.y) + i * a.y_stride + c, left, x, a.stream);
+      store_row<YT, WHOLE>(static_cast<typename Fmt<YT>::S*>(a.y) + i * a.y_stride + c, left, x, a.stream);
     }
   }
 }
@@ -164,202 +133,13 @@ __global__ __launch_bounds__(kBlock) void lookup_rank_kernel(const void* ids, in
 }
 
 // ---------------------------------------------------------------------------
-// backward: sums
+// backward: joins
 // ---------------------------------------------------------------------------
-struct LookupGradArgs {
-  int64_t items;
-  const uint32_t* keys;      // sorted
-  const uint32_t* pay;       // their positions
-  const int32_t* n_sorted;
-  const void* gy;
-  int64_t gy_stride;
-  float scale;
-  void* grad;
-  int64_t grad_stride;
-  int32_t add;
-  int32_t stream;            // overwriting, grad's rows start on 16 bytes
-  int32_t share;             // length of a share
-  int32_t shares;
-  float* part;               // [shares][2][width]: the sum of a row that began before the share and ends in it, of one that
-                             // goes on behind it
-  int32_t* begun;            // [shares] of such a first row, the share in which it began; -1: none ends here
-  int32_t* row;              // [shares] and which row it is
-  Columns c;
-};
-
-// Lanes of this lane's group of G whose predicate holds, as bits 0 .. G - 1.
-template <int G>
-__device__ __forceinline__ uint64_t group_ballot(bool p) {
-  const uint64_t b = __ballot(p);
-  if constexpr (G == kWave) return b;
-  else return (b >> (lane_id() / G * G)) & ((uint64_t{1} << G) - 1);
-}
-
-// First i of [lo, hi] with value(i) >= d for i < hi (value does not decrease): a group of lanes probes G places at a time.
-template <int G, typename F>
-__device__ __forceinline__ int64_t first_at_least(int64_t lo, int64_t hi, int64_t d, F value) {
-  const int l = lane_id() % G;
-  while (lo < hi) {
-    const int64_t step = (hi - lo + G) / (G + 1);  // >= 1
-    const int64_t i = lo + (l + 1) * step - 1;     // probes at lo + step - 1, lo + 2 step - 1, ...
-    const bool below = i < hi && value(i) < d;
-    const int n = __popcll(group_ballot<G>(below));  // the first n probes are below
-    const int64_t from = lo + n * step;              // at most hi: probe n - 1 lies before hi
-    if (n < G) hi = min(hi, from + step - 1);
-    lo = from;
-  }
-  return lo;
-}
-
-// A cut of the merged sequence: positions before i and the ends of the rows before row lie before it.
-struct Cut {
-  int64_t i, row;
-  bool split;  // row has positions on both sides
-};
-template <int G>
-__device__ __forceinline__ Cut cut_at(const LookupGradArgs& a, int64_t n, int64_t d) {
-  Cut c;
-  const int64_t all = a.add ? n : n + a.items;
-  if (d >= all) return Cut{n, a.items, false};
-  if (a.add) {
-    c.i = d;
-    c.row = a.keys[d];
-  } else {
-    c.i = first_at_least<G>(max(int64_t{0}, d - a.items), min(n, d), d, [&](int64_t i) { return i + static_cast<int64_t>(a.keys[i]); });
-    c.row = d - c.i;
-  }
-  c.split = false;
-  if (c.i > 0 && a.keys[c.i - 1] == c.row) {
-    // the row has begun: what is left of it, up to kKeep positions
-    int more = 0;
-    const int l = lane_id() % G;
-#pragma unroll
-    for (int k = 0; k < kKeep; k += G) {
-      const int64_t i = c.i + k + l;
-      more += __popcll(group_ballot<G>(k + l < kKeep && i < n && a.keys[i] == c.row));
-    }
-    if (more == kKeep) {
-      c.split = true;
-    } else {
-      c.i += more;
-      c.row += 1;
-    }
-  }
-  return c;
-}
-
-template <int YT, int WT, int G>
-__global__ __launch_bounds__(kBlock) void lookup_sum_kernel(LookupGradArgs a) {
-  using SY = typename Fmt<YT>::S;
-  using SW = typename Fmt<WT>::S;
-  constexpr int kGroups = kBlock / G;
-  const int l = threadIdx.x % G;
-  const int64_t share = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / G;
-  const int64_t n = *a.n_sorted;
-  const int64_t d = share * a.share;
-  // all lanes take part in the searches
-  const Cut from = cut_at<G>(a, n, d), to = cut_at<G>(a, n, share + 1 < a.shares ? d + a.share : n + a.items);
-  if (share >= a.shares) return;
-  if (blockIdx.y == 0) {
-    // a row that began earlier and ends here: the share that has its first position, whose place in the sequence is i + row, or
-    // i (a share whose end was moved behind that place would not have split the row)
-    int32_t begun = -1;
-    if (from.split && !(to.split && to.row == from.row)) {
-      const int64_t i = first_at_least<G>(0, n, from.row, [&](int64_t k) { return static_cast<int64_t>(a.keys[k]); });
-      begun = static_cast<int32_t>((a.add ? i : i + from.row) / a.share);
-    }
-    if (l == 0) {
-      a.begun[share] = begun;
-      a.row[share] = static_cast<int32_t>(from.row);
-    }
-  }
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * a.c.cols + l * kVec;
-  const int left = l * kVec < a.c.cols ? static_cast<int>(min(a.c.width - c, static_cast<int64_t>(kVec))) : 0;
-  if (left <= 0) return;
-  float acc[kVec];
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) acc[e] = 0.0f;
-  bool open = from.split;  // the row began in an earlier share
-  auto keep = [&](int which) {
-    Vec<float, kVec> v;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) v.e[e] = acc[e];
-    store_vec_part<float, kVec>(a.part + (share * 2 + which) * a.c.width + c, left, v);
-  };
-  auto finish = [&](int64_t row) {  // the row's sum is whole, or its last part
-    if (open) {
-      keep(0);
-      open = false;
-    } else {
-      SW* p = static_cast<SW*>(a.grad) + row * a.grad_stride + c;
-      float x[kVec];
-      if (a.add) {
-        RowVec<WT> old;
-        old.load(p, left);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) x[e] = old.at(e) + acc[e] * a.scale;
-      } else {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) x[e] = acc[e] * a.scale;
-      }
-      store_row<WT>(p, left, x, a.stream);
-    }
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) acc[e] = 0.0f;
-  };
-  auto zeros = [&](int64_t row, int64_t end) {
-    const float x[kVec] = {};
-    for (; row < end; ++row) store_row<WT>(static_cast<SW*>(a.grad) + row * a.grad_stride + c, left, x, a.stream);
-  };
-  int64_t row = from.row;      // the row whose end comes next
-  bool begun = from.split;     // it has positions already
-  uint32_t at[kWalk];          // the next positions, loaded ahead of their rows
-#pragma unroll
-  for (int u = 0; u < kWalk; ++u) at[u] = from.i + u < to.i ? a.pay[from.i + u] : 0;
-  for (int64_t i = from.i; i < to.i; i += kWalk) {
-    RowVec<YT> r[kWalk];
-    uint32_t key[kWalk];
-#pragma unroll
-    for (int u = 0; u < kWalk; ++u) {
-      if (i + u < to.i) {
-        r[u].load(static_cast<const SY*>(a.gy) + at[u] * a.gy_stride + c, left);
-        key[u] = a.keys[i + u];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kWalk; ++u) at[u] = i + kWalk + u < to.i ? a.pay[i + kWalk + u] : 0;
-#pragma unroll
-    for (int u = 0; u < kWalk; ++u) {
-      if (i + u < to.i) {
-        const int64_t k = key[u];
-        if (k != row) {
-          if (begun) {
-            finish(row);
-            ++row;
-          }
-          if (!a.add) zeros(row, k);
-          row = k;
-        }
-        begun = true;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) acc[e] += r[u].at(e);
-      }
-    }
-  }
-  if (begun) {
-    if (to.split && to.row == row) {
-      keep(1);
-      return;
-    }
-    finish(row);
-    ++row;
-  }
-  if (!a.add) zeros(row, to.row);
-}
-
-// Joins the sums of the rows that several shares have parts of: a workgroup looks at 64 shares for those in which such a row
-// ends, 256 columns of it.  16 waves add the shares' sums, each wave a contiguous part of them, then the waves' sums are
-// added in order.  (A workgroup for every share took 105 us where few had anything to join.)
+// Joins the sums of the rows that several shares have parts of, 256 columns of a row at a time.  A workgroup looks at 16 shares
+// for those in which such a row ends, a wave each, which adds up to kAlone parts by itself; where there are more all 16 waves
+// add a contiguous part of them each, then the waves' sums are added in order.  (One row after the other by all waves took 55
+// us with 1 M ids, 2 M rows of 128.)
+constexpr int kAlone = 64;
 template <int WT>
 __global__ __launch_bounds__(1024) void lookup_join_kernel(LookupGradArgs a) {
   using SW = typename Fmt<WT>::S;
@@ -368,34 +148,46 @@ __global__ __launch_bounds__(1024) void lookup_join_kernel(LookupGradArgs a) {
   const int w = threadIdx.x / kWave, l = lane_id();
   const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + 4 * l;
   const int left = static_cast<int>(min(max(a.c.width - c, int64_t{0}), int64_t{4}));
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kWave;
-  const int32_t mine = base + l < a.shares ? a.begun[base + l] : -1;
-  for (uint64_t found = __ballot(mine >= 0); found; found &= found - 1) {
-    const int at = __ffsll(static_cast<unsigned long long>(found)) - 1;
-    const int64_t share = base + at, first = read_lane(mine, at);
-    // parts: the shares' from `first` to the one before, then this one's
-    const int64_t parts = share - first + 1, each = (parts + kWaves - 1) / kWaves;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kWaves;
+  const int32_t mine = l < kWaves && base + l < a.shares ? a.begun[base + l] : -1;
+  // parts k of [lo, hi) of a row that ends in `share`: the shares' from `first` to the one before, then this one's
+  auto add = [&](int64_t share, int64_t first, int64_t lo, int64_t hi) {
     f32x4 sum = {0, 0, 0, 0};
     if (left > 0) {
-      const int64_t end = (w + 1) * each < parts ? (w + 1) * each : parts;
 #pragma unroll 8
-      for (int64_t k = w * each; k < end; ++k) {
+      for (int64_t k = lo; k < hi; ++k) {
         Vec<float, 4> v;
-        load_vec_part<float, 4>(a.part + ((first + k) * 2 + (k + 1 < parts ? 1 : 0)) * a.c.width + c, left, v);
+        load_vec_part<float, 4>(a.part + ((first + k) * 2 + (first + k < share ? 1 : 0)) * a.c.width + c, left, v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] += v.e[e];
       }
     }
+    return sum;
+  };
+  auto finish = [&](int64_t share, f32x4 sum) {
+    SW* p = static_cast<SW*>(a.grad) + a.row[share] * a.grad_stride + c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e < left) p[e] = tower_from_f<WT>(a.add ? Fmt<WT>::to_f(p[e]) + sum[e] * a.scale : sum[e] * a.scale);
+    }
+  };
+  const bool alone = base + l - mine + 1 <= kAlone;
+  const uint64_t few = __ballot(mine >= 0 && alone), many = __ballot(mine >= 0 && !alone);
+  if (few >> w & 1) {
+    const int64_t first = read_lane(mine, w);
+    finish(base + w, add(base + w, first, 0, base + w - first + 1));
+  }
+  for (uint64_t found = many; found; found &= found - 1) {
+    const int at = __ffsll(static_cast<unsigned long long>(found)) - 1;
+    const int64_t share = base + at, first = read_lane(mine, at);
+    const int64_t parts = share - first + 1, each = (parts + kWaves - 1) / kWaves;
+    const int64_t lo = w * each < parts ? w * each : parts, hi = lo + each < parts ? lo + each : parts;
+    f32x4 sum = add(share, first, lo, hi);
     *reinterpret_cast<f32x4*>(&s_sum[w][4 * l]) = sum;
     __syncthreads();
     if (w == 0 && left > 0) {
       for (int k = 1; k < kWaves; ++k) sum += *reinterpret_cast<const f32x4*>(&s_sum[k][4 * l]);
-      const int64_t row = a.row[share];
-      SW* p = static_cast<SW*>(a.grad) + row * a.grad_stride + c;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (e < left) p[e] = tower_from_f<WT>(a.add ? Fmt<WT>::to_f(p[e]) + sum[e] * a.scale : sum[e] * a.scale);
-      }
+      finish(share, sum);
     }
     __syncthreads();
   }
@@ -416,20 +208,6 @@ Split split_of(int64_t width) {
   const int64_t vecs = (width + kVec - 1) / kVec;
   s.c = Columns{width, static_cast<int>((vecs + s.parts - 1) / s.parts) * kVec};
   return s;
-}
-
-template <typename F>
-tbe_status by_type(int dt, F f) {
-  if (dt == TBE_F32) return f(std::integral_constant<int, 0>{});
-  if (dt == TBE_F16) return f(std::integral_constant<int, 1>{});
-  return f(std::integral_constant<int, 2>{});
-}
-template <typename F>
-tbe_status by_lanes(int lanes, F f) {
-  if (lanes == 8) return f(std::integral_constant<int, 8>{});
-  if (lanes == 16) return f(std::integral_constant<int, 16>{});
-  if (lanes == 32) return f(std::integral_constant<int, 32>{});
-  return f(std::integral_constant<int, 64>{});
 }
 
 // Length of a share, so that there are about kFewWaves waves (a group of lanes takes a share of a part of the columns), and how
@@ -455,7 +233,7 @@ struct LookupPlan {
 LookupPlan lookup_plan(int64_t n, int64_t items, int64_t width, bool add) {
   LookupPlan p = {};
   sort_segments(n, &p.seg, &p.nblocks);
-  const int64_t all = add ? n : n + items, tiles = (n + kRadixTile - 1) / kRadixTile;
+  const int64_t all = add ? n : n + items, tiles = (n + kBlock * kRadixFewItems - 1) / (kBlock * kRadixFewItems);
   const Split sp = split_of(width);
   const int64_t bound = shares_bound(n + items, sp);
   p.share = static_cast<int>(share_of(all, sp));
@@ -491,12 +269,12 @@ tbe_status launch_lookup_forward(int64_t n, int64_t items, int64_t width, const 
   return by_type(table_dtype, [&](auto wt) {
     return by_type(y_dtype, [&](auto yt) {
       return by_lanes(sp.lanes, [&](auto g) {
-        constexpr int G = decltype(g)::value;
+        constexpr int WT = decltype(wt)::value, YT = decltype(yt)::value, G = decltype(g)::value;
         // a launch has fewer than 2^32 threads
         const int64_t groups = hmin((n + kBlock / G * kFlight - 1) / (kBlock / G * kFlight), int64_t{1} << 23);
+        auto kernel = width % kVec == 0 ? lookup_forward_kernel<WT, YT, G, true> : lookup_forward_kernel<WT, YT, G, false>;
         ProfScope ps("lookup_forward", s);
-        hipLaunchKernelGGL((lookup_forward_kernel<decltype(wt)::value, decltype(yt)::value, G>),
-                           dim3(static_cast<unsigned>(groups), sp.parts), dim3(kBlock), 0, s, a);
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups), sp.parts), dim3(kBlock), 0, s, a);
         return check_launch("lookup_forward");
       });
     });
@@ -545,23 +323,16 @@ tbe_status launch_lookup_backward(int64_t n, int64_t items, int64_t width, const
   a.stream = !add && rows_on_16(grad, grad_stride, table_dtype);
   a.share = p.share; a.shares = static_cast<int32_t>(p.shares); a.part = reinterpret_cast<float*>(ws + p.part); a.c = sp.c;
   a.begun = reinterpret_cast<int32_t*>(ws + p.begun); a.row = reinterpret_cast<int32_t*>(ws + p.row);
-  st = by_type(y_dtype, [&](auto yt) {
-    return by_type(table_dtype, [&](auto wt) {
-      return by_lanes(sp.lanes, [&](auto g) {
-        constexpr int G = decltype(g)::value;
-        ProfScope ps("lookup_sum", s);
-        hipLaunchKernelGGL((lookup_sum_kernel<decltype(yt)::value, decltype(wt)::value, G>),
-                           dim3(static_cast<unsigned>((p.shares + kBlock / G - 1) / (kBlock / G)), sp.parts), dim3(kBlock), 0, s, a);
-        return check_launch("lookup_sum");
-      });
-    });
-  });
+  const dim3 grid(static_cast<unsigned>((p.shares + kBlock / sp.lanes - 1) / (kBlock / sp.lanes)), sp.parts);
+  st = y_dtype == TBE_F32   ? launch_lookup_sum<0>(a, table_dtype, sp.lanes, grid, s)
+       : y_dtype == TBE_F16 ? launch_lookup_sum<1>(a, table_dtype, sp.lanes, grid, s)
+                            : launch_lookup_sum<2>(a, table_dtype, sp.lanes, grid, s);
   // a row has kKeep positions at least on the far side of a cut that splits it
   if (st != TBE_OK || p.shares < 2 || n <= kKeep) return st;
   return by_type(table_dtype, [&](auto wt) {
     ProfScope ps("lookup_join", s);
     hipLaunchKernelGGL((lookup_join_kernel<decltype(wt)::value>),
-                       dim3(static_cast<unsigned>((p.shares + kWave - 1) / kWave), static_cast<unsigned>((width + 4 * kWave - 1) / (4 * kWave))), dim3(1024), 0, s, a);
+                       dim3(static_cast<unsigned>((p.shares + 15) / 16), static_cast<unsigned>((width + 4 * kWave - 1) / (4 * kWave))), dim3(1024), 0, s, a);
     return check_launch("lookup_join");
   });
 }

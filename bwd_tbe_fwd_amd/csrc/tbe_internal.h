@@ -54,6 +54,7 @@ constexpr int kRadixMaxBits = 9;
 constexpr int kRadixDigits = 1 << kRadixMaxBits;
 constexpr int kRadixItems = 16;                       // keys per thread per tile
 constexpr int kRadixTile = kBlock * kRadixItems;      // 4096 keys
+constexpr int kRadixFewItems = 4;                     // of a small sort
 
 struct Config {
   int threshold, chunk, hist_enable, fwd_unroll, bwd_unroll, sort_blocks, bag_windows, fused_long;
@@ -180,12 +181,14 @@ tbe_status launch_transpose(const tbe_tables* tb, const IndexArgs& ia, int weigh
 
 // Stable sort of N pairs (key, payload) by the key's R bits; not by table.  keys[0] and pay[0] hold the input, keys[*final_buf]
 // and pay[*final_buf] (known on the host at once) the result, *n_sorted (device) how many keys differ from `drop`: the others
-// are left out.  nblocks segments of seg keys (a multiple of kRadixTile) cover N, at most 4096; hist: kRadixDigits *
+// are left out.  nblocks segments of seg keys (a multiple of kRadixTile, or one tile of kBlock * kRadixFewItems) cover N, at
+// most 4096; hist: kRadixDigits *
 // (nblocks + 1) words.
 tbe_status launch_radix_sort(int64_t N, int64_t seg, int nblocks, const RadixPlan& R, uint32_t* const (&keys)[2],
                              uint32_t* const (&pay)[2], uint32_t* hist, int32_t* n_sorted, uint32_t drop, int* final_buf,
                              hipStream_t s);
-// Segments of whole tiles for n keys, kMaxSortBlocks at most, and the passes for keys of so many bits.
+// Segments for n keys, kMaxSortBlocks at most: small tiles up to kFewKeys; and the passes for keys of so many bits.
+constexpr int64_t kFewKeys = int64_t{1} << 21;
 constexpr int kMaxSortBlocks = 4096;
 void sort_segments(int64_t n, int64_t* seg, int* nblocks);
 RadixPlan radix_plan(int bits_total);

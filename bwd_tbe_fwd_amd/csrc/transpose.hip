@@ -448,22 +448,24 @@ __global__ __launch_bounds__(kBlock) void radix_scan(uint32_t* __restrict__ hist
 
 // DIG: digits the LDS counters hold (>= 1 << bits).  With at most 128 the kernel takes 36 KB of
 // LDS and is held to 128 registers, so a CU holds 4 workgroups instead of 3 (skewed batch, three
-// 7-bit passes: 1.10 -> 1.05 ms).
-template <bool BY_TABLE, int DIG>
+// 7-bit passes: 1.10 -> 1.05 ms).  ITEMS: keys a thread takes at a time, a tile of kBlock * ITEMS; fewer for sorts whose tiles
+// of 4096 leave CUs idle.
+template <bool BY_TABLE, int DIG, int ITEMS>
 __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(DIG <= 128 ? 4 : 1))) void radix_downsweep(
     const uint32_t* __restrict__ kin, const uint32_t* __restrict__ pin, uint32_t* __restrict__ kout,
     uint32_t* __restrict__ pout, int64_t N, const int32_t* __restrict__ n_eff, int64_t seg,
     int shift, int bits, uint32_t drop, const uint32_t* __restrict__ hist, const uint32_t* __restrict__ tot,
     int nblk, int32_t* __restrict__ n_kept, const int32_t* __restrict__ tstart,
     int32_t* __restrict__ tstart_next, const int64_t* __restrict__ meta, int T) {
+  constexpr int kTile = kBlock * ITEMS;
   // drop: keys equal to it are left out (not ranked, not written); the keys kept, over all
   // blocks, go to *n_kept (block 0), the count every later kernel reads
   __shared__ uint32_t s_base[DIG];
   __shared__ uint32_t s_wcnt[kWavesPerBlock][DIG];
   __shared__ uint32_t s_toff[DIG];
   __shared__ uint32_t s_tcnt[DIG];
-  __shared__ uint32_t s_key[kRadixTile];
-  __shared__ uint32_t s_pay[kRadixTile];
+  __shared__ uint32_t s_key[kTile];
+  __shared__ uint32_t s_pay[kTile];
   __shared__ uint32_t s_tmp[kWavesPerBlock];
   __shared__ uint32_t s_kept;  // keys of the current tile that are kept
   __shared__ int32_t s_rng[5];
@@ -523,12 +525,12 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(DIG <= 1
     hi = min(lo + seg, N);
   }
   __syncthreads();
-  for (int64_t tile = lo; tile < hi; tile += kRadixTile) {
+  for (int64_t tile = lo; tile < hi; tile += kTile) {
     for (int i = lane; i < ndig; i += kWave) s_wcnt[w][i] = 0;
-    uint32_t k[kRadixItems], p[kRadixItems], r[kRadixItems];
-    const int64_t wbase = tile + w * (kRadixItems * kWave);
+    uint32_t k[ITEMS], p[ITEMS], r[ITEMS];
+    const int64_t wbase = tile + w * (ITEMS * kWave);
 #pragma unroll
-    for (int s = 0; s < kRadixItems; ++s) {
+    for (int s = 0; s < ITEMS; ++s) {
       const int64_t i = wbase + s * kWave + lane;
       const bool valid = i < hi;
       k[s] = valid ? kin[i] : 0u;
@@ -543,10 +545,10 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(DIG <= 1
     // place in the group.  r packs the place (bits 0-7) and the lowest lane (bits
     // 8-15).  Two halves of 8 items keep 8 returned bases live instead of 16.
 #pragma unroll
-    for (int h = 0; h < kRadixItems; h += kRadixItems / 2) {
-      uint32_t base[kRadixItems / 2];
+    for (int h = 0; h < ITEMS; h += ITEMS / 2) {
+      uint32_t base[ITEMS / 2];
 #pragma unroll
-      for (int q = 0; q < kRadixItems / 2; ++q) {
+      for (int q = 0; q < ITEMS / 2; ++q) {
         const int s = h + q;
         const bool valid = wbase + s * kWave + lane < hi && k[s] != drop;
         const uint32_t d = ((k[s] - rb) >> shift) & mask;
@@ -557,7 +559,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(DIG <= 1
         r[s] = static_cast<uint32_t>(__popcll(peers & lanemask_lt())) | (static_cast<uint32_t>(lead & 63) << 8);
       }
 #pragma unroll
-      for (int q = 0; q < kRadixItems / 2; ++q) {
+      for (int q = 0; q < ITEMS / 2; ++q) {
         const int s = h + q;
         r[s] = (r[s] & 0xffu) + static_cast<uint32_t>(__shfl(static_cast<int>(base[q]), static_cast<int>(r[s] >> 8)));
       }
@@ -584,7 +586,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(DIG <= 1
     }
     __syncthreads();
 #pragma unroll
-    for (int s = 0; s < kRadixItems; ++s) {
+    for (int s = 0; s < ITEMS; ++s) {
       if (wbase + s * kWave + lane < hi && k[s] != drop) {
         const uint32_t d = ((k[s] - rb) >> shift) & mask;
         const uint32_t pos = s_toff[d] + s_wcnt[w][d] + r[s];
@@ -996,16 +998,19 @@ tbe_status radix_passes(int64_t N, int64_t seg, int nblocks, const RadixPlan& R,
     if ((st = check_launch("radix_scan"))) return st;
     {
       ProfScope ps(nm.down, s);
-#define TBE_DOWN(BT, DG)                                                                             \
-  hipLaunchKernelGGL((radix_downsweep<BT, DG>), dim3(nblocks), dim3(kBlock), 0, s, keys[cur], pay[cur], \
+#define TBE_DOWN(BT, DG, IT)                                                                             \
+  hipLaunchKernelGGL((radix_downsweep<BT, DG, IT>), dim3(nblocks), dim3(kBlock), 0, s, keys[cur], pay[cur], \
                      keys[cur ^ 1], pay[cur ^ 1], N, n_p, seg, R.shift[pass], R.bits[pass], d, hist, tot, \
                      nblocks, pass == 0 ? n_sorted : nullptr, ts_in, ts_out, meta, T)
       if (R.by_table) {
-        if (ndig <= 128) TBE_DOWN(true, 128);
-        else TBE_DOWN(true, kRadixDigits);
+        if (ndig <= 128) TBE_DOWN(true, 128, kRadixItems);
+        else TBE_DOWN(true, kRadixDigits, kRadixItems);
+      } else if (seg % kRadixTile) {
+        if (ndig <= 128) TBE_DOWN(false, 128, kRadixFewItems);
+        else TBE_DOWN(false, kRadixDigits, kRadixFewItems);
       } else {
-        if (ndig <= 128) TBE_DOWN(false, 128);
-        else TBE_DOWN(false, kRadixDigits);
+        if (ndig <= 128) TBE_DOWN(false, 128, kRadixItems);
+        else TBE_DOWN(false, kRadixDigits, kRadixItems);
       }
 #undef TBE_DOWN
     }
