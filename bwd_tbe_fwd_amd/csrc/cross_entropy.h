@@ -2,7 +2,7 @@
 // are in include/tbe_items.h.
 //
 // The rows that have a target are copied side by side first (their count stays on the device): a batch's padding costs no
-// products, and every row starts on 16 bytes.  Then, C(m, n) = sum_k A(m, k) B(n, k) as in tile_products.h:
+// products, and every row starts on 16 bytes.  Weights whose rows do not are copied too, a piece at a time.  Then, C(m, n) = sum_k A(m, k) B(n, k) as in tile_products.h:
 //   logits            m = row,  n = item,   k = column: A = x, B = weight, both along
 //   gradient of x     m = row,  n = column, k = item:   A = z along, B = weight across
 //   of the weights    m = item, n = column, k = row:    A = z across, B = x * grad_loss across
@@ -28,7 +28,8 @@ struct CeRows {
 
 struct CeArgs {
   int64_t rows;            // of the caller's batch: at least as many as have a target
-  int32_t width;
+  int32_t width;           // of x and w as they are read: whole 16 bytes, zeros behind out_width (not for kTile64 through registers)
+  int32_t out_width;       // the caller's
   const void* x;           // [count][x_stride], 16 bits
   int64_t x_stride;
   const void* w;           // the piece's first item
@@ -71,10 +72,10 @@ enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile256x128 = 3 };  // the last
 
 // Defined in translation units of their own (cross_entropy_forward_f16.hip and its siblings).
 template <int DT> tbe_status ce_launch_forward(const CeArgs& a, int tile, bool direct, hipStream_t s);
-template <int DT> tbe_status ce_launch_z(const CeArgs& a, int tile, bool direct, hipStream_t s);
+template <int DT> tbe_status ce_launch_z(const CeArgs& a, int tile, hipStream_t s);
 template <int DT> tbe_status ce_launch_narrow_forward(const CeArgs& a, bool few, hipStream_t s);
 template <int DT> tbe_status ce_launch_fused(const CeArgs& a, bool x, hipStream_t s);
-template <int DT> tbe_status ce_launch_grad_x(const CeArgs& a, int tile, bool direct, hipStream_t s);
+template <int DT> tbe_status ce_launch_grad_x(const CeArgs& a, int tile, hipStream_t s);
 template <int DT> tbe_status ce_launch_grad_w(const CeArgs& a, int tile, hipStream_t s);
 
 }  // namespace tbe

@@ -190,6 +190,21 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
   }
 }
 
+// Weights whose rows do not start on 16 bytes, or are not whole 16 bytes: `items` rows of them at a pitch that is, zeros behind
+// the width.  A wave a row.
+__global__ __launch_bounds__(kBlock) void ce_pad_kernel(const uint16_t* __restrict__ w, int64_t stride, int items, int width, int pitch,
+                                                        uint16_t* __restrict__ out) {
+  const int l = lane_id();
+  for (int64_t v = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6); v < items;
+       v += static_cast<int64_t>(gridDim.x) * kWavesPerBlock) {
+    for (int d = l * 8; d < pitch; d += kWave * 8) {
+      Vec<uint16_t, 8> x;
+      load_vec_part<uint16_t, 8>(w + v * stride + d, width - d, x);
+      store_vec_any<uint16_t, 8>(out + v * pitch + d, x);
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // joins
 // ---------------------------------------------------------------------------
@@ -307,11 +322,14 @@ __global__ __launch_bounds__(1024) void ce_grad_bias_kernel(const float* __restr
 constexpr int64_t kPartBytes = int64_t{64} << 20;    // forward: of the rows' maxima and sums over a piece's tiles
 constexpr int64_t kZElems = int64_t{1} << 27;        // backward: of z
 constexpr int64_t kLeastPiece = 1024, kMostPiece = 131072;  // items of a piece, backward
+constexpr int64_t kCopyBytes = int64_t{32} << 20;    // of a piece's weights, copied: read again from the caches
 constexpr int64_t kSumBytes = int64_t{128} << 20;    // of the sums over shares of k, beyond one share of x's gradient
 constexpr int kMostSplits = 64;
 
 // Rows of up to so many columns stay in registers (cross_entropy_narrow.h).
 constexpr int64_t kNarrowWidth = 128;
+
+constexpr int64_t kFusedGroups = 512;  // two workgroups a CU
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
@@ -324,8 +342,8 @@ struct Carve {
   }
 };
 struct CeLayout {
-  int64_t pitch, piece;
-  size_t counts, tops, count, largest, row, target, slot, lse, grad, xc;
+  int64_t pitch, piece, copied;  // items of a piece, and of a piece whose weights are copied
+  size_t counts, tops, count, largest, row, target, slot, lse, grad, xc, wc;
   size_t bias_over;                         // narrow rows
   size_t part, picked, all;                 // forward
   size_t xg, z, sum_x, sum_w, bias_part;    // backward
@@ -343,6 +361,9 @@ void carve_rows(CeLayout& L, Carve& c, int64_t rows, int64_t items, int64_t widt
   L.target = c.take(up(rows, 64) * 4);
   L.xc = c.take(rows * L.pitch * 2);
   L.bias_over = c.take(width <= kNarrowWidth ? up(items, 64) * 4 : 0);
+  // whether it is asked for depends on addresses and strides
+  L.copied = hmin(up(items, 256), hmax(kLeastPiece, kCopyBytes / (2 * L.pitch) / 256 * 256));
+  L.wc = c.take(L.copied * L.pitch * 2);
 }
 CeLayout forward_layout(int64_t rows, int64_t items, int64_t width) {
   CeLayout L = {};
@@ -371,11 +392,12 @@ CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   const int64_t all = up(items, 256), most = hmin(all, kMostPiece);
   L.piece = hmin(most, hmax(kLeastPiece, kZElems / hmax(rows, 1) / 256 * 256));
   const int64_t z = hmin(rows * most, hmax(kZElems, rows * kLeastPiece));
-  L.z = c.take((z + 64 * most) * 2);  // panels of whole 64 rows
+  const bool narrow = width <= kNarrowWidth;
+  L.z = c.take(narrow ? 0 : (z + 64 * most) * 2);  // panels of whole 64 rows
   L.sum_x = c.take(sum_x_bytes(rows, width));
   L.sum_w = c.take(kSumBytes);
-  // z: of 64 rows a part; narrow rows without z: of fused_splits shares of the rows
-  L.bias_part = c.take(hmax(z / 64 * 4 + most * 4, width <= kNarrowWidth ? (items + 131072) * 4 : 0));
+  // of 64 rows a part; of narrow rows fused_splits of them
+  L.bias_part = c.take(narrow ? (items + kFusedGroups * 256) * 4 : z / 64 * 4 + most * 4);
   L.ref = c.take(up(rows, 64) * 4);
   L.part_of = c.take(up(rows, 64) * 4);
   L.total = c.at;
@@ -386,8 +408,12 @@ CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
 struct TilePick {
   int tile, splits;
 };
+// What sharing costs: the weights' sums are written, read and added by another kernel, the rows' are there anyway, once.
+double weight_shares_us(int split, double bytes) { return 4.0 + 2.0 * split * bytes / 4e6; }
+double x_shares_us(int split, double bytes) { return 2.0 * (split - 1) * bytes / 6e6; }
 template <int N>
-TilePick pick_tile(const TileCost (&costs)[N], int64_t m, int64_t n, int64_t k, int most_splits, int64_t most_bytes) {
+TilePick pick_tile(const TileCost (&costs)[N], int64_t m, int64_t n, int64_t k, int most_splits, int64_t most_bytes,
+                   double (*shares_us)(int, double)) {
   TilePick best = {0, 1};
   double least = -1.0;
   for (int t = 0; t < N; ++t) {
@@ -396,7 +422,7 @@ TilePick pick_tile(const TileCost (&costs)[N], int64_t m, int64_t n, int64_t k, 
     for (int split = 1; split <= most_splits; split *= 2) {
       if (split > 1 && (k / split < 256 || split * m * n * 4 > most_bytes)) break;
       const double kk = static_cast<double>(up((k + split - 1) / split, 64));
-      const double us = tiles_us(c, tiles * split, kk, kk) + (split > 1 ? 4.0 + 2.0 * split * static_cast<double>(m * n) * 4 / 4e6 : 0.0);
+      const double us = tiles_us(c, tiles * split, kk, kk) + (split > 1 ? shares_us(split, static_cast<double>(m * n) * 4) : 0.0);
       if (least < 0.0 || us < least) {
         least = us;
         best = TilePick{t, split};
@@ -405,10 +431,8 @@ TilePick pick_tile(const TileCost (&costs)[N], int64_t m, int64_t n, int64_t k, 
   }
   return best;
 }
-// Costs of the kernels here: grouped_linear.h's, with square tiles through registers as well.
+// The gradient of x: a tile more.  Its shares' sums go on from piece to piece, whether there is one share or several.
 constexpr TileCost kGradX[4] = {kDirectTiles[0], kDirectTiles[1], kDirectTiles[2], {256, 128, 512, 256, 5.0, 0.8, 0.8}};
-constexpr TileCost kGradXRegisters[4] = {kRegisterTiles[0], {128, 128, 256, 512, 5.0, 0.8, 1.5}, kRegisterTiles[2], kRegisterTiles[1]};
-constexpr TileCost kAlongRegisters[3] = {{256, 256, 512, 256, 6.0, 1.3, 2.05}, {128, 128, 256, 512, 5.0, 0.8, 1.5}, {64, 64, 256, 1024, 3.0, 0.55, 1.35}};
 
 // Into how many ranges their items go: about 2048 workgroups, of 16 tiles of 64 items at least, of fewer where that leaves
 // CUs idle.
@@ -420,7 +444,7 @@ int narrow_splits(int64_t rows, int64_t items, bool few) {
 // Into how many shares the passing side of the fused kernels goes: what stays fills two workgroups a CU, the shares make up for
 // what it does not.  Four tiles a share at least.
 int fused_splits(int64_t stay, int64_t pass, int64_t of, int64_t most) {
-  return static_cast<int>(hmax(1, hmin(hmin(512 / ((stay + of - 1) / of), (pass + 63) / 64 / 4), most)));
+  return static_cast<int>(hmax(1, hmin(hmin(kFusedGroups / ((stay + of - 1) / of), (pass + 63) / 64 / 4), most)));
 }
 
 bool whole_16(const void* p, int64_t stride, int64_t width) {
@@ -469,8 +493,15 @@ tbe_status launch_grad_w_sum(const CeArgs& a, bool f16, const float* largest, hi
   ProfScope ps("ce_grad_w_sum", s);
   auto kernel = f16 ? ce_grad_w_kernel<1> : ce_grad_w_kernel<2>;
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((a.items + 3) / 4, 8192))), dim3(kBlock), 0, s, a.sum, a.sum_pitch, a.splits,
-                     a.items, a.width, a.factor, largest, static_cast<uint16_t*>(a.out), a.out_stride);
+                     a.items, a.out_width, a.factor, largest, static_cast<uint16_t*>(a.out), a.out_stride);
   return check_launch("ce_grad_w_sum");
+}
+// A piece's weights into the workspace.
+tbe_status launch_pad(const CeArgs& a, const void* w, int64_t stride, void* out, hipStream_t s) {
+  ProfScope ps("ce_pad", s);
+  hipLaunchKernelGGL(ce_pad_kernel, dim3(static_cast<unsigned>(hmin((a.items + 3) / 4, 16384))), dim3(kBlock), 0, s,
+                     static_cast<const uint16_t*>(w), stride, a.items, a.out_width, a.width, static_cast<uint16_t*>(out));
+  return check_launch("ce_pad");
 }
 CeRows rows_of(const CeBatch& b) { return CeRows{b.count, b.row, b.target, b.lse, b.grad, b.largest, b.ref, b.part}; }
 
@@ -484,7 +515,8 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
                                         float scale, float* loss, float* lse, void* workspace, hipStream_t s) {
   const CeLayout L = forward_layout(rows, items, width);
   char* ws = static_cast<char*>(workspace);
-  const bool direct = whole_16(weight, weight_stride, width), narrow = direct && width <= kNarrowWidth;
+  const bool narrow = width <= kNarrowWidth, few = rows <= 64, f16 = dtype == TBE_F16;
+  const bool on_16 = whole_16(weight, weight_stride, width), copy = !on_16 && (narrow || !few), direct = on_16 || copy;
   CeBatch b = batch_of(ws, L, rows, items, width, x, x_stride, targets, target_type, bias, narrow, scale);
   b.w = static_cast<const uint16_t*>(weight); b.w_stride = weight_stride;
   b.picked = reinterpret_cast<float*>(ws + L.picked);
@@ -493,26 +525,31 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
   tbe_status st = launch_rows(b, dtype, s);
   if (b.bias_over) bias = b.bias_over;
   CeArgs a = {};
-  a.rows = rows; a.width = static_cast<int>(width);
+  a.rows = rows; a.width = static_cast<int>(direct ? L.pitch : width); a.out_width = static_cast<int>(width);
   a.x = ws + L.xc; a.x_stride = L.pitch;
-  a.w_stride = weight_stride; a.scale = scale; a.r = rows_of(b);
+  a.scale = scale; a.r = rows_of(b);
   a.part = reinterpret_cast<float2*>(ws + L.part);
-  const int64_t piece = narrow ? items : L.piece;
+  const int64_t piece = hmin(narrow ? items : L.piece, copy ? L.copied : items);
   for (int64_t first = 0; st == TBE_OK && first < items; first += piece) {
     a.first = static_cast<int>(first);
     a.items = static_cast<int>(hmin(piece, items - first));
     a.w = static_cast<const uint16_t*>(weight) + first * weight_stride;
+    a.w_stride = weight_stride;
     a.bias = bias ? bias + first : nullptr;
+    if (copy) {
+      st = launch_pad(a, a.w, weight_stride, ws + L.wc, s);
+      a.w = ws + L.wc;
+      a.w_stride = L.pitch;
+    }
+    if (st != TBE_OK) break;
     int parts;  // of a row
     if (narrow) {
-      const bool few = rows <= 64;
       parts = a.splits = narrow_splits(rows, a.items, few);
-      st = dtype == TBE_F16 ? ce_launch_narrow_forward<1>(a, few, s) : ce_launch_narrow_forward<2>(a, few, s);
+      st = f16 ? ce_launch_narrow_forward<1>(a, few, s) : ce_launch_narrow_forward<2>(a, few, s);
     } else {
-      const TileCost(&costs)[3] = direct ? kDirectTiles : kAlongRegisters;
-      const int tile = pick_tile(costs, rows, a.items, width, 1, 0).tile;
-      parts = (a.items + costs[tile].bn - 1) / costs[tile].bn;
-      st = dtype == TBE_F16 ? ce_launch_forward<1>(a, tile, direct, s) : ce_launch_forward<2>(a, tile, direct, s);
+      const int tile = direct ? pick_tile(kDirectTiles, rows, a.items, width, 1, 0, weight_shares_us).tile : kTile64;
+      parts = (a.items + kDirectTiles[tile].bn - 1) / kDirectTiles[tile].bn;
+      st = f16 ? ce_launch_forward<1>(a, tile, direct, s) : ce_launch_forward<2>(a, tile, direct, s);
     }
     if (st != TBE_OK) break;
     ProfScope ps("ce_join", s);
@@ -531,8 +568,8 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
                                          void* grad_weight, int64_t grad_weight_stride, float* grad_bias, void* workspace, hipStream_t s) {
   const CeLayout L = backward_layout(rows, items, width);
   char* ws = static_cast<char*>(workspace);
-  const bool direct = whole_16(weight, weight_stride, width), narrow = direct && width <= kNarrowWidth;
-  const float factor = scale / (dtype == TBE_F16 ? kUnit<1> : kUnit<2>);  // of a product of z
+  const bool narrow = width <= kNarrowWidth, f16 = dtype == TBE_F16, copy = !whole_16(weight, weight_stride, width);
+  const float unit = f16 ? kUnit<1> : kUnit<2>, x_factor = scale / unit;
   CeBatch b = batch_of(ws, L, rows, items, width, x, x_stride, targets, target_type, bias, narrow, scale);
   b.grad_loss = grad_loss;
   b.lse_in = lse;
@@ -546,86 +583,76 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   }
   tbe_status st = launch_rows(b, dtype, s);
   if (b.bias_over) bias = b.bias_over;
-  const bool f16 = dtype == TBE_F16;
   CeArgs a = {};
-  a.rows = rows; a.width = static_cast<int>(width);
+  a.rows = rows; a.width = static_cast<int>(L.pitch); a.out_width = static_cast<int>(width);
   a.x = ws + L.xc; a.x_stride = L.pitch; a.xg = ws + L.xg;
-  a.w_stride = weight_stride; a.scale = scale; a.r = rows_of(b);
+  a.scale = scale; a.r = rows_of(b);
   a.z = reinterpret_cast<uint16_t*>(ws + L.z); a.panel = up(rows, 64) * 64;
-  a.factor = factor;
+  a.factor = scale / unit;  // of x as it was copied
   a.sum_pitch = up(width, 4);
-  a.bias_part = grad_bias ? reinterpret_cast<float*>(ws + L.bias_part) : nullptr;
-  a.bias_stride = L.piece;
-  const TileCost(&costs)[3] = direct ? kDirectTiles : kAlongRegisters;
-  TilePick x_pick = {0, 1};
+  float* const bias_part = reinterpret_cast<float*>(ws + L.bias_part);
   if (rows == 0) grad_x = nullptr;  // the gradients of the weights and biases are zeros
-  if (narrow && st == TBE_OK) {
-    a.items = static_cast<int>(items);
-    a.w = weight;
-    a.bias = bias;
-    const int64_t stay = width <= 64 ? 256 : 192;  // rows or items of a workgroup
-    if (grad_x) {
-      a.sum = reinterpret_cast<float*>(ws + L.sum_x);
-      x_pick.splits = a.splits = fused_splits(rows, items, stay, sum_x_bytes(rows, width) / (rows * a.sum_pitch * 4));
-      a.bias_part = nullptr;
-      st = f16 ? ce_launch_fused<1>(a, true, s) : ce_launch_fused<2>(a, true, s);
-    }
-    if (st == TBE_OK && (grad_weight || grad_bias)) {
-      a.sum = reinterpret_cast<float*>(ws + L.sum_w);
-      a.splits = fused_splits(items, rows, stay, kSumBytes / (items * a.sum_pitch * 4));
-      a.out = grad_weight; a.out_stride = grad_weight_stride;
-      a.factor = a.scale / (f16 ? kUnit<1> : kUnit<2>);  // x as it was copied
-      a.bias_part = grad_bias ? reinterpret_cast<float*>(ws + L.bias_part) : nullptr;
-      a.bias_stride = items;
-      st = f16 ? ce_launch_fused<1>(a, false, s) : ce_launch_fused<2>(a, false, s);
-      if (st == TBE_OK && grad_weight && a.splits > 1) st = launch_grad_w_sum(a, f16, b.largest, s);
-    }
-    if (st == TBE_OK && grad_bias) {
-      ProfScope ps("ce_grad_bias", s);
-      hipLaunchKernelGGL(ce_grad_bias_kernel, dim3(static_cast<unsigned>((items + kWave - 1) / kWave)), dim3(1024), 0, s, a.bias_part, items, b, 0,
-                         a.splits, 1.0f / (f16 ? kUnit<1> : kUnit<2>), a.items, grad_bias);
-      st = check_launch("ce_grad_bias");
-    }
-  }
-  for (int64_t first = 0; !narrow && st == TBE_OK && first < items; first += L.piece) {
+  const int64_t piece = hmin(narrow ? items : L.piece, copy ? L.copied : items);
+  const int64_t stay = width <= 64 ? 256 : 192;  // narrow: rows or items of a workgroup
+  a.bias_stride = hmin(piece, items);
+  TilePick x_pick = {0, 1};
+  for (int64_t first = 0; st == TBE_OK && first < items; first += piece) {
     a.first = static_cast<int>(first);
-    a.items = static_cast<int>(hmin(L.piece, items - first));
+    a.items = static_cast<int>(hmin(piece, items - first));
     a.w = static_cast<const uint16_t*>(weight) + first * weight_stride;
+    a.w_stride = weight_stride;
     a.bias = bias ? bias + first : nullptr;
-    const int tile = pick_tile(costs, rows, a.items, width, 1, 0).tile;
-    if (rows > 0) st = f16 ? ce_launch_z<1>(a, tile, direct, s) : ce_launch_z<2>(a, tile, direct, s);
-    if (st == TBE_OK && grad_bias) {
-      ProfScope ps("ce_grad_bias", s);
-      hipLaunchKernelGGL(ce_grad_bias_kernel, dim3(static_cast<unsigned>((a.items + kWave - 1) / kWave)), dim3(1024), 0, s, a.bias_part,
-                         a.bias_stride, b, costs[tile].bm, 0, 0.0f, a.items, grad_bias + first);
-      st = check_launch("ce_grad_bias");
+    if (copy) {
+      st = launch_pad(a, a.w, weight_stride, ws + L.wc, s);
+      a.w = ws + L.wc;
+      a.w_stride = L.pitch;
+    }
+    // z, and the parts of the biases' gradient: of each tile of rows, or (bias_rows = 0) as many as there are shares of them
+    a.bias_part = grad_bias && !narrow ? bias_part : nullptr;
+    int bias_rows = 0;
+    if (st == TBE_OK && !narrow && rows > 0) {
+      const int tile = pick_tile(kDirectTiles, rows, a.items, width, 1, 0, weight_shares_us).tile;
+      bias_rows = kDirectTiles[tile].bm;
+      st = f16 ? ce_launch_z<1>(a, tile, s) : ce_launch_z<2>(a, tile, s);
     }
     if (st == TBE_OK && grad_x) {
       // the same shares for every piece: their sums go on
-      if (first == 0 && direct) x_pick = pick_tile(kGradX, rows, a.sum_pitch, a.items, kMostSplits, sum_x_bytes(rows, width));
-      else if (first == 0) x_pick = pick_tile(kGradXRegisters, rows, a.sum_pitch, a.items, kMostSplits, sum_x_bytes(rows, width));
+      if (first == 0 && narrow) x_pick.splits = fused_splits(rows, a.items, stay, sum_x_bytes(rows, width) / (rows * a.sum_pitch * 4));
+      else if (first == 0) x_pick = pick_tile(kGradX, rows, a.sum_pitch, a.items, kMostSplits, sum_x_bytes(rows, width), x_shares_us);
       a.sum = reinterpret_cast<float*>(ws + L.sum_x);
       a.splits = x_pick.splits;
       a.add = first > 0;
-      st = f16 ? ce_launch_grad_x<1>(a, x_pick.tile, direct, s) : ce_launch_grad_x<2>(a, x_pick.tile, direct, s);
+      if (narrow) st = f16 ? ce_launch_fused<1>(a, true, s) : ce_launch_fused<2>(a, true, s);
+      else st = f16 ? ce_launch_grad_x<1>(a, x_pick.tile, s) : ce_launch_grad_x<2>(a, x_pick.tile, s);
     }
-    if (st == TBE_OK && grad_weight) {
-      const TilePick p = pick_tile(kWeightTiles, a.items, a.sum_pitch, rows, kMostSplits, kSumBytes);
-      a.sum = reinterpret_cast<float*>(ws + L.sum_w);
+    a.sum = reinterpret_cast<float*>(ws + L.sum_w);
+    a.add = 0;
+    a.out = grad_weight ? static_cast<uint16_t*>(grad_weight) + first * grad_weight_stride : nullptr;
+    a.out_stride = grad_weight_stride;
+    a.splits = 1;
+    if (st == TBE_OK && narrow && (grad_weight || grad_bias)) {
+      a.splits = fused_splits(a.items, rows, stay, kSumBytes / (a.items * a.sum_pitch * 4));
+      a.bias_part = grad_bias ? bias_part : nullptr;
+      st = f16 ? ce_launch_fused<1>(a, false, s) : ce_launch_fused<2>(a, false, s);
+    } else if (st == TBE_OK && grad_weight) {
+      const TilePick p = pick_tile(kWeightTiles, a.items, a.sum_pitch, rows, kMostSplits, kSumBytes, weight_shares_us);
       a.splits = p.splits;
-      a.add = 0;
-      a.out = static_cast<uint16_t*>(grad_weight) + first * grad_weight_stride;
-      a.out_stride = grad_weight_stride;
       st = f16 ? ce_launch_grad_w<1>(a, p.tile, s) : ce_launch_grad_w<2>(a, p.tile, s);
-      if (st == TBE_OK && p.splits > 1) st = launch_grad_w_sum(a, f16, b.largest, s);
+    }
+    if (st == TBE_OK && grad_weight && a.splits > 1) st = launch_grad_w_sum(a, f16, b.largest, s);
+    if (st == TBE_OK && grad_bias) {
+      ProfScope ps("ce_grad_bias", s);
+      hipLaunchKernelGGL(ce_grad_bias_kernel, dim3(static_cast<unsigned>((a.items + kWave - 1) / kWave)), dim3(1024), 0, s, bias_part,
+                         a.bias_stride, b, bias_rows, narrow ? a.splits : 0, 1.0f / unit, a.items, grad_bias + first);
+      st = check_launch("ce_grad_bias");
     }
   }
   if (st != TBE_OK || !grad_x) return st;
   ProfScope ps("ce_grad_x_sum", s);
   auto kernel = f16 ? ce_grad_x_kernel<1> : ce_grad_x_kernel<2>;
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((rows + 3) / 4, 8192))), dim3(kBlock), 0, s, b,
-                     reinterpret_cast<const float*>(ws + L.sum_x), a.sum_pitch, x_pick.splits, static_cast<int>(width),
-                     factor, static_cast<uint16_t*>(grad_x), grad_x_stride);
+                     reinterpret_cast<const float*>(ws + L.sum_x), a.sum_pitch, x_pick.splits, static_cast<int>(width), x_factor,
+                     static_cast<uint16_t*>(grad_x), grad_x_stride);
   return check_launch("ce_grad_x_sum");
 }
 

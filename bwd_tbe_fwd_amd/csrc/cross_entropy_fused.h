@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256, 2) void ce_fused_kernel(CeArgs a) {
     sum[i] = 0.0f;
     if constexpr (X) {
       ref[i] = in ? a.r.ref[s] : -kInfinity;
-      target[i] = in ? a.r.target[s] : -1;
+      target[i] = in ? a.r.target[s] - a.first : -1;
     } else {
       const float b = in ? a.bias[s] : -kInfinity;
       from[i] = f32x4{b, b, b, b};
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(256, 2) void ce_fused_kernel(CeArgs a) {
     uint64_t hits = 0;  // not X: rows whose target is one of this wave's items
     int hit = 0;
     if constexpr (!X) {
-      hit = static_cast<int>(s_more[slot][2][l]) - s0;
+      hit = static_cast<int>(s_more[slot][2][l]) - a.first - s0;
       hits = __ballot(static_cast<unsigned>(hit) < 16u * MF);
     }
 #pragma unroll
@@ -211,14 +211,16 @@ __global__ __launch_bounds__(256, 2) void ce_fused_kernel(CeArgs a) {
 #pragma unroll
       for (int c = 0; c < CG; ++c) {
         const int n = 16 * c + 4 * g;
-        if (n >= a.width) continue;
+        if (n >= a.out_width) continue;
         if (whole) {
           Vec<uint16_t, 4> v;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v.e[e] = tower_from_f<DT>(out[i][c][e] * factor);
-          store_vec_part<uint16_t, 4>(static_cast<uint16_t*>(a.out) + s * a.out_stride + n, a.width - n, v);
+          store_vec_part<uint16_t, 4>(static_cast<uint16_t*>(a.out) + s * a.out_stride + n, a.out_width - n, v);
         } else {
-          store_f4(a.sum + (static_cast<int64_t>(split) * (X ? a.rows : a.items) + s) * a.sum_pitch + n, out[i][c]);
+          float* p = a.sum + (static_cast<int64_t>(split) * (X ? a.rows : a.items) + s) * a.sum_pitch + n;
+          if (X && a.add) out[i][c] += load_f4(p);
+          store_f4(p, out[i][c]);
         }
       }
     }

@@ -4,6 +4,6 @@
 namespace tbe {
 template <>
 tbe_status ce_launch_grad_w<2>(const CeArgs& a, int tile, hipStream_t s) {
-  return ce_grad<2, false, true>(a, tile, s);
+  return ce_grad<2, false>(a, tile, s);
 }
 }  // namespace tbe

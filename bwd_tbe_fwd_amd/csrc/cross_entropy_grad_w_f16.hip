@@ -4,6 +4,6 @@
 namespace tbe {
 template <>
 tbe_status ce_launch_grad_w<1>(const CeArgs& a, int tile, hipStream_t s) {
-  return ce_grad<1, false, true>(a, tile, s);
+  return ce_grad<1, false>(a, tile, s);
 }
 }  // namespace tbe

@@ -141,21 +141,21 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
 }
 
 // The two products of z.  X: the gradient of x, else of the weights.  blockIdx.y: the part of k.
-template <int DT, bool X, int BM, int BN, int WM, int WN, bool DIRECT>
+template <int DT, bool X, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void ce_grad_kernel(CeArgs a) {
   constexpr int T = WM * WN * kWave;
   constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
-  using OA = PanelOperand<X, BM, 4, T, DIRECT>;
-  using OB = Operand<false, BN, 4 * NF, T, DIRECT>;
+  using OA = PanelOperand<X, BM, 4, T, true>;
+  using OB = Operand<false, BN, 4 * NF, T, true>;
   constexpr int kBytes = 2 * 2 * (OA::kElems + OB::kElems);
   __shared__ __align__(16) char lds[kBytes];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
   const int wm = (w / WN) * (MF * 16), wn = (w % WN) * (NF * 16);
   const int count = *a.r.count, ms = X ? count : a.items, ks = X ? a.items : count;
   TilePlace t;
-  if (!tile_place((ms + BM - 1) / BM, (a.width + BN - 1) / BN, t)) return;
+  if (!tile_place((ms + BM - 1) / BM, (a.out_width + BN - 1) / BN, t)) return;
   const int m0 = t.m * BM, n0 = t.n * BN;
-  const int m_left = ms - m0, n_left = a.width - n0;
+  const int m_left = ms - m0, n_left = a.out_width - n0;
   // parts of whole steps
   const int each = ((ks + a.splits - 1) / a.splits + kStepK - 1) / kStepK * kStepK;
   const int64_t k0 = min(static_cast<int64_t>(blockIdx.y) * each, static_cast<int64_t>(ks));
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
       }
     }
   }
-  tile_products<DT, X, false, DIRECT>(A, B, lds, wm, wn, (k + kStepK - 1) / kStepK, acc, [](int, u16x8_t) {});
+  tile_products<DT, X, false, true>(A, B, lds, wm, wn, (k + kStepK - 1) / kStepK, acc, [](int, u16x8_t) {});
   constexpr int kWaveBytes = kBytes / (WM * WN) / 16 * 16;
   char* s = lds + w * kWaveBytes;
   if (!X && a.splits == 1) {
@@ -214,23 +214,23 @@ tbe_status ce_launch(K* kernel, const char* what, int threads, int64_t tiles, in
 }
 inline int64_t ce_tiles(int64_t m, int bm, int64_t n, int bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
 
-template <int DT, bool BACK, bool DIRECT>
+template <int DT, bool BACK>
 tbe_status ce_logits(const CeArgs& a, int tile, hipStream_t s) {
   const char* what = BACK ? "ce_z" : "ce_logits";
-  if (tile == kTile256) return ce_launch(ce_logits_kernel<DT, BACK, 256, 256, 2, 4, DIRECT>, what, 512, ce_tiles(a.rows, 256, a.items, 256), 1, a, s);
-  if (tile == kTile128) return ce_launch(ce_logits_kernel<DT, BACK, 128, 128, 2, 2, DIRECT>, what, 256, ce_tiles(a.rows, 128, a.items, 128), 1, a, s);
-  return ce_launch(ce_logits_kernel<DT, BACK, 64, 64, 2, 2, DIRECT>, what, 256, ce_tiles(a.rows, 64, a.items, 64), 1, a, s);
+  if (tile == kTile256) return ce_launch(ce_logits_kernel<DT, BACK, 256, 256, 2, 4, true>, what, 512, ce_tiles(a.rows, 256, a.items, 256), 1, a, s);
+  if (tile == kTile128) return ce_launch(ce_logits_kernel<DT, BACK, 128, 128, 2, 2, true>, what, 256, ce_tiles(a.rows, 128, a.items, 128), 1, a, s);
+  return ce_launch(ce_logits_kernel<DT, BACK, 64, 64, 2, 2, true>, what, 256, ce_tiles(a.rows, 64, a.items, 64), 1, a, s);
 }
-template <int DT, bool X, bool DIRECT>
+template <int DT, bool X>
 tbe_status ce_grad(const CeArgs& a, int tile, hipStream_t s) {
   const char* what = X ? "ce_grad_x" : "ce_grad_w";
-  const int64_t m = X ? a.rows : a.items;
-  if (tile == kTile256) return ce_launch(ce_grad_kernel<DT, X, 256, 256, 2, 4, DIRECT>, what, 512, ce_tiles(m, 256, a.width, 256), a.splits, a, s);
+  const int64_t m = X ? a.rows : a.items, n = a.out_width;
+  if (tile == kTile256) return ce_launch(ce_grad_kernel<DT, X, 256, 256, 2, 4>, what, 512, ce_tiles(m, 256, n, 256), a.splits, a, s);
   if constexpr (X) {
-    if (tile == kTile256x128) return ce_launch(ce_grad_kernel<DT, X, 256, 128, 4, 2, DIRECT>, what, 512, ce_tiles(m, 256, a.width, 128), a.splits, a, s);
+    if (tile == kTile256x128) return ce_launch(ce_grad_kernel<DT, X, 256, 128, 4, 2>, what, 512, ce_tiles(m, 256, n, 128), a.splits, a, s);
   }
-  if (tile == kTile128) return ce_launch(ce_grad_kernel<DT, X, 128, 128, 2, 2, DIRECT>, what, 256, ce_tiles(m, 128, a.width, 128), a.splits, a, s);
-  return ce_launch(ce_grad_kernel<DT, X, 64, 64, 2, 2, DIRECT>, what, 256, ce_tiles(m, 64, a.width, 64), a.splits, a, s);
+  if (tile == kTile128) return ce_launch(ce_grad_kernel<DT, X, 128, 128, 2, 2>, what, 256, ce_tiles(m, 128, n, 128), a.splits, a, s);
+  return ce_launch(ce_grad_kernel<DT, X, 64, 64, 2, 2>, what, 256, ce_tiles(m, 64, n, 64), a.splits, a, s);
 }
 
 }  // namespace tbe

@@ -3,7 +3,7 @@
 
 namespace tbe {
 template <>
-tbe_status ce_launch_z<1>(const CeArgs& a, int tile, bool direct, hipStream_t s) {
-  return direct ? ce_logits<1, true, true>(a, tile, s) : ce_logits<1, true, false>(a, tile, s);
+tbe_status ce_launch_z<1>(const CeArgs& a, int tile, hipStream_t s) {
+  return ce_logits<1, true>(a, tile, s);
 }
 }  // namespace tbe
