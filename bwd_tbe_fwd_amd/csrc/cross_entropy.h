@@ -41,7 +41,7 @@ struct CeArgs {
   float2* part;            // forward: [tiles of items][rows] maximum and sum
   uint16_t* z;             // backward: panels of 64 items, each [rows][64], `panel` elements apart
   int64_t panel;
-  float* bias_part;        // backward: [tiles of rows][items of a piece at most]; NULL: none
+  float* bias_part;        // backward: [tiles or shares of rows][items of the piece]; NULL: none
   int64_t bias_stride;
   // products of z
   const void* xg;          // x * grad_loss / largest, like x

@@ -594,11 +594,11 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   if (rows == 0) grad_x = nullptr;  // the gradients of the weights and biases are zeros
   const int64_t piece = hmin(narrow ? items : L.piece, copy ? L.copied : items);
   const int64_t stay = width <= 64 ? 256 : 192;  // narrow: rows or items of a workgroup
-  a.bias_stride = hmin(piece, items);
   TilePick x_pick = {0, 1};
   for (int64_t first = 0; st == TBE_OK && first < items; first += piece) {
     a.first = static_cast<int>(first);
     a.items = static_cast<int>(hmin(piece, items - first));
+    a.bias_stride = a.items;
     a.w = static_cast<const uint16_t*>(weight) + first * weight_stride;
     a.w_stride = weight_stride;
     a.bias = bias ? bias + first : nullptr;

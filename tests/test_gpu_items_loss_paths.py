@@ -1,0 +1,97 @@
+"""Softmax cross entropy at the sizes and calls where its plan changes: weights copied a piece at a time, many rows, few
+rows of a large vocabulary, shares of the rows, a single item, two streams.  Tolerances as in test_gpu_items_loss.py."""
+import pytest
+import torch
+
+import bwd_tbe_fwd_amd as tbe
+from gpu_util import flush_print
+from test_gpu_items_loss import BF16, F16, Exact, backward, forward, matrix, some_targets
+
+pytestmark = pytest.mark.gpu
+
+
+def one_case(rows, items, width, dtype, stride=None, offset=0, pad=0.2, scale=1.0, grad=None):
+    flush_print(f"loss {rows} {items} {width} {dtype} stride {stride} scale {scale}")
+    x, w = matrix(rows, width, dtype, 1), matrix(items, width, dtype, 2, 2 * width ** -0.5, stride, offset)
+    bias, t = matrix(1, items, torch.float32, 3, 1.5)[0], some_targets(rows, items, pad, 4)
+    exact = Exact(x, w, bias, t, scale)
+    loss, lse = forward(x, w, bias, t, scale)
+    exact.check_forward(loss, lse)
+    grad = torch.rand(rows, generator=torch.Generator().manual_seed(5)).cuda() + 0.25 if grad is None else grad
+    out = backward(x, w, bias, t, scale, lse, grad)
+    exact.check_backward(grad, *out)
+    return out
+
+
+# pieces of 131072 items of 127 and of 16640 of 1001: the last has few, whose rows are then shared among many workgroups
+@pytest.mark.parametrize("rows,items,width", [(2000, 131072 + 70, 127), (2000, 131072 + 1, 125), (100, 16640 + 33, 1001)])
+def test_copied_weights_whose_last_piece_is_small(rows, items, width):
+    one_case(rows, items, width, BF16, stride=width, offset=1)
+
+
+@pytest.mark.parametrize("rows,items,width,dtype", [(33000, 40, 24, BF16), (140000, 33, 8, F16), (132000, 9, 136, BF16),
+                                                    (40000, 300, 64, F16)])
+def test_many_rows(rows, items, width, dtype):
+    one_case(rows, items, width, dtype)
+
+
+@pytest.mark.parametrize("rows,items,width,dtype", [(3, 70000, 264, BF16), (64, 66001, 1000, F16), (20, 200000, 136, BF16),
+                                                    (300, 30000, 512, BF16)])
+def test_few_rows_of_a_large_vocabulary(rows, items, width, dtype):
+    one_case(rows, items, width, dtype)
+
+
+@pytest.mark.parametrize("rows,items,width", [(9000, 10000, 128), (8000, 52000, 96), (5000, 3000, 64), (6000, 49152, 128)])
+def test_shares_of_the_rows(rows, items, width):
+    one_case(rows, items, width, BF16)
+
+
+@pytest.mark.parametrize("rows,width", [(50, 8), (70, 200), (1, 128)])
+def test_one_item(rows, width):
+    """The only item's probability is 1: losses are 0, and so are the gradients."""
+    gx, gw, gb = one_case(rows, 1, width, F16, pad=0.0)
+    assert float(gb.abs().max()) < 1e-4 * rows and gx.shape == (rows, width) and gw.shape == (1, width)
+
+
+def test_scale_of_zero_and_gradients_of_zero():
+    for width in (64, 200):
+        gx, gw, gb = one_case(90, 700, width, BF16, scale=0.0)
+        assert bool((gx == 0).all()) and bool((gw == 0).all()) and bool((gb != 0).any())
+        for out in one_case(90, 700, width, BF16, grad=torch.zeros(90, device="cuda")):
+            assert bool((out == 0).all())
+
+
+def test_one_target_for_every_row():
+    for width in (40, 328):
+        rows, items = 500, 900
+        x, w = matrix(rows, width, F16, 1), matrix(items, width, F16, 2, width ** -0.5)
+        t = torch.full((rows,), 899, dtype=torch.int32, device="cuda")
+        exact = Exact(x, w, None, t, 1.0)
+        loss, lse = forward(x, w, None, t, 1.0)
+        exact.check_forward(loss, lse)
+        grad = torch.ones(rows, device="cuda")
+        exact.check_backward(grad, *backward(x, w, None, t, 1.0, lse, grad))
+
+
+def test_two_streams_with_a_workspace_each():
+    side = [torch.cuda.Stream() for _ in range(2)]
+    for rows, items, width in ((700, 9000, 64), (600, 5000, 264)):
+        w, grad = matrix(items, width, BF16, 2, width ** -0.5), torch.ones(rows, device="cuda")
+        need = (tbe.tbe_cross_entropy_forward_workspace_bytes(rows, items, width),
+                tbe.tbe_cross_entropy_backward_workspace_bytes(rows, items, width))
+        x = [matrix(rows, width, BF16, 10 + k) for k in range(2)]
+        t = [some_targets(rows, items, 0.2, 20 + k) for k in range(2)]
+        loss, lse = [[torch.empty(rows, device="cuda") for _ in range(2)] for _ in range(2)]
+        gx, gw = [torch.empty_like(v) for v in x], [torch.empty_like(w) for _ in range(2)]
+        ws = [[tbe.workspace(n) for n in need] for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for k, s in enumerate(side):
+                tbe.tbe_cross_entropy_forward(x[k], w, None, t[k], 1.0, loss[k], lse[k], ws[k][0], stream=s)
+                tbe.tbe_cross_entropy_backward(x[k], w, None, t[k], 1.0, lse[k], grad, gx[k], gw[k], None, ws[k][1], stream=s)
+        torch.cuda.synchronize()
+        for k in range(2):
+            e_loss, e_lse = forward(x[k], w, None, t[k], 1.0)
+            e_gx, e_gw, _ = backward(x[k], w, None, t[k], 1.0, e_lse, grad, with_bias=False)
+            for a, b in zip((loss[k], lse[k], gx[k], gw[k]), (e_loss, e_lse, e_gx, e_gw)):
+                assert torch.equal(a, b)
