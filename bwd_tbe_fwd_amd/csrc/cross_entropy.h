@@ -67,8 +67,8 @@ __device__ __forceinline__ float2 ce_join(float2 a, float2 b) {
   return make_float2(top, a.y * expf(a.x - from) + b.y * expf(b.x - from));
 }
 
-// A tile of C and how it is walked, as for the grouped layers.
-enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile256x128 = 3 };  // the last for the gradient of x
+// A tile of C and how it is walked, as for the grouped layers; the logits and the gradient of x have one more.
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile64x256 = 3, kTile256x128 = 3 };
 
 // Defined in translation units of their own (cross_entropy_forward_f16.hip and its siblings).
 template <int DT> tbe_status ce_launch_forward(const CeArgs& a, int tile, bool direct, hipStream_t s);

@@ -329,8 +329,6 @@ constexpr int kMostSplits = 64;
 // Rows of up to so many columns stay in registers (cross_entropy_narrow.h).
 constexpr int64_t kNarrowWidth = 128;
 
-constexpr int64_t kFusedGroups = 512;  // two workgroups a CU
-
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 struct Carve {
@@ -396,8 +394,8 @@ CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   L.z = c.take(narrow ? 0 : (z + 64 * most) * 2);  // panels of whole 64 rows
   L.sum_x = c.take(sum_x_bytes(rows, width));
   L.sum_w = c.take(kSumBytes);
-  // of 64 rows a part; of narrow rows fused_splits of them
-  L.bias_part = c.take(narrow ? (items + kFusedGroups * 256) * 4 : z / 64 * 4 + most * 4);
+  // of 64 rows a part; of narrow rows fused_splits of them, which are one or fit kSumBytes with 16 bytes a sum
+  L.bias_part = c.take(narrow ? items * 4 + kSumBytes / 4 : z / 64 * 4 + most * 4);
   L.ref = c.take(up(rows, 64) * 4);
   L.part_of = c.take(up(rows, 64) * 4);
   L.total = c.at;
@@ -431,6 +429,10 @@ TilePick pick_tile(const TileCost (&costs)[N], int64_t m, int64_t n, int64_t k, 
   }
   return best;
 }
+// Logits: of few rows the weights' bytes decide, and 64 x 256 reads the rows a quarter as often as 64 x 64 (64 rows, 131072 items of
+// 1000, backward: 65 and 81 us; 64 rows, 400000 items of 1000, forward: 184 and 219; 300 rows, 131072 items of 1024, forward: 107,
+// and 111 with 128 x 128).
+constexpr TileCost kLogits[4] = {kDirectTiles[0], kDirectTiles[1], kDirectTiles[2], {64, 256, 256, 512, 4.0, 0.95, 0.95}};
 // The gradient of x: a tile more.  Its shares' sums go on from piece to piece, whether there is one share or several.
 constexpr TileCost kGradX[4] = {kDirectTiles[0], kDirectTiles[1], kDirectTiles[2], {256, 128, 512, 256, 5.0, 0.8, 0.8}};
 
@@ -441,10 +443,22 @@ int narrow_splits(int64_t rows, int64_t items, bool few) {
   return static_cast<int>(hmax(1, hmin(tiles, hmin(2048 / row_tiles, hmax(tiles / 16, 512 / row_tiles)))));
 }
 
-// Into how many shares the passing side of the fused kernels goes: what stays fills two workgroups a CU, the shares make up for
-// what it does not.  Four tiles a share at least.
-int fused_splits(int64_t stay, int64_t pass, int64_t of, int64_t most) {
-  return static_cast<int>(hmax(1, hmin(hmin(kFusedGroups / ((stay + of - 1) / of), (pass + 63) / 64 / 4), most)));
+// Into how many shares the passing side of the fused kernels goes.  The fullest CU's workgroups count, two at a time in the time
+// of a pair, one alone in 0.7 of it; four tiles a share at least.  A share more costs its sums, which are written, read and added.
+int fused_splits(int64_t stay_tiles, int64_t pass, double pair_us, double share_bytes, int64_t most) {
+  const int64_t tiles = (pass + 63) / 64, end = hmax(1, hmin(hmin(kMostSplits, tiles / 4), most));
+  int best = 1;
+  double least = -1.0;
+  for (int n = 1; n <= end; ++n) {
+    const int64_t a_cu = (stay_tiles * n + 255) / 256;
+    const double pairs = static_cast<double>(a_cu / 2) + (a_cu % 2 ? 0.7 : 0.0);
+    const double us = pairs * static_cast<double>((tiles + n - 1) / n + 4) * pair_us + (n > 1 ? 2.0 * n * share_bytes / 4e6 : 0.0);
+    if (least < 0.0 || us < least) {
+      least = us;
+      best = n;
+    }
+  }
+  return best;
 }
 
 bool whole_16(const void* p, int64_t stride, int64_t width) {
@@ -547,8 +561,8 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
       parts = a.splits = narrow_splits(rows, a.items, few);
       st = f16 ? ce_launch_narrow_forward<1>(a, few, s) : ce_launch_narrow_forward<2>(a, few, s);
     } else {
-      const int tile = direct ? pick_tile(kDirectTiles, rows, a.items, width, 1, 0, weight_shares_us).tile : kTile64;
-      parts = (a.items + kDirectTiles[tile].bn - 1) / kDirectTiles[tile].bn;
+      const int tile = direct ? pick_tile(kLogits, rows, a.items, width, 1, 0, weight_shares_us).tile : kTile64;
+      parts = (a.items + kLogits[tile].bn - 1) / kLogits[tile].bn;
       st = f16 ? ce_launch_forward<1>(a, tile, direct, s) : ce_launch_forward<2>(a, tile, direct, s);
     }
     if (st != TBE_OK) break;
@@ -594,6 +608,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   if (rows == 0) grad_x = nullptr;  // the gradients of the weights and biases are zeros
   const int64_t piece = hmin(narrow ? items : L.piece, copy ? L.copied : items);
   const int64_t stay = width <= 64 ? 256 : 192;  // narrow: rows or items of a workgroup
+  const double pair_us = width <= 64 ? 2.6 : 3.0;                // of two workgroups with a tile each
   TilePick x_pick = {0, 1};
   for (int64_t first = 0; st == TBE_OK && first < items; first += piece) {
     a.first = static_cast<int>(first);
@@ -611,14 +626,17 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
     a.bias_part = grad_bias && !narrow ? bias_part : nullptr;
     int bias_rows = 0;
     if (st == TBE_OK && !narrow && rows > 0) {
-      const int tile = pick_tile(kDirectTiles, rows, a.items, width, 1, 0, weight_shares_us).tile;
-      bias_rows = kDirectTiles[tile].bm;
+      const int tile = pick_tile(kLogits, rows, a.items, width, 1, 0, weight_shares_us).tile;
+      bias_rows = kLogits[tile].bm;
       st = f16 ? ce_launch_z<1>(a, tile, s) : ce_launch_z<2>(a, tile, s);
     }
     if (st == TBE_OK && grad_x) {
       // the same shares for every piece: their sums go on
-      if (first == 0 && narrow) x_pick.splits = fused_splits(rows, a.items, stay, sum_x_bytes(rows, width) / (rows * a.sum_pitch * 4));
-      else if (first == 0) x_pick = pick_tile(kGradX, rows, a.sum_pitch, a.items, kMostSplits, sum_x_bytes(rows, width), x_shares_us);
+      if (first == 0 && narrow) {
+        const int64_t share = rows * a.sum_pitch * 4;
+        x_pick.splits = fused_splits((rows + stay - 1) / stay, a.items, pair_us, static_cast<double>(share), sum_x_bytes(rows, width) / share);
+      }
+      if (first == 0 && !narrow) x_pick = pick_tile(kGradX, rows, a.sum_pitch, a.items, kMostSplits, sum_x_bytes(rows, width), x_shares_us);
       a.sum = reinterpret_cast<float*>(ws + L.sum_x);
       a.splits = x_pick.splits;
       a.add = first > 0;
@@ -631,7 +649,8 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
     a.out_stride = grad_weight_stride;
     a.splits = 1;
     if (st == TBE_OK && narrow && (grad_weight || grad_bias)) {
-      a.splits = fused_splits(a.items, rows, stay, kSumBytes / (a.items * a.sum_pitch * 4));
+      const int64_t share = a.items * a.sum_pitch * 4;
+      a.splits = fused_splits((a.items + stay - 1) / stay, rows, pair_us, static_cast<double>(share), kSumBytes / share);
       a.bias_part = grad_bias ? bias_part : nullptr;
       st = f16 ? ce_launch_fused<1>(a, false, s) : ce_launch_fused<2>(a, false, s);
     } else if (st == TBE_OK && grad_weight) {

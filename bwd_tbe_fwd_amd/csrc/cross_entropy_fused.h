@@ -236,8 +236,8 @@ template <int DT, bool X, bool BIAS>
 tbe_status ce_fused(const CeArgs& a, hipStream_t s) {
   const int64_t stay = X ? a.rows : a.items;
   const char* what = X ? "ce_grad_x" : "ce_grad_w";
-  if (a.width <= 64) return ce_launch(ce_fused_kernel<DT, X, 2, 4, BIAS>, what, 256, (stay + 255) / 256 * a.splits, 1, a, s);
-  return ce_launch(ce_fused_kernel<DT, X, 4, 3, BIAS>, what, 256, (stay + 191) / 192 * a.splits, 1, a, s);
+  if (a.width <= 64) return ce_launch(ce_fused_kernel<DT, X, 2, 4, BIAS>, what, 256, (stay + 255) / 256 * a.splits, a, s);
+  return ce_launch(ce_fused_kernel<DT, X, 4, 3, BIAS>, what, 256, (stay + 191) / 192 * a.splits, a, s);
 }
 
 }  // namespace tbe

@@ -6,16 +6,18 @@
 
 namespace tbe {
 
-// Workgroup blockIdx.x's place among m_tiles x n_tiles: a contiguous share for each chiplet, and in it bands of 8 tiles of m
-// walked along n, so that the 32 workgroups that a chiplet runs at once read 8 + 4 tiles of operands and not 1 + 32.  False:
-// none.
+// Workgroup blockIdx.x's place among m_tiles x n_tiles of each share of k: a contiguous part for each chiplet, and in it bands
+// of 8 tiles of m walked along n, so that the 32 workgroups that a chiplet runs at once read 8 + 4 tiles of operands and not
+// 1 + 32.  False: none.
 struct TilePlace {
-  int m, n;
+  int m, n, share;
 };
-__device__ __forceinline__ bool tile_place(int64_t m_tiles, int64_t n_tiles, TilePlace& t) {
-  const int64_t total = m_tiles * n_tiles, x = blockIdx.x % 8;
-  const int64_t id = total * x / 8 + blockIdx.x / 8;
+__device__ __forceinline__ bool tile_place(int64_t m_tiles, int64_t n_tiles, int shares, TilePlace& t) {
+  const int64_t tiles = m_tiles * n_tiles, total = tiles * shares, x = blockIdx.x % 8;
+  int64_t id = total * x / 8 + blockIdx.x / 8;
   if (id >= total * (x + 1) / 8) return false;
+  t.share = static_cast<int>(id / tiles);
+  id -= t.share * tiles;
   const int64_t band = id / (8 * n_tiles);
   const int r = static_cast<int>(id - band * 8 * n_tiles);
   const int high = static_cast<int>(m_tiles - band * 8 < 8 ? m_tiles - band * 8 : 8);
@@ -37,7 +39,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
   const int wm = (w / WN) * (MF * 16), wn = (w % WN) * (NF * 16);
   const int count = *a.r.count;
   TilePlace t;
-  if (!tile_place((count + BM - 1) / BM, (a.items + BN - 1) / BN, t)) return;
+  if (!tile_place((count + BM - 1) / BM, (a.items + BN - 1) / BN, 1, t)) return;
   const int m0 = t.m * BM, n0 = t.n * BN;
   const int m_left = count - m0, n_left = a.items - n0;
   OA A;
@@ -140,7 +142,8 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
   }
 }
 
-// The two products of z.  X: the gradient of x, else of the weights.  blockIdx.y: the part of k.
+// The two products of z.  X: the gradient of x, else of the weights.  A chiplet takes whole shares of k where there are many: few
+// rows' weights are then read by one (64 rows, 131072 items of 1000: 61 us, and 85 with each share's tiles dealt to all eight).
 template <int DT, bool X, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void ce_grad_kernel(CeArgs a) {
   constexpr int T = WM * WN * kWave;
@@ -153,12 +156,12 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
   const int wm = (w / WN) * (MF * 16), wn = (w % WN) * (NF * 16);
   const int count = *a.r.count, ms = X ? count : a.items, ks = X ? a.items : count;
   TilePlace t;
-  if (!tile_place((ms + BM - 1) / BM, (a.out_width + BN - 1) / BN, t)) return;
+  if (!tile_place((ms + BM - 1) / BM, (a.out_width + BN - 1) / BN, a.splits, t)) return;
   const int m0 = t.m * BM, n0 = t.n * BN;
   const int m_left = ms - m0, n_left = a.out_width - n0;
   // parts of whole steps
   const int each = ((ks + a.splits - 1) / a.splits + kStepK - 1) / kStepK * kStepK;
-  const int64_t k0 = min(static_cast<int64_t>(blockIdx.y) * each, static_cast<int64_t>(ks));
+  const int64_t k0 = min(static_cast<int64_t>(t.share) * each, static_cast<int64_t>(ks));
   const int k = min(each, static_cast<int>(ks - k0));
   OA A;
   OB B;
@@ -170,7 +173,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
     B.init(static_cast<const uint16_t*>(a.xg) + k0 * a.x_stride + n0, a.x_stride, n_left, k, a.width);
   }
   const int64_t pitch = a.sum_pitch;
-  float* const sum = a.sum + (static_cast<int64_t>(blockIdx.y) * (X ? a.rows : a.items) + m0 + wm) * pitch + n0 + wn;
+  float* const sum = a.sum + (static_cast<int64_t>(t.share) * (X ? a.rows : a.items) + m0 + wm) * pitch + n0 + wn;
   f32x4 acc[MF][NF];
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
@@ -202,14 +205,14 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
 }
 
 template <typename K>
-tbe_status ce_launch(K* kernel, const char* what, int threads, int64_t tiles, int splits, const CeArgs& a, hipStream_t s) {
+tbe_status ce_launch(K* kernel, const char* what, int threads, int64_t tiles, const CeArgs& a, hipStream_t s) {
   const int64_t groups = (tiles + 7) / 8 * 8;  // for the chiplets' shares
   if (groups * threads >= (int64_t{1} << 32)) {
     set_error("cross entropy: %lld tiles are more than a launch takes", static_cast<long long>(groups));
     return TBE_ERR_UNSUPPORTED;
   }
   ProfScope ps(what, s);
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups), splits), dim3(threads), 0, s, a);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s, a);
   return check_launch(what);
 }
 inline int64_t ce_tiles(int64_t m, int bm, int64_t n, int bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
@@ -217,20 +220,22 @@ inline int64_t ce_tiles(int64_t m, int bm, int64_t n, int bn) { return ((m + bm 
 template <int DT, bool BACK>
 tbe_status ce_logits(const CeArgs& a, int tile, hipStream_t s) {
   const char* what = BACK ? "ce_z" : "ce_logits";
-  if (tile == kTile256) return ce_launch(ce_logits_kernel<DT, BACK, 256, 256, 2, 4, true>, what, 512, ce_tiles(a.rows, 256, a.items, 256), 1, a, s);
-  if (tile == kTile128) return ce_launch(ce_logits_kernel<DT, BACK, 128, 128, 2, 2, true>, what, 256, ce_tiles(a.rows, 128, a.items, 128), 1, a, s);
-  return ce_launch(ce_logits_kernel<DT, BACK, 64, 64, 2, 2, true>, what, 256, ce_tiles(a.rows, 64, a.items, 64), 1, a, s);
+  if (tile == kTile256) return ce_launch(ce_logits_kernel<DT, BACK, 256, 256, 2, 4, true>, what, 512, ce_tiles(a.rows, 256, a.items, 256), a, s);
+  if (tile == kTile128) return ce_launch(ce_logits_kernel<DT, BACK, 128, 128, 2, 2, true>, what, 256, ce_tiles(a.rows, 128, a.items, 128), a, s);
+  if (tile == kTile64x256)
+    return ce_launch(ce_logits_kernel<DT, BACK, 64, 256, 1, 4, true>, what, 256, ce_tiles(a.rows, 64, a.items, 256), a, s);
+  return ce_launch(ce_logits_kernel<DT, BACK, 64, 64, 2, 2, true>, what, 256, ce_tiles(a.rows, 64, a.items, 64), a, s);
 }
 template <int DT, bool X>
 tbe_status ce_grad(const CeArgs& a, int tile, hipStream_t s) {
   const char* what = X ? "ce_grad_x" : "ce_grad_w";
   const int64_t m = X ? a.rows : a.items, n = a.out_width;
-  if (tile == kTile256) return ce_launch(ce_grad_kernel<DT, X, 256, 256, 2, 4>, what, 512, ce_tiles(m, 256, n, 256), a.splits, a, s);
+  if (tile == kTile256) return ce_launch(ce_grad_kernel<DT, X, 256, 256, 2, 4>, what, 512, ce_tiles(m, 256, n, 256) * a.splits, a, s);
   if constexpr (X) {
-    if (tile == kTile256x128) return ce_launch(ce_grad_kernel<DT, X, 256, 128, 4, 2>, what, 512, ce_tiles(m, 256, n, 128), a.splits, a, s);
+    if (tile == kTile256x128) return ce_launch(ce_grad_kernel<DT, X, 256, 128, 4, 2>, what, 512, ce_tiles(m, 256, n, 128) * a.splits, a, s);
   }
-  if (tile == kTile128) return ce_launch(ce_grad_kernel<DT, X, 128, 128, 2, 2>, what, 256, ce_tiles(m, 128, n, 128), a.splits, a, s);
-  return ce_launch(ce_grad_kernel<DT, X, 64, 64, 2, 2>, what, 256, ce_tiles(m, 64, n, 64), a.splits, a, s);
+  if (tile == kTile128) return ce_launch(ce_grad_kernel<DT, X, 128, 128, 2, 2>, what, 256, ce_tiles(m, 128, n, 128) * a.splits, a, s);
+  return ce_launch(ce_grad_kernel<DT, X, 64, 64, 2, 2>, what, 256, ce_tiles(m, 64, n, 64) * a.splits, a, s);
 }
 
 }  // namespace tbe
