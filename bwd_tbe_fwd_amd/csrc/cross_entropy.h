@@ -74,8 +74,8 @@ enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile64x256 = 3, kTile256x128 = 
 template <int DT> tbe_status ce_launch_forward(const CeArgs& a, int tile, bool direct, hipStream_t s);
 template <int DT> tbe_status ce_launch_z(const CeArgs& a, int tile, hipStream_t s);
 template <int DT> tbe_status ce_launch_narrow_forward(const CeArgs& a, bool few, hipStream_t s);
-template <int DT> tbe_status ce_launch_fused(const CeArgs& a, bool x, hipStream_t s);
-template <int DT> tbe_status ce_launch_grad_x(const CeArgs& a, int tile, hipStream_t s);
-template <int DT> tbe_status ce_launch_grad_w(const CeArgs& a, int tile, hipStream_t s);
+// The gradients of x and of the weights; one of them where the other's splits are 0.
+template <int DT> tbe_status ce_launch_fused(const CeArgs& x, const CeArgs& w, hipStream_t s);
+template <int DT> tbe_status ce_launch_grads(const CeArgs& x, int x_tile, const CeArgs& w, int w_tile, hipStream_t s);
 
 }  // namespace tbe

@@ -72,24 +72,49 @@ __global__ __launch_bounds__(kBlock) void ce_count_kernel(CeBatch b) {
   }
 }
 
+// Weights whose rows do not start on 16 bytes, or are not whole 16 bytes: a piece's items at a pitch that is, zeros behind the
+// width.  A wave a row; workgroup `block` of `blocks`.
+struct CePad {
+  const uint16_t* from;
+  int64_t stride;
+  int32_t items, width, pitch;
+  uint16_t* to;
+};
+__device__ __forceinline__ void ce_pad_rows(const CePad& p, unsigned block, unsigned blocks) {
+  const int l = lane_id();
+  for (int64_t v = static_cast<int64_t>(block) * kWavesPerBlock + (threadIdx.x >> 6); v < p.items; v += static_cast<int64_t>(blocks) * kWavesPerBlock) {
+    for (int d = l * 8; d < p.pitch; d += kWave * 8) {
+      Vec<uint16_t, 8> x;
+      load_vec_part<uint16_t, 8>(p.from + v * p.stride + d, p.width - d, x);
+      store_vec_any<uint16_t, 8>(p.to + v * p.pitch + d, x);
+    }
+  }
+}
+__global__ __launch_bounds__(kBlock) void ce_pad_kernel(CePad p) { ce_pad_rows(p, blockIdx.x, gridDim.x); }
+
 // Places the rows that have a target and copies what the products need of them.  A workgroup takes `each` rows (a multiple of
 // kRowsAtOnce that 256 is a multiple of).  With `counted` it finds the rows before its own in ce_count_kernel's counts, else in
-// the targets themselves: one launch for up to kCountHere rows.
+// the targets themselves: one launch for up to kCountHere rows.  `more` workgroups behind those of the rows take the biases of
+// narrow rows, the ones behind them the copies of the first piece's weights.
 constexpr int kRowsAtOnce = 4;  // a wave each
 constexpr int64_t kCountHere = 4096;
 template <int DT>
-__global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, int groups, int counted) {
+__global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, int groups, int more, int counted, CePad pad) {
   __shared__ uint32_t s_n[kWavesPerBlock];
   __shared__ float s_top[kWavesPerBlock];
   __shared__ int s_target[kRowsAtOnce];
   __shared__ int s_slot[kRowsAtOnce];
   const int64_t first = static_cast<int64_t>(blockIdx.x) * each, end = min(first + each, b.rows);
   const int w = threadIdx.x >> 6, l = lane_id();
+  if (static_cast<int>(blockIdx.x) >= groups + more) {
+    ce_pad_rows(pad, blockIdx.x - (groups + more), gridDim.x - (groups + more));
+    return;
+  }
   if (static_cast<int>(blockIdx.x) >= groups) {
     // the biases' workgroups.  Finite ones stay finite: the lowest value is no mask where every item has it
     const int64_t end = (b.items + 63) / 64 * 64;
     for (int64_t v = static_cast<int64_t>(blockIdx.x - groups) * kBlock + threadIdx.x; v < end;
-         v += static_cast<int64_t>(gridDim.x - groups) * kBlock) {
+         v += static_cast<int64_t>(more) * kBlock) {
       const float x = v >= b.items ? -kInfinity : b.bias ? b.bias[v] : 0.0f, y = x * b.over;
       b.bias_over[v] = y == -kInfinity && x != y ? -3.4028234664e38f : y;
     }
@@ -186,21 +211,6 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
     if (threadIdx.x == 0) {
       *b.count = static_cast<int32_t>(before);
       *b.largest = top;
-    }
-  }
-}
-
-// Weights whose rows do not start on 16 bytes, or are not whole 16 bytes: `items` rows of them at a pitch that is, zeros behind
-// the width.  A wave a row.
-__global__ __launch_bounds__(kBlock) void ce_pad_kernel(const uint16_t* __restrict__ w, int64_t stride, int items, int width, int pitch,
-                                                        uint16_t* __restrict__ out) {
-  const int l = lane_id();
-  for (int64_t v = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6); v < items;
-       v += static_cast<int64_t>(gridDim.x) * kWavesPerBlock) {
-    for (int d = l * 8; d < pitch; d += kWave * 8) {
-      Vec<uint16_t, 8> x;
-      load_vec_part<uint16_t, 8>(w + v * stride + d, width - d, x);
-      store_vec_any<uint16_t, 8>(out + v * pitch + d, x);
     }
   }
 }
@@ -489,7 +499,8 @@ CeBatch batch_of(char* ws, const CeLayout& L, int64_t rows, int64_t items, int64
   }
   return b;
 }
-tbe_status launch_rows(const CeBatch& b, int dtype, hipStream_t s) {
+int pad_groups(const CePad& p) { return static_cast<int>(hmin((static_cast<int64_t>(p.items) + 3) / 4, 16384)); }
+tbe_status launch_rows(const CeBatch& b, int dtype, const CePad& pad, hipStream_t s) {
   const bool counted = b.rows > kCountHere;
   ProfScope ps("ce_rows", s);
   if (counted) {
@@ -500,7 +511,8 @@ tbe_status launch_rows(const CeBatch& b, int dtype, hipStream_t s) {
   const int groups = static_cast<int>(hmax(1, (b.rows + each - 1) / each));  // no rows: their count, 0
   const int more = b.bias_over ? static_cast<int>(hmin(2048, (b.items + 4 * kBlock - 1) / (4 * kBlock))) : 0;
   auto kernel = dtype == TBE_F16 ? ce_rows_kernel<1> : ce_rows_kernel<2>;
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups + more)), dim3(kBlock), 0, s, b, each, groups, counted ? 1 : 0);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups + more + pad_groups(pad))), dim3(kBlock), 0, s, b, each, groups, more,
+                     counted ? 1 : 0, pad);
   return check_launch("ce_rows");
 }
 tbe_status launch_grad_w_sum(const CeArgs& a, bool f16, const float* largest, hipStream_t s) {
@@ -510,11 +522,14 @@ tbe_status launch_grad_w_sum(const CeArgs& a, bool f16, const float* largest, hi
                      a.items, a.out_width, a.factor, largest, static_cast<uint16_t*>(a.out), a.out_stride);
   return check_launch("ce_grad_w_sum");
 }
-// A piece's weights into the workspace.
-tbe_status launch_pad(const CeArgs& a, const void* w, int64_t stride, void* out, hipStream_t s) {
+// A piece's weights into the workspace: the first one's beside the rows.
+CePad pad_of(const void* weight, int64_t stride, int64_t items, int64_t width, char* ws, const CeLayout& L) {
+  return CePad{static_cast<const uint16_t*>(weight), stride, static_cast<int32_t>(items), static_cast<int32_t>(width), static_cast<int32_t>(L.pitch),
+               reinterpret_cast<uint16_t*>(ws + L.wc)};
+}
+tbe_status launch_pad(const CePad& p, hipStream_t s) {
   ProfScope ps("ce_pad", s);
-  hipLaunchKernelGGL(ce_pad_kernel, dim3(static_cast<unsigned>(hmin((a.items + 3) / 4, 16384))), dim3(kBlock), 0, s,
-                     static_cast<const uint16_t*>(w), stride, a.items, a.out_width, a.width, static_cast<uint16_t*>(out));
+  hipLaunchKernelGGL(ce_pad_kernel, dim3(static_cast<unsigned>(pad_groups(p))), dim3(kBlock), 0, s, p);
   return check_launch("ce_pad");
 }
 CeRows rows_of(const CeBatch& b) { return CeRows{b.count, b.row, b.target, b.lse, b.grad, b.largest, b.ref, b.part}; }
@@ -536,14 +551,14 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
   b.picked = reinterpret_cast<float*>(ws + L.picked);
   b.loss = loss;
   b.lse_out = lse;
-  tbe_status st = launch_rows(b, dtype, s);
+  const int64_t piece = hmin(narrow ? items : L.piece, copy ? L.copied : items);
+  tbe_status st = launch_rows(b, dtype, copy ? pad_of(weight, weight_stride, hmin(piece, items), width, ws, L) : CePad{}, s);
   if (b.bias_over) bias = b.bias_over;
   CeArgs a = {};
   a.rows = rows; a.width = static_cast<int>(direct ? L.pitch : width); a.out_width = static_cast<int>(width);
   a.x = ws + L.xc; a.x_stride = L.pitch;
   a.scale = scale; a.r = rows_of(b);
   a.part = reinterpret_cast<float2*>(ws + L.part);
-  const int64_t piece = hmin(narrow ? items : L.piece, copy ? L.copied : items);
   for (int64_t first = 0; st == TBE_OK && first < items; first += piece) {
     a.first = static_cast<int>(first);
     a.items = static_cast<int>(hmin(piece, items - first));
@@ -551,7 +566,7 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
     a.w_stride = weight_stride;
     a.bias = bias ? bias + first : nullptr;
     if (copy) {
-      st = launch_pad(a, a.w, weight_stride, ws + L.wc, s);
+      if (first > 0) st = launch_pad(pad_of(a.w, weight_stride, a.items, width, ws, L), s);
       a.w = ws + L.wc;
       a.w_stride = L.pitch;
     }
@@ -595,7 +610,8 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
     b.ref = reinterpret_cast<float*>(ws + L.ref);
     b.part = reinterpret_cast<float*>(ws + L.part_of);
   }
-  tbe_status st = launch_rows(b, dtype, s);
+  const int64_t piece = hmin(narrow ? items : L.piece, copy ? L.copied : items);
+  tbe_status st = launch_rows(b, dtype, copy ? pad_of(weight, weight_stride, hmin(piece, items), width, ws, L) : CePad{}, s);
   if (b.bias_over) bias = b.bias_over;
   CeArgs a = {};
   a.rows = rows; a.width = static_cast<int>(L.pitch); a.out_width = static_cast<int>(width);
@@ -606,7 +622,6 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   a.sum_pitch = up(width, 4);
   float* const bias_part = reinterpret_cast<float*>(ws + L.bias_part);
   if (rows == 0) grad_x = nullptr;  // the gradients of the weights and biases are zeros
-  const int64_t piece = hmin(narrow ? items : L.piece, copy ? L.copied : items);
   const int64_t stay = width <= 64 ? 256 : 192;  // narrow: rows or items of a workgroup
   const double pair_us = width <= 64 ? 2.6 : 3.0;                // of two workgroups with a tile each
   TilePick x_pick = {0, 1};
@@ -618,7 +633,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
     a.w_stride = weight_stride;
     a.bias = bias ? bias + first : nullptr;
     if (copy) {
-      st = launch_pad(a, a.w, weight_stride, ws + L.wc, s);
+      if (first > 0) st = launch_pad(pad_of(a.w, weight_stride, a.items, width, ws, L), s);
       a.w = ws + L.wc;
       a.w_stride = L.pitch;
     }
@@ -630,39 +645,43 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
       bias_rows = kLogits[tile].bm;
       st = f16 ? ce_launch_z<1>(a, tile, s) : ce_launch_z<2>(a, tile, s);
     }
-    if (st == TBE_OK && grad_x) {
+    CeArgs to_x = a, to_w = a;
+    to_x.splits = to_w.splits = 0;
+    to_x.bias_part = nullptr;
+    TilePick w_pick = {0, 1};
+    if (grad_x) {
       // the same shares for every piece: their sums go on
       if (first == 0 && narrow) {
         const int64_t share = rows * a.sum_pitch * 4;
         x_pick.splits = fused_splits((rows + stay - 1) / stay, a.items, pair_us, static_cast<double>(share), sum_x_bytes(rows, width) / share);
       }
       if (first == 0 && !narrow) x_pick = pick_tile(kGradX, rows, a.sum_pitch, a.items, kMostSplits, sum_x_bytes(rows, width), x_shares_us);
-      a.sum = reinterpret_cast<float*>(ws + L.sum_x);
-      a.splits = x_pick.splits;
-      a.add = first > 0;
-      if (narrow) st = f16 ? ce_launch_fused<1>(a, true, s) : ce_launch_fused<2>(a, true, s);
-      else st = f16 ? ce_launch_grad_x<1>(a, x_pick.tile, s) : ce_launch_grad_x<2>(a, x_pick.tile, s);
+      to_x.sum = reinterpret_cast<float*>(ws + L.sum_x);
+      to_x.splits = x_pick.splits;
+      to_x.add = first > 0;
     }
-    a.sum = reinterpret_cast<float*>(ws + L.sum_w);
-    a.add = 0;
-    a.out = grad_weight ? static_cast<uint16_t*>(grad_weight) + first * grad_weight_stride : nullptr;
-    a.out_stride = grad_weight_stride;
-    a.splits = 1;
-    if (st == TBE_OK && narrow && (grad_weight || grad_bias)) {
-      const int64_t share = a.items * a.sum_pitch * 4;
-      a.splits = fused_splits((a.items + stay - 1) / stay, rows, pair_us, static_cast<double>(share), kSumBytes / share);
-      a.bias_part = grad_bias ? bias_part : nullptr;
-      st = f16 ? ce_launch_fused<1>(a, false, s) : ce_launch_fused<2>(a, false, s);
-    } else if (st == TBE_OK && grad_weight) {
-      const TilePick p = pick_tile(kWeightTiles, a.items, a.sum_pitch, rows, kMostSplits, kSumBytes, weight_shares_us);
-      a.splits = p.splits;
-      st = f16 ? ce_launch_grad_w<1>(a, p.tile, s) : ce_launch_grad_w<2>(a, p.tile, s);
+    if (grad_weight || (grad_bias && narrow)) {
+      if (narrow) {
+        const int64_t share = a.items * a.sum_pitch * 4;
+        w_pick.splits = fused_splits((a.items + stay - 1) / stay, rows, pair_us, static_cast<double>(share), kSumBytes / share);
+      } else {
+        w_pick = pick_tile(kWeightTiles, a.items, a.sum_pitch, rows, kMostSplits, kSumBytes, weight_shares_us);
+      }
+      to_w.sum = reinterpret_cast<float*>(ws + L.sum_w);
+      to_w.out = grad_weight ? static_cast<uint16_t*>(grad_weight) + first * grad_weight_stride : nullptr;
+      to_w.out_stride = grad_weight_stride;
+      to_w.splits = w_pick.splits;
+      if (narrow) to_w.bias_part = grad_bias ? bias_part : nullptr;
     }
-    if (st == TBE_OK && grad_weight && a.splits > 1) st = launch_grad_w_sum(a, f16, b.largest, s);
+    if (st == TBE_OK && narrow && (to_x.splits || to_w.splits))
+      st = f16 ? ce_launch_fused<1>(to_x, to_w, s) : ce_launch_fused<2>(to_x, to_w, s);
+    if (st == TBE_OK && !narrow && (to_x.splits || to_w.splits))
+      st = f16 ? ce_launch_grads<1>(to_x, x_pick.tile, to_w, w_pick.tile, s) : ce_launch_grads<2>(to_x, x_pick.tile, to_w, w_pick.tile, s);
+    if (st == TBE_OK && grad_weight && w_pick.splits > 1) st = launch_grad_w_sum(to_w, f16, b.largest, s);
     if (st == TBE_OK && grad_bias) {
       ProfScope ps("ce_grad_bias", s);
       hipLaunchKernelGGL(ce_grad_bias_kernel, dim3(static_cast<unsigned>((a.items + kWave - 1) / kWave)), dim3(1024), 0, s, bias_part,
-                         a.bias_stride, b, bias_rows, narrow ? a.splits : 0, 1.0f / unit, a.items, grad_bias + first);
+                         a.bias_stride, b, bias_rows, narrow ? w_pick.splits : 0, 1.0f / unit, a.items, grad_bias + first);
       st = check_launch("ce_grad_bias");
     }
   }

@@ -20,22 +20,23 @@ namespace tbe {
 
 constexpr int kPassing = 64;  // t of a tile
 
+constexpr int kRing = 3;
+
+// `block`: the workgroup among this gradient's.  s_more: X: the items' biases; else the rows' references, factors and targets;
+// each 64 t in the order of the lanes that ask for them.
 template <int DT, bool X, int KS, int MF, bool BIAS>
-__global__ __launch_bounds__(256, 2) void ce_fused_kernel(CeArgs a) {
-  constexpr int T = 256, KT = KS / 2, CG = 2 * KS, kStay = 64 * MF, kRing = 3;
+__device__ __forceinline__ void ce_fused_part(const CeArgs& a, unsigned block, uint16_t* lds, uint32_t (*s_more)[4][kPassing]) {
+  constexpr int T = 256, KT = KS / 2, CG = 2 * KS, kStay = 64 * MF;
   using OT = Operand<true, kPassing, 0, T, true>;
   constexpr int kTile = KT * OT::kElems;
   constexpr int kLoads = KT * OT::kEach + 1;  // a wave's, of a tile
-  __shared__ __align__(16) uint16_t lds[kRing * kTile];
-  // X: the items' biases; else the rows' references, factors and targets; each 64 t in the order of the lanes that ask for them
-  __shared__ __align__(16) uint32_t s_more[kRing][4][kPassing];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id(), g = l >> 4;
   const int count = *a.r.count, stay = X ? count : a.items, pass = X ? a.items : count;
   // 0 of them too, and as many as an int holds
   const int stay_tiles = stay / kStay + (stay % kStay != 0), pass_tiles = pass / kPassing + (pass % kPassing != 0);
   // this workgroup's s and tiles of t: a chiplet's workgroups share ranges of t
-  const int64_t total = static_cast<int64_t>(stay_tiles) * a.splits, x = blockIdx.x % 8;
-  const int64_t id = total * x / 8 + blockIdx.x / 8;
+  const int64_t total = static_cast<int64_t>(stay_tiles) * a.splits, x = block % 8;
+  const int64_t id = total * x / 8 + block / 8;
   if (id >= total * (x + 1) / 8) return;
   const int split = static_cast<int>(id / stay_tiles), s0 = static_cast<int>(id % stay_tiles) * kStay + w * (16 * MF);  // the wave's first s
   const int t0 = static_cast<int>(static_cast<int64_t>(pass_tiles) * split / a.splits), t1 = static_cast<int>(static_cast<int64_t>(pass_tiles) * (split + 1) / a.splits);
@@ -232,12 +233,22 @@ __global__ __launch_bounds__(256, 2) void ce_fused_kernel(CeArgs a) {
   }
 }
 
-template <int DT, bool X, bool BIAS>
-tbe_status ce_fused(const CeArgs& a, hipStream_t s) {
-  const int64_t stay = X ? a.rows : a.items;
-  const char* what = X ? "ce_grad_x" : "ce_grad_w";
-  if (a.width <= 64) return ce_launch(ce_fused_kernel<DT, X, 2, 4, BIAS>, what, 256, (stay + 255) / 256 * a.splits, a, s);
-  return ce_launch(ce_fused_kernel<DT, X, 4, 3, BIAS>, what, 256, (stay + 191) / 192 * a.splits, a, s);
+// Both gradients in one launch, the rows' workgroups first: the one's last workgroups run beside the other's first.
+template <int DT, int KS, int MF, bool BIAS>
+__global__ __launch_bounds__(256, 2) void ce_fused_kernel(CeArgs ax, CeArgs aw, unsigned x_groups) {
+  __shared__ __align__(16) uint16_t lds[kRing * (KS / 2) * kPassing * kStepK];
+  __shared__ __align__(16) uint32_t s_more[kRing][4][kPassing];
+  if (blockIdx.x < x_groups) ce_fused_part<DT, true, KS, MF, false>(ax, blockIdx.x, lds, s_more);
+  else ce_fused_part<DT, false, KS, MF, BIAS>(aw, blockIdx.x - x_groups, lds, s_more);
+}
+
+template <int DT, int KS, int MF>
+tbe_status ce_fused(const CeArgs& x, const CeArgs& w, hipStream_t s) {
+  constexpr int kStay = 64 * MF;
+  const int64_t xg = ce_groups((x.rows + kStay - 1) / kStay * x.splits), wg = ce_groups((w.items + int64_t{kStay} - 1) / kStay * w.splits);
+  const unsigned x_groups = static_cast<unsigned>(xg);
+  if (w.bias_part) return ce_launch(ce_fused_kernel<DT, KS, MF, true>, "ce_grads", 256, xg + wg, s, x, w, x_groups);
+  return ce_launch(ce_fused_kernel<DT, KS, MF, false>, "ce_grads", 256, xg + wg, s, x, w, x_groups);
 }
 
 }  // namespace tbe

@@ -3,7 +3,7 @@
 
 namespace tbe {
 template <>
-tbe_status ce_launch_fused<1>(const CeArgs& a, bool x, hipStream_t s) {
-  return x ? ce_fused<1, true, false>(a, s) : a.bias_part ? ce_fused<1, false, true>(a, s) : ce_fused<1, false, false>(a, s);
+tbe_status ce_launch_fused<1>(const CeArgs& x, const CeArgs& w, hipStream_t s) {
+  return w.width <= 64 ? ce_fused<1, 2, 4>(x, w, s) : ce_fused<1, 4, 3>(x, w, s);
 }
 }  // namespace tbe

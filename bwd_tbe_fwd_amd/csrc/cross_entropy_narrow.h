@@ -180,7 +180,7 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
 
 template <int DT, int KS, int MF>
 tbe_status ce_narrow_go(const CeArgs& a, hipStream_t s) {
-  return ce_launch(ce_narrow_kernel<DT, KS, MF>, "ce_logits", 256, (a.rows + 64 * MF - 1) / (64 * MF) * a.splits, a, s);
+  return ce_launch(ce_narrow_kernel<DT, KS, MF>, "ce_logits", 256, (a.rows + 64 * MF - 1) / (64 * MF) * a.splits, s, a);
 }
 template <int DT>
 tbe_status ce_narrow(const CeArgs& a, bool few, hipStream_t s) {

@@ -6,15 +6,15 @@
 
 namespace tbe {
 
-// Workgroup blockIdx.x's place among m_tiles x n_tiles of each share of k: a contiguous part for each chiplet, and in it bands
+// Workgroup `block`'s place among m_tiles x n_tiles of each share of k: a contiguous part for each chiplet, and in it bands
 // of 8 tiles of m walked along n, so that the 32 workgroups that a chiplet runs at once read 8 + 4 tiles of operands and not
 // 1 + 32.  False: none.
 struct TilePlace {
   int m, n, share;
 };
-__device__ __forceinline__ bool tile_place(int64_t m_tiles, int64_t n_tiles, int shares, TilePlace& t) {
-  const int64_t tiles = m_tiles * n_tiles, total = tiles * shares, x = blockIdx.x % 8;
-  int64_t id = total * x / 8 + blockIdx.x / 8;
+__device__ __forceinline__ bool tile_place(int64_t m_tiles, int64_t n_tiles, int shares, unsigned block, TilePlace& t) {
+  const int64_t tiles = m_tiles * n_tiles, total = tiles * shares, x = block % 8;
+  int64_t id = total * x / 8 + block / 8;
   if (id >= total * (x + 1) / 8) return false;
   t.share = static_cast<int>(id / tiles);
   id -= t.share * tiles;
@@ -39,7 +39,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
   const int wm = (w / WN) * (MF * 16), wn = (w % WN) * (NF * 16);
   const int count = *a.r.count;
   TilePlace t;
-  if (!tile_place((count + BM - 1) / BM, (a.items + BN - 1) / BN, 1, t)) return;
+  if (!tile_place((count + BM - 1) / BM, (a.items + BN - 1) / BN, 1, blockIdx.x, t)) return;
   const int m0 = t.m * BM, n0 = t.n * BN;
   const int m_left = count - m0, n_left = a.items - n0;
   OA A;
@@ -142,21 +142,27 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
   }
 }
 
-// The two products of z.  X: the gradient of x, else of the weights.  A chiplet takes whole shares of k where there are many: few
-// rows' weights are then read by one (64 rows, 131072 items of 1000: 61 us, and 85 with each share's tiles dealt to all eight).
-template <int DT, bool X, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void ce_grad_kernel(CeArgs a) {
-  constexpr int T = WM * WN * kWave;
-  constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
+// The two products of z.  X: the gradient of x, else of the weights; `block`: the workgroup among this gradient's.  A chiplet
+// takes whole shares of k where there are many: few rows' weights are then read by one (64 rows, 131072 items of 1000: 61 us,
+// and 85 with each share's tiles dealt to all eight).
+template <bool X, int BM, int BN, int WM, int WN>
+struct GradTile {
+  static constexpr int T = WM * WN * kWave, MF = BM / WM / 16, NF = BN / WN / 16;
   using OA = PanelOperand<X, BM, 4, T, true>;
   using OB = Operand<false, BN, 4 * NF, T, true>;
-  constexpr int kBytes = 2 * 2 * (OA::kElems + OB::kElems);
-  __shared__ __align__(16) char lds[kBytes];
+  static constexpr int kBytes = 2 * 2 * (OA::kElems + OB::kElems);
+};
+template <int DT, bool X, int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void ce_grad_part(const CeArgs& a, unsigned block, char* lds) {
+  using G = GradTile<X, BM, BN, WM, WN>;
+  constexpr int MF = G::MF, NF = G::NF, kBytes = G::kBytes;
+  using OA = typename G::OA;
+  using OB = typename G::OB;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
   const int wm = (w / WN) * (MF * 16), wn = (w % WN) * (NF * 16);
   const int count = *a.r.count, ms = X ? count : a.items, ks = X ? a.items : count;
   TilePlace t;
-  if (!tile_place((ms + BM - 1) / BM, (a.out_width + BN - 1) / BN, a.splits, t)) return;
+  if (!tile_place((ms + BM - 1) / BM, (a.out_width + BN - 1) / BN, a.splits, block, t)) return;
   const int m0 = t.m * BM, n0 = t.n * BN;
   const int m_left = ms - m0, n_left = a.out_width - n0;
   // parts of whole steps
@@ -204,15 +210,29 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
   }
 }
 
-template <typename K>
-tbe_status ce_launch(K* kernel, const char* what, int threads, int64_t tiles, const CeArgs& a, hipStream_t s) {
-  const int64_t groups = (tiles + 7) / 8 * 8;  // for the chiplets' shares
+// Both in one launch, the rows' workgroups first, where their tiles are alike; X: the gradient of x alone, of a tile that the
+// weights' has not.
+template <int DT, bool X, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void ce_grad_kernel(CeArgs ax, CeArgs aw, unsigned x_groups) {
+  constexpr int kX = GradTile<true, BM, BN, WM, WN>::kBytes, kW = GradTile<false, BM, BN, WM, WN>::kBytes;
+  __shared__ __align__(16) char lds[X || kX > kW ? kX : kW];
+  if (X || blockIdx.x < x_groups) {
+    ce_grad_part<DT, true, BM, BN, WM, WN>(ax, blockIdx.x, lds);
+    return;
+  }
+  if constexpr (!X) ce_grad_part<DT, false, BM, BN, WM, WN>(aw, blockIdx.x - x_groups, lds);
+}
+
+inline int64_t ce_groups(int64_t tiles) { return (tiles + 7) / 8 * 8; }  // for the chiplets' shares
+template <typename K, typename... A>
+tbe_status ce_launch(K* kernel, const char* what, int threads, int64_t groups, hipStream_t s, const A&... args) {
+  groups = ce_groups(groups);
   if (groups * threads >= (int64_t{1} << 32)) {
     set_error("cross entropy: %lld tiles are more than a launch takes", static_cast<long long>(groups));
     return TBE_ERR_UNSUPPORTED;
   }
   ProfScope ps(what, s);
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s, a);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s, args...);
   return check_launch(what);
 }
 inline int64_t ce_tiles(int64_t m, int bm, int64_t n, int bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
@@ -220,22 +240,34 @@ inline int64_t ce_tiles(int64_t m, int bm, int64_t n, int bn) { return ((m + bm 
 template <int DT, bool BACK>
 tbe_status ce_logits(const CeArgs& a, int tile, hipStream_t s) {
   const char* what = BACK ? "ce_z" : "ce_logits";
-  if (tile == kTile256) return ce_launch(ce_logits_kernel<DT, BACK, 256, 256, 2, 4, true>, what, 512, ce_tiles(a.rows, 256, a.items, 256), a, s);
-  if (tile == kTile128) return ce_launch(ce_logits_kernel<DT, BACK, 128, 128, 2, 2, true>, what, 256, ce_tiles(a.rows, 128, a.items, 128), a, s);
+  if (tile == kTile256) return ce_launch(ce_logits_kernel<DT, BACK, 256, 256, 2, 4, true>, what, 512, ce_tiles(a.rows, 256, a.items, 256), s, a);
+  if (tile == kTile128) return ce_launch(ce_logits_kernel<DT, BACK, 128, 128, 2, 2, true>, what, 256, ce_tiles(a.rows, 128, a.items, 128), s, a);
   if (tile == kTile64x256)
-    return ce_launch(ce_logits_kernel<DT, BACK, 64, 256, 1, 4, true>, what, 256, ce_tiles(a.rows, 64, a.items, 256), a, s);
-  return ce_launch(ce_logits_kernel<DT, BACK, 64, 64, 2, 2, true>, what, 256, ce_tiles(a.rows, 64, a.items, 64), a, s);
+    return ce_launch(ce_logits_kernel<DT, BACK, 64, 256, 1, 4, true>, what, 256, ce_tiles(a.rows, 64, a.items, 256), s, a);
+  return ce_launch(ce_logits_kernel<DT, BACK, 64, 64, 2, 2, true>, what, 256, ce_tiles(a.rows, 64, a.items, 64), s, a);
 }
-template <int DT, bool X>
-tbe_status ce_grad(const CeArgs& a, int tile, hipStream_t s) {
-  const char* what = X ? "ce_grad_x" : "ce_grad_w";
-  const int64_t m = X ? a.rows : a.items, n = a.out_width;
-  if (tile == kTile256) return ce_launch(ce_grad_kernel<DT, X, 256, 256, 2, 4>, what, 512, ce_tiles(m, 256, n, 256) * a.splits, a, s);
-  if constexpr (X) {
-    if (tile == kTile256x128) return ce_launch(ce_grad_kernel<DT, X, 256, 128, 4, 2>, what, 512, ce_tiles(m, 256, n, 128) * a.splits, a, s);
+// One of them where the other has no shares.
+template <int DT, int BM, int BN, int WM, int WN>
+tbe_status ce_grad(const CeArgs& x, const CeArgs& w, hipStream_t s) {
+  const int64_t xg = ce_groups(ce_tiles(x.rows, BM, x.out_width, BN) * x.splits), wg = ce_groups(ce_tiles(w.items, BM, w.out_width, BN) * w.splits);
+  return ce_launch(ce_grad_kernel<DT, false, BM, BN, WM, WN>, "ce_grads", WM * WN * kWave, xg + wg, s, x, w, static_cast<unsigned>(xg));
+}
+template <int DT>
+tbe_status ce_grads(const CeArgs& x, int x_tile, const CeArgs& w, int w_tile, hipStream_t s) {
+  if (x.splits && w.splits && x_tile != w_tile) {
+    CeArgs none = w;
+    none.splits = 0;
+    const tbe_status st = ce_grads<DT>(x, x_tile, none, x_tile, s);
+    if (st != TBE_OK) return st;
+    none = x;
+    none.splits = 0;
+    return ce_grads<DT>(none, w_tile, w, w_tile, s);
   }
-  if (tile == kTile128) return ce_launch(ce_grad_kernel<DT, X, 128, 128, 2, 2>, what, 256, ce_tiles(m, 128, n, 128) * a.splits, a, s);
-  return ce_launch(ce_grad_kernel<DT, X, 64, 64, 2, 2>, what, 256, ce_tiles(m, 64, n, 64) * a.splits, a, s);
+  const int tile = x.splits ? x_tile : w_tile;
+  if (tile == kTile256) return ce_grad<DT, 256, 256, 2, 4>(x, w, s);
+  if (tile == kTile128) return ce_grad<DT, 128, 128, 2, 2>(x, w, s);
+  if (tile == kTile64) return ce_grad<DT, 64, 64, 2, 2>(x, w, s);
+  return ce_launch(ce_grad_kernel<DT, true, 256, 128, 4, 2>, "ce_grads", 512, ce_tiles(x.rows, 256, x.out_width, 128) * x.splits, s, x, w, 0u);
 }
 
 }  // namespace tbe
