@@ -93,13 +93,28 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
     float columns[LEN];
 #pragma unroll
     for (int c = 0; c < LEN; ++c) columns[c] = 0.0f;
+    // the rows' loads under way together
+    float lses[MF], grads[MF];
+    int targets[MF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      const int m = wm + 16 * i + (l & 15);
+      lses[i] = 0.0f;
+      grads[i] = 0.0f;
+      targets[i] = -1;
+      if (m < m_left) {
+        lses[i] = a.r.lse[m0 + m];
+        targets[i] = a.r.target[m0 + m];
+        if (a.bias_part) grads[i] = a.r.grad[m0 + m];
+      }
+    }
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
       const int m = wm + 16 * i + (l & 15);
       const bool in = m < m_left;
-      const float lse = in ? a.r.lse[m0 + m] : 0.0f;
+      const float lse = lses[i];
       const float base = lse < kFloor ? -kInfinity : fmaf(lse, -kLog2e, shift);  // every item masked: no probability
-      const unsigned at = in ? static_cast<unsigned>(a.r.target[m0 + m] - a.first - n0 - n) : ~0u;
+      const unsigned at = in ? static_cast<unsigned>(targets[i] - a.first - n0 - n) : ~0u;
 #pragma unroll
       for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] = __builtin_amdgcn_exp2f(fmaf(logit(i, c), kLog2e, base));
       if (__any(at < LEN)) {
@@ -114,7 +129,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
           if (n + c >= n_left) acc[i][c / 4][c % 4] = 0.0f;
       }
       if (a.bias_part) {
-        const float g = in ? a.r.grad[m0 + m] / kOne : 0.0f;
+        const float g = grads[i] / kOne;
 #pragma unroll
         for (int c = 0; c < LEN; ++c) columns[c] = in ? fmaf(acc[i][c / 4][c % 4], g, columns[c]) : columns[c];
       }
