@@ -61,6 +61,15 @@ constexpr float kInfinity = __builtin_huge_valf();
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kFloor = -1e38f;  // lower logits count as masked where they would overflow as powers of two
 
+// What the backward's exponentials of base 2 add: -lse in powers of two and `shift` more; no probability where every item is
+// masked.  Past 2^20 the roundings of a logit and of lse may lie powers of two apart, so a little more is taken off than they can
+// be (8 units): no probability overflows.
+__device__ __forceinline__ float ce_reference(float lse, float shift) {
+  if (lse < kFloor) return -kInfinity;
+  const float at = fmaf(lse, -kLog2e, shift), size = fabsf(lse);
+  return size > 0x1p20f ? at - size * 0x1p-21f : at;
+}
+
 // Two parts of a row: their maximum, and the sum of the exponentials less it.
 __device__ __forceinline__ float2 ce_join(float2 a, float2 b) {
   const float top = fmaxf(a.x, b.x), from = top == -kInfinity ? 0.0f : top;

@@ -111,12 +111,14 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
     return;
   }
   if (static_cast<int>(blockIdx.x) >= groups) {
-    // the biases' workgroups.  Finite ones stay finite: the lowest value is no mask where every item has it
+    // the biases' workgroups.  Finite ones stay finite: the lowest value is no mask where every item has it.  Those above 1e38, or
+    // 1e38 scale, count as that: neither they nor their logits overflow as powers of two
     const int64_t end = (b.items + 63) / 64 * 64;
+    const float most = 1e38f * fminf(b.over, 1.0f);
     for (int64_t v = static_cast<int64_t>(blockIdx.x - groups) * kBlock + threadIdx.x; v < end;
          v += static_cast<int64_t>(more) * kBlock) {
       const float x = v >= b.items ? -kInfinity : b.bias ? b.bias[v] : 0.0f, y = x * b.over;
-      b.bias_over[v] = y == -kInfinity && x != y ? -3.4028234664e38f : y;
+      b.bias_over[v] = y == -kInfinity && x != y ? -3.4028234664e38f : y > most && x != kInfinity ? most : y;
     }
     return;
   }
@@ -157,7 +159,7 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
           b.lse[slot] = lse;
           b.grad[slot] = grad;
           if (b.ref) {
-            b.ref[slot] = lse < kFloor ? -kInfinity : fmaf(lse, -kLog2e, DT == 1 ? 15.0f : 0.0f);  // every item masked: no probability
+            b.ref[slot] = ce_reference(lse, DT == 1 ? 15.0f : 0.0f);
             b.part[slot] = top > 0.0f ? grad / top : 0.0f * grad;
           }
         }
@@ -311,18 +313,21 @@ __global__ __launch_bounds__(kBlock) void ce_grad_w_kernel(const float* __restri
 __global__ __launch_bounds__(1024) void ce_grad_bias_kernel(const float* __restrict__ part, int64_t stride, CeBatch b, int bm, int parts,
                                                             float factor, int items, float* __restrict__ gb) {
   __shared__ float s_sum[16][kWave];
-  const int q = threadIdx.x / kWave, l = lane_id();
-  const int v = blockIdx.x * kWave + l, tiles = bm ? (*b.count + bm - 1) / bm : parts;
-  float sum = 0.0f;
-  if (v < items) {
+  const int q = threadIdx.x / kWave, l = lane_id(), tiles = bm ? (*b.count + bm - 1) / bm : parts;
+  for (int64_t v0 = static_cast<int64_t>(blockIdx.x) * kWave; v0 < items; v0 += static_cast<int64_t>(gridDim.x) * kWave) {
+    const int64_t v = v0 + l;
+    float sum = 0.0f;
+    if (v < items) {
 #pragma unroll 4
-    for (int t = q; t < tiles; t += 16) sum += part[t * stride + v];
+      for (int t = q; t < tiles; t += 16) sum += part[t * stride + v];
+    }
+    __syncthreads();
+    s_sum[q][l] = sum;
+    __syncthreads();
+    if (q || v >= items) continue;
+    for (int k = 1; k < 16; ++k) sum += s_sum[k][l];
+    gb[v] = bm ? sum : sum * (factor * *b.largest);
   }
-  s_sum[q][l] = sum;
-  __syncthreads();
-  if (q || v >= items) return;
-  for (int k = 1; k < 16; ++k) sum += s_sum[k][l];
-  gb[v] = bm ? sum : sum * (factor * *b.largest);
 }
 
 // ---------------------------------------------------------------------------
@@ -680,7 +685,8 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
     if (st == TBE_OK && grad_weight && w_pick.splits > 1) st = launch_grad_w_sum(to_w, f16, b.largest, s);
     if (st == TBE_OK && grad_bias) {
       ProfScope ps("ce_grad_bias", s);
-      hipLaunchKernelGGL(ce_grad_bias_kernel, dim3(static_cast<unsigned>((a.items + kWave - 1) / kWave)), dim3(1024), 0, s, bias_part,
+      const int64_t groups = hmin((static_cast<int64_t>(a.items) + kWave - 1) / kWave, 1 << 20);  // a launch has fewer than 2^32 threads
+      hipLaunchKernelGGL(ce_grad_bias_kernel, dim3(static_cast<unsigned>(groups)), dim3(1024), 0, s, bias_part,
                          a.bias_stride, b, bias_rows, narrow ? w_pick.splits : 0, 1.0f / unit, a.items, grad_bias + first);
       st = check_launch("ce_grad_bias");
     }

@@ -123,6 +123,8 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
       for (int i = 0; i < MF; ++i) {
         float now = fmaxf(top[i], kFloor);
         asm volatile("" : "+v"(now));  // keeps what follows from being worked out where it is not needed
+        // far out, above the largest by more than a product's rounding: no exponential overflows
+        if (fabsf(now) * unit > 0x1p20f && now > kFloor) now += fabsf(now) * 0x1p-22f;
         sum[i] *= __builtin_amdgcn_exp2f((ref[i] - now) * unit);
         ref[i] = now;
       }
@@ -166,7 +168,8 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
   wait_loads<0>();  // nothing is on its way into LDS when the workgroup ends
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
-    // the lanes that share a row; where no logit was above kFloor the sum is 0 and the maximum tells what there was
+    // the lanes that share a row; where no logit was above kFloor the sum is 0 and the maximum tells what there was (far out the
+    // sum may be 0 too: the reference is the largest but for 2^-22 of it)
     const int m = m0 + 16 * i + (l & 15);
     float all = fmaxf(ref[i], __shfl_xor(ref[i], 16)), most = fmaxf(top[i], __shfl_xor(top[i], 16));
     all = fmaxf(all, __shfl_xor(all, 32));

@@ -112,8 +112,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
     for (int i = 0; i < MF; ++i) {
       const int m = wm + 16 * i + (l & 15);
       const bool in = m < m_left;
-      const float lse = lses[i];
-      const float base = lse < kFloor ? -kInfinity : fmaf(lse, -kLog2e, shift);  // every item masked: no probability
+      const float base = ce_reference(lses[i], shift);
       const unsigned at = in ? static_cast<unsigned>(targets[i] - a.first - n0 - n) : ~0u;
 #pragma unroll
       for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] = __builtin_amdgcn_exp2f(fmaf(logit(i, c), kLog2e, base));

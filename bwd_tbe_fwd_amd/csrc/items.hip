@@ -74,6 +74,11 @@ tbe_status check_loss(int64_t rows, int64_t items, int64_t width, const void* x,
     set_error("cross entropy: scale is not finite");
     return TBE_ERR_ARG;
   }
+  const float size = scale < 0.0f ? -scale : scale;  // biases are divided by it
+  if (size != 0.0f && (size < 0x1p-64f || size > 0x1p64f)) {
+    set_error("cross entropy: scale %g (0, or from 2^-64 to 2^64)", static_cast<double>(scale));
+    return TBE_ERR_UNSUPPORTED;
+  }
   tbe_status st = check_matrix("x", x, dtype, rows, width, x_stride);
   if (st == TBE_OK) st = check_matrix("weight", weight, dtype, items, width, weight_stride);
   if (st == TBE_OK && bias) st = check_matrix("bias", bias, TBE_F32, 1, items, items);

@@ -74,10 +74,14 @@ tbe_status tbe_lookup_backward(int64_t num_ids, int64_t items, int64_t width, co
  * bias is -infinity is masked: its probability is 0, and the loss of a row
  * with such a target is +infinity; a row with every item masked has lse
  * -infinity.  A row with an infinity or a NaN gives NaN (or an infinity) in
- * that row only.  Products, maxima and sums are kept in fp32; the logits go
- * through registers, a tile of items at a time, and are never stored.  rows may
- * be 0 and at most TBE_CROSS_ENTROPY_MAX_ROWS; 1 <= items < 2^31 - 1;
- * 1 <= width <= TBE_CROSS_ENTROPY_MAX_WIDTH.  workspace: at least
+ * that row only.  scale is 0 or from 2^-64 to 2^64, of either sign.  Finite
+ * biases are meant to be masks (of the lowest value) or below 1e38 and 1e38
+ * |scale|; higher ones count as that.  Products, maxima and sums are kept in
+ * fp32; where logits past 2^20 in size have no digits left behind the point,
+ * losses and probabilities still stay finite.  The logits go through registers,
+ * a tile of items at a time, and are never stored.  rows may be 0 and at most
+ * TBE_CROSS_ENTROPY_MAX_ROWS; 1 <= items < 2^31 - 1; 1 <= width <=
+ * TBE_CROSS_ENTROPY_MAX_WIDTH.  workspace: at least
  * tbe_cross_entropy_forward_workspace_bytes bytes, 256-byte aligned; the bytes
  * grow with the rows, so one for the largest batch serves every smaller one.
  */
@@ -102,9 +106,11 @@ tbe_status tbe_cross_entropy_forward(int64_t rows, int64_t items, int64_t width,
  * for rows without a target).  The logits are computed again, a piece of the
  * items at a time.  exp(...) - [...] is rounded to dtype for its two products,
  * as x times grad_loss over the largest |grad_loss| is (exactly x where all
- * are equal); sums are kept in fp32 and rounded once.  In fp16 probabilities
- * keep their digits down to 2^-29, and the weights' gradient those of rows
- * whose |grad_loss| is not below 2^-14 of the largest.
+ * are equal); rows of up to 128 columns have exp(...) - [...] times grad_loss
+ * over the largest rounded instead for the weights' gradient.  Sums are kept in
+ * fp32 and rounded once.  In fp16 probabilities keep their digits down to
+ * 2^-29, and the weights' gradient those of rows whose |grad_loss| is not below
+ * 2^-14 of the largest.
  */
 size_t tbe_cross_entropy_backward_workspace_bytes(int64_t rows, int64_t items, int64_t width);
 tbe_status tbe_cross_entropy_backward(int64_t rows, int64_t items, int64_t width, const void* x,

@@ -95,3 +95,59 @@ def test_two_streams_with_a_workspace_each():
             e_gx, e_gw, _ = backward(x[k], w, None, t[k], 1.0, e_lse, grad, with_bias=False)
             for a, b in zip((loss[k], lse[k], gx[k], gw[k]), (e_loss, e_lse, e_gx, e_gw)):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("width", [64, 200])
+def test_scales_and_biases_at_their_ends(width):
+    rows, items = 70, 500
+    x, w, t = matrix(rows, width, BF16, 1), matrix(items, width, BF16, 2, width ** -0.5), some_targets(rows, items, 0.2, 3)
+    grad = torch.ones(rows, device="cuda")
+    for scale, size in ((2.0 ** -64, 1.0), (-2.0 ** -40, 0.1), (2.0 ** 12, 500.0)):
+        bias = matrix(1, items, torch.float32, 4, size)[0]
+        exact = Exact(x, w, bias, t, scale)
+        loss, lse = forward(x, w, bias, t, scale)
+        exact.check_forward(loss, lse)
+        exact.check_backward(grad, *backward(x, w, bias, t, scale, lse, grad))
+    for scale in (2.0 ** 64, -2.0 ** 45, 2.0 ** 31, 2.0 ** 25, 2.0 ** 20):  # logits without digits behind the point
+        exact = Exact(x, w, None, t, scale)
+        loss, lse = forward(x, w, None, t, scale)
+        exact.check_forward(loss, lse)
+        gx, gw, gb = backward(x, w, None, t, scale, lse, grad)
+        # a probability is 1 but for the roundings of lse and the logit, 8 units of it at most
+        assert bool(gb.isfinite().all()) and float(gb.abs().max()) <= rows * 2
+        if abs(scale) < 2.0 ** 40:
+            assert bool(gx.isfinite().all()) and bool(gw.isfinite().all())
+    # biases that are out of range once divided by the scale count as 1e38 of it
+    bias = torch.zeros(items, device="cuda")
+    bias[7], bias[9] = torch.finfo(torch.float32).max, torch.finfo(torch.float32).min
+    loss, lse = forward(x, w, bias, t, 0.25)
+    assert bool(loss.isfinite().all()) and bool(lse.isfinite().all()) and bool((lse[(t >= 0) & (t < items)] >= 2.4e37).all())
+
+
+def test_items_past_the_threads_of_a_launch():
+    """2^28 + 70 items: their biases' gradients take more than a launch of a workgroup for every 64."""
+    rows, items, width = 3, (1 << 28) + 70, 8
+    w = torch.empty(items, width, dtype=BF16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    x, t = matrix(rows, width, BF16, 2), torch.tensor([items - 1, 0, 5], device="cuda")
+    grad = torch.tensor([1.0, -2.0, 0.5], device="cuda")
+    loss, lse = forward(x, w, None, t, 1.0)
+    gb = torch.empty(items, device="cuda")
+    ws = tbe.workspace(tbe.tbe_cross_entropy_backward_workspace_bytes(rows, items, width))
+    tbe.tbe_cross_entropy_backward(x, w, None, t, 1.0, lse, grad, None, None, gb, ws)
+    part = 1 << 25
+    total = torch.zeros(rows, dtype=torch.float64, device="cuda")
+    for v in range(0, items, part):
+        total += (w[v:v + part].double() @ x.double().t()).exp().sum(0)
+    exact = total.log()
+    # sums of e^l with chains of fewer than 256 + items / 2048 additions of values off by 4 + 3 |l - lse| < 100 roundings
+    assert bool(((lse.double() - exact).abs() <= (400 + items / 2048) * 2.0 ** -24).all())
+    for v in (0, part, 5 * part, items - 70):
+        some = w[v:v + 4096].double()
+        p = (some @ x.double().t() - exact).exp()
+        z = p.clone()
+        for i in range(rows):
+            if v <= int(t[i]) < v + 4096:
+                z[int(t[i]) - v, i] -= 1
+        z *= grad.double()
+        tol = (p * grad.abs().double()).sum(1) * (600 + items / 2048) * 2.0 ** -24 + 8 * 2.0 ** -24 * z.abs().sum(1) + 1e-37
+        assert bool(((gb[v:v + 4096].double() - z.sum(1)).abs() <= tol).all())

@@ -159,3 +159,12 @@ def test_loss_binding_checks_shapes_and_types(monkeypatch):
                        (lambda: backward(gw=w.half()), "grad_weight is not"), (lambda: backward(gb=torch.zeros(4)), "grad_bias has shape")):
         with pytest.raises(tbe.TbeError, match=word):
             call()
+
+
+def test_cross_entropy_scales():
+    need = tbe.tbe_cross_entropy_forward_workspace_bytes(4, 5, 8)
+    for scale in (2.0 ** -65, -2.0 ** -100, 1e-40, 2.0 ** 65, -3e38):
+        assert loss_forward(scale=scale) == UNSUPPORTED and b"scale" in error()
+        assert loss_backward(scale=scale) == UNSUPPORTED and b"scale" in error()
+    for scale in (0.0, 2.0 ** -64, -2.0 ** 64):  # what comes after the scale is looked at
+        assert loss_forward(scale=scale, nb=need - 1) == WORKSPACE
