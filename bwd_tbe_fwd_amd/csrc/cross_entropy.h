@@ -1,13 +1,20 @@
 // Softmax cross entropy over all items of a table: what its kernels share.  Declarations and the meaning of every argument
 // are in include/tbe_items.h.
 //
+//   l_iv = s (x_i . w_v) + b_v,  lse_i = log sum_v exp l_iv,  loss_i = lse_i - l_it;   p_iv = exp(l_iv - lse_i)
+//   z_iv = p_iv - [v = t_i];  dx_i = s g_i sum_v z_iv w_v,  dw_v = s sum_i g_i z_iv x_i,  db_v = sum_i g_i z_iv
+//
 // The rows that have a target are copied side by side first (their count stays on the device): a batch's padding costs no
-// products, and every row starts on 16 bytes.  Weights whose rows do not are copied too, a piece at a time.  Then, C(m, n) = sum_k A(m, k) B(n, k) as in tile_products.h:
+// products, and every row starts on 16 bytes.  Weights whose rows do not are copied too, a piece at a time.  Then, with
+// C(m, n) = sum_k A(m, k) B(n, k) as in tile_products.h:
 //   logits            m = row,  n = item,   k = column: A = x, B = weight, both along
 //   gradient of x     m = row,  n = column, k = item:   A = z along, B = weight across
 //   of the weights    m = item, n = column, k = row:    A = z across, B = x * grad_loss across
 // Forward, the logits' tile ends in each row's maximum and sum of exponentials over the tile's items.  Backward, it ends in
-// z, 16 bits each, for a piece of the items: small enough for the Infinity Cache, large enough for its two products.
+// z, 16 bits each, for a piece of the items: small enough for the Infinity Cache, large enough for its two products.  Rows of
+// up to 128 columns have kernels of their own in both directions (cross_entropy_narrow.h, cross_entropy_fused.h).
+// z in 16 bits is what the matrix instructions take; the row's loss weight is applied in fp32 to the sums of dx, and to x's copy
+// for dw, so that z, between -1 and 1, needs no range of its own (fp16: times 2^15, kUnit).
 #pragma once
 
 #include "items.h"

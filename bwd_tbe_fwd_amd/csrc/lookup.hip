@@ -40,7 +40,9 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int id64, int64_t i) {
   return id64 ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
 }
 
-// A group of G lanes takes kFlight rows, a workgroup consecutive ones.
+// A group of G lanes takes kFlight rows, a workgroup consecutive ones.  Bound by memory: 1 M ids, 128 columns fp16 to bf16, 0.1 of
+// them padding: 84 us, 4.5 TB/s of the bytes that differ and 6.2 of all that are read and written (loads and stores of 16
+// bytes, y past the caches).
 template <int WT, int YT, int G, bool WHOLE>
 __global__ __launch_bounds__(kBlock) void lookup_forward_kernel(LookupArgs a) {
   using S = typename Fmt<WT>::S;
@@ -91,8 +93,8 @@ __global__ __launch_bounds__(kBlock) void lookup_keys_kernel(const void* ids, in
 }
 
 // Up to kRankMost ids: an id's place is the number of smaller ones and of equal ones before it.  A workgroup places 64
-// ids, each of its 4 waves counts a quarter of all of them.  One launch of a few microseconds, where the radix sort takes
-// ten launches.  (512 ids.)
+// ids, each of its 4 waves counts a quarter of all of them.  One launch, 8 us with 517 ids, where the radix sort takes
+// seven to ten of 4 us and more.
 __global__ __launch_bounds__(kBlock) void lookup_rank_kernel(const void* ids, int id64, int n, int64_t items,
                                                              uint32_t* __restrict__ keys, uint32_t* __restrict__ pay,
                                                              int32_t* __restrict__ n_sorted) {
