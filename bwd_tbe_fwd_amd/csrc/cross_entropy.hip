@@ -73,7 +73,8 @@ __global__ __launch_bounds__(kBlock) void ce_count_kernel(CeBatch b) {
 }
 
 // Weights whose rows do not start on 16 bytes, or are not whole 16 bytes: a piece's items at a pitch that is, zeros behind the
-// width.  A wave a row; workgroup `block` of `blocks`.
+// width.  16 bytes a lane, rows one after the other; workgroup `block` of `blocks`.  213712 rows of 15: 11 us beside the batch's
+// rows, where a wave a row took 37.
 struct CePad {
   const uint16_t* from;
   int64_t stride;
@@ -81,13 +82,12 @@ struct CePad {
   uint16_t* to;
 };
 __device__ __forceinline__ void ce_pad_rows(const CePad& p, unsigned block, unsigned blocks) {
-  const int l = lane_id();
-  for (int64_t v = static_cast<int64_t>(block) * kWavesPerBlock + (threadIdx.x >> 6); v < p.items; v += static_cast<int64_t>(blocks) * kWavesPerBlock) {
-    for (int d = l * 8; d < p.pitch; d += kWave * 8) {
-      Vec<uint16_t, 8> x;
-      load_vec_part<uint16_t, 8>(p.from + v * p.stride + d, p.width - d, x);
-      store_vec_any<uint16_t, 8>(p.to + v * p.pitch + d, x);
-    }
+  const unsigned each = p.pitch / 8, all = p.items * each;  // a piece's are fewer than 2^24
+  for (unsigned k = block * kBlock + threadIdx.x; k < all; k += blocks * kBlock) {
+    const unsigned v = k / each, d = k % each * 8;
+    Vec<uint16_t, 8> x;
+    load_vec_part<uint16_t, 8>(p.from + v * p.stride + d, p.width - static_cast<int>(d), x);
+    store_vec_any<uint16_t, 8>(p.to + static_cast<int64_t>(k) * 8, x);
   }
 }
 __global__ __launch_bounds__(kBlock) void ce_pad_kernel(CePad p) { ce_pad_rows(p, blockIdx.x, gridDim.x); }
@@ -290,6 +290,30 @@ __global__ __launch_bounds__(kBlock) void ce_grad_x_kernel(const CeBatch b, cons
   }
 }
 
+// The same for few rows with many parts: a workgroup a row, `lanes` lanes (a power of two) hold its columns, 4 each, and the
+// groups of them a part each at a time.
+template <int DT>
+__global__ __launch_bounds__(1024) void ce_grad_x_each_kernel(const CeBatch b, const float* __restrict__ sum, int64_t pitch, int splits, int width, int lanes,
+                                                              float factor, uint16_t* __restrict__ gx, int64_t stride) {
+  __shared__ f32x4 s_sum[1024];
+  const int q = threadIdx.x / lanes, d = threadIdx.x % lanes * 4, groups = 1024 / lanes;
+  const int64_t i = blockIdx.x, c = b.slot[i];
+  f32x4 all = {0, 0, 0, 0};
+  if (c >= 0 && d < width && q < splits) all = sum_parts(sum + (q * b.rows + c) * pitch + d, groups * b.rows * pitch, (splits - q + groups - 1) / groups);
+  s_sum[threadIdx.x] = all;
+  __syncthreads();
+  for (int n = groups / 2; n > 0; n /= 2) {
+    if (q < n) s_sum[threadIdx.x] += s_sum[threadIdx.x + n * lanes];
+    __syncthreads();
+  }
+  if (q || d >= width) return;
+  const float g = c >= 0 ? b.grad[c] * factor : 0.0f;
+  Vec<uint16_t, 4> out;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out.e[e] = c >= 0 ? tower_from_f<DT>(s_sum[threadIdx.x][e] * g) : static_cast<uint16_t>(0);
+  store_vec_part<uint16_t, 4>(gx + i * stride + d, width - d, out);
+}
+
 // The weights' gradients of a piece whose rows were shared.
 template <int DT>
 __global__ __launch_bounds__(kBlock) void ce_grad_w_kernel(const float* __restrict__ sum, int64_t pitch, int splits, int items, int width, float scale,
@@ -337,9 +361,17 @@ __global__ __launch_bounds__(1024) void ce_grad_bias_kernel(const float* __restr
 constexpr int64_t kPartBytes = int64_t{64} << 20;    // forward: of the rows' maxima and sums over a piece's tiles
 constexpr int64_t kZElems = int64_t{1} << 27;        // backward: of z
 constexpr int64_t kLeastPiece = 1024, kMostPiece = 131072;  // items of a piece, backward
-constexpr int64_t kCopyBytes = int64_t{32} << 20;    // of a piece's weights, copied: read again from the caches
+// Of a piece's weights, copied: read again from the caches.  At least the first, and up to the second where the workspace has no
+// more than its share without them (few rows, whose small pieces would leave CUs idle: 439 rows, 543790 items of 1363 backward
+// 5.0 -> 3.7 ms).
+constexpr int64_t kCopyBytes = int64_t{32} << 20, kCopyMost = int64_t{128} << 20;
+constexpr int64_t kForwardShare = int64_t{110} << 20, kBackwardShare = int64_t{600} << 20;
 constexpr int64_t kSumBytes = int64_t{128} << 20;    // of the sums over shares of k, beyond one share of x's gradient
 constexpr int kMostSplits = 64;
+// Of the items, for the gradient of so few narrow rows that their sums are joined by a workgroup each (17 rows, 693510 items of
+// 13: 245 us with 64 shares, 76 with up to 512; 64 rows of 1000, 64 shares: 20 us by waves, 7 by workgroups).
+constexpr int kMostFew = 512;
+constexpr int64_t kFewRows = 1024;
 
 // Rows of up to so many columns stay in registers (cross_entropy_narrow.h).
 constexpr int64_t kNarrowWidth = 128;
@@ -363,6 +395,16 @@ struct CeLayout {
   size_t ref, part_of;                      // backward, narrow rows
   size_t total;
 };
+// The last to be carved.  Bytes never shrink with the rows here either: max(others + 32 MB, min(others + 128 MB, share)), or what
+// all items or kLeastPiece of them take.
+void carve_copies(CeLayout& L, Carve& c, int64_t items, int64_t share) {
+  const int64_t most = hmax(kCopyBytes, hmin(kCopyMost, share - static_cast<int64_t>(c.at)));
+  // whether it is asked for depends on addresses and strides
+  const int64_t all = up(items, 256), row = 2 * L.pitch;
+  L.copied = hmin(all, hmax(kLeastPiece, most / row / 256 * 256));
+  L.wc = c.take(hmax(hmin(most, all * row), hmin(all, kLeastPiece) * row));
+  L.total = c.at;
+}
 void carve_rows(CeLayout& L, Carve& c, int64_t rows, int64_t items, int64_t width) {
   const int64_t blocks = (rows + kBlock - 1) / kBlock;
   L.pitch = up(width, 8);
@@ -374,9 +416,6 @@ void carve_rows(CeLayout& L, Carve& c, int64_t rows, int64_t items, int64_t widt
   L.target = c.take(up(rows, 64) * 4);
   L.xc = c.take(rows * L.pitch * 2);
   L.bias_over = c.take(width <= kNarrowWidth ? up(items, 64) * 4 : 0);
-  // whether it is asked for depends on addresses and strides
-  L.copied = hmin(up(items, 256), hmax(kLeastPiece, kCopyBytes / (2 * L.pitch) / 256 * 256));
-  L.wc = c.take(L.copied * L.pitch * 2);
 }
 CeLayout forward_layout(int64_t rows, int64_t items, int64_t width) {
   CeLayout L = {};
@@ -387,12 +426,12 @@ CeLayout forward_layout(int64_t rows, int64_t items, int64_t width) {
   L.part = c.take(hmin(rows * (up(items, 256) / 64) * 8, hmax(kPartBytes, rows * 4 * 8)));
   L.picked = c.take(rows * 4);
   L.all = c.take(rows * 8);
-  L.total = c.at;
+  carve_copies(L, c, items, kForwardShare);
   return L;
 }
 int64_t sum_x_bytes(int64_t rows, int64_t width) {
   const int64_t one = rows * up(width, 4) * 4;
-  return hmax(one, hmin(kSumBytes, kMostSplits * one));
+  return hmax(one, hmin(kSumBytes, (width <= kNarrowWidth ? kMostFew : kMostSplits) * one));
 }
 CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   CeLayout L = {};
@@ -413,7 +452,7 @@ CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   L.bias_part = c.take(narrow ? items * 4 + kSumBytes / 4 : z / 64 * 4 + most * 4);
   L.ref = c.take(up(rows, 64) * 4);
   L.part_of = c.take(up(rows, 64) * 4);
-  L.total = c.at;
+  carve_copies(L, c, items, kBackwardShare);
   return L;
 }
 
@@ -461,7 +500,7 @@ int narrow_splits(int64_t rows, int64_t items, bool few) {
 // Into how many shares the passing side of the fused kernels goes.  The fullest CU's workgroups count, two at a time in the time
 // of a pair, one alone in 0.7 of it; four tiles a share at least.  A share more costs its sums, which are written, read and added.
 int fused_splits(int64_t stay_tiles, int64_t pass, double pair_us, double share_bytes, int64_t most) {
-  const int64_t tiles = (pass + 63) / 64, end = hmax(1, hmin(hmin(kMostSplits, tiles / 4), most));
+  const int64_t tiles = (pass + 63) / 64, end = hmax(1, hmin(tiles / 4, most));
   int best = 1;
   double least = -1.0;
   for (int n = 1; n <= end; ++n) {
@@ -479,6 +518,10 @@ int fused_splits(int64_t stay_tiles, int64_t pass, double pair_us, double share_
 bool whole_16(const void* p, int64_t stride, int64_t width) {
   return !(reinterpret_cast<uintptr_t>(p) & 15) && stride % 8 == 0 && width % 8 == 0 && stride < (int64_t{1} << 21);
 }
+
+// Forward, rows of up to so many go without a copy of the weights (kTile64 through registers): 123 rows, 110262 items of 861: 68
+// us, and 113 with copies; 250 rows 120 and 134; 500 rows 226 and 190.
+constexpr int64_t kRegisterRows = 256;
 
 // One CeBatch for both directions.  A negative scale of narrow rows goes into x (their kernel looks for the largest product),
 // and so does 0, by which no bias can be divided.
@@ -504,7 +547,7 @@ CeBatch batch_of(char* ws, const CeLayout& L, int64_t rows, int64_t items, int64
   }
   return b;
 }
-int pad_groups(const CePad& p) { return static_cast<int>(hmin((static_cast<int64_t>(p.items) + 3) / 4, 16384)); }
+int pad_groups(const CePad& p) { return static_cast<int>(hmin((static_cast<int64_t>(p.items) * (p.pitch / 8) + kBlock - 1) / kBlock, 16384)); }
 tbe_status launch_rows(const CeBatch& b, int dtype, const CePad& pad, hipStream_t s) {
   const bool counted = b.rows > kCountHere;
   ProfScope ps("ce_rows", s);
@@ -550,7 +593,7 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
   const CeLayout L = forward_layout(rows, items, width);
   char* ws = static_cast<char*>(workspace);
   const bool narrow = width <= kNarrowWidth, few = rows <= 64, f16 = dtype == TBE_F16;
-  const bool on_16 = whole_16(weight, weight_stride, width), copy = !on_16 && (narrow || !few), direct = on_16 || copy;
+  const bool on_16 = whole_16(weight, weight_stride, width), copy = !on_16 && (narrow || rows > kRegisterRows), direct = on_16 || copy;
   CeBatch b = batch_of(ws, L, rows, items, width, x, x_stride, targets, target_type, bias, narrow, scale);
   b.w = static_cast<const uint16_t*>(weight); b.w_stride = weight_stride;
   b.picked = reinterpret_cast<float*>(ws + L.picked);
@@ -658,7 +701,8 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
       // the same shares for every piece: their sums go on
       if (first == 0 && narrow) {
         const int64_t share = rows * a.sum_pitch * 4;
-        x_pick.splits = fused_splits((rows + stay - 1) / stay, a.items, pair_us, static_cast<double>(share), sum_x_bytes(rows, width) / share);
+        x_pick.splits = fused_splits((rows + stay - 1) / stay, a.items, pair_us, static_cast<double>(share),
+                                     hmin(sum_x_bytes(rows, width) / share, rows <= kFewRows ? kMostFew : kMostSplits));
       }
       if (first == 0 && !narrow) x_pick = pick_tile(kGradX, rows, a.sum_pitch, a.items, kMostSplits, sum_x_bytes(rows, width), x_shares_us);
       to_x.sum = reinterpret_cast<float*>(ws + L.sum_x);
@@ -668,7 +712,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
     if (grad_weight || (grad_bias && narrow)) {
       if (narrow) {
         const int64_t share = a.items * a.sum_pitch * 4;
-        w_pick.splits = fused_splits((a.items + stay - 1) / stay, rows, pair_us, static_cast<double>(share), kSumBytes / share);
+        w_pick.splits = fused_splits((a.items + stay - 1) / stay, rows, pair_us, static_cast<double>(share), hmin(kMostSplits, kSumBytes / share));
       } else {
         w_pick = pick_tile(kWeightTiles, a.items, a.sum_pitch, rows, kMostSplits, kSumBytes, weight_shares_us);
       }
@@ -693,6 +737,14 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   }
   if (st != TBE_OK || !grad_x) return st;
   ProfScope ps("ce_grad_x_sum", s);
+  if (rows <= kFewRows && x_pick.splits >= 32 && width <= 1024) {
+    int lanes = 1;
+    while (lanes * 4 < width) lanes *= 2;
+    auto each = f16 ? ce_grad_x_each_kernel<1> : ce_grad_x_each_kernel<2>;
+    hipLaunchKernelGGL(each, dim3(static_cast<unsigned>(rows)), dim3(1024), 0, s, b, reinterpret_cast<const float*>(ws + L.sum_x), a.sum_pitch,
+                       x_pick.splits, static_cast<int>(width), lanes, x_factor, static_cast<uint16_t*>(grad_x), grad_x_stride);
+    return check_launch("ce_grad_x_sum");
+  }
   auto kernel = f16 ? ce_grad_x_kernel<1> : ce_grad_x_kernel<2>;
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(hmin((rows + 3) / 4, 8192))), dim3(kBlock), 0, s, b,
                      reinterpret_cast<const float*>(ws + L.sum_x), a.sum_pitch, x_pick.splits, static_cast<int>(width), x_factor,

@@ -151,3 +151,11 @@ def test_items_past_the_threads_of_a_launch():
         z *= grad.double()
         tol = (p * grad.abs().double()).sum(1) * (600 + items / 2048) * 2.0 ** -24 + 8 * 2.0 ** -24 * z.abs().sum(1) + 1e-37
         assert bool(((gb[v:v + 4096].double() - z.sum(1)).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("rows,items,width,dtype,stride", [
+    (17, 69351, 13, BF16, 13), (1, 200000, 5, F16, 7), (1024, 40000, 20, F16, 24), (1025, 40000, 20, BF16, 21),
+    (40, 90001, 1000, BF16, 1000), (256, 9001, 301, F16, 301), (257, 9001, 301, F16, 301), (30, 40003, 1024, BF16, 1027),
+    (30, 40003, 1030, BF16, 1030)])
+def test_many_shares_of_the_items(rows, items, width, dtype, stride):
+    one_case(rows, items, width, dtype, stride=stride)
