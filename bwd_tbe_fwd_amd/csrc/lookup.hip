@@ -19,7 +19,7 @@ namespace tbe {
 namespace {
 
 constexpr int kFlight = 4;       // forward: rows of a group of lanes whose loads are under way together
-constexpr int kRankMost = 4096;  // ids that are sorted by counting, in one launch
+constexpr int kRankMost = 8192;  // ids that are sorted by counting, in one launch
 
 // ---------------------------------------------------------------------------
 // forward
@@ -92,17 +92,19 @@ __global__ __launch_bounds__(kBlock) void lookup_keys_kernel(const void* ids, in
   pay[i] = static_cast<uint32_t>(i);
 }
 
-// Up to kRankMost ids: an id's place is the number of smaller ones and of equal ones before it.  A workgroup places 64
-// ids, each of its 4 waves counts a quarter of all of them.  One launch, 8 us with 517 ids, where the radix sort takes
-// seven to ten of 4 us and more.
-__global__ __launch_bounds__(kBlock) void lookup_rank_kernel(const void* ids, int id64, int n, int64_t items,
-                                                             uint32_t* __restrict__ keys, uint32_t* __restrict__ pay,
-                                                             int32_t* __restrict__ n_sorted) {
+// Up to kRankMost ids: an id's place is the number of smaller ones and of equal ones before it.  A workgroup places 64 ids, each
+// of its 16 waves counts a sixteenth of all of them.  One launch, where the radix sort takes seven to ten of 4 us and more: a
+// call with 4096 ids added to rows of 64 columns takes 35 us (67 with 4 waves and two comparisons an id), 8190 48 (54 by the
+// sort), 12000 57 (54).
+constexpr int kRankWaves = 16;
+__global__ __launch_bounds__(kRankWaves * kWave) void lookup_rank_kernel(const void* ids, int id64, int n, int64_t items,
+                                                                         uint32_t* __restrict__ keys, uint32_t* __restrict__ pay,
+                                                                         int32_t* __restrict__ n_sorted) {
   __shared__ __align__(16) uint32_t s_key[kRankMost];
-  __shared__ int s_rank[kWavesPerBlock][kWave];
-  const int n4 = (n + 15) / 16 * 16;  // a whole number of fours for each wave
+  __shared__ int s_rank[kRankWaves][kWave];
+  const int n4 = (n + 4 * kRankWaves - 1) / (4 * kRankWaves) * (4 * kRankWaves);  // a whole number of fours for each wave
   int valid = 0;
-  for (int i = threadIdx.x; i < n4; i += kBlock) {
+  for (int i = threadIdx.x; i < n4; i += kRankWaves * kWave) {
     const int64_t id = i < n ? id_at(ids, id64, i) : -1;
     const bool in = static_cast<uint64_t>(id) < static_cast<uint64_t>(items);
     s_key[i] = i < n ? static_cast<uint32_t>(in ? id : items) : ~0u;  // behind all others
@@ -113,16 +115,19 @@ __global__ __launch_bounds__(kBlock) void lookup_rank_kernel(const void* ids, in
   const int mine = blockIdx.x * kWave + l;
   const uint32_t k = mine < n ? s_key[mine] : ~0u;
   int rank = 0;
-  const int part = n4 / kWavesPerBlock;
+  const int part = n4 / kRankWaves;
+#pragma unroll 2
   for (int j = w * part; j < (w + 1) * part; j += 4) {
     const u32x4 v = *reinterpret_cast<const u32x4*>(s_key + j);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) rank += v[e] < k || (v[e] == k && j + e < mine) ? 1 : 0;
+    for (int e = 0; e < 4; ++e) rank += v[e] < k + (j + e < mine ? 1u : 0u) ? 1 : 0;  // of the equal ones those before
   }
   s_rank[w][l] = rank;
   __syncthreads();
   if (w == 0 && mine < n) {
-    rank = s_rank[0][l] + s_rank[1][l] + s_rank[2][l] + s_rank[3][l];
+    rank = 0;
+#pragma unroll
+    for (int q = 0; q < kRankWaves; ++q) rank += s_rank[q][l];
     keys[rank] = k;
     pay[rank] = static_cast<uint32_t>(mine);
   }
@@ -131,7 +136,11 @@ __global__ __launch_bounds__(kBlock) void lookup_rank_kernel(const void* ids, in
   for (int d = 1; d < kWave; d <<= 1) valid += __shfl_xor(valid, d);
   if (l == 0) s_rank[0][w] = valid;
   __syncthreads();
-  if (threadIdx.x == 0) *n_sorted = s_rank[0][0] + s_rank[0][1] + s_rank[0][2] + s_rank[0][3];
+  if (threadIdx.x == 0) {
+    int all = 0;
+    for (int q = 0; q < kRankWaves; ++q) all += s_rank[0][q];
+    *n_sorted = all;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -302,7 +311,7 @@ tbe_status launch_lookup_backward(int64_t n, int64_t items, int64_t width, const
     if ((st = launch_fill_i32(n_sorted, 0, 1, s))) return st;
   } else if (n <= kRankMost) {
     ProfScope ps("lookup_rank", s);
-    hipLaunchKernelGGL(lookup_rank_kernel, dim3(static_cast<unsigned>((n + kWave - 1) / kWave)), dim3(kBlock), 0, s, ids, id64,
+    hipLaunchKernelGGL(lookup_rank_kernel, dim3(static_cast<unsigned>((n + kWave - 1) / kWave)), dim3(kRankWaves * kWave), 0, s, ids, id64,
                        static_cast<int>(n), items, keys[0], pay[0], n_sorted);
     if ((st = check_launch("lookup_rank"))) return st;
   } else {
