@@ -159,3 +159,43 @@ def test_items_past_the_threads_of_a_launch():
     (30, 40003, 1030, BF16, 1030)])
 def test_many_shares_of_the_items(rows, items, width, dtype, stride):
     one_case(rows, items, width, dtype, stride=stride)
+
+
+@pytest.mark.parametrize("rows,width", [(20, 200), (300, 200), (20, 72)])
+def test_rows_further_apart_than_a_tile_reaches(rows, width):
+    """Strides past 2^21 elements, of weights, rows and both gradients."""
+    items, stride = 700, (1 << 21) + 8
+    w, gw = [torch.empty(items * stride, dtype=BF16, device="cuda").view(items, stride)[:, :width] for _ in range(2)]
+    x, gx = [torch.empty(rows * stride, dtype=BF16, device="cuda").view(rows, stride)[:, :width] for _ in range(2)]
+    w.copy_(matrix(items, width, BF16, 2, 2 * width ** -0.5))
+    x.copy_(matrix(rows, width, BF16, 1))
+    t, grad = some_targets(rows, items, 0.2, 3), torch.full((rows,), 0.25, device="cuda")
+    exact = Exact(x.contiguous(), w.contiguous(), None, t, 1.0)
+    loss, lse = forward(x, w, None, t, 1.0)
+    exact.check_forward(loss, lse)
+    exact.check_backward(grad, *backward(x, w, None, t, 1.0, lse, grad, gx, gw))
+
+
+def test_captured_with_copies_and_shares():
+    """Captured and replayed at sizes with copied weights, shares of the items and of the rows, beside eager calls."""
+    for rows, items, width in ((30, 40003, 13), (9000, 3000, 100), (70, 9001, 301), (20, 9001, 301)):
+        x, w = matrix(rows, width, F16, 1), matrix(items, width, F16, 2, width ** -0.5)
+        t, bias = some_targets(rows, items, 0.2, 3), matrix(1, items, torch.float32, 4)[0]
+        grad, loss, lse = torch.full((rows,), 0.5, device="cuda"), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        gx, gw, gb = torch.empty_like(x), torch.empty_like(w), torch.empty_like(bias)
+        fws = tbe.workspace(tbe.tbe_cross_entropy_forward_workspace_bytes(rows, items, width))
+        bws = tbe.workspace(tbe.tbe_cross_entropy_backward_workspace_bytes(rows, items, width))
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=stream):
+            tbe.tbe_cross_entropy_forward(x, w, bias, t, 1.1, loss, lse, fws)
+            tbe.tbe_cross_entropy_backward(x, w, bias, t, 1.1, lse, grad, gx, gw, gb, bws)
+        for seed in range(3):
+            t.copy_(some_targets(rows, items, (0.0, 0.9, 1.0)[seed], 30 + seed))
+            w.copy_(matrix(items, width, F16, 40 + seed, width ** -0.5))
+            graph.replay()
+            torch.cuda.synchronize()
+            e_loss, e_lse = forward(x, w, bias, t, 1.1)
+            e = (e_loss, e_lse) + backward(x, w, bias, t, 1.1, e_lse, grad)
+            for name, a, b in zip(("loss", "lse", "grad_x", "grad_weight", "grad_bias"), (loss, lse, gx, gw, gb), e):
+                assert torch.equal(a, b), f"{rows} {items} {width} replay {seed}: {name}"
