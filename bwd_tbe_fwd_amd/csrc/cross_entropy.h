@@ -29,7 +29,8 @@ struct CeRows {
   const float* lse;        // backward
   const float* grad;       // backward: grad_loss
   const float* largest;    // backward: of |grad_loss|
-  const float* ref;        // backward, narrow rows: -lse in powers of two, -infinity up to a whole 64 rows
+  const float* ref;        // backward, narrow rows: -lse in powers of two, -infinity up to a whole 64 rows; for the gradient of
+                           // the weights less what |part| is below 1
   const float* part;       // backward, narrow rows: grad_loss over the largest
 };
 

@@ -45,6 +45,7 @@ struct CeBatch {
   uint16_t* xg;            // x times grad_loss over the largest; NULL: not asked for
   float* ref;              // narrow rows: -lse in powers of two (fp16: 15 more, kUnit), and grad_loss over the largest, with
   float* part;             // -infinity and 0 up to a whole 64 rows; NULL: not asked for
+  float* weighed;          // ref and the factor's size in powers of two: the reference of probabilities times |part|
 };
 __device__ __forceinline__ int target_of(const CeBatch& b, int64_t i) {
   if (i >= b.rows) return -1;
@@ -161,6 +162,7 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
           if (b.ref) {
             b.ref[slot] = ce_reference(lse, DT == 1 ? 15.0f : 0.0f);
             b.part[slot] = top > 0.0f ? grad / top : 0.0f * grad;
+            b.weighed[slot] = b.ref[slot] + log2f(fabsf(b.part[slot]));
           }
         }
       } else if (l < kRowsAtOnce && i < b.rows && b.loss) {
@@ -208,6 +210,7 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
     if (b.ref && more < (static_cast<int>(before) + 63) / 64 * 64) {
       b.ref[more] = -kInfinity;
       b.part[more] = 0.0f;
+      b.weighed[more] = -kInfinity;
       b.target[more] = -1;
     }
     if (threadIdx.x == 0) {
@@ -392,7 +395,7 @@ struct CeLayout {
   size_t bias_over;                         // narrow rows
   size_t part, picked, all;                 // forward
   size_t xg, z, sum_x, sum_w, bias_part;    // backward
-  size_t ref, part_of;                      // backward, narrow rows
+  size_t ref, part_of, weighed;                      // backward, narrow rows
   size_t total;
 };
 // The last to be carved.  Bytes never shrink with the rows here either: max(others + 32 MB, min(others + 128 MB, share)), or what
@@ -452,6 +455,7 @@ CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   L.bias_part = c.take(narrow ? items * 4 + kSumBytes / 4 : z / 64 * 4 + most * 4);
   L.ref = c.take(up(rows, 64) * 4);
   L.part_of = c.take(up(rows, 64) * 4);
+  L.weighed = c.take(up(rows, 64) * 4);
   carve_copies(L, c, items, kBackwardShare);
   return L;
 }
@@ -657,6 +661,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   if (narrow) {
     b.ref = reinterpret_cast<float*>(ws + L.ref);
     b.part = reinterpret_cast<float*>(ws + L.part_of);
+    b.weighed = reinterpret_cast<float*>(ws + L.weighed);
   }
   const int64_t piece = hmin(narrow ? items : L.piece, copy ? L.copied : items);
   tbe_status st = launch_rows(b, dtype, copy ? pad_of(weight, weight_stride, hmin(piece, items), width, ws, L) : CePad{}, s);
@@ -720,6 +725,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
       to_w.out = grad_weight ? static_cast<uint16_t*>(grad_weight) + first * grad_weight_stride : nullptr;
       to_w.out_stride = grad_weight_stride;
       to_w.splits = w_pick.splits;
+      if (narrow) to_w.r.ref = b.weighed;
       if (narrow) to_w.bias_part = grad_bias ? bias_part : nullptr;
     }
     if (st == TBE_OK && narrow && (to_x.splits || to_w.splits))

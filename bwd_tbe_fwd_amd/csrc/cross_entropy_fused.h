@@ -10,10 +10,12 @@
 //  * The passing matrix is therefore read from LDS in two ways: along, 16 t and 32 columns, for the logits, and turned, 4 t
 //    and 16 columns, for the gradient.  t = q + 4 r (q, r < 4) is row 4 q + r of the logits' first operand, and the 16-byte
 //    columns of row t are exchanged by 2 ((t / 4) % 4): both reads then find their banks free.
+//  * A row's factor goes into the exponent, ahead of the rounding of z; its sign is looked at where there is a negative one (a
+//    product each instead: 1 to 3.5% more).
 //  * A ring of three tiles of 64 t, loaded two ahead, one barrier a tile; two workgroups a CU, so that one's exponentials
 //    are taken while the other's products are.  192 s a workgroup at 128 columns, 256 at 64: what the registers hold.
-// Bound by the matrix instructions and the vector unit together (2048 rows, 500000 items of 128, all three gradients 0.99 to 1.02
-// ms, 1.05 PFLOP/s of products, the logits' counted twice as they are taken; matrix instructions busy 48% of the cycles; with z in
+// Bound by the matrix instructions and the vector unit together (2048 rows, 500000 items of 128, all three gradients 0.96 to 0.99
+// ms, 1.08 PFLOP/s of products, the logits' counted twice as they are taken; matrix instructions busy 48% of the cycles; with z in
 // memory 1.99 ms).
 #pragma once
 
@@ -116,7 +118,11 @@ __device__ __forceinline__ void ce_fused_part(const CeArgs& a, unsigned block, u
     const int slot = (t - t0) % kRing, n0 = t * kPassing;
     const uint16_t* const tile = lds + slot * kTile;
     uint64_t hits = 0;  // not X: rows whose target is one of this wave's items
-    if constexpr (!X) hits = __ballot(s_more[slot][2][l] - static_cast<unsigned>(a.first + s0) < 16u * MF);
+    bool minus = false;
+    if constexpr (!X) {
+      minus = __any(__uint_as_float(s_more[slot][1][l]) < 0.0f);
+      hits = __ballot(s_more[slot][2][l] - static_cast<unsigned>(a.first + s0) < 16u * MF);
+    }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       f32x4 acc[MF][2];
@@ -165,20 +171,28 @@ __device__ __forceinline__ void ce_fused_part(const CeArgs& a, unsigned block, u
             for (int e = 0; e < 4; ++e) {
               unsigned at = s_more[slot][2][half * 32 + 16 * j + 4 * e + g] - static_cast<unsigned>(a.first + s0 + (l & 15));
               asm volatile("" : "+v"(at));  // keeps what follows from being worked out where it is not needed
+              const float one = fabsf(__uint_as_float(s_more[slot][1][half * 32 + 16 * j + 4 * g + e])) * kUnit<DT>;
 #pragma unroll
-              for (int i = 0; i < MF; ++i) acc[i][j][e] -= at == 16u * i ? kUnit<DT> : 0.0f;
+              for (int i = 0; i < MF; ++i) acc[i][j][e] -= at == 16u * i ? one : 0.0f;
             }
         }
+        if (minus) {  // rows with a negative factor: its size is in the reference
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const f32x4 part = *reinterpret_cast<const f32x4*>(&s_more[slot][1][half * 32 + 16 * j + 4 * g]);
+          for (int j = 0; j < 2; ++j) {
+            const f32x4 part = *reinterpret_cast<const f32x4*>(&s_more[slot][1][half * 32 + 16 * j + 4 * g]);
 #pragma unroll
-          for (int i = 0; i < MF; ++i)
+            for (int i = 0; i < MF; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              acc[i][j][e] *= part[e];
-              if constexpr (BIAS) sum[i] += acc[i][j][e];
-            }
+              for (int e = 0; e < 4; ++e) acc[i][j][e] = part[e] < 0.0f ? -acc[i][j][e] : acc[i][j][e];
+          }
+        }
+        if constexpr (BIAS) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum[i] += acc[i][j][e];
         }
       }
       u16x8_t z[MF];
