@@ -119,7 +119,7 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
     for (int64_t v = static_cast<int64_t>(blockIdx.x - groups) * kBlock + threadIdx.x; v < end;
          v += static_cast<int64_t>(more) * kBlock) {
       const float x = v >= b.items ? -kInfinity : b.bias ? b.bias[v] : 0.0f, y = x * b.over;
-      b.bias_over[v] = y == -kInfinity && x != y ? -3.4028234664e38f : y > most && x != kInfinity ? most : y;
+      b.bias_over[v] = y == -kInfinity && x != y ? kLowest : y > most && x != kInfinity ? most : y;
     }
     return;
   }

@@ -61,6 +61,12 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
   stage(t0);
   stage(t0 + 1);
 
+  // what the exponential of base 2 takes: the sum of products times `unit`, less the row's reference
+  const float unit = a.scale * kLog2e;
+  // the lowest reference, before a lane has seen a logit that is not masked: times unit it stays finite, so that a masked one's
+  // exponential is 0 beside it.  Lower logits count as masked
+  const float floor = kFloor / fmaxf(a.scale, 1.0f);
+
   // the rows: lane l holds row l % 16 of each 16, 8 columns from 8 (l / 16) on of each 32
   u16x8_t fa[MF][KS];
   float ref[MF], top[MF], sum[MF];
@@ -76,10 +82,8 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
     }
     top[i] = -kInfinity;
     sum[i] = 0.0f;
-    ref[i] = kFloor;
+    ref[i] = floor;
   }
-  // what the exponential of base 2 takes: the sum of products times `unit`, less the row's reference
-  const float unit = a.scale * kLog2e;
 
   const int b_place = OB::read_place(((l & 15) >> 2) * LEN + (l & 3));
   // 32 items from `half` * 32 on of the tile in `slot`
@@ -109,7 +113,7 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
   };
   // Ahead of 32 items' exponentials: whether a logit asks for another reference.
   auto look = [&](const f32x4 (&acc)[MF][NF]) {
-    float over = kFloor;
+    float over = -kInfinity;
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
       float most = acc[i][0][0];  // NaN stays NaN: no instruction to make sure that it is a quiet one
@@ -121,10 +125,10 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
     if (__any(over > kSlack)) {
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
-        float now = fmaxf(top[i], kFloor);
+        float now = fmaxf(top[i], floor);
         asm volatile("" : "+v"(now));  // keeps what follows from being worked out where it is not needed
         // far out, above the largest by more than a product's rounding: no exponential overflows
-        if (fabsf(now) * unit > 0x1p20f && now > kFloor) now += fabsf(now) * 0x1p-22f;
+        if (fabsf(now) * unit > 0x1p20f && now > floor) now += fabsf(now) * 0x1p-22f;
         sum[i] *= __builtin_amdgcn_exp2f((ref[i] - now) * unit);
         ref[i] = now;
       }
@@ -168,7 +172,7 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
   wait_loads<0>();  // nothing is on its way into LDS when the workgroup ends
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
-    // the lanes that share a row; where no logit was above kFloor the sum is 0 and the maximum tells what there was (far out the
+    // the lanes that share a row; where no logit was above the floor the sum is 0 and the maximum tells what there was (far out the
     // sum may be 0 too: the reference is the largest but for 2^-22 of it)
     const int m = m0 + 16 * i + (l & 15);
     float all = fmaxf(ref[i], __shfl_xor(ref[i], 16)), most = fmaxf(top[i], __shfl_xor(top[i], 16));
@@ -177,7 +181,11 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
     float s = sum[i] * __builtin_amdgcn_exp2f((ref[i] - all) * unit);
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (l < 16 && m < count) a.part[split * a.rows + m] = make_float2(most <= kFloor ? (most == -kInfinity ? most : most * a.scale) : all * a.scale, s);
+    if (l < 16 && m < count) {
+      // the lowest bias over the scale, times the scale, may round to -infinity, which would mean a mask
+      const float low = most == -kInfinity ? most : fmaxf(most * a.scale, kLowest);
+      a.part[split * a.rows + m] = make_float2(most <= floor ? low : all * a.scale, s);
+    }
   }
 }
 
