@@ -120,7 +120,7 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
 #pragma unroll
       for (int c = 1; c < LEN; ++c) most = __builtin_elementwise_maximum(most, acc[i][c / 4][c % 4]);
       top[i] = __builtin_elementwise_maximum(top[i], most);
-      over = __builtin_elementwise_maximum(over, (most - ref[i]) * unit);
+      over = fmaxf(over, (most - ref[i]) * unit);  // drops NaN: such a row asks for nothing, the lane's others for themselves
     }
     if (__any(over > kSlack)) {
 #pragma unroll
