@@ -68,6 +68,7 @@ template <int DT> constexpr float kUnit = DT == 1 ? 32768.0f : 1.0f;
 constexpr float kInfinity = __builtin_huge_valf();
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLowest = -3.4028234663852886e38f;  // of all finite ones
+constexpr float kFar = 0x1p20f;  // logits of that size and more: a rounding of one times kLog2e is worth a tenth of it as a power of two
 constexpr float kFloor = -1e38f;  // lower logits count as masked where they would overflow as powers of two
 
 // What the backward's exponentials of base 2 add: -lse in powers of two and `shift` more; no probability where every item is
