@@ -32,6 +32,7 @@ struct CeRows {
   const float* ref;        // backward, narrow rows: -lse in powers of two, -infinity up to a whole 64 rows; for the gradient of
                            // the weights less what |part| is below 1
   const float* part;       // backward, narrow rows: grad_loss over the largest
+  const float* far;        // backward, narrow rows: lse where it is past kFar, else 0
 };
 
 struct CeArgs {
@@ -43,7 +44,7 @@ struct CeArgs {
   const void* w;           // the piece's first item
   int64_t w_stride;
   const float* bias;       // the piece's; NULL: none; for narrow rows over the scale
-  float scale;
+  float scale, over;       // over: narrow rows, 1 / scale
   CeRows r;
   int32_t first, items;    // of the piece
   float2* part;            // forward: [tiles of items][rows] maximum and sum
@@ -68,16 +69,22 @@ template <int DT> constexpr float kUnit = DT == 1 ? 32768.0f : 1.0f;
 constexpr float kInfinity = __builtin_huge_valf();
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLowest = -3.4028234663852886e38f;  // of all finite ones
-constexpr float kFar = 0x1p20f;  // logits of that size and more: a rounding of one times kLog2e is worth a tenth of it as a power of two
+// Logits of that size: one times kLog2e is rounded by 2^-10 powers of two, 0.07% of an exponential, and by more the larger it is.
+constexpr float kFar = 0x1p14f;
 constexpr float kFloor = -1e38f;  // lower logits count as masked where they would overflow as powers of two
 
-// What the backward's exponentials of base 2 add: -lse in powers of two and `shift` more; no probability where every item is
-// masked.  Past 2^20 the roundings of a logit and of lse may lie powers of two apart, so a little more is taken off than they can
-// be (8 units): no probability overflows.
+// What the backward's exponentials of base 2 add for narrow rows: -lse in powers of two and `shift` more; no probability where
+// every item is masked.  lse past kFar is taken off the logits by ce_near instead.
+__device__ __forceinline__ bool ce_is_far(float lse) { return fabsf(lse) > kFar && lse != -kInfinity; }
 __device__ __forceinline__ float ce_reference(float lse, float shift) {
-  if (lse < kFloor) return -kInfinity;
-  const float at = fmaf(lse, -kLog2e, shift), size = fabsf(lse);
-  return size > 0x1p20f ? at - size * 0x1p-21f : at;
+  return lse == -kInfinity ? -kInfinity : ce_is_far(lse) ? shift : fmaf(lse, -kLog2e, shift);
+}
+// A logit less lse, both over the scale.  lse is at least the largest rounded product with the scale, so that product is rounded here as
+// well: the largest logit's difference is 0 to the bit, and none is above.
+__device__ __forceinline__ float ce_near(float product, float scale, float over, float lse) {
+#pragma clang fp contract(off)
+  const float logit = product * scale, less = logit - lse;
+  return (less > 0.0f ? 0.0f : less) * over;
 }
 
 // Two parts of a row: their maximum, and the sum of the exponentials less it.

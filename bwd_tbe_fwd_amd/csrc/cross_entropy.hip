@@ -46,6 +46,7 @@ struct CeBatch {
   float* ref;              // narrow rows: -lse in powers of two (fp16: 15 more, kUnit), and grad_loss over the largest, with
   float* part;             // -infinity and 0 up to a whole 64 rows; NULL: not asked for
   float* weighed;          // ref and the factor's size in powers of two: the reference of probabilities times |part|
+  float* far;              // lse where it is past kFar, else 0
 };
 __device__ __forceinline__ int target_of(const CeBatch& b, int64_t i) {
   if (i >= b.rows) return -1;
@@ -163,6 +164,7 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
             b.ref[slot] = ce_reference(lse, DT == 1 ? 15.0f : 0.0f);
             b.part[slot] = top > 0.0f ? grad / top : 0.0f * grad;
             b.weighed[slot] = b.ref[slot] + log2f(fabsf(b.part[slot]));
+            b.far[slot] = ce_is_far(lse) ? lse : 0.0f;
           }
         }
       } else if (l < kRowsAtOnce && i < b.rows && b.loss) {
@@ -211,6 +213,7 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
       b.ref[more] = -kInfinity;
       b.part[more] = 0.0f;
       b.weighed[more] = -kInfinity;
+      b.far[more] = 0.0f;
       b.target[more] = -1;
     }
     if (threadIdx.x == 0) {
@@ -395,7 +398,7 @@ struct CeLayout {
   size_t bias_over;                         // narrow rows
   size_t part, picked, all;                 // forward
   size_t xg, z, sum_x, sum_w, bias_part;    // backward
-  size_t ref, part_of, weighed;                      // backward, narrow rows
+  size_t ref, part_of, weighed, far;        // backward, narrow rows
   size_t total;
 };
 // The last to be carved.  Bytes never shrink with the rows here either: max(others + 32 MB, min(others + 128 MB, share)), or what
@@ -456,6 +459,7 @@ CeLayout backward_layout(int64_t rows, int64_t items, int64_t width) {
   L.ref = c.take(up(rows, 64) * 4);
   L.part_of = c.take(up(rows, 64) * 4);
   L.weighed = c.take(up(rows, 64) * 4);
+  L.far = c.take(up(rows, 64) * 4);
   carve_copies(L, c, items, kBackwardShare);
   return L;
 }
@@ -584,7 +588,7 @@ tbe_status launch_pad(const CePad& p, hipStream_t s) {
   hipLaunchKernelGGL(ce_pad_kernel, dim3(static_cast<unsigned>(pad_groups(p))), dim3(kBlock), 0, s, p);
   return check_launch("ce_pad");
 }
-CeRows rows_of(const CeBatch& b) { return CeRows{b.count, b.row, b.target, b.lse, b.grad, b.largest, b.ref, b.part}; }
+CeRows rows_of(const CeBatch& b) { return CeRows{b.count, b.row, b.target, b.lse, b.grad, b.largest, b.ref, b.part, b.far}; }
 
 }  // namespace
 
@@ -609,7 +613,7 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
   CeArgs a = {};
   a.rows = rows; a.width = static_cast<int>(direct ? L.pitch : width); a.out_width = static_cast<int>(width);
   a.x = ws + L.xc; a.x_stride = L.pitch;
-  a.scale = scale; a.r = rows_of(b);
+  a.scale = scale; a.over = b.over; a.r = rows_of(b);
   a.part = reinterpret_cast<float2*>(ws + L.part);
   for (int64_t first = 0; st == TBE_OK && first < items; first += piece) {
     a.first = static_cast<int>(first);
@@ -662,6 +666,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
     b.ref = reinterpret_cast<float*>(ws + L.ref);
     b.part = reinterpret_cast<float*>(ws + L.part_of);
     b.weighed = reinterpret_cast<float*>(ws + L.weighed);
+    b.far = reinterpret_cast<float*>(ws + L.far);
   }
   const int64_t piece = hmin(narrow ? items : L.piece, copy ? L.copied : items);
   tbe_status st = launch_rows(b, dtype, copy ? pad_of(weight, weight_stride, hmin(piece, items), width, ws, L) : CePad{}, s);
@@ -669,7 +674,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   CeArgs a = {};
   a.rows = rows; a.width = static_cast<int>(L.pitch); a.out_width = static_cast<int>(width);
   a.x = ws + L.xc; a.x_stride = L.pitch; a.xg = ws + L.xg;
-  a.scale = scale; a.r = rows_of(b);
+  a.scale = scale; a.over = b.over; a.r = rows_of(b);
   a.z = reinterpret_cast<uint16_t*>(ws + L.z); a.panel = up(rows, 64) * 64;
   a.factor = scale / unit;  // of x as it was copied
   a.sum_pitch = up(width, 4);

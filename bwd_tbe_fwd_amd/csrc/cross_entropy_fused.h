@@ -27,8 +27,8 @@ constexpr int kPassing = 64;  // t of a tile
 
 constexpr int kRing = 3;
 
-// `block`: the workgroup among this gradient's.  s_more: X: the items' biases; else the rows' references, factors and targets;
-// each 64 t in the order of the lanes that ask for them.
+// `block`: the workgroup among this gradient's.  s_more: X: the items' biases; else the rows' references, factors, targets and far
+// lse; each 64 t in the order of the lanes that ask for them.
 template <int DT, bool X, int KS, int MF, bool BIAS>
 __device__ __forceinline__ void ce_fused_part(const CeArgs& a, unsigned block, uint16_t* lds, uint32_t (*s_more)[4][kPassing]) {
   constexpr int T = 256, KT = KS / 2, CG = 2 * KS, kStay = 64 * MF;
@@ -50,8 +50,8 @@ __device__ __forceinline__ void ce_fused_part(const CeArgs& a, unsigned block, u
   const uint16_t* const pass_from = static_cast<const uint16_t*>(X ? a.w : a.x);
   const int64_t stay_pitch = X ? a.x_stride : a.w_stride, pass_pitch = X ? a.w_stride : a.x_stride;
   // wave w brings one of the arrays of s_more
-  const void* const more_from = X ? static_cast<const void*>(a.bias) : w == 0 ? static_cast<const void*>(a.r.ref) : w == 1 ? static_cast<const void*>(a.r.part) : static_cast<const void*>(a.r.target);
-  const bool more = X ? w == 0 : w < 3;
+  const void* const more_from = X ? static_cast<const void*>(a.bias) : w == 0 ? static_cast<const void*>(a.r.ref) : w == 1 ? static_cast<const void*>(a.r.part) : w == 2 ? static_cast<const void*>(a.r.target) : static_cast<const void*>(a.r.far);
+  const bool more = !X || w == 0;
   // place l of a tile's 64: t = 16 (l / 16) + (l / 4) % 4 + 4 (l % 4); targets in their own order
   const int more_at = !X && w == 2 ? l : (l & 48) + ((l >> 2) & 3) + 4 * (l & 3);
 
@@ -97,6 +97,12 @@ __device__ __forceinline__ void ce_fused_part(const CeArgs& a, unsigned block, u
     }
   }
   const float unit = a.scale * kLog2e;
+  bool away = false;  // the wave has rows whose lse is past kFar
+  if constexpr (X) {
+#pragma unroll
+    for (int i = 0; i < MF; ++i) away |= s0 + 16 * i + (l & 15) < stay && a.r.far[s0 + 16 * i + (l & 15)] != 0.0f;
+    away = __any(away);
+  }
   f32x4 out[MF][CG];
 #pragma unroll
   for (int i = 0; i < MF; ++i)
@@ -121,6 +127,7 @@ __device__ __forceinline__ void ce_fused_part(const CeArgs& a, unsigned block, u
     bool minus = false;
     if constexpr (!X) {
       minus = __any(__uint_as_float(s_more[slot][1][l]) < 0.0f);
+      away = __any(s_more[slot][3][l] != 0);
       hits = __ballot(s_more[slot][2][l] - static_cast<unsigned>(a.first + s0) < 16u * MF);
     }
 #pragma unroll
@@ -135,6 +142,20 @@ __device__ __forceinline__ void ce_fused_part(const CeArgs& a, unsigned block, u
           const u16x8_t ft = *reinterpret_cast<const u16x8_t*>(tile + k / 2 * OT::kElems + ((k & 1) ? along ^ 32 : along) + (half * 32 + 16 * j) * kStepK);
 #pragma unroll
           for (int i = 0; i < MF; ++i) acc[i][j] = mfma16<DT>(ft, fs[i][k], k > 0 ? acc[i][j] : X ? begin : from[i]);
+        }
+      }
+      if (__builtin_expect(away, 0)) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          float lse = 0.0f;
+          if constexpr (X) lse = s0 + 16 * i + (l & 15) < stay ? a.r.far[s0 + 16 * i + (l & 15)] : 0.0f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (!X) lse = __uint_as_float(s_more[slot][3][half * 32 + 16 * j + 4 * g + e]);
+              if (lse != 0.0f) acc[i][j][e] = ce_near(acc[i][j][e], a.scale, a.over, lse);
+            }
         }
       }
 #pragma unroll

@@ -111,6 +111,12 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
       __builtin_amdgcn_sched_group_barrier(0x400, (MF * LEN + kProducts - 1) / kProducts, 0);
     }
   };
+  // What an exponential's argument has a reference as.  Far out its rounding is worth powers of two, but a lane's exponentials of a
+  // row all have the same, so it is taken out again where the reference moves and at the end.
+  auto rounded = [&](float of) {
+#pragma clang fp contract(off)
+    return of * unit;
+  };
   // Ahead of 32 items' exponentials: whether a logit asks for another reference.
   auto look = [&](const f32x4 (&acc)[MF][NF]) {
     float over = -kInfinity;
@@ -127,9 +133,7 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
       for (int i = 0; i < MF; ++i) {
         float now = fmaxf(top[i], floor);
         asm volatile("" : "+v"(now));  // keeps what follows from being worked out where it is not needed
-        // far out, above the largest by more than a product's rounding: no exponential overflows
-        if (fabsf(now) * unit > 0x1p20f && now > floor) now += fabsf(now) * 0x1p-22f;
-        sum[i] *= __builtin_amdgcn_exp2f((ref[i] - now) * unit);
+        sum[i] *= __builtin_amdgcn_exp2f(rounded(ref[i]) - rounded(now));
         ref[i] = now;
       }
     }
@@ -137,7 +141,7 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
   auto exponentials = [&](const f32x4 (&acc)[MF][NF]) {
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
-      const float base = -ref[i] * unit;
+      const float base = -rounded(ref[i]);
       float p[LEN];
 #pragma unroll
       for (int c = 0; c < LEN; ++c) p[c] = __builtin_amdgcn_exp2f(fmaf(acc[i][c / 4][c % 4], unit, base));
@@ -172,19 +176,20 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
   wait_loads<0>();  // nothing is on its way into LDS when the workgroup ends
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
-    // the lanes that share a row; where no logit was above the floor the sum is 0 and the maximum tells what there was (far out the
-    // sum may be 0 too: the reference is the largest but for 2^-22 of it)
+    // the lanes that share a row, each sum less the lane's largest logit; where no logit was above the floor the sum is 0 and the
+    // maximum tells what there was.  Past 2^28 powers of two the sum may have overflowed, but its logarithm, of the number of items
+    // at most, is no more than half a unit of lse there
     const int m = m0 + 16 * i + (l & 15);
-    float all = fmaxf(ref[i], __shfl_xor(ref[i], 16)), most = fmaxf(top[i], __shfl_xor(top[i], 16));
-    all = fmaxf(all, __shfl_xor(all, 32));
+    float most = fmaxf(top[i], __shfl_xor(top[i], 16)), s = sum[i] * __builtin_amdgcn_exp2f(-fmaf(top[i], unit, -rounded(ref[i])));
     most = fmaxf(most, __shfl_xor(most, 32));
-    float s = sum[i] * __builtin_amdgcn_exp2f((ref[i] - all) * unit);
+    if (fabsf(top[i]) * unit > 0x1p28f) s = 1.0f;
+    s = top[i] <= floor ? 0.0f : s * __builtin_amdgcn_exp2f((top[i] - most) * unit);
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
     if (l < 16 && m < count) {
       // the lowest bias over the scale, times the scale, may round to -infinity, which would mean a mask
       const float low = most == -kInfinity ? most : fmaxf(most * a.scale, kLowest);
-      a.part[split * a.rows + m] = make_float2(most <= floor ? low : all * a.scale, s);
+      a.part[split * a.rows + m] = make_float2(most <= floor ? low : most * a.scale, s);
     }
   }
 }
