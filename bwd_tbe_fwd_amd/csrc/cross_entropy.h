@@ -45,6 +45,7 @@ struct CeArgs {
   int64_t w_stride;
   const float* bias;       // the piece's; NULL: none; for narrow rows over the scale
   float scale, over;       // over: narrow rows, 1 / scale
+  float most;              // what finite biases count as at most
   CeRows r;
   int32_t first, items;    // of the piece
   float2* part;            // forward: [tiles of items][rows] maximum and sum
@@ -68,7 +69,7 @@ template <int DT> constexpr float kUnit = DT == 1 ? 32768.0f : 1.0f;
 
 constexpr float kInfinity = __builtin_huge_valf();
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLowest = -3.4028234663852886e38f;  // of all finite ones
+constexpr float kLargest = 3.4028234663852886e38f;  // of all finite ones
 // Logits of that size: one times kLog2e is rounded by 2^-10 powers of two, 0.07% of an exponential, and by more the larger it is.
 constexpr float kFar = 0x1p14f;
 constexpr float kFloor = -1e38f;  // lower logits count as masked where they would overflow as powers of two
@@ -85,6 +86,14 @@ __device__ __forceinline__ float ce_near(float product, float scale, float over,
 #pragma clang fp contract(off)
   const float logit = product * scale, less = logit - lse;
   return (less > 0.0f ? 0.0f : less) * over;
+}
+
+// A bias as it counts: finite ones no higher than `most`, the largest value times the scale where that is below 1.  The narrow
+// rows' kernels hold biases over the scale, and there is one rule for all widths.
+__device__ __forceinline__ float ce_bias(float b, float most) { return b > most && b != kInfinity ? most : b; }
+// A finite value's product with the scale or its inverse, at most the largest value.
+__device__ __forceinline__ float ce_times(float x, float by) {
+  return fabsf(x) == kInfinity ? x : x != x ? x : fminf(fmaxf(x * by, -kLargest), kLargest);
 }
 
 // Two parts of a row: their maximum, and the sum of the exponentials less it.

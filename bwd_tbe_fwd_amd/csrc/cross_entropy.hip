@@ -29,6 +29,7 @@ struct CeBatch {
   const float* bias;       // NULL: none
   float* bias_over;        // narrow rows: the biases over the scale (0 without), -infinity up to a whole 64 items; else NULL
   float over;              // 1 / scale
+  float most;              // what finite biases count as at most
   // forward
   const uint16_t* w;
   int64_t w_stride;
@@ -113,14 +114,11 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
     return;
   }
   if (static_cast<int>(blockIdx.x) >= groups) {
-    // the biases' workgroups.  Finite ones stay finite: the lowest value is no mask where every item has it.  Those above 1e38, or
-    // 1e38 scale, count as that: neither they nor their logits overflow as powers of two
+    // the biases' workgroups.  Finite ones stay finite: the lowest value is no mask where every item has it
     const int64_t end = (b.items + 63) / 64 * 64;
-    const float most = 1e38f * fminf(b.over, 1.0f);
     for (int64_t v = static_cast<int64_t>(blockIdx.x - groups) * kBlock + threadIdx.x; v < end;
          v += static_cast<int64_t>(more) * kBlock) {
-      const float x = v >= b.items ? -kInfinity : b.bias ? b.bias[v] : 0.0f, y = x * b.over;
-      b.bias_over[v] = y == -kInfinity && x != y ? kLowest : y > most && x != kInfinity ? most : y;
+      b.bias_over[v] = ce_times(v >= b.items ? -kInfinity : b.bias ? ce_bias(b.bias[v], b.most) : 0.0f, b.over);
     }
     return;
   }
@@ -203,7 +201,7 @@ __global__ __launch_bounds__(kBlock) void ce_rows_kernel(CeBatch b, int each, in
       }
       if (b.picked) {
         dot = lanes_sum<64>(dot);
-        if (l == 0) b.picked[slot] = fmaf(dot, b.scale, b.bias ? b.bias[t] : 0.0f);
+        if (l == 0) b.picked[slot] = fmaf(dot, b.scale, b.bias ? ce_bias(b.bias[t], b.most) : 0.0f);
       }
     }
   }
@@ -266,8 +264,9 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(const float2* __restrict_
   }
   // no sum is left where every item is masked, or by the lowest value
   const float lse = sum.y == 0.0f ? sum.x : sum.x + logf(sum.y), at = b.picked[c];
+  const float loss = at == -kInfinity && !(lse != lse) ? kInfinity : lse - at;
   b.lse_out[b.row[c]] = lse;
-  b.loss[b.row[c]] = at == -kInfinity && !(lse != lse) ? kInfinity : lse - at;
+  b.loss[b.row[c]] = loss < 0.0f ? 0.0f : loss;  // lse and the target's logit are rounded for themselves
 }
 
 // The rows' gradients: the parts' sums times scale * grad_loss; zero for a row without a target.
@@ -547,9 +546,11 @@ CeBatch batch_of(char* ws, const CeLayout& L, int64_t rows, int64_t items, int64
   b.target = reinterpret_cast<int32_t*>(ws + L.target);
   b.bias = bias;
   b.scale = scale;
+  const float size = scale < 0.0f ? -scale : scale == 0.0f ? 1.0f : scale;
+  b.most = size < 1.0f ? kLargest * size : kLargest;
   if (narrow) {
     b.flip = scale < 0.0f ? 1 : scale == 0.0f ? 2 : 0;
-    scale = scale < 0.0f ? -scale : scale == 0.0f ? 1.0f : scale;
+    scale = size;
     b.bias_over = reinterpret_cast<float*>(ws + L.bias_over);
     b.over = 1.0f / scale;
   }
@@ -613,7 +614,7 @@ tbe_status launch_cross_entropy_forward(int64_t rows, int64_t items, int64_t wid
   CeArgs a = {};
   a.rows = rows; a.width = static_cast<int>(direct ? L.pitch : width); a.out_width = static_cast<int>(width);
   a.x = ws + L.xc; a.x_stride = L.pitch;
-  a.scale = scale; a.over = b.over; a.r = rows_of(b);
+  a.scale = scale; a.over = b.over; a.most = b.most; a.r = rows_of(b);
   a.part = reinterpret_cast<float2*>(ws + L.part);
   for (int64_t first = 0; st == TBE_OK && first < items; first += piece) {
     a.first = static_cast<int>(first);
@@ -674,7 +675,7 @@ tbe_status launch_cross_entropy_backward(int64_t rows, int64_t items, int64_t wi
   CeArgs a = {};
   a.rows = rows; a.width = static_cast<int>(L.pitch); a.out_width = static_cast<int>(width);
   a.x = ws + L.xc; a.x_stride = L.pitch; a.xg = ws + L.xg;
-  a.scale = scale; a.over = b.over; a.r = rows_of(b);
+  a.scale = scale; a.over = b.over; a.most = b.most; a.r = rows_of(b);
   a.z = reinterpret_cast<uint16_t*>(ws + L.z); a.panel = up(rows, 64) * 64;
   a.factor = scale / unit;  // of x as it was copied
   a.sum_pitch = up(width, 4);

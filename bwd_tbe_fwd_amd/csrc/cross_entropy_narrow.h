@@ -187,9 +187,8 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
     if (l < 16 && m < count) {
-      // the lowest bias over the scale, times the scale, may round to -infinity, which would mean a mask
-      const float low = most == -kInfinity ? most : fmaxf(most * a.scale, kLowest);
-      a.part[split * a.rows + m] = make_float2(most <= floor ? low : most * a.scale, s);
+      // the largest and the lowest bias, over the scale and times the scale, may round to infinity
+      a.part[split * a.rows + m] = make_float2(ce_times(most, a.scale), s);
     }
   }
 }

@@ -62,7 +62,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
   const int n = wn + (l >> 4) * LEN;
   float bias[LEN];
 #pragma unroll
-  for (int c = 0; c < LEN; ++c) bias[c] = a.bias && n + c < n_left ? a.bias[n0 + n + c] : 0.0f;
+  for (int c = 0; c < LEN; ++c) bias[c] = a.bias && n + c < n_left ? ce_bias(a.bias[n0 + n + c], a.most) : 0.0f;
   auto logit = [&](int i, int c) { return fmaf(acc[i][c / 4][c % 4], a.scale, bias[c]); };
   if constexpr (!BACK) {
     float2* stat = reinterpret_cast<float2*>(lds);  // [WN][BM]

@@ -1,5 +1,5 @@
-"""Biases of the largest and the lowest values: finite ones count as no higher than 1e38 and 1e38 |scale|, for the
-probabilities and for the target's logit alike, at every width."""
+"""Biases of the largest and the lowest values: where |scale| is below 1, finite ones count as no higher than the largest value times
+|scale|, for the probabilities and for the target's logit alike, at every width."""
 import pytest
 import torch
 
@@ -25,8 +25,8 @@ def test_an_item_of_the_largest_bias(width, scale, high):
         bias = matrix(1, items, torch.float32, 4)[0]
         bias[7], bias[9] = high, torch.finfo(torch.float32).min
         loss, lse = forward(x, w, bias, t, scale)
-        counts_as = 1e38 * min(1.0, abs(scale) or 1.0)
-        # lse is that but for its roundings, the reference's step of 2^-22 among them
+        counts_as = min(high, LARGEST * min(1.0, abs(scale) or 1.0))
+        # lse is that but for the roundings of the scale's inverse, the bias over the scale and the product
         assert bool(((lse[there].double() - counts_as).abs() <= 16 * U * counts_as).all())
         assert bool((loss[there & (t == 7)].abs() <= 16 * U * counts_as).all())
         assert bool((loss >= 0).all()) and bool(loss.isfinite().all())
@@ -34,22 +34,41 @@ def test_an_item_of_the_largest_bias(width, scale, high):
         assert bool(((loss[other].double() - counts_as).abs() <= 16 * U * counts_as).all())
         grad = torch.ones(rows, device="cuda")
         gx, gw, gb = backward(x, w, bias, t, scale, lse, grad)
-        # z is 1 for item 7 and -1 for the target: p as far as the roundings of numbers so far out allow, 8 units of them
-        assert bool(gb.isfinite().all()) and bool(gx.isfinite().all()) and bool(gw.isfinite().all())
-        hits = torch.bincount(t[there], minlength=items).float()
-        rest = torch.arange(items, device="cuda") != 7
-        assert torch.equal(gb[rest], -hits[rest])
+        # p is 1 for item 7 and 0 for the others, so z is 1, 0 and -1
+        assert bool(gx.isfinite().all()) and bool(gw.isfinite().all())
+        exp = -torch.bincount(t[there], minlength=items).double()
+        exp[7] += int(there.sum())
+        assert torch.equal(gb.double(), exp)
+        exp_x = torch.where(there[:, None], (w[7].double() - w[torch.where(there, t, 0)].double()) * scale, 0.0)
+        size = (w[7].double().abs() + w[torch.where(there, t, 0)].double().abs()) * abs(scale)
+        assert bool(((gx.double() - exp_x).abs() <= 2.0 ** -8 * exp_x.abs() + 8 * U * size).all())
 
 
 @pytest.mark.parametrize("width", WIDTHS)
-def test_the_same_rule_at_every_width(width):
-    """One row with one item above 1e38 in a table of two: its target's loss is 0 and its gradients are too, but for roundings."""
+def test_a_table_of_two(width):
+    """One row, one item near the largest value: its target's loss and gradients are 0."""
     x, w = torch.zeros(1, width, dtype=BF16, device="cuda"), matrix(2, width, BF16, 2)
     t = torch.zeros(1, dtype=torch.int64, device="cuda")
-    for scale in (1.0, 0.5, 8.0):
-        bias = torch.tensor([3e38, 0.0], device="cuda")
+    for scale in (1.0, 0.5, 8.0, 3.0):
+        for high in (3e38, LARGEST, 1e38):
+            bias = torch.tensor([high, 0.0], device="cuda")
+            loss, lse = forward(x, w, bias, t, scale)
+            counts_as = min(high, LARGEST * min(1.0, scale))
+            assert abs(float(lse) - counts_as) <= 16 * U * counts_as and 0 <= float(loss) <= 16 * U * counts_as
+            _, _, gb = backward(x, w, bias, t, scale, lse, torch.ones(1, device="cuda"))
+            assert bool((gb == 0).all())
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("low", [-1e38, -2e38, -1e30, -9e36])
+def test_the_same_low_bias_everywhere(width, low):
+    """No item is masked against the others: lse is that bias, and every probability exp(logit - lse), at most 1."""
+    rows, items = 90, 300
+    x, w, t = matrix(rows, width, BF16, 1), matrix(items, width, BF16, 2, width ** -0.5), some_targets(rows, items, 0.0, 3)
+    for scale in (1.0, 0.75, 8.0, -3.0):
+        bias = torch.full((items,), low, device="cuda")
         loss, lse = forward(x, w, bias, t, scale)
-        counts_as = 1e38 * min(1.0, scale)
-        assert abs(float(lse) - counts_as) <= 16 * U * counts_as and 0 <= float(loss) <= 16 * U * counts_as
-        _, _, gb = backward(x, w, bias, t, scale, lse, torch.ones(1, device="cuda"))
-        assert bool(gb.isfinite().all()) and float(gb[1]) == 0
+        assert bool(((lse.double() - low).abs() <= 16 * U * abs(low)).all())
+        assert bool((loss >= 0).all()) and bool((loss <= 16 * U * abs(low)).all())
+        gx, gw, gb = backward(x, w, bias, t, scale, lse, torch.ones(rows, device="cuda"))
+        assert all(bool(g.isfinite().all()) for g in (gx, gw, gb)) and bool((gb.abs() <= rows).all())
