@@ -74,7 +74,7 @@ __device__ __forceinline__ void ce_fused_part(const CeArgs& a, unsigned block, u
 
   // what stays: lane l holds s = l % 16 of each 16, 8 columns from 8 (l / 16) on of each 32
   u16x8_t fs[MF][KS];
-  float ref[MF], sum[MF];
+  float ref[MF], sum[MF], far[MF];
   f32x4 from[MF];  // not X: the items' biases, where the sums begin
   int target[MF];
 #pragma unroll
@@ -91,6 +91,7 @@ __device__ __forceinline__ void ce_fused_part(const CeArgs& a, unsigned block, u
     if constexpr (X) {
       ref[i] = in ? a.r.ref[s] : -kInfinity;
       target[i] = in ? a.r.target[s] - a.first : -1;
+      far[i] = in ? a.r.far[s] : 0.0f;
     } else {
       const float b = in ? a.bias[s] : -kInfinity;
       from[i] = f32x4{b, b, b, b};
@@ -100,7 +101,7 @@ __device__ __forceinline__ void ce_fused_part(const CeArgs& a, unsigned block, u
   bool away = false;  // the wave has rows whose lse is past kFar
   if constexpr (X) {
 #pragma unroll
-    for (int i = 0; i < MF; ++i) away |= s0 + 16 * i + (l & 15) < stay && a.r.far[s0 + 16 * i + (l & 15)] != 0.0f;
+    for (int i = 0; i < MF; ++i) away |= far[i] != 0.0f;
     away = __any(away);
   }
   f32x4 out[MF][CG];

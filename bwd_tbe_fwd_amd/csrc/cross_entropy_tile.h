@@ -62,10 +62,16 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
   const int n = wn + (l >> 4) * LEN;
   float bias[LEN];
 #pragma unroll
-  for (int c = 0; c < LEN; ++c) bias[c] = a.bias && n + c < n_left ? ce_bias(a.bias[n0 + n + c], a.most) : 0.0f;
+  for (int c = 0; c < LEN; ++c) bias[c] = a.bias && n + c < n_left ? a.bias[n0 + n + c] : 0.0f;
+  // behind the other loads, so that nothing waits between them
+  auto as_counted = [&] {
+#pragma unroll
+    for (int c = 0; c < LEN; ++c) bias[c] = ce_bias(bias[c], a.most);
+  };
   auto logit = [&](int i, int c) { return fmaf(acc[i][c / 4][c % 4], a.scale, bias[c]); };
   if constexpr (!BACK) {
     float2* stat = reinterpret_cast<float2*>(lds);  // [WN][BM]
+    as_counted();
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
       const int m = wm + 16 * i + (l & 15);
@@ -109,9 +115,28 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
       targets[i] = -1;
       if (m < m_left) {
         lses[i] = a.r.lse[m0 + m];
-        if (lses[i] == -kInfinity) lses[i] = kInfinity;  // every item is masked: no probability
         targets[i] = a.r.target[m0 + m];
         if (a.bias_part) grads[i] = a.r.grad[m0 + m];
+      }
+    }
+    as_counted();
+    bool far = false;
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      far |= fabsf(lses[i]) > kFar;
+#pragma unroll
+      for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] = logit(i, c);
+    }
+    if (__builtin_expect(__any(far), 0)) {
+      // lse is taken off before anything is rounded to powers of two: it is at least the row's largest logit, to the bit, so that
+      // no probability passes 1 however large they are
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        float less = lses[i] == -kInfinity ? kInfinity : lses[i];  // every item is masked: no probability
+        asm volatile("" : "+v"(less));  // keeps what follows from being worked out where it is not needed
+#pragma unroll
+        for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] -= less;
+        lses[i] = 0.0f;
       }
     }
 #pragma unroll
@@ -119,18 +144,9 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
       const int m = wm + 16 * i + (l & 15);
       const bool in = m < m_left;
       const unsigned at = in ? static_cast<unsigned>(targets[i] - a.first - n0 - n) : ~0u;
-      if (__any(fabsf(lses[i]) > kFar)) {
-        // lse is taken off before anything is rounded to powers of two: it is at least the row's largest logit, to the bit, so that
-        // no probability passes 1 however large they are (in every wave: training batch 5296 -> 5359 us)
-        float less = lses[i];
-        asm volatile("" : "+v"(less));  // keeps what follows from being worked out where it is not needed
+      const float base = fmaf(lses[i], -kLog2e, shift);
 #pragma unroll
-        for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] = __builtin_amdgcn_exp2f(fmaf(logit(i, c) - less, kLog2e, shift));
-      } else {
-        const float base = fmaf(lses[i], -kLog2e, shift);
-#pragma unroll
-        for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] = __builtin_amdgcn_exp2f(fmaf(logit(i, c), kLog2e, base));
-      }
+      for (int c = 0; c < LEN; ++c) acc[i][c / 4][c % 4] = __builtin_amdgcn_exp2f(fmaf(acc[i][c / 4][c % 4], kLog2e, base));
       if (__any(at < LEN)) {
         int here = static_cast<int>(at);
         asm volatile("" : "+v"(here));  // keeps what follows from being worked out where it is not needed
