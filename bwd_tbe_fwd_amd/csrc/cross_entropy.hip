@@ -263,7 +263,11 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(const float2* __restrict_
     return;
   }
   // no sum is left where every item is masked, or by the lowest value
-  const float lse = sum.y == 0.0f ? sum.x : sum.x + logf(sum.y), at = b.picked[c];
+  const float at = b.picked[c];
+  float lse = sum.y == 0.0f ? sum.x : sum.x + logf(sum.y);
+  // narrow rows that have only items whose biases over the scale are past the lowest value: these are not told apart, and lse is the
+  // target's logit
+  if (sum.y == 0.0f && lse <= b.most * -0.999999f && at < lse && at != -kInfinity) lse = at;
   const float loss = at == -kInfinity && !(lse != lse) ? kInfinity : lse - at;
   b.lse_out[b.row[c]] = lse;
   b.loss[b.row[c]] = loss < 0.0f ? 0.0f : loss;  // lse and the target's logit are rounded for themselves

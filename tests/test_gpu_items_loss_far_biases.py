@@ -72,3 +72,30 @@ def test_the_same_low_bias_everywhere(width, low):
         assert bool((loss >= 0).all()) and bool((loss <= 16 * U * abs(low)).all())
         gx, gw, gb = backward(x, w, bias, t, scale, lse, torch.ones(rows, device="cuda"))
         assert all(bool(g.isfinite().all()) for g in (gx, gw, gb)) and bool((gb.abs() <= rows).all())
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("scale", [0.5, -0.125, 2.0 ** -40])
+@pytest.mark.parametrize("low", [-LARGEST, -2e38, -1e38, -1e30])
+def test_only_low_biases_below_a_scale_of_one(width, scale, low):
+    """Over the scale such biases are past the lowest value.  Every item has the same one, so lse is that and the losses are 0 but
+    for roundings."""
+    for rows, items in ((90, 300), (5, 1), (300, 5000)):
+        x, w, t = matrix(rows, width, BF16, 1), matrix(items, width, BF16, 2, width ** -0.5), some_targets(rows, items, 0.2, 3)
+        there = (t >= 0) & (t < items)
+        bias = torch.full((items,), low, device="cuda")
+        loss, lse = forward(x, w, bias, t, scale)
+        assert bool(((lse[there].double() - low).abs() <= 16 * U * abs(low)).all())
+        assert bool((loss >= 0).all()) and bool((loss <= 16 * U * abs(low)).all())
+        gx, gw, gb = backward(x, w, bias, t, scale, lse, torch.ones(rows, device="cuda"))
+        assert all(bool(g.isfinite().all()) for g in (gx, gw, gb)) and bool((gb.abs() <= rows).all())
+        if items > 1:  # one item that is open takes all of the probability
+            bias[items // 2] = 0.0
+            loss, lse = forward(x, w, bias, t, scale)
+            assert bool((lse.abs() <= 20).all())
+            far = there & (t != items // 2)
+            assert bool(((loss[far].double() + low).abs() <= 16 * U * abs(low)).all())
+            gb = backward(x, w, bias, t, scale, lse, torch.ones(rows, device="cuda"))[2]
+            exp = -torch.bincount(t[there], minlength=items).double()
+            exp[items // 2] += int(there.sum())
+            assert bool(((gb.double() - exp).abs() <= 8 * U * rows).all())
