@@ -3,7 +3,8 @@
 // So few columns leave the matrix instructions no more to do for a logit than the exponential and what stands around it
 // leave the vector unit: at 128 columns 64 cycles of products for the 64 logits that a wave holds in a register, and 8 for
 // their exponential and 4 for each other instruction.  So the rows stay in registers, the items pass through LDS, and a
-// wave's products of 32 items are taken between the exponentials of the 32 items before.
+// wave's products of 32 items stand beside the exponentials of the 32 items before, which they do not wait for: the matrix unit
+// works on the ones while the vector unit takes the others, of this wave or of the other one of its SIMD.
 //  * A workgroup takes 64 MF rows, 16 MF a wave, and a range of the items.  MF = 4; MF = 1 for few rows, where the items'
 //    way from memory bounds it.
 //  * A ring of three tiles of 64 items in LDS, loaded two ahead, one barrier a tile.
@@ -13,7 +14,9 @@
 //    powers of two above it: most tiles change nothing but the sums.  A logit costs a multiply-add, an exponential, an
 //    addition and less than one instruction more.
 // 2048 rows, 2 M items of 128 columns: 1.06 to 1.11 ms, 0.99 PFLOP/s (2.49 ms by tiles of 256 x 256 without rows that
-// stay; 3% more without products between the exponentials).  Matrix instructions are busy 46% of the cycles.
+// stay).  Matrix instructions are busy 46% of the cycles.  An order of single products between the exponentials, asked of the
+// compiler, was not followed in this kernel (1104 us with the request, 1095 without), and where it was it cost 1 to 6% (2048 rows, 1 M
+// items of 64: 375 and 370; 64 rows, 1 M items of 128: 62 and 59).
 #pragma once
 
 #include "cross_entropy_tile.h"
@@ -101,16 +104,6 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
       }
     }
   };
-  // Products between the exponentials' instructions, an equal share each.
-  auto interleave = [&] {
-    constexpr int kProducts = MF * NF * KS, kVector = MF * (2 * LEN + 2);
-#pragma unroll
-    for (int q = 0; q < kProducts; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, (kVector + kProducts - 1) / kProducts, 0);
-      __builtin_amdgcn_sched_group_barrier(0x400, (MF * LEN + kProducts - 1) / kProducts, 0);
-    }
-  };
   // What an exponential's argument has a reference as.  Far out its rounding is worth powers of two, but a lane's exponentials of a
   // row all have the same, so it is taken out again where the reference moves and at the end.
   auto rounded = [&](float of) {
@@ -160,14 +153,12 @@ __global__ __launch_bounds__(256, 2) void ce_narrow_kernel(CeArgs a) {
       look(second);
       products(first, slot, 0);
       exponentials(second);
-      interleave();
     } else {
       products(first, slot, 0);
     }
     look(first);
     products(second, slot, 1);
     exponentials(first);
-    interleave();
   }
   if (t1 > t0) {
     look(second);
