@@ -12,11 +12,13 @@
 //    columns of row t are exchanged by 2 ((t / 4) % 4): both reads then find their banks free.
 //  * A row's factor goes into the exponent, ahead of the rounding of z; its sign is looked at where there is a negative one (a
 //    product each instead: 1 to 3.5% more).
+//  * Rows whose lse is past kFar have it taken off the logits ahead of the exponentials, behind a branch that other tiles jump over
+//    (0.3%).
 //  * A ring of three tiles of 64 t, loaded two ahead, one barrier a tile; two workgroups a CU, so that one's exponentials
 //    are taken while the other's products are.  192 s a workgroup at 128 columns, 256 at 64: what the registers hold.
-// Bound by the matrix instructions and the vector unit together (2048 rows, 500000 items of 128, all three gradients 0.96 to 0.99
-// ms, 1.08 PFLOP/s of products, the logits' counted twice as they are taken; matrix instructions busy 48% of the cycles; with z in
-// memory 1.99 ms).
+// Bound by the matrix instructions and the vector unit together (2048 rows, 500000 items of 128, all three gradients 0.93 ms, 1.12
+// PFLOP/s of products, the logits' counted twice as they are taken; matrix instructions busy 50% of the cycles; a call 0.95 to
+// 0.99 ms, with z in memory 1.99).
 #pragma once
 
 #include "cross_entropy_tile.h"

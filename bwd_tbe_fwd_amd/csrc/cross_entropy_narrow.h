@@ -13,7 +13,7 @@
 //  * A lane keeps a sum for each of its rows over all its items, less a reference that moves only when a logit is kSlack
 //    powers of two above it: most tiles change nothing but the sums.  A logit costs a multiply-add, an exponential, an
 //    addition and less than one instruction more.
-// 2048 rows, 2 M items of 128 columns: 1.06 to 1.11 ms, 0.99 PFLOP/s (2.49 ms by tiles of 256 x 256 without rows that
+// 2048 rows, 2 M items of 128 columns: 1.05 to 1.1 ms, 0.98 PFLOP/s (2.49 ms by tiles of 256 x 256 without rows that
 // stay).  Matrix instructions are busy 46% of the cycles.  An order of single products between the exponentials, asked of the
 // compiler, was not followed in this kernel (1104 us with the request, 1095 without), and where it was it cost 1 to 6% (2048 rows, 1 M
 // items of 64: 375 and 370; 64 rows, 1 M items of 128: 62 and 59).

@@ -29,9 +29,10 @@ __device__ __forceinline__ bool tile_place(int64_t m_tiles, int64_t n_tiles, int
 // Logits of BM rows and BN items, and what becomes of them.  The logits leave the matrix instructions 16 or 32 a lane and are
 // used up there: forward, a maximum and a sum of 16 bytes for every BN items leave the workgroup; backward, z.  Bound by the
 // matrix instructions, which wait while a tile's exponentials are taken, since 256 x 256 leave room for one workgroup a CU.
-// 8192 rows (0.9 of them with a target), 65536 items of 1024, bf16: forward 820 us, 1.21 PFLOP/s (busy 56% of the cycles; the
-// library's product alone, logits stored, all rows, takes 920); backward 16384 items 263 us (0.94, 40%): 0.24 GB of z are stored
-// in each.  8 rows, 131072 items: 41 us, 6.5 TB/s.
+// 8192 rows (0.9 of them with a target), 65536 items of 1024, bf16: forward 857 us, 1.15 PFLOP/s (busy 56% of the cycles; the
+// library's product alone, logits stored, all rows, takes 920); backward 16384 items 276 us (0.90, 40%): 0.24 GB of z are stored
+// in each.  8 rows, 131072 items: 51 us, 5.2 TB/s (41 where the last pass left half of the weights in the Infinity Cache).  Rows
+// with a far lse are looked for once a wave, behind all loads (right behind each row's: 16384 items 6 us more).
 template <int DT, bool BACK, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void ce_logits_kernel(CeArgs a) {
   constexpr int T = WM * WN * kWave;
@@ -190,7 +191,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM * BN <= 64 * 64 ? 4 : 2) void c
 // The two products of z.  X: the gradient of x, else of the weights; `block`: the workgroup among this gradient's.  A chiplet
 // takes whole shares of k where there are many: few rows' weights are then read by one (64 rows, 131072 items of 1000: 61 us,
 // and 85 with each share's tiles dealt to all eight).  Bound by the matrix instructions: 16384 items and 8192 rows (0.9 with a
-// target) of 1024, both 349 us, 1.42 PFLOP/s, busy 64% of the cycles.
+// target) of 1024, both 371 us, 1.33 PFLOP/s, busy 64% of the cycles.
 template <bool X, int BM, int BN, int WM, int WN>
 struct GradTile {
   static constexpr int T = WM * WN * kWave, MF = BM / WM / 16, NF = BN / WN / 16;

@@ -74,12 +74,16 @@ tbe_status tbe_lookup_backward(int64_t num_ids, int64_t items, int64_t width, co
  * bias is -infinity is masked: its probability is 0, and the loss of a row
  * with such a target is +infinity; a row with every item masked has lse
  * -infinity.  A row with an infinity or a NaN gives NaN (or an infinity) in
- * that row only.  scale is 0 or from 2^-64 to 2^64, of either sign.  Finite
- * biases are meant to be masks (of the lowest value) or below 1e38 and 1e38
- * |scale|; higher ones count as that.  Products, maxima and sums are kept in
- * fp32; where logits past 2^20 in size have no digits left behind the point,
- * losses and probabilities still stay finite.  The logits go through registers,
- * a tile of items at a time, and are never stored.  rows may be 0 and at most
+ * that row only.  scale is 0 or from 2^-64 to 2^64, of either sign.  Biases of
+ * the lowest value mask an item beside others that are not masked.  Where |scale|
+ * is below 1, finite biases count as the largest value times |scale| at most, in
+ * the target's logit too; items with biases below the lowest value times |scale|
+ * are not told apart by rows of up to 128 columns, and where a row has no others
+ * its lse is the target's logit.  Products, logits, maxima and sums are kept in
+ * fp32.  Logits that are so large that fp32 has no digits behind their point have
+ * the probabilities of the rounded logits: the largest one's is 1 where no other
+ * is near.  Losses are not below 0.  The logits go through registers, a tile of
+ * items at a time, and are never stored.  rows may be 0 and at most
  * TBE_CROSS_ENTROPY_MAX_ROWS; 1 <= items < 2^31 - 1; 1 <= width <=
  * TBE_CROSS_ENTROPY_MAX_WIDTH.  workspace: at least
  * tbe_cross_entropy_forward_workspace_bytes bytes, 256-byte aligned; the bytes
